@@ -324,6 +324,57 @@ ND_API int nd_swa_sink_decode_noalloc(const void *q, const nd_kv_cache *cache,
                                       int n_q_heads, int window, void *out,
                                       float *lse, nd_stream_t stream);
 
+/*
+ * Reads a cache back: every sequence's visible keys and values, dequantised
+ * (the fp32 product code * scale, then rounded to dtype), in position order
+ * and in the layout a prefill has them -- the way back from nd_kv_cache_from_prefill, e.g. to
+ * move a session to a cache of another shape, to prefill after it, or to
+ * inspect it.
+ *   row r of sequence b, r < lengths[b] = sink_len + min(ring_len, window):
+ *     r < sink_len: sink slot r (position r); then the newest
+ *     min(ring_len, window) ring entries, oldest first (positions ending at
+ *     seq_len - 1)
+ *   k_out, v_out  dtype [batch][n_rows][n_kv_heads][head_dim]; rows from
+ *                 lengths[b] on are left as they were
+ *   positions     int32 [batch][n_rows], or NULL; -1 from lengths[b] on
+ *   lengths       int32 [batch], or NULL
+ * n_rows >= sink_cap + min(ring_cap, window), the most rows a sequence can
+ * have; window >= 1; head_dim 32, 64, 128 or 256; batch <= 65535.  A sequence
+ * whose metadata is out of range sets device error flag 2, has length 0 and
+ * no row written.
+ */
+ND_API int nd_kv_cache_read(const nd_kv_cache *cache, int window, nd_dtype dtype, int n_rows,
+                            void *k_out, void *v_out, int32_t *positions, int32_t *lengths,
+                            nd_stream_t stream);
+
+/*
+ * One decode step of a batch whose sequences share one pinned prefix (the
+ * same tool definitions, [N2] "KV Sinks for Tools", in front of every
+ * session): the prefix is kept once, as the sink region of a one-row cache,
+ * and its keys are read and multiplied once for the whole batch.  Each
+ * query attends one softmax over [the prefix's sink slots, its own sequence's
+ * sink slots, its ring entries within `window`]; otherwise as
+ * nd_swa_sink_decode, whose result on caches that each hold a copy of the
+ * prefix in front of their own sinks this equals up to rounding.
+ *   prefix  batch 1, sink_cap >= 1, the n_kv_heads and head_dim of cache.
+ *           sink_len may be anything from 0 to sink_cap; the prefix's ring is
+ *           not read.  nd_kv_cache_from_prefill with a sink flag on every
+ *           position fills it from a prefill of the prompt.
+ *   q, out, lse, window, n_q_heads  as nd_swa_sink_decode; batch <= 65535
+ * A sequence that sees no key gets out = 0, lse = -inf.  The prefix's keys
+ * and values are taken as fp16 after a power-of-two scaling (each within
+ * 2^-11 of code * scale, relative), products and sums in fp32.
+ * Partial results go to the workspace (device, 16-byte aligned) of
+ * nd_shared_prefix_decode_workspace_size(batch, n_q_heads, n_kv_heads,
+ * head_dim, prefix->sink_cap, cache->sink_cap + cache->ring_cap) bytes.
+ */
+ND_API size_t nd_shared_prefix_decode_workspace_size(int batch, int n_q_heads, int n_kv_heads,
+                                                     int head_dim, int prefix_cap, int max_slots);
+ND_API int nd_shared_prefix_decode(const void *q, const nd_kv_cache *prefix,
+                                   const nd_kv_cache *cache, int n_q_heads, int window,
+                                   void *out, float *lse, void *workspace,
+                                   size_t workspace_bytes, nd_stream_t stream);
+
 /* ------------------------------------------------------------------------ */
 /* Compressed-attention decode                                               */
 /* ------------------------------------------------------------------------ */
@@ -536,6 +587,52 @@ ND_API int nd_swa_sink_prefill_tiles(const void *workspace, int batch, int T, in
  */
 ND_API int nd_rope_apply(const void *x, void *y, int batch, int T, int n_heads,
                   int head_dim, float rope_theta, nd_stream_t stream);
+
+/*
+ * RMS norm of each query and key head, with the rotation in the same pass:
+ * for a head's row x of a token at position p and weight w,
+ *   y = x * rsqrt(mean(x^2) + eps) * w, then nd_rope_apply's rotation at p,
+ * in fp32 throughout, rounded once to dtype.
+ *   q  dtype, rows of [n_q_heads][head_dim], q_stride elements from one token
+ *      to the next (token b*T + t; n_q_heads*head_dim when q is contiguous,
+ *      the row length of a fused projection when q is a slice of one)
+ *   k  likewise with n_k_heads and k_stride; either of q, k may have 0 heads
+ *      (its pointers are then not read)
+ *   q_weight, k_weight  fp32 [head_dim], 16-byte aligned, or NULL (ones)
+ *   positions  int32 [batch][T], or NULL (position t); any int32
+ *   q_out, k_out  dtype [batch][T][heads][head_dim], contiguous; may equal q / k
+ *      where those are contiguous
+ * rope_theta 0 = no rotation.  eps >= 0.  Strides are multiples of 16 bytes.
+ * head_dim 32, 64, 128 or 256.  p * theta^(-2i/head_dim) is reduced to a
+ * fraction of a turn in 64-bit integers; sine and cosine are fp32.
+ */
+ND_API int nd_qk_norm_rope(const void *q, const void *k, nd_dtype dtype, int batch, int T,
+                           int n_q_heads, int n_k_heads, int head_dim, int64_t q_stride,
+                           int64_t k_stride, const float *q_weight, const float *k_weight,
+                           float eps, float rope_theta, const int32_t *positions, void *q_out,
+                           void *k_out, nd_stream_t stream);
+
+/*
+ * The same for one decode token per sequence, with the cache append: the
+ * token's position is p = seq_len + *pos_base; q is normalised and rotated
+ * into q_out, k_new is normalised, rotated, rounded to bf16 and quantised, and
+ * v_new quantised, into the slot that nd_kv_append_quant gives them (ring, or
+ * sink with to_sink = 1), and the metadata advances.  The codes are those of
+ * nd_qk_norm_rope followed by nd_kv_append_quant.
+ *   q      bf16 [batch][n_q_heads][head_dim], q_stride elements between sequences
+ *   k_new, v_new  bf16 [batch][n_kv_heads][head_dim], k_stride / v_stride likewise
+ *   pos_base  device int32, or NULL (0): what stands before the cache's first
+ *          token, e.g. the seq_len of a shared prefix
+ *   q_out  bf16 [batch][n_q_heads][head_dim], contiguous
+ * A rejected sink append writes nothing for that sequence, q_out included, and
+ * sets device error flag 2.
+ */
+ND_API int nd_qk_norm_rope_append(const void *q, const nd_kv_cache *cache, const void *k_new,
+                                  const void *v_new, int n_q_heads, int64_t q_stride,
+                                  int64_t k_stride, int64_t v_stride, const float *q_weight,
+                                  const float *k_weight, float eps, float rope_theta,
+                                  const int32_t *pos_base, int to_sink, void *q_out,
+                                  nd_stream_t stream);
 
 /*
  * Block pooling with midpoint rotation ([C3] "Pool before rotating, not

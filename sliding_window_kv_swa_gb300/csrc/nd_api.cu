@@ -747,6 +747,108 @@ int nd_rope_apply(const void *x, void *y, int batch, int T, int n_heads, int hea
                             reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// Token (or sequence) strides of an input whose rows of `heads` x `head_dim`
+// lie inside a wider one: at least the row, and 16-byte aligned.
+static bool stride_ok(int64_t stride, int heads, int head_dim, int elem) {
+  return stride >= int64_t(heads) * head_dim && stride % (16 / elem) == 0;
+}
+
+static bool norm_args_ok(float eps, float theta, const float *q_weight, const float *k_weight) {
+  // (NaN fails every comparison)
+  return eps >= 0.f && eps < 1e30f && theta >= 0.f && theta < 1e30f && aligned16(q_weight) && aligned16(k_weight);
+}
+
+int nd_qk_norm_rope(const void *q, const void *k, nd_dtype dtype, int batch, int T, int n_q_heads, int n_k_heads,
+                    int head_dim, int64_t q_stride, int64_t k_stride, const float *q_weight, const float *k_weight,
+                    float eps, float rope_theta, const int32_t *positions, void *q_out, void *k_out,
+                    nd_stream_t stream) {
+  if (dtype != ND_F32 && dtype != ND_BF16) return ND_ERR_INVALID_ARG;
+  if (batch < 0 || T < 0 || n_q_heads < 0 || n_k_heads < 0 || n_q_heads + int64_t(n_k_heads) > 65536) return ND_ERR_INVALID_ARG;
+  if (head_dim <= 0 || head_dim % 32) return ND_ERR_INVALID_ARG;
+  if (head_dim != 32 && head_dim != 64 && head_dim != 128 && head_dim != 256) return ND_ERR_UNSUPPORTED;
+  if (!norm_args_ok(eps, rope_theta, q_weight, k_weight)) return ND_ERR_INVALID_ARG;
+  if (size_t(batch) * T == 0 || n_q_heads + n_k_heads == 0) return ND_OK;
+  const int elem = dtype == ND_F32 ? 4 : 2;
+  if (n_q_heads && (!q || !q_out || !aligned16(q) || !aligned16(q_out) || !stride_ok(q_stride, n_q_heads, head_dim, elem)))
+    return ND_ERR_INVALID_ARG;
+  if (n_k_heads && (!k || !k_out || !aligned16(k) || !aligned16(k_out) || !stride_ok(k_stride, n_k_heads, head_dim, elem)))
+    return ND_ERR_INVALID_ARG;
+  int st = check_device(nullptr);
+  if (st != ND_OK) return st;
+  QkNormRope a = {q, k, q_stride, k_stride, batch, T, n_q_heads, n_k_heads, head_dim, q_weight, k_weight, eps,
+                  rope_theta, positions, q_out, k_out};
+  return finish(launch_qk_norm_rope(a, dtype == ND_F32, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int nd_qk_norm_rope_append(const void *q, const nd_kv_cache *cache, const void *k_new, const void *v_new,
+                           int n_q_heads, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                           const float *q_weight, const float *k_weight, float eps, float rope_theta,
+                           const int32_t *pos_base, int to_sink, void *q_out, nd_stream_t stream) {
+  int st = validate_cache(cache);
+  if (st != ND_OK) return st;
+  const int d = cache->head_dim, Hkv = cache->n_kv_heads;
+  if (n_q_heads <= 0 || n_q_heads > 65536) return ND_ERR_INVALID_ARG;
+  if (!to_sink && cache->ring_cap <= 0) return ND_ERR_INVALID_ARG;
+  if (to_sink && cache->sink_cap <= 0) return ND_ERR_INVALID_ARG;
+  if (d != 32 && d != 64 && d != 128 && d != 256) return ND_ERR_UNSUPPORTED;
+  if (!norm_args_ok(eps, rope_theta, q_weight, k_weight)) return ND_ERR_INVALID_ARG;
+  if (cache->batch == 0) return ND_OK;
+  if (!q || !k_new || !v_new || !q_out || !aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(q_out))
+    return ND_ERR_INVALID_ARG;
+  if (!stride_ok(q_stride, n_q_heads, d, 2) || !stride_ok(k_stride, Hkv, d, 2) || !stride_ok(v_stride, Hkv, d, 2))
+    return ND_ERR_INVALID_ARG;
+  if ((st = check_device(nullptr)) != ND_OK) return st;
+  QkNormRope a = {q, k_new, q_stride, k_stride, cache->batch, 1, n_q_heads, Hkv, d, q_weight, k_weight, eps,
+                  rope_theta, nullptr, q_out, nullptr};
+  return finish(launch_qk_norm_append(*cache, a, v_new, v_stride, pos_base, to_sink ? 1 : 0, device_error_word(),
+                                      reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int nd_kv_cache_read(const nd_kv_cache *cache, int window, nd_dtype dtype, int n_rows, void *k_out, void *v_out,
+                     int32_t *positions, int32_t *lengths, nd_stream_t stream) {
+  int st = validate_cache(cache);
+  if (st != ND_OK) return st;
+  if ((dtype != ND_F32 && dtype != ND_BF16) || window < 1) return ND_ERR_INVALID_ARG;
+  const int d = cache->head_dim;
+  if (d != 32 && d != 64 && d != 128 && d != 256) return ND_ERR_UNSUPPORTED;
+  if (cache->batch > 65535) return ND_ERR_UNSUPPORTED;
+  // every row that any metadata can make visible has its place in the output
+  const int64_t need = int64_t(cache->sink_cap) + (cache->ring_cap < window ? cache->ring_cap : window);
+  if (n_rows < need) return ND_ERR_INVALID_ARG;
+  if (cache->batch == 0 || n_rows == 0) return ND_OK;
+  if (!k_out || !v_out || !aligned16(k_out) || !aligned16(v_out)) return ND_ERR_INVALID_ARG;
+  if ((st = check_device(nullptr)) != ND_OK) return st;
+  return finish(launch_cache_read(*cache, window, dtype == ND_F32, n_rows, k_out, v_out, positions, lengths,
+                                  device_error_word(), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t nd_shared_prefix_decode_workspace_size(int batch, int n_q_heads, int n_kv_heads, int head_dim,
+                                              int prefix_cap, int max_slots) {
+  if (batch <= 0 || n_q_heads <= 0 || n_kv_heads <= 0 || n_q_heads % n_kv_heads || head_dim <= 0 || prefix_cap <= 0 ||
+      max_slots <= 0)
+    return 0;
+  return round_up(shared_decode_workspace_bytes(batch, n_q_heads, n_kv_heads, head_dim, prefix_cap, max_slots), 256);
+}
+
+int nd_shared_prefix_decode(const void *q, const nd_kv_cache *prefix, const nd_kv_cache *cache, int n_q_heads,
+                            int window, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                            nd_stream_t stream) {
+  int st = validate_decode(q, cache, n_q_heads, window, out);
+  if (st != ND_OK) return st;
+  if ((st = validate_cache(prefix)) != ND_OK) return st;
+  if (prefix->batch != 1 || prefix->sink_cap < 1 || prefix->n_kv_heads != cache->n_kv_heads ||
+      prefix->head_dim != cache->head_dim)
+    return ND_ERR_INVALID_ARG;
+  if (cache->batch == 0) return ND_OK;
+  if (cache->batch > 65535) return ND_ERR_UNSUPPORTED;
+  const size_t need = nd_shared_prefix_decode_workspace_size(cache->batch, n_q_heads, cache->n_kv_heads, cache->head_dim,
+                                                             prefix->sink_cap, cache->sink_cap + cache->ring_cap);
+  if (!workspace || workspace_bytes < need || !aligned16(workspace)) return ND_ERR_WORKSPACE;
+  if ((st = check_device(nullptr)) != ND_OK) return st;
+  return finish(launch_shared_decode(q, *prefix, *cache, n_q_heads, window, out, lse, workspace, device_error_word(),
+                                     reinterpret_cast<cudaStream_t>(stream)));
+}
+
 int nd_kv_compress_pool(const void *k, const void *v, int batch, int T, int n_heads, int head_dim,
                         int block, float rope_theta, void *pooled_k, void *pooled_v,
                         nd_stream_t stream) {

@@ -57,6 +57,13 @@ cudaError_t launch_decode(const void *q, const nd_kv_cache &c, int n_q_heads, in
                           const void *v_new = nullptr);
 bool decode_step_fuses(int batch, int n_kv_heads, int max_slots, int head_dim);
 
+// Decode of a batch that shares the sink prefix of `prefix` (one row): each
+// sequence's own slots and the prefix, merged.
+size_t shared_decode_workspace_bytes(int batch, int n_q_heads, int n_kv_heads, int head_dim, int prefix_cap,
+                                     int max_slots);
+cudaError_t launch_shared_decode(const void *q, const nd_kv_cache &prefix, const nd_kv_cache &c, int n_q_heads,
+                                 int window, void *out, float *lse, void *ws, int *err, cudaStream_t stream);
+
 // Per sequence: rotate q into q_rot, append the token to the compressed
 // cache (pinned slot or ring, block sums, a pooled slot when the token closes
 // its block) and advance the metadata; a dependent launch.
@@ -102,6 +109,28 @@ struct Freqs {
   double f[kMaxHalf];
 };
 Freqs make_freqs(int head_dim, float theta);
+
+// Per-head RMS norm and rotation of q (Hq heads) and k (Hk heads) of every
+// token; positions NULL: t within its row.  Strides in elements between
+// tokens (sequences, for the append).  launch_qk_norm_append takes one token
+// per sequence at position seq_len + *pos_base (NULL: 0), and quantises k and
+// v into the cache.
+struct QkNormRope {
+  const void *q, *k;
+  int64_t q_stride, k_stride;
+  int batch, T, Hq, Hk, head_dim;
+  const float *q_weight, *k_weight;  // NULL: ones
+  float eps, theta;
+  const int32_t *positions;
+  void *q_out, *k_out;
+};
+cudaError_t launch_qk_norm_rope(const QkNormRope &a, bool f32, cudaStream_t stream);
+cudaError_t launch_qk_norm_append(const nd_kv_cache &c, const QkNormRope &a, const void *v, int64_t v_stride,
+                                  const int32_t *pos_base, int to_sink, int *err, cudaStream_t stream);
+
+// Reads the cache back in position order into [B][n_rows][Hkv][d].
+cudaError_t launch_cache_read(const nd_kv_cache &c, int window, bool f32, int n_rows, void *k, void *v,
+                              int32_t *positions, int32_t *lengths, int *err, cudaStream_t stream);
 
 size_t rope_table_bytes(int T, int head_dim);
 // Builds the (cos, sin) table of positions 0..T-1 into `table` (float2

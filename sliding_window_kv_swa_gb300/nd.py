@@ -92,6 +92,11 @@ def _lib():
             "nd_swa_sink_chunk_prefill_workspace_size": (S, [I, I, I, I, I, I, I, I]),
             "nd_swa_sink_chunk_prefill": (I, [P, P, P, I, P, I, I, P, P, P, S, P]),
             "nd_swa_sink_chunk_prefill_tiles": (I, [P, I, I, I, I, I, I, I, I, P]),
+            "nd_kv_cache_read": (I, [P, I, I, I, P, P, P, P, P]),
+            "nd_shared_prefix_decode_workspace_size": (S, [I, I, I, I, I, I]),
+            "nd_shared_prefix_decode": (I, [P, P, P, I, I, P, P, P, S, P]),
+            "nd_qk_norm_rope": (I, [P, P, I, I, I, I, I, I, L, L, P, P, F, F, P, P, P, P]),
+            "nd_qk_norm_rope_append": (I, [P, P, P, P, I, L, L, L, P, P, F, F, P, I, P, P]),
             "nd_rope_apply": (I, [P, P, I, I, I, I, F, P]),
             "nd_kv_compress_pool": (I, [P, P, I, I, I, I, I, F, P, P, P]),
             "nd_kv_compress_pool_rope_workspace_size": (S, [I, I, F]),
@@ -123,6 +128,8 @@ EXPORTED = ("nd_version", "nd_status_string", "nd_last_cuda_error", "nd_device_e
             "nd_compressed_prefill_workspace_size", "nd_compressed_prefill",
             "nd_swa_sink_chunk_prefill_workspace_size", "nd_swa_sink_chunk_prefill",
             "nd_swa_sink_chunk_prefill_tiles",
+            "nd_kv_cache_read", "nd_shared_prefix_decode_workspace_size", "nd_shared_prefix_decode",
+            "nd_qk_norm_rope", "nd_qk_norm_rope_append",
             "nd_rope_apply", "nd_kv_compress_pool", "nd_kv_compress_pool_rope_workspace_size",
             "nd_kv_compress_pool_rope", "nd_kv_budget_window")
 
@@ -400,6 +407,180 @@ def nd_swa_sink_decode_noalloc(q: torch.Tensor, cache: KVCache, window: int, out
     _check("nd_swa_sink_decode_noalloc", _lib().nd_swa_sink_decode_noalloc(
         _ptr(q), ctypes.byref(s), Hq, int(window), _ptr(out), _ptr(lse), _stream(stream)))
     return out
+
+
+def _want(cond: bool, what: str) -> None:
+    if not cond:
+        raise ValueError(what)
+
+
+def _like(t: Optional[torch.Tensor], name: str, shape, dtype, device, none_ok: bool = False) -> Optional[int]:
+    """The address of a contiguous device tensor of this shape, type and device."""
+    if t is None and none_ok:
+        return None
+    if t is None or t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, name: str) -> int:
+    """The stride (elements) from one token to the next of [..., heads, d] rows
+    that may lie inside wider ones (a slice of a fused projection)."""
+    *lead, H, d = t.shape
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    if t.numel() == 0:
+        return H * d
+    st = t.stride()
+    ok = st[-1] == 1 and (st[-2] == d or H == 1)
+    step = st[-3]
+    if len(lead) == 2:  # [B, T]: one stride for the tokens of all rows
+        if lead[1] == 1:
+            step = st[-4]
+        elif lead[0] > 1:
+            ok = ok and st[-4] == lead[1] * step
+    elif lead[0] == 1:
+        step = H * d
+    if lead[0] * lead[-1] == 1:
+        step = H * d
+    if not ok:
+        raise ValueError(f"{name}: heads and channels must be contiguous, and the tokens evenly spaced")
+    return step
+
+
+def _on_current(device) -> None:
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {device}; libnd launches on the current CUDA device")
+
+
+def nd_kv_cache_read(cache: KVCache, window: int, dtype: torch.dtype = torch.bfloat16,
+                     k_out: Optional[torch.Tensor] = None, v_out: Optional[torch.Tensor] = None,
+                     positions: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None, stream=None):
+    """The cache's visible keys and values in position order: (k, v
+    [B][rows][Hkv][d], positions int32 [B][rows], lengths int32 [B]), rows =
+    sink_cap + min(ring_cap, window) unless k_out has more.  Rows from
+    lengths[b] on keep what k_out / v_out held (nothing in particular when they
+    are made here); their positions are -1."""
+    dev = cache.k_codes.device
+    _on_current(dev)
+    B, Hkv, d = cache.batch, cache.n_kv_heads, cache.head_dim
+    if k_out is not None:
+        dtype = k_out.dtype
+        _want(k_out.dim() == 4, "k_out must have shape [B, rows, Hkv, d]")
+    rows = k_out.shape[1] if k_out is not None else cache.sink_cap + min(cache.ring_cap, int(window))
+    code = {torch.float32: ND_F32, torch.bfloat16: ND_BF16}.get(dtype)
+    _want(code is not None, f"unsupported dtype {dtype}")
+    shape = (B, rows, Hkv, d)
+    if k_out is None:
+        _want(rows >= 0, "window must be at least 1")
+        k_out = torch.empty(shape, dtype=dtype, device=dev)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=dtype, device=dev)
+    if positions is None:
+        positions = torch.empty((B, rows), dtype=torch.int32, device=dev)
+    if lengths is None:
+        lengths = torch.empty(B, dtype=torch.int32, device=dev)
+    s = cache.struct()
+    _check("nd_kv_cache_read", _lib().nd_kv_cache_read(
+        ctypes.byref(s), int(window), code, rows, _like(k_out, "k_out", shape, dtype, dev),
+        _like(v_out, "v_out", shape, dtype, dev), _like(positions, "positions", (B, rows), torch.int32, dev),
+        _like(lengths, "lengths", (B,), torch.int32, dev), _stream(stream)))
+    return k_out, v_out, positions, lengths
+
+
+def nd_shared_prefix_decode_workspace_size(batch: int, n_q_heads: int, n_kv_heads: int, head_dim: int,
+                                           prefix_cap: int, max_slots: int) -> int:
+    return int(_lib().nd_shared_prefix_decode_workspace_size(batch, n_q_heads, n_kv_heads, head_dim, prefix_cap,
+                                                             max_slots))
+
+
+def nd_shared_prefix_decode(q: torch.Tensor, prefix: KVCache, cache: KVCache, window: int,
+                            out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                            workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """nd_swa_sink_decode for sequences that share the sink region of `prefix`
+    (a cache of one row) in front of their own cache; returns out."""
+    dev = q.device
+    _on_current(dev)
+    _want(q.dim() == 3, "q must have shape [B, Hq, d]")
+    B, Hq, d = q.shape
+    _want((B, d) == (cache.batch, cache.head_dim), "q and the cache disagree on batch or head_dim")
+    _want(prefix.k_codes.device == dev and cache.k_codes.device == dev, f"the caches must be on {dev}")
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+    if workspace is None:
+        nbytes = nd_shared_prefix_decode_workspace_size(B, Hq, cache.n_kv_heads, d, prefix.sink_cap,
+                                                        cache.sink_cap + cache.ring_cap)
+        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+    ps, cs = prefix.struct(), cache.struct()
+    _check("nd_shared_prefix_decode", _lib().nd_shared_prefix_decode(
+        _like(q, "q", q.shape, torch.bfloat16, dev), ctypes.byref(ps), ctypes.byref(cs), Hq, int(window),
+        _like(out, "out", q.shape, torch.bfloat16, dev), _like(lse, "lse", (B, Hq), torch.float32, dev, True),
+        _ptr(workspace), workspace.nbytes, _stream(stream)))
+    return out
+
+
+def nd_qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], q_weight: Optional[torch.Tensor] = None,
+                    k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, rope_theta: float = 0.0,
+                    positions: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                    k_out: Optional[torch.Tensor] = None, stream=None):
+    """RMS norm of each head of q [B, T, Hq, d] and k [B, T, Hk, d] (bf16 or
+    fp32; slices of a fused projection are taken as they are; either may be
+    None) with weights fp32 [d], then the rotation at positions int32 [B, T]
+    (None: t).  Returns (q_out, k_out), contiguous."""
+    one = q if q is not None else k
+    _want(one is not None, "q or k must be given")
+    dev = one.device
+    _on_current(dev)
+    args = []
+    for t, o, name in ((q, q_out, "q"), (k, k_out, "k")):
+        if t is None:
+            args.append((0, 0, None, None, None))
+            continue
+        _want(t.dim() == 4 and t.shape[:2] == one.shape[:2] and t.shape[3] == one.shape[3] and t.dtype == one.dtype
+              and t.device == dev, f"{name} must have shape [B, T, heads, d], q's type and device")
+        if o is None:
+            o = torch.empty(t.shape, dtype=t.dtype, device=dev)
+        args.append((t.shape[2], _rows(t, name), t.data_ptr(), _like(o, name + "_out", t.shape, t.dtype, dev), o))
+    B, T, _, d = one.shape
+    (Hq, sq, pq, oq, q_out), (Hk, sk, pk, ok, k_out) = args
+    _check("nd_qk_norm_rope", _lib().nd_qk_norm_rope(
+        pq, pk, _dtype_code(one), B, T, Hq, Hk, d, sq, sk, _like(q_weight, "q_weight", (d,), torch.float32, dev, True),
+        _like(k_weight, "k_weight", (d,), torch.float32, dev, True), float(eps), float(rope_theta),
+        _like(positions, "positions", (B, T), torch.int32, dev, True), oq, ok, _stream(stream)))
+    return q_out, k_out
+
+
+def nd_qk_norm_rope_append(q: torch.Tensor, cache: KVCache, k_new: torch.Tensor, v_new: torch.Tensor,
+                           q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                           eps: float = 1e-6, rope_theta: float = 0.0, pos_base: Optional[torch.Tensor] = None,
+                           to_sink: bool = False, q_out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """One decode token per sequence: q [B, Hq, d] and k_new [B, Hkv, d] (bf16,
+    slices of a fused projection are taken as they are) are normalised per head
+    and rotated at seq_len + pos_base (int32 tensor of one element, or None);
+    k_new and v_new are quantised into the cache.  Returns q_out."""
+    dev = q.device
+    _on_current(dev)
+    B, Hkv, d = cache.batch, cache.n_kv_heads, cache.head_dim
+    _want(q.dim() == 3 and q.shape[0] == B and q.shape[2] == d and q.dtype == torch.bfloat16 and
+          cache.k_codes.device == dev, "q must be bf16 [B, Hq, d] on the cache's device")
+    strides = [_rows(q, "q")]
+    for t, name in ((k_new, "k_new"), (v_new, "v_new")):
+        _want(t.shape == (B, Hkv, d) and t.dtype == torch.bfloat16 and t.device == dev,
+              f"{name} must be bf16 [B, Hkv, d] on the cache's device")
+        strides.append(_rows(t, name))
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+    if pos_base is not None:
+        _want(pos_base.numel() == 1 and pos_base.dtype == torch.int32 and pos_base.device == dev,
+              "pos_base must be one int32 on the cache's device")
+    s = cache.struct()
+    _check("nd_qk_norm_rope_append", _lib().nd_qk_norm_rope_append(
+        q.data_ptr(), ctypes.byref(s), k_new.data_ptr(), v_new.data_ptr(), q.shape[1], *strides,
+        _like(q_weight, "q_weight", (d,), torch.float32, dev, True),
+        _like(k_weight, "k_weight", (d,), torch.float32, dev, True), float(eps), float(rope_theta),
+        None if pos_base is None else pos_base.data_ptr(), 1 if to_sink else 0,
+        _like(q_out, "q_out", q.shape, torch.bfloat16, dev), _stream(stream)))
+    return q_out
 
 
 def nd_compressed_decode_step_workspace_size(batch: int, n_q_heads: int, n_kv_heads: int, head_dim: int,
