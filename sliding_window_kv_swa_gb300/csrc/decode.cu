@@ -39,6 +39,7 @@
 
 #include "nd_common.cuh"
 #include "nd_internal.h"
+#include "shared_prefix.cuh"
 
 namespace nd {
 
@@ -65,9 +66,6 @@ struct DecodeParams {
   // (NULL: plain decode).  The launch is then a thread-block cluster over one
   // sequence's (split, KV head) CTAs.
   const uint16_t *k_new, *v_new;
-  // kPart builds only (the partials of a shared-prefix decode): slots walked
-  // (a prefix of the pair's slots) and whether every sequence reads row 0
-  int walk, shared;
 };
 
 // Cluster barrier halves: every thread arrives once it no longer needs the
@@ -215,9 +213,6 @@ __global__ void __launch_bounds__(NW * 32, D == 128 ? (ST == 4 ? 3 : 2) : (NW ==
   const int G = p.G;
   const int nslot = c.sink_cap + c.ring_cap;
   const size_t pair = size_t(b) * c.n_kv_heads + hkv;
-  // the cache row read: sequence b's own, or the one shared row
-  const int cb = kPart && p.shared ? 0 : b;
-  const size_t cpair = kPart ? size_t(cb) * c.n_kv_heads + hkv : pair;
 
   // The launch allows programmatic dependent launch: this grid may be
   // scheduled while the previous kernel on the stream is still running.
@@ -236,7 +231,7 @@ __global__ void __launch_bounds__(NW * 32, D == 128 ? (ST == 4 ? 3 : 2) : (NW ==
     v_row = load_row_words<D>(p.v_new + pair * D, lane);
   }
   if (threadIdx.x == 0) {
-    int sl = c.sink_len[cb], rs = c.ring_start[cb], rl = c.ring_len[cb];
+    int sl = c.sink_len[b], rs = c.ring_start[b], rl = c.ring_len[b];
     const bool sane = sl >= 0 && sl <= c.sink_cap && rl >= 0 && rl <= c.ring_cap && rs >= 0 &&
                       (c.ring_cap == 0 || rs < c.ring_cap);
     int n_vis = 0, rs_eff = 0, new_slot = -1;
@@ -280,12 +275,12 @@ __global__ void __launch_bounds__(NW * 32, D == 128 ? (ST == 4 ? 3 : 2) : (NW ==
   // so the copies start before the metadata read lands, and the metadata only
   // masks slots that are not visible.
   const int v_begin = split * p.slots_per_cta;
-  const int v_end = min(v_begin + p.slots_per_cta, kPart ? p.walk : nslot);
+  const int v_end = min(v_begin + p.slots_per_cta, nslot);
 
-  const int8_t *kc = c.k_codes + cpair * nslot * D;
-  const int8_t *vc = c.v_codes + cpair * nslot * D;
-  const float *ks = c.k_scale + cpair * nslot * NG;
-  const float *vs = c.v_scale + cpair * nslot * NG;
+  const int8_t *kc = c.k_codes + pair * nslot * D;
+  const int8_t *vc = c.v_codes + pair * nslot * D;
+  const float *ks = c.k_scale + pair * nslot * NG;
+  const float *vs = c.v_scale + pair * nslot * NG;
 
   const uint32_t my_stages = smem_u32(smem) + warp * kStages * S::kBytes;
   // step n of this warp covers virtual slots base(n) .. base(n)+15
@@ -652,28 +647,43 @@ __global__ void __launch_bounds__(D) decode_combine_kernel(const DecodeParams p)
   if (ch == 0 && p.lse) p.lse[row] = L > 0.f ? (M + __log2f(L)) * 0.6931471805599453f : -INFINITY;
 }
 
-// Merge the own and the shared partials of one (sequence, query head) per block.
+// Merge the own partials and the shared prefix's of one (sequence, query head)
+// per block.
 template <int D>
-__global__ void __launch_bounds__(D) shared_combine_kernel(const DecodeParams own, const DecodeParams pre) {
+__global__ void __launch_bounds__(D) shared_combine_kernel(const DecodeParams p, const PrefixParts pre,
+                                                           const int32_t *prefix_len, int prefix_cap, int prefix_grid) {
+  pdl_wait();
   const int row = blockIdx.x;  // b * Hq + h
-  const int b = row / own.Hq, hq = row % own.Hq;
-  const int hkv = hq / own.G, h = hq % own.G;
-  const size_t pair = size_t(b) * own.c.n_kv_heads + hkv;
+  const int b = row / p.Hq, hq = row % p.Hq;
+  const int hkv = hq / p.G, h = hq % p.G;
+  const size_t pair = size_t(b) * p.c.n_kv_heads + hkv;
   const int ch = threadIdx.x;
   float M = -INFINITY, L = 0.f, O = 0.f;
-  for (int s = 0; s < own.n_split + pre.n_split; ++s) {
-    const DecodeParams &p = s < own.n_split ? own : pre;
-    const size_t part = (pair * p.n_split + (s < own.n_split ? s : s - own.n_split)) * p.G + h;
-    const float m = p.ws_ml[part * 2];
-    if (m == -INFINITY) continue;
-    const float m_new = fmaxf(M, m), f_old = M == -INFINITY ? 0.f : ex2(M - m_new), f = ex2(m - m_new);
-    L = L * f_old + f * p.ws_ml[part * 2 + 1];
-    O = O * f_old + f * p.ws_o[part * D + ch];
+  auto merge = [&](float m, float l, float o) {
+    if (m == -INFINITY) return;
+    const float m_new = fmaxf(M, m), f_old = ex2(M - m_new), f = ex2(m - m_new);
+    L = L * f_old + f * l;
+    O = O * f_old + f * o;
     M = m_new;
+  };
+  const PrefixPlan pl = prefix_plan(*prefix_len, prefix_cap, p.c.n_kv_heads, p.c.batch * p.G, prefix_grid);
+  if (pl.nt > 0) {
+    const int r = b * p.G + h, rr = r % (2 * kPrefixBlock);
+    const int item = hkv * pl.pairs + r / (2 * kPrefixBlock);
+    const int c0 = pl.owner((long long)item * pl.nt), c1 = pl.owner((long long)(item + 1) * pl.nt - 1);
+    for (int c = c0; c <= c1; ++c) {
+      const size_t slot = (size_t(c) + item) * 2 + rr / kPrefixBlock;
+      const float2 ml = pre.ml[slot * kPrefixBlock + rr % kPrefixBlock];
+      merge(ml.x, ml.y, pre.o[((slot * (D / 4) + ch / 4) * kPrefixBlock + rr % kPrefixBlock) * 4 + ch % 4]);
+    }
+  }
+  for (int s = 0; s < p.n_split; ++s) {
+    const size_t part = (pair * p.n_split + s) * p.G + h;
+    merge(p.ws_ml[part * 2], p.ws_ml[part * 2 + 1], p.ws_o[part * D + ch]);
   }
   const float val = L > 0.f ? O / L : 0.f;
-  own.out[size_t(row) * D + ch] = __bfloat16_as_ushort(__float2bfloat16_rn(val));
-  if (ch == 0 && own.lse) own.lse[row] = L > 0.f ? (M + __log2f(L)) * 0.6931471805599453f : -INFINITY;
+  p.out[size_t(row) * D + ch] = __bfloat16_as_ushort(__float2bfloat16_rn(val));
+  if (ch == 0 && p.lse) p.lse[row] = L > 0.f ? (M + __log2f(L)) * 0.6931471805599453f : -INFINITY;
 }
 
 // Warps per CTA: 20 at head_dim 64 (one CTA per SM covers a whole short
@@ -809,44 +819,41 @@ cudaError_t launch_decode(const void *q, const nd_kv_cache &c, int n_q_heads, in
 size_t shared_decode_workspace_bytes(int batch, int n_q_heads, int n_kv_heads, int head_dim, int prefix_cap,
                                      int max_slots) {
   const DecodePlan own = plan_decode(batch, n_kv_heads, max_slots, head_dim);
-  const DecodePlan pre = plan_decode(batch, n_kv_heads, prefix_cap, head_dim);
-  return size_t(batch) * n_q_heads * (own.n_split + pre.n_split) * (head_dim + 2) * sizeof(float);
+  const size_t rows = prefix_slots(prefix_cap, n_kv_heads, batch * (n_q_heads / n_kv_heads)) * 2 * kPrefixBlock;
+  return (rows + size_t(batch) * n_q_heads * own.n_split) * (head_dim + 2) * sizeof(float);
 }
 
 cudaError_t launch_shared_decode(const void *q, const nd_kv_cache &prefix, const nd_kv_cache &c, int n_q_heads,
                                  int window, void *out, float *lse, void *ws, int *err, cudaStream_t stream) {
-  DecodeParams part[2];
-  float *w = static_cast<float *>(ws);
-  for (int i = 0; i < 2; ++i) {
-    DecodeParams &p = part[i];
-    p.c = i ? prefix : c;
-    p.walk = i ? prefix.sink_cap : c.sink_cap + c.ring_cap;
-    p.shared = i;
-    const DecodePlan pl = plan_decode(c.batch, c.n_kv_heads, p.walk, c.head_dim);
-    p.q = static_cast<const uint16_t *>(q);
-    p.Hq = n_q_heads;
-    p.G = n_q_heads / c.n_kv_heads;
-    p.window = i ? 0 : window;  // the prefix's ring is not part of it
-    p.n_split = pl.n_split;
-    p.slots_per_cta = pl.slots_per_cta;
-    p.out = static_cast<uint16_t *>(out);
-    p.lse = lse;
-    p.err = err;
-    p.k_new = p.v_new = nullptr;
-    const size_t parts = size_t(c.batch) * n_q_heads * pl.n_split;
-    p.ws_o = w;
-    p.ws_ml = w + parts * c.head_dim;
-    w += parts * (c.head_dim + 2);
-    const dim3 grid(pl.n_split, c.n_kv_heads, c.batch);
-    cudaError_t e = cudaErrorInvalidValue;
-    if (c.head_dim == 128) e = launch_d<128, 4, 4, true>(p, grid, stream);
-    if (c.head_dim == 64) e = launch_d<64, 4, 4, true>(p, grid, stream);
-    if (e != cudaSuccess) return e;
-  }
-  const unsigned rows = unsigned(c.batch) * n_q_heads;
-  if (c.head_dim == 128) shared_combine_kernel<128><<<rows, 128, 0, stream>>>(part[0], part[1]);
-  else shared_combine_kernel<64><<<rows, 64, 0, stream>>>(part[0], part[1]);
-  return cudaGetLastError();
+  const int d = c.head_dim, rows = c.batch * (n_q_heads / c.n_kv_heads);
+  const size_t pre_rows = prefix_slots(prefix.sink_cap, c.n_kv_heads, rows) * 2 * kPrefixBlock;
+  PrefixParts pre;
+  pre.o = static_cast<float *>(ws);
+  pre.ml = reinterpret_cast<float2 *>(pre.o + pre_rows * d);
+  cudaError_t e = launch_shared_prefix(q, prefix, c.batch, n_q_heads, pre, err, stream);
+  if (e != cudaSuccess) return e;
+  const DecodePlan pl = plan_decode(c.batch, c.n_kv_heads, c.sink_cap + c.ring_cap, d);
+  DecodeParams p;
+  p.q = static_cast<const uint16_t *>(q);
+  p.c = c;
+  p.Hq = n_q_heads;
+  p.G = n_q_heads / c.n_kv_heads;
+  p.window = window;
+  p.n_split = pl.n_split;
+  p.slots_per_cta = pl.slots_per_cta;
+  p.out = static_cast<uint16_t *>(out);
+  p.lse = lse;
+  p.err = err;
+  p.k_new = p.v_new = nullptr;
+  p.ws_o = reinterpret_cast<float *>(pre.ml + pre_rows);
+  p.ws_ml = p.ws_o + size_t(c.batch) * n_q_heads * pl.n_split * d;
+  const dim3 grid(pl.n_split, c.n_kv_heads, c.batch);
+  e = d == 128 ? launch_d<128, 4, 4, true>(p, grid, stream) : launch_d<64, 4, 4, true>(p, grid, stream);
+  if (e != cudaSuccess) return e;
+  auto combine = d == 128 ? shared_combine_kernel<128> : shared_combine_kernel<64>;
+  return launch_pdl(combine, dim3(unsigned(c.batch) * n_q_heads), dim3(d), 0, stream, p, pre,
+                    static_cast<const int32_t *>(prefix.sink_len), prefix.sink_cap,
+                    prefix_grid(prefix.sink_cap, c.n_kv_heads, rows));
 }
 
 }  // namespace nd

@@ -1,0 +1,611 @@
+// shared_prefix.cu -- the shared part of a decode step whose sequences have one
+// pinned prefix in common: every query of the batch against the prefix's int8
+// keys and values, on the 5th-generation tensor cores.
+//
+// Mathematics.  A KV head's rows are the R = batch * G queries that read it
+// (row r: sequence r / G, head of the group r % G).  With the prefix's keys
+// k_j = code_j * scale_j the row's part of the softmax is the triple
+//   m = max_j s_j,  l = sum_j 2^(s_j - m),  O = sum_j 2^(s_j - m) v_j,
+//   s_j = (q . k_j) log2(e) / sqrt(D),
+// taken in one pass over the keys; triples of different key ranges, and of the
+// sequence's own slots, merge exactly (decode.cu).
+//
+// Types.  The tensor cores multiply fp16 with fp32 sums.  q (bf16) becomes
+// fp16 exactly after a power-of-two scaling per row (channels 2^-28 below the
+// row's largest lose bits).  Keys and values are code * fp16(scale * 2^e),
+// rounded to fp16: at most 2^-11 + 2^-11 of the value, an eighth of what bf16
+// operands would cost.  e is chosen per 64-key tile for K (its inverse is one
+// factor of the tile's scores) and follows the largest value scale seen for V,
+// with 4 bits of headroom, so that O is rescaled for it only where scales grow
+// by more than 2^3.  P is fp16 with the running maximum up to 2^8 behind and
+// all of it scaled by 2^7, so it stays below 2^15 and keys 2^-21 below the
+// maximum still have all bits.  Sums, maxima and partials are fp32.
+//
+// What bounds it.  4 R D flops per key and KV head on the tensor cores, and as
+// many exponentials as scores (16 per clock and SM: at D = 128 as long as the
+// products); below about 40 rows per KV head the read of the codes (2 (D +
+// D/8) bytes per key).  Each CTA therefore keeps two 128-row blocks and turns
+// a tile's codes into fp16 once for both.
+//
+// Work split.  The (KV head, 256-row pair, 64-key tile) triples, key tiles
+// fastest, form one line that is cut into equal stretches, one per CTA (one
+// CTA per SM): the line's length comes from the prefix's sink_len on the
+// device.  A stretch is one or more segments (a run of tiles of one row pair);
+// each segment writes its rows' triples to its own slot, CTA + row pair, which
+// both sides compute.
+//
+// Roles (16 warps):
+//   warps 0-3, 4-7 : softmax of row block 0, 1 (thread = row = TMEM lane):
+//                    stage Q; per tile read S, write P over it; at a segment's
+//                    end read O and write the partials
+//   warps 8-11     : codes of the staged tile -> fp16 K and V operands in
+//                    shared memory (16 rows each)
+//   warp 12        : copies codes (bulk) and scales of the tiles ahead
+//   warps 13, 14   : MMA issuer of row block 0, 1: S(g) = Q K(g)^T, then
+//                    O += P(g-1) V(g-1)
+// Every wait is bounded: one that gives up raises the device error flag and
+// the abort flag, and all roles leave through the common exit.
+#include <atomic>
+#include <climits>
+
+#include "nd_common.cuh"
+#include "nd_internal.h"
+#include "shared_prefix.cuh"
+#include "tc_ptx.cuh"
+
+namespace nd {
+
+namespace {
+
+constexpr int BM = kPrefixBlock;   // rows per block = TMEM lanes
+constexpr int BN = kPrefixTile;    // keys per tile
+constexpr int kThreads = 16 * 32;
+constexpr int kWarpDeq0 = 8, kDeqWarps = 4, kWarpLoad = 12, kWarpMma0 = 13;
+constexpr int kRegsSoftmax = 168, kRegsOther = 88;
+static_assert(2 * 128 * kRegsSoftmax + 2 * 128 * kRegsOther == kThreads * 128, "register split");
+constexpr float kLazyLog2 = 8.f;   // the maximum used may lag the true one by 2^8
+constexpr float kPBias = 7.f;      // P is scaled by 2^7
+constexpr int kInfo = 8;           // tile records in flight
+
+template <int D>
+struct Lay {
+  static constexpr int NG = D / 32;
+  static constexpr int kBoxes = D / 64;
+  static constexpr int kQ = kBoxes * BM * 128;          // one block's Q, fp16
+  static constexpr int kKV = kBoxes * BN * 128;         // one K or V operand tile, fp16
+  static constexpr int kCodes = BN * D, kScales = BN * NG * 4;
+  static constexpr int kRaw = 2 * kCodes + 2 * kScales; // K codes, V codes, K scales, V scales
+  static constexpr int NK = D == 128 ? 2 : 3, NV = NK, NR = D == 128 ? 4 : 6;
+  static constexpr int oQ = 0, oK = 2 * kQ, oV = oK + NK * kKV, oR = oV + NV * kKV;
+  static constexpr int kBytes = oR + NR * kRaw + 1024;  // + alignment slack
+  static_assert(kBytes <= 227 * 1024, "shared memory");
+  static constexpr int NS = D == 64 ? 3 : 2;            // S buffers per block
+  static constexpr int cO = 2 * NS * BN;                // TMEM columns: S[2][NS], O[2]
+  static constexpr int kTmemCols = 512;
+  static_assert(cO + 2 * D <= kTmemCols, "TMEM");
+};
+
+struct PrefixParams {
+  const uint16_t *q;
+  nd_kv_cache c;     // the prefix: one row, its sink region
+  int B, Hq, G, R;
+  PrefixParts out;
+  int *err;
+};
+
+// exponent of the power of two at or below x (x >= 0; 0, subnormals and
+// non-finite values included)
+__device__ __forceinline__ int ilog2(float x) {
+  return int((__float_as_uint(x) >> 23) & 0xffu) - 127;
+}
+__device__ __forceinline__ float pow2i(int e) {  // e in [-126, 127]
+  return __uint_as_float(uint32_t(e + 127) << 23);
+}
+__device__ __forceinline__ int clamp_exp(int e) { return max(-120, min(120, e)); }
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar, uint32_t leader) {
+  asm volatile(
+      "{\n .reg .pred e;\n setp.ne.b32 e, %4, 0;\n"
+      " @e cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n}\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar)), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ float lds_f32(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const PrefixParams p) {
+  using Y = Lay<D>;
+  constexpr int NK = Y::NK, NV = Y::NV, NR = Y::NR, NS = Y::NS, NG = Y::NG;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t raw_full[NR], raw_empty[NR], k_full[NK], k_empty[NK], v_full[NV], v_empty[NV],
+      s_full[2][NS], p_full[2][NS], pv_done[2][NS], q_full[2];
+  // per tile: 2^-e of K; the factor that O needs before this tile's V; 2^-e of V
+  __shared__ float4 s_info[kInfo];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int *abort_flag = &s_abort;
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  auto sQ = [&](int rb) { return base + Y::oQ + rb * Y::kQ; };
+  auto sK = [&](int st) { return base + Y::oK + st * Y::kKV; };
+  auto sV = [&](int st) { return base + Y::oV + st * Y::kKV; };
+  auto sR = [&](int st) { return base + Y::oR + st * Y::kRaw; };
+
+  if (tid == 0) {
+    for (int s = 0; s < NR; ++s) {
+      mbar_init(&raw_full[s], 33);          // the bulk copies' transaction and 32 lanes' scale copies
+      mbar_init(&raw_empty[s], kDeqWarps);
+    }
+    for (int s = 0; s < NK; ++s) {
+      mbar_init(&k_full[s], kDeqWarps);
+      mbar_init(&k_empty[s], 2);            // one arrival per row block
+    }
+    for (int s = 0; s < NV; ++s) {
+      mbar_init(&v_full[s], kDeqWarps);
+      mbar_init(&v_empty[s], 2);
+    }
+    for (int r = 0; r < 2; ++r) {
+      for (int u = 0; u < NS; ++u) {
+        mbar_init(&s_full[r][u], 1);
+        mbar_init(&p_full[r][u], 4);
+        mbar_init(&pv_done[r][u], 1);
+      }
+      mbar_init(&q_full[r], 4);
+    }
+    s_abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == kWarpMma0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
+                 "r"(Y::kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  pdl_wait();
+  auto tS = [&](int rb, int buf) { return tmem + (NS * rb + buf) * BN; };
+  auto tO = [&](int rb) { return tmem + Y::cO + rb * D; };
+
+  // ---- this CTA's stretch of the line of tiles
+  const PrefixPlan pl = prefix_plan(p.c.sink_len[0], p.c.sink_cap, p.c.n_kv_heads, p.R, gridDim.x);
+  if (!pl.sane && blockIdx.x == 0 && tid == 0) raise_device_error(p.err, ND_DEVERR_METADATA);
+  const bool has_work = int(blockIdx.x) < pl.ctas;
+  const long long x0 = has_work ? pl.start(blockIdx.x) : 0, x1 = has_work ? pl.start(blockIdx.x + 1) : 0;
+  struct Seg {
+    int item, t0, n, hk, r0, nb;
+  };
+  auto seg_at = [&](long long x) {
+    Seg s;
+    s.item = int(x / pl.nt);
+    s.t0 = int(x - (long long)s.item * pl.nt);
+    s.n = int(min((long long)(pl.nt - s.t0), x1 - x));
+    s.hk = s.item / pl.pairs;
+    s.r0 = (s.item % pl.pairs) * 2 * BM;
+    s.nb = p.R - s.r0 > BM ? 2 : 1;
+    return s;
+  };
+  bool fail = false;
+
+  if (warp >= 8) {
+    regs_dec<kRegsOther>();
+    if (warp == kWarpLoad) {
+      // ------------------------------------------------ loader
+      const uint32_t leader = elect_one();
+      const size_t nslot = size_t(p.c.sink_cap) + p.c.ring_cap;
+      int g = 0;
+      for (long long x = x0; x < x1 && !fail;) {
+        const Seg s = seg_at(x);
+        const int8_t *kc = p.c.k_codes + s.hk * nslot * D, *vc = p.c.v_codes + s.hk * nslot * D;
+        const float *ks = p.c.k_scale + s.hk * nslot * NG, *vs = p.c.v_scale + s.hk * nslot * NG;
+        for (int t = s.t0; t < s.t0 + s.n; ++t, ++g) {
+          const int st = g % NR, rows = min(BN, pl.len - t * BN);
+          if (g >= NR && !warp_wait(&raw_empty[st], ((g / NR) - 1) & 1, p.err, abort_flag)) {
+            fail = true;
+            break;
+          }
+          const uint32_t dst = sR(st);
+          const size_t slot = size_t(t) * BN;
+          expect_tx(&raw_full[st], 2u * rows * D, leader);
+          bulk_load(dst, kc + slot * D, rows * D, &raw_full[st], leader);
+          bulk_load(dst + Y::kCodes, vc + slot * D, rows * D, &raw_full[st], leader);
+          // scales: a slot's row is 16 (D = 128) or 8 bytes, and a head's
+          // first one aligned to no more than that
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int r = lane + 32 * i;
+            if (r < rows) {
+              if constexpr (NG == 4) {
+                cp_async16(dst + 2 * Y::kCodes + r * 16, ks + (slot + r) * NG);
+                cp_async16(dst + 2 * Y::kCodes + Y::kScales + r * 16, vs + (slot + r) * NG);
+              } else {
+                cp_async8(dst + 2 * Y::kCodes + r * 8, ks + (slot + r) * NG);
+                cp_async8(dst + 2 * Y::kCodes + Y::kScales + r * 8, vs + (slot + r) * NG);
+              }
+            }
+          }
+          cp_async_arrive(&raw_full[st]);
+          __syncwarp();
+        }
+        x += s.n;
+      }
+    } else if (warp < kWarpDeq0 + kDeqWarps) {
+      // ------------------------------------------------ codes -> fp16 operands
+      const int dw = warp - kWarpDeq0;
+      constexpr int kPieces = D / 16, kRowsIt = 32 / kPieces, kIts = 16 / kRowsIt;
+      const int piece = lane % kPieces, row_l = lane / kPieces;
+      // K-major (and for V MN-major) 128-byte swizzle: row * 128 + 16-byte
+      // chunk ^ (row & 7) inside a box of 64 channels; a lane's two chunks.
+      // The upper box's lanes store their odd chunk first, so the eight lanes
+      // of a row cover the eight chunk positions (all banks) at once.
+      const int box = piece / 4, c0 = (2 * piece) & 7;
+      const bool odd_first = box == 1;
+      int g = 0;
+      for (long long x = x0; x < x1 && !fail;) {
+        const Seg s = seg_at(x);
+        int e_v = INT_MAX;  // the exponent that V's operands have in O (unset)
+        for (int t = s.t0; t < s.t0 + s.n && !fail; ++t, ++g) {
+          const int st = g % NR, rows = min(BN, pl.len - t * BN);
+          if (!warp_wait(&raw_full[st], (g / NR) & 1, p.err, abort_flag)) {
+            fail = true;
+            break;
+          }
+          const uint32_t raw = sR(st), rks = raw + 2 * Y::kCodes, rvs = rks + Y::kScales;
+          // the tile's largest scales (every warp for itself: no exchange)
+          float km = 0.f, vm = 0.f;
+#pragma unroll
+          for (int i = 0; i < BN * NG / 32; ++i) {
+            const int idx = lane + 32 * i;
+            if (idx / NG < rows) {
+              km = fmaxf(km, fabsf(lds_f32(rks + 4 * idx)));
+              vm = fmaxf(vm, fabsf(lds_f32(rvs + 4 * idx)));
+            }
+          }
+#pragma unroll
+          for (int off = 16; off >= 1; off >>= 1) {
+            km = fmaxf(km, __shfl_xor_sync(0xffffffffu, km, off));
+            vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, off));
+          }
+          // |code * scale| < 2^(ilog2 + 8): K below 2^15, V first below 2^12
+          const int e_k = clamp_exp(7 - ilog2(km));
+          float fix = 1.f;
+          if (vm > 0.f) {
+            const int want = clamp_exp(4 - ilog2(vm));
+            if (e_v == INT_MAX) {
+              e_v = want;  // every value so far was 0, and so is O
+            } else if (want + 3 < e_v) {
+              fix = pow2i(max(want - e_v, -126));
+              e_v = want;
+            }
+          }
+          const float up_v = e_v == INT_MAX ? 1.f : pow2i(e_v);
+          if (dw == 0 && lane == 0)
+            s_info[g % kInfo] = make_float4(pow2i(-e_k), fix, e_v == INT_MAX ? 1.f : pow2i(-e_v), 0.f);
+          const float up_k = pow2i(e_k);
+#pragma unroll
+          for (int which = 0; which < 2; ++which) {
+            const int so = g % (which ? NV : NK);
+            uint64_t *full = which ? &v_full[so] : &k_full[so], *empty = which ? &v_empty[so] : &k_empty[so];
+            const int ph = g / (which ? NV : NK);
+            if (ph >= 1 && !warp_wait(empty, (ph - 1) & 1, p.err, abort_flag)) {
+              fail = true;
+              break;
+            }
+            const uint32_t dst = which ? sV(so) : sK(so);
+#pragma unroll
+            for (int it = 0; it < kIts; ++it) {
+              const int row = 16 * dw + it * kRowsIt + row_l;
+              uint32_t w[4];
+              ld_shared_v4(raw + which * Y::kCodes + row * D + piece * 16, w[0], w[1], w[2], w[3]);
+              float sc = lds_f32((which ? rvs : rks) + 4 * (row * NG + piece / 2)) * (which ? up_v : up_k);
+              sc = row < rows ? sc : 0.f;  // a slot behind the prefix: whatever is staged counts 0
+              const uint32_t s2 = pack_half2(sc, sc);
+              uint32_t h[8];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t wb = w[i] ^ 0x80808080u;
+                h[2 * i] = hmul2(codes_to_half2(wb, kSelBytes01), s2);
+                h[2 * i + 1] = hmul2(codes_to_half2(wb, kSelBytes23), s2);
+              }
+              const uint32_t at = dst + box * (BN * 128) + row * 128;
+              const uint32_t a0 = at + ((c0 ^ (row & 7)) << 4), a1 = at + (((c0 + 1) ^ (row & 7)) << 4);
+              if (odd_first) {
+                st_shared_v4(a1, h[4], h[5], h[6], h[7]);
+                st_shared_v4(a0, h[0], h[1], h[2], h[3]);
+              } else {
+                st_shared_v4(a0, h[0], h[1], h[2], h[3]);
+                st_shared_v4(a1, h[4], h[5], h[6], h[7]);
+              }
+            }
+            // the MMA reads the tile through the async proxy
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full);
+          }
+          if (lane == 0) mbar_arrive(&raw_empty[st]);
+        }
+        x += s.n;
+      }
+    } else if (warp == kWarpMma0 || warp == kWarpMma0 + 1) {
+      // ------------------------------------------------ MMA issuers, one per block
+      const int rb = warp - kWarpMma0;
+      const uint32_t leader = elect_one();
+      constexpr uint32_t kIdS = idesc_f16(BM, BN, 0);
+      constexpr uint32_t kIdPV = idesc_f16(BM, D, 1);
+      int g = 0, gb = 0, nseg = 0;  // tiles, this block's tiles, this block's segments
+      for (long long x = x0; x < x1 && !fail;) {
+        const Seg s = seg_at(x);
+        if (rb >= s.nb) {
+          // no rows: only the hand-back of the operand stages
+          for (int j = 0; j < s.n && !fail; ++j, ++g) {
+            if (!warp_wait(&k_full[g % NK], (g / NK) & 1, p.err, abort_flag) ||
+                !warp_wait(&v_full[g % NV], (g / NV) & 1, p.err, abort_flag)) {
+              fail = true;
+              break;
+            }
+            if (lane == 0) {
+              mbar_arrive(&k_empty[g % NK]);
+              mbar_arrive(&v_empty[g % NV]);
+            }
+            __syncwarp();
+          }
+          x += s.n;
+          continue;
+        }
+        if (!warp_wait(&q_full[rb], nseg & 1, p.err, abort_flag)) {
+          fail = true;
+          break;
+        }
+        auto issue_pv = [&](int j) {  // tile j of the segment
+          const int gg = g + j, bb = gb + j, u = bb % NS, sv = gg % NV;
+          if (!warp_wait(&p_full[rb][u], (bb / NS) & 1, p.err, abort_flag) ||
+              !warp_wait(&v_full[sv], (gg / NV) & 1, p.err, abort_flag))
+            return false;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < BN / 16; ++kk)  // 16 keys = 8 TMEM columns of fp16 pairs
+            mma_ts(tO(rb), tS(rb, u) + kk * 8, sdesc_sw128(sV(sv) + kk * 16 * 128, BN * 128, 1024), kIdPV,
+                   (j > 0 || kk > 0) ? 1u : 0u, leader);
+          mma_commit(&pv_done[rb][u], leader);
+          mma_commit(&v_empty[sv], leader);
+          return true;
+        };
+        for (int j = 0; j < s.n && !fail; ++j) {
+          const int gg = g + j, bb = gb + j, st = gg % NK;
+          // S(j) goes over the P that PV(j - NS) read: this thread issued that
+          // product earlier, and one thread's MMAs run in order
+          if (!warp_wait(&k_full[st], (gg / NK) & 1, p.err, abort_flag)) {
+            fail = true;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk & 3) * 32;
+            mma_ss(tS(rb, bb % NS), sdesc_sw128(sQ(rb) + (kk >> 2) * BM * 128 + off, 16, 1024),
+                   sdesc_sw128(sK(st) + (kk >> 2) * BN * 128 + off, 16, 1024), kIdS, kk > 0 ? 1u : 0u, leader);
+          }
+          mma_commit(&s_full[rb][bb % NS], leader);
+          mma_commit(&k_empty[st], leader);
+          if (j >= 1 && !issue_pv(j - 1)) fail = true;
+        }
+        if (!fail && !issue_pv(s.n - 1)) fail = true;
+        g += s.n;
+        gb += s.n;
+        ++nseg;
+        x += s.n;
+      }
+    }
+  } else {
+    // ------------------------------------------------ softmax warpgroups
+    regs_inc<kRegsSoftmax>();
+    const int rb = warp >> 2, r = tid & (BM - 1);
+    const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
+    int g = 0, gb = 0;
+    for (long long x = x0; x < x1 && !fail;) {
+      const Seg s = seg_at(x);
+      if (rb >= s.nb) {
+        g += s.n;
+        x += s.n;
+        continue;
+      }
+      const int row = s.r0 + rb * BM + r;
+      // a warp none of whose rows exists keeps the handshakes only; its part
+      // of P is whatever TMEM holds, which reaches no other row
+      const bool active = s.r0 + rb * BM + (warp & 3) * 32 < p.R;
+      float c_row = 0.f;
+      if (active) {
+        // Q: this thread's row as fp16 times 2^eq.  The previous segment's
+        // products, the last readers of the buffer, are done: this thread
+        // waited for them before it read O.
+        uint4 w[D / 8];
+        const uint16_t *src = p.q + (size_t(row / p.G) * p.Hq + s.hk * p.G + row % p.G) * D;
+        float qm = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          w[i] = row < p.R ? reinterpret_cast<const uint4 *>(src)[i] : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) qm = fmaxf(qm, fmaxf(fabsf(bf16_lo(u[e])), fabsf(bf16_hi(u[e]))));
+        }
+        const int eq = clamp_exp(14 - ilog2(qm));
+        const float up = pow2i(eq);
+        c_row = pow2i(-eq) * (1.4426950408889634f * rsqrtf(float(D)));
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+          uint32_t h[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) h[e] = pack_half2(bf16_lo(u[e]) * up, bf16_hi(u[e]) * up);
+          st_shared_v4(sQ(rb) + (i / 8) * (BM * 128) + r * 128 + (((i & 7) ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[rb]);
+
+      float m_used = -INFINITY, l = 0.f, down = 1.f;
+      for (int j = 0; j < s.n; ++j) {
+        const int gg = g + j, bb = gb + j, u = bb % NS;
+        if (!fail) fail = !warp_wait(&s_full[rb][u], (bb / NS) & 1, p.err, abort_flag);
+        tc_fence_after();
+        if (!active) {
+          if (lane == 0) mbar_arrive(&p_full[rb][u]);
+          continue;
+        }
+        const float4 info = s_info[gg % kInfo];
+        uint32_t v[BN];
+        tmem_ld32(tS(rb, u) + lane_base, v);
+        tmem_ld32(tS(rb, u) + lane_base + 32, v + 32);
+        tmem_ld_wait();
+        const int rows = min(BN, pl.len - (s.t0 + j) * BN);
+        if (rows < BN) {
+#pragma unroll
+          for (int i = 0; i < BN; ++i) v[i] = i < rows ? v[i] : 0xff800000u;
+        }
+        const float ct = c_row * info.x;
+        down = info.z;
+        float mxp[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          mxp[i] = max3(__uint_as_float(v[i]), __uint_as_float(v[8 + i]), __uint_as_float(v[16 + i]));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          mxp[i] = max3(mxp[i], __uint_as_float(v[24 + i]), __uint_as_float(v[32 + i]));
+          mxp[i] = max3(mxp[i], __uint_as_float(v[40 + i]), __uint_as_float(v[48 + i]));
+          mxp[i] = fmaxf(mxp[i], __uint_as_float(v[56 + i]));
+        }
+        const float mx =
+            ct * max3(max3(mxp[0], mxp[1], mxp[2]), max3(mxp[3], mxp[4], mxp[5]), fmaxf(mxp[6], mxp[7]));
+        const bool need = mx > m_used + kLazyLog2;  // the first tile included
+        float alpha = info.y;  // what V's new exponent asks of O
+        if (need) {
+          const float a = ex2(m_used - mx);  // 0 at the first tile
+          alpha *= a;
+          l *= a;
+          m_used = mx;
+        }
+        const uint64_t c2 = pack_f32x2(ct, ct), nmc2 = pack_f32x2(kPBias - m_used, kPBias - m_used);
+        float rsp[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < BN; i += 2) {
+          float a, b;
+          fma_f32x2(a, b, __uint_as_float(v[i]), __uint_as_float(v[i + 1]), c2, nmc2);
+          a = ex2(a);
+          b = ex2(b);
+          add_f32x2(rsp[(i >> 1) & 1 ? 2 : 0], rsp[(i >> 1) & 1 ? 3 : 1], a, b);
+          v[i / 2] = pack_half2(a, b);
+        }
+        l += (rsp[0] + rsp[1]) + (rsp[2] + rsp[3]);
+        if (j >= 1 && __any_sync(0xffffffffu, alpha != 1.f)) {
+          // O once PV(j-1) has landed
+          if (!fail) fail = !warp_wait(&pv_done[rb][(bb - 1) % NS], ((bb - 1) / NS) & 1, p.err, abort_flag);
+          tc_fence_after();
+#pragma unroll 1
+          for (int ch = 0; ch < D; ch += 32) {
+            uint32_t ov[32];
+            tmem_ld32(tO(rb) + lane_base + ch, ov);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+            tmem_st32(tO(rb) + lane_base + ch, ov);
+          }
+        }
+        tmem_st32(tS(rb, u) + lane_base, v);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[rb][u]);
+      }
+      // ---- the segment's partials
+      const int bl = gb + s.n - 1;
+      if (!fail) fail = !warp_wait(&pv_done[rb][bl % NS], (bl / NS) & 1, p.err, abort_flag);
+      tc_fence_after();
+      if (active && !fail) {
+        const size_t slot = size_t(blockIdx.x) + s.item;
+        float4 *o = reinterpret_cast<float4 *>(p.out.o) + (slot * 2 + rb) * (D / 4) * BM + r;
+#pragma unroll 1
+        for (int ch = 0; ch < D; ch += 32) {
+          uint32_t ov[32];
+          tmem_ld32(tO(rb) + lane_base + ch, ov);
+          tmem_ld_wait();
+          if (row < p.R) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              o[size_t(ch + i) / 4 * BM] =
+                  make_float4(__uint_as_float(ov[i]) * down, __uint_as_float(ov[i + 1]) * down,
+                              __uint_as_float(ov[i + 2]) * down, __uint_as_float(ov[i + 3]) * down);
+          }
+        }
+        if (row < p.R) p.out.ml[(slot * 2 + rb) * BM + r] = make_float2(m_used - kPBias, l);
+        tc_fence_before();
+      }
+      g += s.n;
+      gb += s.n;
+      x += s.n;
+    }
+  }
+
+  // ---- common exit: on the error path give copies and MMAs still in flight a
+  //      bounded time (about 2 ms) to land before shared memory and TMEM go
+  tc_fence_before();
+  if (__syncthreads_or(fail || *abort_flag))
+    for (int i = 0; i < 2000; ++i) __nanosleep(1000);
+  __syncthreads();
+  if (warp == kWarpMma0) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(Y::kTmemCols) : "memory");
+  }
+}
+
+template <int D>
+cudaError_t launch_d(const PrefixParams &p, int grid, cudaStream_t stream) {
+  auto kern = shared_prefix_kernel<D>;
+  static std::atomic<unsigned long long> smem_set{0};  // the opt-in, once per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev >= 0 && dev < 64 ? 1ull << dev : 0ull;
+  if (!bit || !(smem_set.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::kBytes);
+    if (e != cudaSuccess) return e;
+    smem_set.fetch_or(bit, std::memory_order_release);
+  }
+  return launch_pdl(kern, dim3(grid), dim3(kThreads), size_t(Lay<D>::kBytes), stream, p);
+}
+
+}  // namespace
+
+cudaError_t launch_shared_prefix(const void *q, const nd_kv_cache &prefix, int batch, int n_q_heads,
+                                 const PrefixParts &out, int *err, cudaStream_t stream) {
+  PrefixParams p;
+  p.q = static_cast<const uint16_t *>(q);
+  p.c = prefix;
+  p.B = batch;
+  p.Hq = n_q_heads;
+  p.G = n_q_heads / prefix.n_kv_heads;
+  p.R = batch * p.G;
+  p.out = out;
+  p.err = err;
+  const int grid = prefix_grid(prefix.sink_cap, prefix.n_kv_heads, p.R);
+  if (prefix.head_dim == 128) return launch_d<128>(p, grid, stream);
+  if (prefix.head_dim == 64) return launch_d<64>(p, grid, stream);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace nd

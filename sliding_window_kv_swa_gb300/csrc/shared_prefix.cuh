@@ -1,0 +1,65 @@
+// shared_prefix.cuh -- how the shared prefix's work is split, and where its
+// partial results lie: used by the kernel that makes them (shared_prefix.cu)
+// and by the one that merges them (decode.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "nd.h"
+
+namespace nd {
+
+constexpr int kPrefixTile = 64;    // keys per tile
+constexpr int kPrefixBlock = 128;  // rows per block; a CTA holds two (a pair)
+constexpr int kPrefixCtas = 152;   // one per SM
+constexpr int kPrefixMinTiles = 2; // fewest tiles worth a CTA
+
+// Partials: slot s holds a row pair's O [2][D/4][128][4] and (max, sum)
+// [2][128], maxima in log2 units.
+struct PrefixParts {
+  float *o;
+  float2 *ml;
+};
+
+__host__ __device__ inline int prefix_pairs(int rows) { return (rows + 2 * kPrefixBlock - 1) / (2 * kPrefixBlock); }
+
+// The line of (item, tile): an item is a (KV head, row pair), its nt key tiles
+// lie side by side.  CTA c has tiles [start(c), start(c + 1)); the segment of
+// item i in CTA c has partial slot c + i, unique because a segment follows the
+// one before it in the same CTA with the next item, or in the next CTA.
+struct PrefixPlan {
+  int len, nt, pairs, items, ctas;
+  bool sane;
+  __host__ __device__ long long tiles() const { return (long long)items * nt; }
+  __host__ __device__ long long start(int c) const { return tiles() * c / ctas; }
+  // the CTA whose stretch holds tile x
+  __host__ __device__ int owner(long long x) const { return int(((x + 1) * ctas - 1) / tiles()); }
+};
+
+__host__ __device__ inline PrefixPlan prefix_plan(int sink_len, int sink_cap, int n_kv_heads, int rows, int grid) {
+  PrefixPlan p;
+  p.sane = sink_len >= 0 && sink_len <= sink_cap;
+  p.len = p.sane ? sink_len : 0;
+  p.nt = (p.len + kPrefixTile - 1) / kPrefixTile;
+  p.pairs = prefix_pairs(rows);
+  p.items = n_kv_heads * p.pairs;
+  const long long want = (p.tiles() + kPrefixMinTiles - 1) / kPrefixMinTiles;
+  p.ctas = int(want < grid ? want : grid);
+  return p;
+}
+
+// Blocks to launch for a prefix of up to sink_cap slots, and partial slots.
+inline int prefix_grid(int sink_cap, int n_kv_heads, int rows) {
+  const int c = prefix_plan(sink_cap, sink_cap, n_kv_heads, rows, kPrefixCtas).ctas;
+  return c > 0 ? c : 1;
+}
+inline size_t prefix_slots(int sink_cap, int n_kv_heads, int rows) {
+  return size_t(prefix_grid(sink_cap, n_kv_heads, rows)) + size_t(n_kv_heads) * prefix_pairs(rows);
+}
+
+cudaError_t launch_shared_prefix(const void *q, const nd_kv_cache &prefix, int batch, int n_q_heads,
+                                 const PrefixParts &out, int *err, cudaStream_t stream);
+
+}  // namespace nd

@@ -149,9 +149,12 @@ def _ptr(t: Optional[torch.Tensor]):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream) -> ctypes.c_void_p:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+def _stream(stream) -> int:
+    # the current stream's handle alone: building the Stream object around it
+    # takes longer than a small launch (2.8 us against 0.3 us on the GB300's CPU)
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -201,10 +204,15 @@ class KVCache:
         return self.k_codes.shape[3]
 
     def struct(self) -> _Cache:
-        return _Cache(self.batch, self.n_kv_heads, self.head_dim, self.sink_cap, self.ring_cap,
-                      *(t.data_ptr() for t in (self.k_codes, self.v_codes, self.k_scale, self.v_scale,
-                                               self.sink_len, self.ring_start, self.ring_len,
-                                               self.seq_len)))
+        # (built again only when a tensor or a size changed: half the time of
+        # a call on a per-token path)
+        key = (self.k_codes.shape, self.sink_cap, self.ring_cap, self.k_codes.data_ptr(), self.v_codes.data_ptr(),
+               self.k_scale.data_ptr(), self.v_scale.data_ptr(), self.sink_len.data_ptr(),
+               self.ring_start.data_ptr(), self.ring_len.data_ptr(), self.seq_len.data_ptr())
+        if self.__dict__.get("_key") != key:
+            self._struct = _Cache(self.batch, self.n_kv_heads, self.head_dim, *key[1:])
+            self._key = key
+        return self._struct
 
 
 @dataclass
