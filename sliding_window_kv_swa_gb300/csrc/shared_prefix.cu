@@ -38,9 +38,10 @@
 //   warps 0-3, 4-7 : softmax of row block 0, 1 (thread = row = TMEM lane):
 //                    stage Q; per tile read S, write P over it; at a segment's
 //                    end read O and write the partials
-//   warps 8-11     : codes of the staged tile -> fp16 K and V operands in
-//                    shared memory (16 rows each)
+//   warps 8-9, 10-11 : codes of the staged tile -> fp16 K, V operands in shared
+//                    memory
 //   warp 12        : copies codes (bulk) and scales of the tiles ahead
+//   warp 15        : the staged tile's scales -> its exponents, fp16 scales
 //   warps 13, 14   : MMA issuer of row block 0, 1: S(g) = Q K(g)^T, then
 //                    O += P(g-1) V(g-1)
 // Every wait is bounded: one that gives up raises the device error flag and
@@ -60,12 +61,17 @@ namespace {
 constexpr int BM = kPrefixBlock;   // rows per block = TMEM lanes
 constexpr int BN = kPrefixTile;    // keys per tile
 constexpr int kThreads = 16 * 32;
-constexpr int kWarpDeq0 = 8, kDeqWarps = 4, kWarpLoad = 12, kWarpMma0 = 13;
+constexpr int kWarpDeq0 = 8, kDeqWarps = 4, kWarpLoad = 12, kWarpMma0 = 13, kWarpScan = 15;
+// Register split (setmaxnreg, per warpgroup) of the 128 a thread at launch:
+// the softmax holds a 64-score row per thread.  (Four more warps for the
+// conversion, on alternate tiles, measured slower -- 63 against 60 us at 4
+// sequences over 65536 slots -- their share of the registers made the softmax
+// spill.)
 constexpr int kRegsSoftmax = 168, kRegsOther = 88;
 static_assert(2 * 128 * kRegsSoftmax + 2 * 128 * kRegsOther == kThreads * 128, "register split");
 constexpr float kLazyLog2 = 8.f;   // the maximum used may lag the true one by 2^8
 constexpr float kPBias = 7.f;      // P is scaled by 2^7
-constexpr int kInfo = 8;           // tile records in flight
+constexpr int kInfo = 16;          // tile records in flight
 
 template <int D>
 struct Lay {
@@ -75,7 +81,7 @@ struct Lay {
   static constexpr int kKV = kBoxes * BN * 128;         // one K or V operand tile, fp16
   static constexpr int kCodes = BN * D, kScales = BN * NG * 4;
   static constexpr int kRaw = 2 * kCodes + 2 * kScales; // K codes, V codes, K scales, V scales
-  static constexpr int NK = D == 128 ? 2 : 3, NV = NK, NR = D == 128 ? 4 : 6;
+  static constexpr int NK = D == 128 ? 2 : 3, NV = 3, NR = D == 128 ? 4 : 6;
   static constexpr int oQ = 0, oK = 2 * kQ, oV = oK + NK * kKV, oR = oV + NV * kKV;
   static constexpr int kBytes = oR + NR * kRaw + 1024;  // + alignment slack
   static_assert(kBytes <= 227 * 1024, "shared memory");
@@ -118,10 +124,61 @@ __device__ __forceinline__ float lds_f32(uint32_t a) {
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
   return v;
 }
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts32(uint32_t a, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
+}
+
+// A position in a ring of N stages and the parity of its current use (counters
+// instead of divisions: every role's loop has to stay small, see the head of
+// this file).
+template <int N>
+struct Ring {
+  int i = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++i == N) {
+      i = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+// A bounded wait of a whole warp that sleeps between polls (up to 2 us each):
+// the polls of those that wait take issue slots from those
+// that work (80 -> 70 us for 4 sequences over 65536 slots).
+__device__ __forceinline__ bool ring_wait(uint64_t *bar, uint32_t parity, int *err, volatile int *abort_flag) {
+  bool ok = mbar_test_wait(bar, parity);
+  for (uint32_t i = 0; i < kWaitLimit / 64 && !ok; ++i) {
+    uint32_t r;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(r)
+        : "r"(smem_u32(bar)), "r"(parity), "n"(2000)
+        : "memory");
+    ok = r != 0;
+    if (!ok && *abort_flag) break;
+  }
+  if (!ok && !*abort_flag) {
+    raise_device_error(err, ND_DEVERR_TIMEOUT);
+    *abort_flag = 1;
+  }
+  return __all_sync(0xffffffffu, ok);
 }
 
 template <int D>
@@ -129,10 +186,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Prefix
   using Y = Lay<D>;
   constexpr int NK = Y::NK, NV = Y::NV, NR = Y::NR, NS = Y::NS, NG = Y::NG;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t raw_full[NR], raw_empty[NR], k_full[NK], k_empty[NK], v_full[NV], v_empty[NV],
+  __shared__ __align__(8) uint64_t raw_full[NR], raw_empty[NR], scan_full[NR], k_full[NK], k_empty[NK], v_full[NV], v_empty[NV],
       s_full[2][NS], p_full[2][NS], pv_done[2][NS], q_full[2];
-  // per tile: 2^-e of K; the factor that O needs before this tile's V; 2^-e of V
-  __shared__ float4 s_info[kInfo];
+  __shared__ float4 s_info[kInfo];  // per tile, for the softmax
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
 
@@ -147,14 +203,15 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Prefix
   if (tid == 0) {
     for (int s = 0; s < NR; ++s) {
       mbar_init(&raw_full[s], 33);          // the bulk copies' transaction and 32 lanes' scale copies
-      mbar_init(&raw_empty[s], kDeqWarps);
+      mbar_init(&raw_empty[s], 4 + 1);  // the four warps that turn the tile, and the scan
+      mbar_init(&scan_full[s], 1);
     }
     for (int s = 0; s < NK; ++s) {
-      mbar_init(&k_full[s], kDeqWarps);
+      mbar_init(&k_full[s], 2);
       mbar_init(&k_empty[s], 2);            // one arrival per row block
     }
     for (int s = 0; s < NV; ++s) {
-      mbar_init(&v_full[s], kDeqWarps);
+      mbar_init(&v_full[s], 2);
       mbar_init(&v_empty[s], 2);
     }
     for (int r = 0; r < 2; ++r) {
@@ -208,73 +265,148 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Prefix
       // ------------------------------------------------ loader
       const uint32_t leader = elect_one();
       const size_t nslot = size_t(p.c.sink_cap) + p.c.ring_cap;
-      int g = 0;
+      Ring<NR> raw;
+      raw.phase = 1;  // the first round of an empty ring does not wait
       for (long long x = x0; x < x1 && !fail;) {
         const Seg s = seg_at(x);
-        const int8_t *kc = p.c.k_codes + s.hk * nslot * D, *vc = p.c.v_codes + s.hk * nslot * D;
-        const float *ks = p.c.k_scale + s.hk * nslot * NG, *vs = p.c.v_scale + s.hk * nslot * NG;
-        for (int t = s.t0; t < s.t0 + s.n; ++t, ++g) {
-          const int st = g % NR, rows = min(BN, pl.len - t * BN);
-          if (g >= NR && !warp_wait(&raw_empty[st], ((g / NR) - 1) & 1, p.err, abort_flag)) {
+        const size_t slot0 = s.hk * nslot + size_t(s.t0) * BN;
+        const int8_t *kc = p.c.k_codes + slot0 * D, *vc = p.c.v_codes + slot0 * D;
+        // scales: a slot's row is 16 (D = 128) or 8 bytes, and a head's first
+        // one aligned to no more than that
+        const float *ks = p.c.k_scale + (slot0 + lane) * NG, *vs = p.c.v_scale + (slot0 + lane) * NG;
+        int left = pl.len - s.t0 * BN;
+#pragma unroll 1
+        for (int j = 0; j < s.n; ++j, raw.next(), left -= BN) {
+          if (!ring_wait(&raw_empty[raw.i], raw.phase, p.err, abort_flag)) {
             fail = true;
             break;
           }
-          const uint32_t dst = sR(st);
-          const size_t slot = size_t(t) * BN;
-          expect_tx(&raw_full[st], 2u * rows * D, leader);
-          bulk_load(dst, kc + slot * D, rows * D, &raw_full[st], leader);
-          bulk_load(dst + Y::kCodes, vc + slot * D, rows * D, &raw_full[st], leader);
-          // scales: a slot's row is 16 (D = 128) or 8 bytes, and a head's
-          // first one aligned to no more than that
+          uint64_t *bar = &raw_full[raw.i];
+          const uint32_t dst = sR(raw.i), bytes = min(BN, left) * D;
+          expect_tx(bar, 2 * bytes, leader);
+          bulk_load(dst, kc, bytes, bar, leader);
+          bulk_load(dst + Y::kCodes, vc, bytes, bar, leader);
+          const uint32_t sd = dst + 2 * Y::kCodes + lane * (NG * 4);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int r = lane + 32 * i;
-            if (r < rows) {
+          for (int i = 0; i < 2; ++i)
+            if (lane + 32 * i < left) {
               if constexpr (NG == 4) {
-                cp_async16(dst + 2 * Y::kCodes + r * 16, ks + (slot + r) * NG);
-                cp_async16(dst + 2 * Y::kCodes + Y::kScales + r * 16, vs + (slot + r) * NG);
+                cp_async16(sd + i * 32 * NG * 4, ks + i * 32 * NG);
+                cp_async16(sd + i * 32 * NG * 4 + Y::kScales, vs + i * 32 * NG);
               } else {
-                cp_async8(dst + 2 * Y::kCodes + r * 8, ks + (slot + r) * NG);
-                cp_async8(dst + 2 * Y::kCodes + Y::kScales + r * 8, vs + (slot + r) * NG);
+                cp_async8(sd + i * 32 * NG * 4, ks + i * 32 * NG);
+                cp_async8(sd + i * 32 * NG * 4 + Y::kScales, vs + i * 32 * NG);
               }
             }
-          }
-          cp_async_arrive(&raw_full[st]);
+          cp_async_arrive(bar);
           __syncwarp();
+          kc += BN * D, vc += BN * D, ks += BN * NG, vs += BN * NG;
         }
         x += s.n;
       }
     } else if (warp < kWarpDeq0 + kDeqWarps) {
       // ------------------------------------------------ codes -> fp16 operands
-      const int dw = warp - kWarpDeq0;
-      constexpr int kPieces = D / 16, kRowsIt = 32 / kPieces, kIts = 16 / kRowsIt;
+      // two warps turn K, two turn V, 32 rows each: neither operand waits
+      // behind the other's stages
+      const int half = warp & 1;
+      const bool is_v = warp & 2;
+      constexpr int kPieces = D / 16, kRowsIt = 32 / kPieces, kIts = 32 / kRowsIt, kU = 2;
       const int piece = lane % kPieces, row_l = lane / kPieces;
       // K-major (and for V MN-major) 128-byte swizzle: row * 128 + 16-byte
       // chunk ^ (row & 7) inside a box of 64 channels; a lane's two chunks.
       // The upper box's lanes store their odd chunk first, so the eight lanes
       // of a row cover the eight chunk positions (all banks) at once.
       const int box = piece / 4, c0 = (2 * piece) & 7;
-      const bool odd_first = box == 1;
+      const uint32_t odd_first = box == 1 ? 1u : 0u;
+      uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
+      const int n_st = is_v ? NV : NK;
+      const uint32_t codes_off = (is_v ? Y::kCodes : 0) + (32 * half + row_l) * D + piece * 16 + 8 * odd_first;
+      const uint32_t scale_off = 2 * Y::kCodes + (is_v ? Y::kScales : 0) + 4 * ((32 * half + row_l) * NG + piece / 2);
+      const uint32_t row_off = (is_v ? sV(0) : sK(0)) + (32 * half + row_l) * 128 + box * (BN * 128);
+      // a lane's rows are kRowsIt (4 or 8) apart: the swizzle of the second of
+      // a pair differs from the first's in one bit at most
+      const uint32_t first_c = ((c0 + odd_first) ^ (row_l & 7)) << 4;  // and the other chunk: ^ 16
+      Ring<NR> raw;
+      int so = 0;
+      uint32_t so_phase = 1;
+      for (long long x = x0; x < x1 && !fail;) {
+        const Seg s = seg_at(x);
+#pragma unroll 1
+        for (int j = 0; j < s.n; ++j, raw.next()) {
+          // the scan waited for the tile's copies before it arrived
+          if (!ring_wait(&scan_full[raw.i], raw.phase, p.err, abort_flag) ||
+              !ring_wait(&empty[so], so_phase, p.err, abort_flag)) {
+            fail = true;
+            break;
+          }
+          const uint32_t raw_at = sR(raw.i) + codes_off, sc_at = sR(raw.i) + scale_off;
+          const uint32_t dst = row_off + so * Y::kKV;
+#pragma unroll 1
+          for (int i0 = 0; i0 < kIts; i0 += kU) {
+            uint2 w[kU][2];
+            uint32_t s2[kU];
+#pragma unroll
+            for (int i = 0; i < kU; ++i) {
+              w[i][0] = lds64(raw_at + (i0 + i) * kRowsIt * D);
+              w[i][1] = lds64((raw_at ^ 8u) + (i0 + i) * kRowsIt * D);
+              s2[i] = lds32(sc_at + (i0 + i) * kRowsIt * NG * 4);
+            }
+#pragma unroll
+            for (int i = 0; i < kU; ++i) {
+              const uint32_t at = dst + (i0 + i) * kRowsIt * 128 + (first_c ^ ((i * kRowsIt & 4) << 4));
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                const uint32_t wa = w[i][q].x ^ 0x80808080u, wb = w[i][q].y ^ 0x80808080u;
+                st_shared_v4(q ? at ^ 16u : at, hmul2(codes_to_half2(wa, kSelBytes01), s2[i]),
+                             hmul2(codes_to_half2(wa, kSelBytes23), s2[i]),
+                             hmul2(codes_to_half2(wb, kSelBytes01), s2[i]),
+                             hmul2(codes_to_half2(wb, kSelBytes23), s2[i]));
+              }
+            }
+          }
+          // the MMA reads the tile through the async proxy
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&full[so]);
+            mbar_arrive(&raw_empty[raw.i]);
+          }
+          if (++so == n_st) {
+            so = 0;
+            so_phase ^= 1u;
+          }
+        }
+        x += s.n;
+      }
+    } else if (warp == kWarpScan) {
+      // ------------------------------------------------ scales' exponents
+      // ahead of the conversion: a tile's largest scales fix the powers of
+      // two that its keys and values are taken with, and the scales become the
+      // fp16 pairs that multiply the codes, in place
+      Ring<NR> raw;
       int g = 0;
       for (long long x = x0; x < x1 && !fail;) {
         const Seg s = seg_at(x);
         int e_v = INT_MAX;  // the exponent that V's operands have in O (unset)
-        for (int t = s.t0; t < s.t0 + s.n && !fail; ++t, ++g) {
-          const int st = g % NR, rows = min(BN, pl.len - t * BN);
-          if (!warp_wait(&raw_full[st], (g / NR) & 1, p.err, abort_flag)) {
+        int left = pl.len - s.t0 * BN;
+#pragma unroll 1
+        for (int j = 0; j < s.n; ++j, ++g, raw.next(), left -= BN) {
+          const int st = raw.i;
+          if (!ring_wait(&raw_full[st], raw.phase, p.err, abort_flag)) {
             fail = true;
             break;
           }
-          const uint32_t raw = sR(st), rks = raw + 2 * Y::kCodes, rvs = rks + Y::kScales;
-          // the tile's largest scales (every warp for itself: no exchange)
-          float km = 0.f, vm = 0.f;
+          const uint32_t rks = sR(st) + 2 * Y::kCodes, rvs = rks + Y::kScales;
+          constexpr int kPer = BN * NG / 32;
+          float ksc[kPer], vsc[kPer], km = 0.f, vm = 0.f;
 #pragma unroll
-          for (int i = 0; i < BN * NG / 32; ++i) {
+          for (int i = 0; i < kPer; ++i) {
             const int idx = lane + 32 * i;
-            if (idx / NG < rows) {
-              km = fmaxf(km, fabsf(lds_f32(rks + 4 * idx)));
-              vm = fmaxf(vm, fabsf(lds_f32(rvs + 4 * idx)));
-            }
+            // a slot behind the prefix: whatever is staged counts 0
+            ksc[i] = idx / NG < left ? lds_f32(rks + 4 * idx) : 0.f;
+            vsc[i] = idx / NG < left ? lds_f32(rvs + 4 * idx) : 0.f;
+            km = fmaxf(km, fabsf(ksc[i]));
+            vm = fmaxf(vm, fabsf(vsc[i]));
           }
 #pragma unroll
           for (int off = 16; off >= 1; off >>= 1) {
@@ -293,51 +425,21 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Prefix
               e_v = want;
             }
           }
-          const float up_v = e_v == INT_MAX ? 1.f : pow2i(e_v);
-          if (dw == 0 && lane == 0)
-            s_info[g % kInfo] = make_float4(pow2i(-e_k), fix, e_v == INT_MAX ? 1.f : pow2i(-e_v), 0.f);
-          const float up_k = pow2i(e_k);
+          const float up_k = pow2i(e_k), up_v = e_v == INT_MAX ? 1.f : pow2i(e_v);
 #pragma unroll
-          for (int which = 0; which < 2; ++which) {
-            const int so = g % (which ? NV : NK);
-            uint64_t *full = which ? &v_full[so] : &k_full[so], *empty = which ? &v_empty[so] : &k_empty[so];
-            const int ph = g / (which ? NV : NK);
-            if (ph >= 1 && !warp_wait(empty, (ph - 1) & 1, p.err, abort_flag)) {
-              fail = true;
-              break;
-            }
-            const uint32_t dst = which ? sV(so) : sK(so);
-#pragma unroll
-            for (int it = 0; it < kIts; ++it) {
-              const int row = 16 * dw + it * kRowsIt + row_l;
-              uint32_t w[4];
-              ld_shared_v4(raw + which * Y::kCodes + row * D + piece * 16, w[0], w[1], w[2], w[3]);
-              float sc = lds_f32((which ? rvs : rks) + 4 * (row * NG + piece / 2)) * (which ? up_v : up_k);
-              sc = row < rows ? sc : 0.f;  // a slot behind the prefix: whatever is staged counts 0
-              const uint32_t s2 = pack_half2(sc, sc);
-              uint32_t h[8];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const uint32_t wb = w[i] ^ 0x80808080u;
-                h[2 * i] = hmul2(codes_to_half2(wb, kSelBytes01), s2);
-                h[2 * i + 1] = hmul2(codes_to_half2(wb, kSelBytes23), s2);
-              }
-              const uint32_t at = dst + box * (BN * 128) + row * 128;
-              const uint32_t a0 = at + ((c0 ^ (row & 7)) << 4), a1 = at + (((c0 + 1) ^ (row & 7)) << 4);
-              if (odd_first) {
-                st_shared_v4(a1, h[4], h[5], h[6], h[7]);
-                st_shared_v4(a0, h[0], h[1], h[2], h[3]);
-              } else {
-                st_shared_v4(a0, h[0], h[1], h[2], h[3]);
-                st_shared_v4(a1, h[4], h[5], h[6], h[7]);
-              }
-            }
-            // the MMA reads the tile through the async proxy
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) mbar_arrive(full);
+          for (int i = 0; i < kPer; ++i) {
+            const int idx = lane + 32 * i;
+            const float a = ksc[i] * up_k, b = vsc[i] * up_v;
+            sts32(rks + 4 * idx, pack_half2(a, a));
+            sts32(rvs + 4 * idx, pack_half2(b, b));
           }
-          if (lane == 0) mbar_arrive(&raw_empty[st]);
+          __syncwarp();
+          if (lane == 0) {
+            // 2^-e of K; the factor that O needs before this tile's V; 2^-e of V
+            s_info[g % kInfo] = make_float4(pow2i(-e_k), fix, e_v == INT_MAX ? 1.f : pow2i(-e_v), 0.f);
+            mbar_arrive(&scan_full[st]);
+            mbar_arrive(&raw_empty[st]);
+          }
         }
         x += s.n;
       }
@@ -347,68 +449,71 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Prefix
       const uint32_t leader = elect_one();
       constexpr uint32_t kIdS = idesc_f16(BM, BN, 0);
       constexpr uint32_t kIdPV = idesc_f16(BM, D, 1);
-      int g = 0, gb = 0, nseg = 0;  // tiles, this block's tiles, this block's segments
+      Ring<NK> kr;
+      Ring<NV> vr;
+      Ring<NS> sr, pr;  // S buffers by the order of S and of PV
+      uint32_t q_phase = 0;
+      // descriptors of the first stage's first 16 channels (or keys)
+      const uint64_t dq = sdesc_sw128(sQ(rb), 16, 1024), dk = sdesc_sw128(sK(0), 16, 1024),
+                     dv = sdesc_sw128(sV(0), BN * 128, 1024);
       for (long long x = x0; x < x1 && !fail;) {
         const Seg s = seg_at(x);
+        x += s.n;
         if (rb >= s.nb) {
           // no rows: only the hand-back of the operand stages
-          for (int j = 0; j < s.n && !fail; ++j, ++g) {
-            if (!warp_wait(&k_full[g % NK], (g / NK) & 1, p.err, abort_flag) ||
-                !warp_wait(&v_full[g % NV], (g / NV) & 1, p.err, abort_flag)) {
-              fail = true;
-              break;
-            }
-            if (lane == 0) {
-              mbar_arrive(&k_empty[g % NK]);
-              mbar_arrive(&v_empty[g % NV]);
+#pragma unroll 1
+          for (int j = 0; j < s.n && !fail; ++j, kr.next(), vr.next()) {
+            fail = !ring_wait(&k_full[kr.i], kr.phase, p.err, abort_flag) ||
+                   !ring_wait(&v_full[vr.i], vr.phase, p.err, abort_flag);
+            if (lane == 0 && !fail) {
+              mbar_arrive(&k_empty[kr.i]);
+              mbar_arrive(&v_empty[vr.i]);
             }
             __syncwarp();
           }
-          x += s.n;
           continue;
         }
-        if (!warp_wait(&q_full[rb], nseg & 1, p.err, abort_flag)) {
-          fail = true;
-          break;
-        }
-        auto issue_pv = [&](int j) {  // tile j of the segment
-          const int gg = g + j, bb = gb + j, u = bb % NS, sv = gg % NV;
-          if (!warp_wait(&p_full[rb][u], (bb / NS) & 1, p.err, abort_flag) ||
-              !warp_wait(&v_full[sv], (gg / NV) & 1, p.err, abort_flag))
-            return false;
-          tc_fence_after();
+        fail = !ring_wait(&q_full[rb], q_phase, p.err, abort_flag);
+        q_phase ^= 1u;
+        // step j: S(j), then PV(j - 1).  S(j) goes over the P that PV(j - NS)
+        // read: this thread issued that product earlier, and one thread's MMAs
+        // run in order
+#pragma unroll 1
+        for (int j = 0; j <= s.n && !fail; ++j) {
+          if (j < s.n) {
+            if (!ring_wait(&k_full[kr.i], kr.phase, p.err, abort_flag)) {
+              fail = true;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t kd = dk + uint64_t(kr.i * (Y::kKV >> 4));
 #pragma unroll
-          for (int kk = 0; kk < BN / 16; ++kk)  // 16 keys = 8 TMEM columns of fp16 pairs
-            mma_ts(tO(rb), tS(rb, u) + kk * 8, sdesc_sw128(sV(sv) + kk * 16 * 128, BN * 128, 1024), kIdPV,
-                   (j > 0 || kk > 0) ? 1u : 0u, leader);
-          mma_commit(&pv_done[rb][u], leader);
-          mma_commit(&v_empty[sv], leader);
-          return true;
-        };
-        for (int j = 0; j < s.n && !fail; ++j) {
-          const int gg = g + j, bb = gb + j, st = gg % NK;
-          // S(j) goes over the P that PV(j - NS) read: this thread issued that
-          // product earlier, and one thread's MMAs run in order
-          if (!warp_wait(&k_full[st], (gg / NK) & 1, p.err, abort_flag)) {
-            fail = true;
-            break;
+            for (int kk = 0; kk < D / 16; ++kk)
+              mma_ss(tS(rb, sr.i), dq + (kk >> 2) * (BM * 128 >> 4) + (kk & 3) * 2,
+                     kd + (kk >> 2) * (BN * 128 >> 4) + (kk & 3) * 2, kIdS, kk > 0 ? 1u : 0u, leader);
+            mma_commit(&s_full[rb][sr.i], leader);
+            mma_commit(&k_empty[kr.i], leader);
+            kr.next();
+            sr.next();
           }
-          tc_fence_after();
+          if (j > 0) {
+            if (!ring_wait(&p_full[rb][pr.i], pr.phase, p.err, abort_flag) ||
+                !ring_wait(&v_full[vr.i], vr.phase, p.err, abort_flag)) {
+              fail = true;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t vd = dv + uint64_t(vr.i * (Y::kKV >> 4));
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk & 3) * 32;
-            mma_ss(tS(rb, bb % NS), sdesc_sw128(sQ(rb) + (kk >> 2) * BM * 128 + off, 16, 1024),
-                   sdesc_sw128(sK(st) + (kk >> 2) * BN * 128 + off, 16, 1024), kIdS, kk > 0 ? 1u : 0u, leader);
+            for (int kk = 0; kk < BN / 16; ++kk)  // 16 keys = 8 TMEM columns of fp16 pairs
+              mma_ts(tO(rb), tS(rb, pr.i) + kk * 8, vd + kk * (16 * 128 >> 4), kIdPV, (j > 1 || kk > 0) ? 1u : 0u,
+                     leader);
+            mma_commit(&pv_done[rb][pr.i], leader);
+            mma_commit(&v_empty[vr.i], leader);
+            vr.next();
+            pr.next();
           }
-          mma_commit(&s_full[rb][bb % NS], leader);
-          mma_commit(&k_empty[st], leader);
-          if (j >= 1 && !issue_pv(j - 1)) fail = true;
         }
-        if (!fail && !issue_pv(s.n - 1)) fail = true;
-        g += s.n;
-        gb += s.n;
-        ++nseg;
-        x += s.n;
       }
     }
   } else {
@@ -416,12 +521,13 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Prefix
     regs_inc<kRegsSoftmax>();
     const int rb = warp >> 2, r = tid & (BM - 1);
     const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
-    int g = 0, gb = 0;
+    int g = 0;
+    Ring<NS> sr;
     for (long long x = x0; x < x1 && !fail;) {
       const Seg s = seg_at(x);
+      x += s.n;
       if (rb >= s.nb) {
         g += s.n;
-        x += s.n;
         continue;
       }
       const int row = s.r0 + rb * BM + r;
@@ -460,23 +566,30 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Prefix
       if (lane == 0) mbar_arrive(&q_full[rb]);
 
       float m_used = -INFINITY, l = 0.f, down = 1.f;
-      for (int j = 0; j < s.n; ++j) {
-        const int gg = g + j, bb = gb + j, u = bb % NS;
-        if (!fail) fail = !warp_wait(&s_full[rb][u], (bb / NS) & 1, p.err, abort_flag);
+      int left = pl.len - s.t0 * BN;
+      uint64_t *pv_last = nullptr;  // PV of the tile before: its barrier and parity
+      uint32_t pv_phase = 0;
+#pragma unroll 1
+      for (int j = 0; j < s.n; ++j, ++g, sr.next(), left -= BN) {
+        const int u = sr.i;
+        if (!fail) fail = !ring_wait(&s_full[rb][u], sr.phase, p.err, abort_flag);
         tc_fence_after();
+        uint64_t *const pv_prev = pv_last;
+        const uint32_t pv_prev_phase = pv_phase;
+        pv_last = &pv_done[rb][u];
+        pv_phase = sr.phase;
         if (!active) {
           if (lane == 0) mbar_arrive(&p_full[rb][u]);
           continue;
         }
-        const float4 info = s_info[gg % kInfo];
+        const float4 info = s_info[g % kInfo];
         uint32_t v[BN];
         tmem_ld32(tS(rb, u) + lane_base, v);
         tmem_ld32(tS(rb, u) + lane_base + 32, v + 32);
         tmem_ld_wait();
-        const int rows = min(BN, pl.len - (s.t0 + j) * BN);
-        if (rows < BN) {
+        if (left < BN) {
 #pragma unroll
-          for (int i = 0; i < BN; ++i) v[i] = i < rows ? v[i] : 0xff800000u;
+          for (int i = 0; i < BN; ++i) v[i] = i < left ? v[i] : 0xff800000u;
         }
         const float ct = c_row * info.x;
         down = info.z;
@@ -514,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Prefix
         l += (rsp[0] + rsp[1]) + (rsp[2] + rsp[3]);
         if (j >= 1 && __any_sync(0xffffffffu, alpha != 1.f)) {
           // O once PV(j-1) has landed
-          if (!fail) fail = !warp_wait(&pv_done[rb][(bb - 1) % NS], ((bb - 1) / NS) & 1, p.err, abort_flag);
+          if (!fail) fail = !ring_wait(pv_prev, pv_prev_phase, p.err, abort_flag);
           tc_fence_after();
 #pragma unroll 1
           for (int ch = 0; ch < D; ch += 32) {
@@ -533,8 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Prefix
         if (lane == 0) mbar_arrive(&p_full[rb][u]);
       }
       // ---- the segment's partials
-      const int bl = gb + s.n - 1;
-      if (!fail) fail = !warp_wait(&pv_done[rb][bl % NS], (bl / NS) & 1, p.err, abort_flag);
+      if (!fail) fail = !ring_wait(pv_last, pv_phase, p.err, abort_flag);
       tc_fence_after();
       if (active && !fail) {
         const size_t slot = size_t(blockIdx.x) + s.item;
@@ -555,9 +667,6 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Prefix
         if (row < p.R) p.out.ml[(slot * 2 + rb) * BM + r] = make_float2(m_used - kPBias, l);
         tc_fence_before();
       }
-      g += s.n;
-      gb += s.n;
-      x += s.n;
     }
   }
 
