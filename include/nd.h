@@ -360,13 +360,15 @@ ND_API int nd_kv_cache_read(const nd_kv_cache *cache, int window, nd_dtype dtype
  *           sink_len may be anything from 0 to sink_cap; the prefix's ring is
  *           not read.  nd_kv_cache_from_prefill with a sink flag on every
  *           position fills it from a prefill of the prompt.
- *   q, out, lse, window, n_q_heads  as nd_swa_sink_decode; batch <= 65535
+ *   q, out, lse, window, n_q_heads  as nd_swa_sink_decode; batch * n_q_heads at
+ *           most 2^24
  * A sequence that sees no key gets out = 0, lse = -inf.  The prefix's keys
  * and values are taken as fp16 after a power-of-two scaling (each within
  * 2^-11 of code * scale, relative), products and sums in fp32.
  * Partial results go to the workspace (device, 16-byte aligned) of
  * nd_shared_prefix_decode_workspace_size(batch, n_q_heads, n_kv_heads,
- * head_dim, prefix->sink_cap, cache->sink_cap + cache->ring_cap) bytes.
+ * head_dim, prefix->sink_cap, cache->sink_cap + cache->ring_cap) bytes (0: none
+ * is needed, NULL allowed).
  */
 ND_API size_t nd_shared_prefix_decode_workspace_size(int batch, int n_q_heads, int n_kv_heads,
                                                      int head_dim, int prefix_cap, int max_slots);

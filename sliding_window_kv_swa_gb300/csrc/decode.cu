@@ -37,17 +37,15 @@
 // ordinary load or store.
 #include <atomic>
 
+#include "decode_step.cuh"
 #include "nd_common.cuh"
 #include "nd_internal.h"
-#include "shared_prefix.cuh"
 
 namespace nd {
 
 namespace {
 
-constexpr int kStep = 16;    // slots per warp step (one MMA k-step)
 constexpr int kTargetCtas = 152;
-constexpr float kLazyLog2 = 8.f;  // p is taken against a max at most 2^8 below the true one
 // Largest cluster the fused step uses.  Clusters are co-scheduled on one GPC;
 // at 8 CTAs that costs the large-batch step more than the saved launch.
 constexpr int kMaxFusedCluster = 4;
@@ -119,85 +117,11 @@ __device__ __forceinline__ uint2 load_row_words(const uint16_t *src, int lane) {
   else return make_uint2(reinterpret_cast<const uint32_t *>(src)[lane], 0u);
 }
 
-template <int D>
-struct Stage {
-  static constexpr int kCodes = kStep * D;              // bytes of K (or V) codes per step
-  static constexpr int kScales = kStep * (D / 32) * 4;  // bytes of K (or V) scales per step
-  static constexpr int kBytes = 2 * kCodes + 2 * kScales;
-};
-
-__device__ __forceinline__ int ilog2_floor(float x) {  // x > 0, finite
-  int e = int((__float_as_uint(x) >> 23) & 0xff) - 127;
-  if (e == -127) e = -127 + (31 - __clz(__float_as_uint(x) & 0x7fffff)) - 22;  // subnormal
-  return e;
-}
-
-// 2^e for e in [-126, 127]
-__device__ __forceinline__ float exp2i(int e) {
-  e = max(-126, min(127, e));
-  return __uint_as_float(uint32_t(e + 127) << 23);
-}
-
-// Byte offset inside a stage: 16-byte chunks XOR-swizzled by the 128-byte
-// line index, a bijection inside every 128-byte line.
-__device__ __forceinline__ uint32_t swz(uint32_t a) { return a ^ (((a >> 7) & 7u) << 4); }
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void *src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ float ldsf(uint32_t a) {
-  float v;
-  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ float4 lds128f(uint32_t a) {
-  float4 v;
-  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
-  return v;
-}
-// The NG group scales of one slot, which sit together in the stage (16 or 8
-// bytes).  At head_dim 128 one 16-byte load replaces four 4-byte loads for
-// each of the eight K and V scale rows a thread reads per step (the kernel
-// is issue-bound there: 4-5 points of HBM at B128-B512); at head_dim 64 the
-// two 4-byte loads stay, since the 8-byte form adds a spill to the 96-register
-// builds.
-template <int NG>
-__device__ __forceinline__ void lds_scales(uint32_t a, float *s) {
-  if constexpr (NG == 4) {
-    const float4 v = lds128f(a);
-    s[0] = v.x, s[1] = v.y, s[2] = v.z, s[3] = v.w;
-  } else {
-    s[0] = ldsf(a);
-    s[1] = ldsf(a + 4);
-  }
-}
-
 // ST: cp.async stages per warp (ST - 1 steps in flight).  d = 128 has two
 // builds: 4 stages at three CTAs per SM, and 5 stages at two CTAs per SM for
 // grids of at most four CTAs per SM, where the bytes each CTA keeps in flight
 // matter more than how many CTAs an SM holds.
-// kPart: the CTA's (max, sum, O) always go to the partials, for a merge with
-// others.
-template <int D, int NW, int ST, bool kPart = false>
+template <int D, int NW, int ST>
 __global__ void __launch_bounds__(NW * 32, D == 128 ? (ST == 4 ? 3 : 2) : (NW == 4 ? 5 : 1))
     decode_kernel(const DecodeParams p) {
   constexpr int kStages = ST;
@@ -344,31 +268,8 @@ __global__ void __launch_bounds__(NW * 32, D == 128 ? (ST == 4 ? 3 : 2) : (NW ==
 
 #pragma unroll
   for (int n = 0; n < kStages - 1; ++n) issue(n);
-  uint32_t qa[NG][2][2];
-  float head_coef;  // 2^-Eq * log2(e) / sqrt(D), for head g
-  {
-    float qm = 0.f;
-#pragma unroll
-    for (int grp = 0; grp < NG; ++grp) {
-      const uint32_t ws[4] = {w[grp].x, w[grp].y, w[grp].z, w[grp].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) qm = fmaxf(qm, fmaxf(fabsf(bf16_lo(ws[i])), fabsf(bf16_hi(ws[i]))));
-    }
-    qm = fmaxf(qm, __shfl_xor_sync(0xffffffffu, qm, 1));
-    qm = fmaxf(qm, __shfl_xor_sync(0xffffffffu, qm, 2));
-    const int eq = qm > 0.f ? 14 - ilog2_floor(qm) : 0;
-    const float up = exp2i(eq);
-    head_coef = exp2i(-eq) * (1.4426950408889634f * rsqrtf(float(D)));
-#pragma unroll
-    for (int grp = 0; grp < NG; ++grp) {
-      const uint32_t ws[4] = {w[grp].x, w[grp].y, w[grp].z, w[grp].w};
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        qa[grp][s][0] = pack_half2(bf16_lo(ws[2 * s]) * up, bf16_hi(ws[2 * s]) * up);
-        qa[grp][s][1] = pack_half2(bf16_lo(ws[2 * s + 1]) * up, bf16_hi(ws[2 * s + 1]) * up);
-      }
-    }
-  }
+  HeadQ<D> hq;
+  make_q<D>(w, hq);
   __syncthreads();  // the metadata is in
   const int sink_len = s_meta[0], rs_eff = s_meta[1], n_vis = s_meta[2], new_slot = s_meta[3];
   if (fused) cluster_arrive();  // this CTA is done reading the sequence's metadata
@@ -381,15 +282,7 @@ __global__ void __launch_bounds__(NW * 32, D == 128 ? (ST == 4 ? 3 : 2) : (NW ==
     return d < n_vis;
   };
 
-  float o[NG][2][4];
-#pragma unroll
-  for (int grp = 0; grp < NG; ++grp)
-#pragma unroll
-    for (int tt = 0; tt < 2; ++tt)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[grp][tt][i] = 0.f;
-  float m_run = -INFINITY, l_run = 0.f;  // m_run: the max p is taken against (log2 units)
-  int e_acc = 127;  // power-of-two pre-scale of P' (never increases; 127 = unset)
+  RunState<D> run;
 
   for (int n = 0; n < n_steps; ++n) {
     issue(n + kStages - 1);
@@ -433,7 +326,7 @@ __global__ void __launch_bounds__(NW * 32, D == 128 ? (ST == 4 ? 3 : 2) : (NW ==
       }
       __syncwarp();
     }
-    const int col[4] = {2 * t, 2 * t + 1, 8 + 2 * t, 9 + 2 * t};
+    const int col[4] = {2 * t, 2 * t + 1, 8 + 2 * t, 9 + 2 * t};  // this thread's slots of the step
     // whole step visible (a filled sink run, or a full ring) -- the common
     // case -- or per slot
     const bool all_vis = base + kStep <= v_end &&
@@ -442,111 +335,7 @@ __global__ void __launch_bounds__(NW * 32, D == 128 ? (ST == 4 ? 3 : 2) : (NW ==
 #pragma unroll
     for (int i = 0; i < 4; ++i) vis[i] = all_vis || visible(base + col[i]);
 
-    // ---- QK: scores for head g at columns 2t, 2t+1 of tiles 0 and 1
-    float sc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int row = 8 * j + g;
-      float ks0[NG], ks1[NG];  // K scales of this thread's two columns
-      lds_scales<NG>(st + 2 * S::kCodes + (8 * j + 2 * t) * NG * 4, ks0);
-      lds_scales<NG>(st + 2 * S::kCodes + (8 * j + 2 * t + 1) * NG * 4, ks1);
-#pragma unroll
-      for (int grp = 0; grp < NG; ++grp) {
-        const uint2 kw = lds64(st + swz(uint32_t(row * D + 32 * grp + 8 * t)));
-        float d0 = 0.f, d1 = 0.f, d2 = 0.f, d3 = 0.f;
-        const uint32_t w0 = kw.x ^ 0x80808080u, w1 = kw.y ^ 0x80808080u;
-        mma_f16_16816(d0, d1, d2, d3, qa[grp][0][0], 0u, qa[grp][0][1], 0u,
-                      codes_to_half2(w0, kSelBytes01), codes_to_half2(w0, kSelBytes23));
-        mma_f16_16816(d0, d1, d2, d3, qa[grp][1][0], 0u, qa[grp][1][1], 0u,
-                      codes_to_half2(w1, kSelBytes01), codes_to_half2(w1, kSelBytes23));
-        sc[2 * j] = fmaf(ks0[grp], d0, sc[2 * j]);
-        sc[2 * j + 1] = fmaf(ks1[grp], d1, sc[2 * j + 1]);
-      }
-    }
-    // ---- online softmax for head g (log2 domain)
-    float mx = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      sc[i] = (vis[i] && g < G) ? sc[i] * head_coef : -INFINITY;
-      mx = fmaxf(mx, sc[i]);
-    }
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    // lazy max: p is taken against m_run, which moves (and O is rescaled)
-    // only when a score exceeds it by more than 2^kLazyLog2, so p <= 2^8
-    const bool need = mx > m_run + kLazyLog2;
-    const float m_new = need ? mx : m_run;
-    const float alpha = need ? (m_run == -INFINITY ? 0.f : ex2(m_run - m_new)) : 1.f;
-    float pr[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) pr[i] = (m_new == -INFINITY) ? 0.f : ex2(sc[i] - m_new);
-    l_run = l_run * alpha + (pr[0] + pr[1]) + (pr[2] + pr[3]);
-    m_run = m_new;
-    // V scales of the step, and one exponent for all groups that keeps
-    // p * v_scale * 2^e below 2^15 (p <= 2^8); the accumulator keeps the
-    // smallest exponent seen so far
-    float vsc[NG][4];
-    float vm = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float vs_i[NG];
-      lds_scales<NG>(st + 2 * S::kCodes + S::kScales + col[i] * NG * 4, vs_i);
-#pragma unroll
-      for (int grp = 0; grp < NG; ++grp) vsc[grp][i] = vs_i[grp];
-    }
-#pragma unroll
-    for (int grp = 0; grp < NG; ++grp)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) vm = fmaxf(vm, vis[i] ? vsc[grp][i] : 0.f);
-    vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 1));
-    vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 2));
-    const int e_step = vm > 0.f ? 14 - int(kLazyLog2) - ilog2_floor(vm) : 127;
-    const bool shrink_e = e_step < e_acc;
-    // rescale O (this thread's columns are heads 2t and 2t+1) only when a
-    // head's max moved or the exponent shrank: warp-uniform, and rare
-    if (__any_sync(0xffffffffu, need || shrink_e)) {
-      const float shrink = shrink_e ? (e_acc == 127 ? 0.f : exp2i(e_step - e_acc)) : 1.f;
-      const float f_lo = __shfl_sync(0xffffffffu, alpha, (2 * t) * 4) * shrink;
-      const float f_hi = __shfl_sync(0xffffffffu, alpha, (2 * t + 1) * 4) * shrink;
-#pragma unroll
-      for (int grp = 0; grp < NG; ++grp)
-#pragma unroll
-        for (int tt = 0; tt < 2; ++tt) {
-          o[grp][tt][0] *= f_lo;
-          o[grp][tt][1] *= f_hi;
-          o[grp][tt][2] *= f_lo;
-          o[grp][tt][3] *= f_hi;
-        }
-      if (shrink_e) e_acc = e_step;
-    }
-    // (while no scale has been seen, every visible scale is 0 and u is moot)
-    const float u = e_acc == 127 ? 1.f : exp2i(e_acc);
-    float pu[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) pu[i] = vis[i] ? pr[i] * u : 0.f;
-    // ---- PV per group: B = P'^T (slot x head), A = V^T (channel x slot)
-#pragma unroll
-    for (int grp = 0; grp < NG; ++grp) {
-      // masked slots contribute 0 (their scale may be anything, even non-finite)
-      const uint32_t b0 = pack_half2(vis[0] ? pu[0] * vsc[grp][0] : 0.f, vis[1] ? pu[1] * vsc[grp][1] : 0.f);
-      const uint32_t b1 = pack_half2(vis[2] ? pu[2] * vsc[grp][2] : 0.f, vis[3] ? pu[3] * vsc[grp][3] : 0.f);
-      uint32_t vw[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        vw[i] = lds32(st + S::kCodes + swz(uint32_t(col[i] * D + 32 * grp + 4 * g)));
-      const uint32_t x01 = prmt(vw[0], vw[1], 0x5140u) ^ 0x80808080u;
-      const uint32_t x23 = prmt(vw[0], vw[1], 0x7362u) ^ 0x80808080u;
-      const uint32_t y01 = prmt(vw[2], vw[3], 0x5140u) ^ 0x80808080u;
-      const uint32_t y23 = prmt(vw[2], vw[3], 0x7362u) ^ 0x80808080u;
-      // tile 0: rows g <-> channel 4g, rows g+8 <-> channel 4g+1
-      mma_f16_16816(o[grp][0][0], o[grp][0][1], o[grp][0][2], o[grp][0][3],
-                    codes_to_half2(x01, kSelBytes01), codes_to_half2(x01, kSelBytes23),
-                    codes_to_half2(y01, kSelBytes01), codes_to_half2(y01, kSelBytes23), b0, b1);
-      // tile 1: rows g <-> channel 4g+2, rows g+8 <-> channel 4g+3
-      mma_f16_16816(o[grp][1][0], o[grp][1][1], o[grp][1][2], o[grp][1][3],
-                    codes_to_half2(x23, kSelBytes01), codes_to_half2(x23, kSelBytes23),
-                    codes_to_half2(y23, kSelBytes01), codes_to_half2(y23, kSelBytes23), b0, b1);
-    }
+    attend_step<D>(st, hq, vis, g < G, lane, run);
     __syncwarp();  // every lane is done with this stage before it is refilled
   }
   cp_async_wait<0>();
@@ -555,32 +344,13 @@ __global__ void __launch_bounds__(NW * 32, D == 128 ? (ST == 4 ? 3 : 2) : (NW ==
   // scheduled from here on; where several CTAs share an SM, early-placed CTAs
   // of the next step crowd unevenly, so there the trigger stays implicit (exit).
   if (D == 64 && NW == 20) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // ---- merge: quad-sum l, then the warps through shared memory (the stage
+  // ---- merge: the warps through shared memory (the stage
   //      buffers are free once every warp is past its loop)
-  l_run += __shfl_xor_sync(0xffffffffu, l_run, 1);
-  l_run += __shfl_xor_sync(0xffffffffu, l_run, 2);
   __syncthreads();
   float *s_o = reinterpret_cast<float *>(smem);  // [NW][8][D]
   float *s_m = s_o + NW * 8 * D;                 // [NW][8]
   float *s_l = s_m + NW * 8;                     // [NW][8]
-  if (t == 0) {
-    s_m[warp * 8 + g] = m_run;
-    s_l[warp * 8 + g] = l_run;
-  }
-  const float down = e_acc == 127 ? 0.f : exp2i(-e_acc);
-#pragma unroll
-  for (int grp = 0; grp < NG; ++grp) {
-#pragma unroll
-    for (int tt = 0; tt < 2; ++tt) {
-      const int ch0 = 32 * grp + 4 * g + 2 * tt;  // row g; row g+8 is ch0 + 1
-      float *w0 = s_o + (warp * 8 + 2 * t) * D;
-      float *w1 = s_o + (warp * 8 + 2 * t + 1) * D;
-      w0[ch0] = o[grp][tt][0] * down;
-      w1[ch0] = o[grp][tt][1] * down;
-      w0[ch0 + 1] = o[grp][tt][2] * down;
-      w1[ch0 + 1] = o[grp][tt][3] * down;
-    }
-  }
+  store_state<D>(run, lane, s_o + warp * 8 * D, s_m + warp * 8, s_l + warp * 8);
   __syncthreads();
   for (int idx = threadIdx.x; idx < G * D; idx += NW * 32) {
     const int h = idx / D, ch = idx % D;
@@ -594,7 +364,7 @@ __global__ void __launch_bounds__(NW * 32, D == 128 ? (ST == 4 ? 3 : 2) : (NW ==
         O += f * s_o[(w * 8 + h) * D + ch];
       }
     }
-    if (!kPart && p.n_split == 1) {
+    if (p.n_split == 1) {
       const size_t row = size_t(b) * p.Hq + hkv * G + h;
       const float val = L > 0.f ? O / L : 0.f;
       p.out[row * D + ch] = __bfloat16_as_ushort(__float2bfloat16_rn(val));
@@ -647,45 +417,6 @@ __global__ void __launch_bounds__(D) decode_combine_kernel(const DecodeParams p)
   if (ch == 0 && p.lse) p.lse[row] = L > 0.f ? (M + __log2f(L)) * 0.6931471805599453f : -INFINITY;
 }
 
-// Merge the own partials and the shared prefix's of one (sequence, query head)
-// per block.
-template <int D>
-__global__ void __launch_bounds__(D) shared_combine_kernel(const DecodeParams p, const PrefixParts pre,
-                                                           const int32_t *prefix_len, int prefix_cap, int prefix_grid) {
-  pdl_wait();
-  const int row = blockIdx.x;  // b * Hq + h
-  const int b = row / p.Hq, hq = row % p.Hq;
-  const int hkv = hq / p.G, h = hq % p.G;
-  const size_t pair = size_t(b) * p.c.n_kv_heads + hkv;
-  const int ch = threadIdx.x;
-  float M = -INFINITY, L = 0.f, O = 0.f;
-  auto merge = [&](float m, float l, float o) {
-    if (m == -INFINITY) return;
-    const float m_new = fmaxf(M, m), f_old = ex2(M - m_new), f = ex2(m - m_new);
-    L = L * f_old + f * l;
-    O = O * f_old + f * o;
-    M = m_new;
-  };
-  const PrefixPlan pl = prefix_plan(*prefix_len, prefix_cap, p.c.n_kv_heads, p.c.batch * p.G, prefix_grid);
-  if (pl.nt > 0) {
-    const int r = b * p.G + h, rr = r % (2 * kPrefixBlock);
-    const int item = hkv * pl.pairs + r / (2 * kPrefixBlock);
-    const int c0 = pl.owner((long long)item * pl.nt), c1 = pl.owner((long long)(item + 1) * pl.nt - 1);
-    for (int c = c0; c <= c1; ++c) {
-      const size_t slot = (size_t(c) + item) * 2 + rr / kPrefixBlock;
-      const float2 ml = pre.ml[slot * kPrefixBlock + rr % kPrefixBlock];
-      merge(ml.x, ml.y, pre.o[((slot * (D / 4) + ch / 4) * kPrefixBlock + rr % kPrefixBlock) * 4 + ch % 4]);
-    }
-  }
-  for (int s = 0; s < p.n_split; ++s) {
-    const size_t part = (pair * p.n_split + s) * p.G + h;
-    merge(p.ws_ml[part * 2], p.ws_ml[part * 2 + 1], p.ws_o[part * D + ch]);
-  }
-  const float val = L > 0.f ? O / L : 0.f;
-  p.out[size_t(row) * D + ch] = __bfloat16_as_ushort(__float2bfloat16_rn(val));
-  if (ch == 0 && p.lse) p.lse[row] = L > 0.f ? (M + __log2f(L)) * 0.6931471805599453f : -INFINITY;
-}
-
 // Warps per CTA: 20 at head_dim 64 (one CTA per SM covers a whole short
 // sequence in one or two steps per warp), 4 at head_dim 128 (two or three CTAs
 // per SM, by ring depth).  Grids of many (sequence, KV head) pairs at head_dim
@@ -701,10 +432,10 @@ size_t decode_smem_bytes() {
   return stages > merge ? stages : merge;
 }
 
-template <int D, int ST, int NW = warps_for(D), bool kPart = false>
+template <int D, int ST, int NW = warps_for(D)>
 cudaError_t launch_d(const DecodeParams &p, dim3 grid, cudaStream_t stream) {
   const size_t smem = decode_smem_bytes<D, NW, ST>();
-  auto kern = decode_kernel<D, NW, ST, kPart>;
+  auto kern = decode_kernel<D, NW, ST>;
   // the shared-memory opt-in once per device (a per-launch call is host
   // time on every decode step)
   static std::atomic<unsigned long long> smem_set{0};
@@ -737,7 +468,7 @@ cudaError_t launch_d(const DecodeParams &p, dim3 grid, cudaStream_t stream) {
   }
   e = cudaLaunchKernelEx(&cfg, kern, p);
   if (e != cudaSuccess) return e;
-  if (!kPart && p.n_split > 1) decode_combine_kernel<D><<<p.c.batch * p.Hq, D, 0, stream>>>(p);
+  if (p.n_split > 1) decode_combine_kernel<D><<<p.c.batch * p.Hq, D, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -814,46 +545,6 @@ cudaError_t launch_decode(const void *q, const nd_kv_cache &c, int n_q_heads, in
     return ctas >= kManyPairs64 ? launch_d<64, 4, 4>(p, grid, stream) : launch_d<64, 4>(p, grid, stream);
   }
   return cudaErrorInvalidValue;
-}
-
-size_t shared_decode_workspace_bytes(int batch, int n_q_heads, int n_kv_heads, int head_dim, int prefix_cap,
-                                     int max_slots) {
-  const DecodePlan own = plan_decode(batch, n_kv_heads, max_slots, head_dim);
-  const size_t rows = prefix_slots(prefix_cap, n_kv_heads, batch * (n_q_heads / n_kv_heads)) * 2 * kPrefixBlock;
-  return (rows + size_t(batch) * n_q_heads * own.n_split) * (head_dim + 2) * sizeof(float);
-}
-
-cudaError_t launch_shared_decode(const void *q, const nd_kv_cache &prefix, const nd_kv_cache &c, int n_q_heads,
-                                 int window, void *out, float *lse, void *ws, int *err, cudaStream_t stream) {
-  const int d = c.head_dim, rows = c.batch * (n_q_heads / c.n_kv_heads);
-  const size_t pre_rows = prefix_slots(prefix.sink_cap, c.n_kv_heads, rows) * 2 * kPrefixBlock;
-  PrefixParts pre;
-  pre.o = static_cast<float *>(ws);
-  pre.ml = reinterpret_cast<float2 *>(pre.o + pre_rows * d);
-  cudaError_t e = launch_shared_prefix(q, prefix, c.batch, n_q_heads, pre, err, stream);
-  if (e != cudaSuccess) return e;
-  const DecodePlan pl = plan_decode(c.batch, c.n_kv_heads, c.sink_cap + c.ring_cap, d);
-  DecodeParams p;
-  p.q = static_cast<const uint16_t *>(q);
-  p.c = c;
-  p.Hq = n_q_heads;
-  p.G = n_q_heads / c.n_kv_heads;
-  p.window = window;
-  p.n_split = pl.n_split;
-  p.slots_per_cta = pl.slots_per_cta;
-  p.out = static_cast<uint16_t *>(out);
-  p.lse = lse;
-  p.err = err;
-  p.k_new = p.v_new = nullptr;
-  p.ws_o = reinterpret_cast<float *>(pre.ml + pre_rows);
-  p.ws_ml = p.ws_o + size_t(c.batch) * n_q_heads * pl.n_split * d;
-  const dim3 grid(pl.n_split, c.n_kv_heads, c.batch);
-  e = d == 128 ? launch_d<128, 4, 4, true>(p, grid, stream) : launch_d<64, 4, 4, true>(p, grid, stream);
-  if (e != cudaSuccess) return e;
-  auto combine = d == 128 ? shared_combine_kernel<128> : shared_combine_kernel<64>;
-  return launch_pdl(combine, dim3(unsigned(c.batch) * n_q_heads), dim3(d), 0, stream, p, pre,
-                    static_cast<const int32_t *>(prefix.sink_len), prefix.sink_cap,
-                    prefix_grid(prefix.sink_cap, c.n_kv_heads, rows));
 }
 
 }  // namespace nd

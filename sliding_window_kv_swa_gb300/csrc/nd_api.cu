@@ -840,10 +840,10 @@ int nd_shared_prefix_decode(const void *q, const nd_kv_cache *prefix, const nd_k
       prefix->head_dim != cache->head_dim)
     return ND_ERR_INVALID_ARG;
   if (cache->batch == 0) return ND_OK;
-  if (cache->batch > 65535) return ND_ERR_UNSUPPORTED;
+  if (int64_t(cache->batch) * n_q_heads > (1 << 24)) return ND_ERR_UNSUPPORTED;
   const size_t need = nd_shared_prefix_decode_workspace_size(cache->batch, n_q_heads, cache->n_kv_heads, cache->head_dim,
                                                              prefix->sink_cap, cache->sink_cap + cache->ring_cap);
-  if (!workspace || workspace_bytes < need || !aligned16(workspace)) return ND_ERR_WORKSPACE;
+  if (need && (!workspace || workspace_bytes < need || !aligned16(workspace))) return ND_ERR_WORKSPACE;
   if ((st = check_device(nullptr)) != ND_OK) return st;
   return finish(launch_shared_decode(q, *prefix, *cache, n_q_heads, window, out, lse, workspace, device_error_word(),
                                      reinterpret_cast<cudaStream_t>(stream)));

@@ -35,7 +35,10 @@ struct PrefixPlan {
   __host__ __device__ long long tiles() const { return (long long)items * nt; }
   __host__ __device__ long long start(int c) const { return tiles() * c / ctas; }
   // the CTA whose stretch holds tile x
-  __host__ __device__ int owner(long long x) const { return int(((x + 1) * ctas - 1) / tiles()); }
+  __host__ __device__ int owner(long long x) const {
+    const long long n = tiles(), y = (x + 1) * ctas - 1;
+    return y < (1ll << 31) ? int(y) / int(n) : int(y / n);  // (a 32-bit division where it suffices)
+  }
 };
 
 __host__ __device__ inline PrefixPlan prefix_plan(int sink_len, int sink_cap, int n_kv_heads, int rows, int grid) {

@@ -36,10 +36,11 @@ def test_shared_prefix_decode():
     assert call(prefix=cache(d=96, S=100), own=cache(d=96)) == UNSUPPORTED
     assert call(own=cache(S=0, W=0)) == INVALID
     assert call(q=None) == INVALID and call(q=BAD) == INVALID and call(out=BAD) == INVALID and call(out=None) == INVALID
-    need = nd.nd_shared_prefix_decode_workspace_size(1, 8, 2, 64, 100, 12)
+    need = nd.nd_shared_prefix_decode_workspace_size(1, 8, 2, 64, 1000, 12)
     assert need > 0
-    assert call(ws=None) == WORKSPACE and call(size=need - 1) == WORKSPACE and call(ws=BAD) == WORKSPACE
-    assert call(own=cache(B=70000)) == UNSUPPORTED
+    long = cache(S=1000)
+    assert call(long, ws=None) == WORKSPACE and call(long, size=need - 1) == WORKSPACE and call(long, ws=BAD) == WORKSPACE
+    assert call(own=cache(B=1 << 22)) == UNSUPPORTED
     assert call(own=cache(B=0)) == OK
 
 
