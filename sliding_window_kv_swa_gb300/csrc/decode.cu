@@ -117,6 +117,23 @@ __device__ __forceinline__ uint2 load_row_words(const uint16_t *src, int lane) {
   else return make_uint2(reinterpret_cast<const uint32_t *>(src)[lane], 0u);
 }
 
+// The NG group scales of one slot, which sit together in the stage (16 or 8
+// bytes).  At head_dim 128 one 16-byte load replaces four 4-byte loads for
+// each of the eight K and V scale rows a thread reads per step (the kernel
+// is issue-bound there: 4-5 points of HBM at B128-B512); at head_dim 64 the
+// two 4-byte loads stay, since the 8-byte form adds a spill to the 96-register
+// builds.
+template <int NG>
+__device__ __forceinline__ void lds_scales(uint32_t a, float *s) {
+  if constexpr (NG == 4) {
+    const float4 v = lds128f(a);
+    s[0] = v.x, s[1] = v.y, s[2] = v.z, s[3] = v.w;
+  } else {
+    s[0] = ldsf(a);
+    s[1] = ldsf(a + 4);
+  }
+}
+
 // ST: cp.async stages per warp (ST - 1 steps in flight).  d = 128 has two
 // builds: 4 stages at three CTAs per SM, and 5 stages at two CTAs per SM for
 // grids of at most four CTAs per SM, where the bytes each CTA keeps in flight
@@ -268,8 +285,31 @@ __global__ void __launch_bounds__(NW * 32, D == 128 ? (ST == 4 ? 3 : 2) : (NW ==
 
 #pragma unroll
   for (int n = 0; n < kStages - 1; ++n) issue(n);
-  HeadQ<D> hq;
-  make_q<D>(w, hq);
+  uint32_t qa[NG][2][2];
+  float head_coef;  // 2^-Eq * log2(e) / sqrt(D), for head g
+  {
+    float qm = 0.f;
+#pragma unroll
+    for (int grp = 0; grp < NG; ++grp) {
+      const uint32_t ws[4] = {w[grp].x, w[grp].y, w[grp].z, w[grp].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) qm = fmaxf(qm, fmaxf(fabsf(bf16_lo(ws[i])), fabsf(bf16_hi(ws[i]))));
+    }
+    qm = fmaxf(qm, __shfl_xor_sync(0xffffffffu, qm, 1));
+    qm = fmaxf(qm, __shfl_xor_sync(0xffffffffu, qm, 2));
+    const int eq = qm > 0.f ? 14 - ilog2_floor(qm) : 0;
+    const float up = exp2i(eq);
+    head_coef = exp2i(-eq) * (1.4426950408889634f * rsqrtf(float(D)));
+#pragma unroll
+    for (int grp = 0; grp < NG; ++grp) {
+      const uint32_t ws[4] = {w[grp].x, w[grp].y, w[grp].z, w[grp].w};
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        qa[grp][s][0] = pack_half2(bf16_lo(ws[2 * s]) * up, bf16_hi(ws[2 * s]) * up);
+        qa[grp][s][1] = pack_half2(bf16_lo(ws[2 * s + 1]) * up, bf16_hi(ws[2 * s + 1]) * up);
+      }
+    }
+  }
   __syncthreads();  // the metadata is in
   const int sink_len = s_meta[0], rs_eff = s_meta[1], n_vis = s_meta[2], new_slot = s_meta[3];
   if (fused) cluster_arrive();  // this CTA is done reading the sequence's metadata
@@ -282,7 +322,15 @@ __global__ void __launch_bounds__(NW * 32, D == 128 ? (ST == 4 ? 3 : 2) : (NW ==
     return d < n_vis;
   };
 
-  RunState<D> run;
+  float o[NG][2][4];
+#pragma unroll
+  for (int grp = 0; grp < NG; ++grp)
+#pragma unroll
+    for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[grp][tt][i] = 0.f;
+  float m_run = -INFINITY, l_run = 0.f;  // m_run: the max p is taken against (log2 units)
+  int e_acc = 127;  // power-of-two pre-scale of P' (never increases; 127 = unset)
 
   for (int n = 0; n < n_steps; ++n) {
     issue(n + kStages - 1);
@@ -326,7 +374,7 @@ __global__ void __launch_bounds__(NW * 32, D == 128 ? (ST == 4 ? 3 : 2) : (NW ==
       }
       __syncwarp();
     }
-    const int col[4] = {2 * t, 2 * t + 1, 8 + 2 * t, 9 + 2 * t};  // this thread's slots of the step
+    const int col[4] = {2 * t, 2 * t + 1, 8 + 2 * t, 9 + 2 * t};
     // whole step visible (a filled sink run, or a full ring) -- the common
     // case -- or per slot
     const bool all_vis = base + kStep <= v_end &&
@@ -335,7 +383,111 @@ __global__ void __launch_bounds__(NW * 32, D == 128 ? (ST == 4 ? 3 : 2) : (NW ==
 #pragma unroll
     for (int i = 0; i < 4; ++i) vis[i] = all_vis || visible(base + col[i]);
 
-    attend_step<D>(st, hq, vis, g < G, lane, run);
+    // ---- QK: scores for head g at columns 2t, 2t+1 of tiles 0 and 1
+    float sc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int row = 8 * j + g;
+      float ks0[NG], ks1[NG];  // K scales of this thread's two columns
+      lds_scales<NG>(st + 2 * S::kCodes + (8 * j + 2 * t) * NG * 4, ks0);
+      lds_scales<NG>(st + 2 * S::kCodes + (8 * j + 2 * t + 1) * NG * 4, ks1);
+#pragma unroll
+      for (int grp = 0; grp < NG; ++grp) {
+        const uint2 kw = lds64(st + swz(uint32_t(row * D + 32 * grp + 8 * t)));
+        float d0 = 0.f, d1 = 0.f, d2 = 0.f, d3 = 0.f;
+        const uint32_t w0 = kw.x ^ 0x80808080u, w1 = kw.y ^ 0x80808080u;
+        mma_f16_16816(d0, d1, d2, d3, qa[grp][0][0], 0u, qa[grp][0][1], 0u,
+                      codes_to_half2(w0, kSelBytes01), codes_to_half2(w0, kSelBytes23));
+        mma_f16_16816(d0, d1, d2, d3, qa[grp][1][0], 0u, qa[grp][1][1], 0u,
+                      codes_to_half2(w1, kSelBytes01), codes_to_half2(w1, kSelBytes23));
+        sc[2 * j] = fmaf(ks0[grp], d0, sc[2 * j]);
+        sc[2 * j + 1] = fmaf(ks1[grp], d1, sc[2 * j + 1]);
+      }
+    }
+    // ---- online softmax for head g (log2 domain)
+    float mx = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      sc[i] = (vis[i] && g < G) ? sc[i] * head_coef : -INFINITY;
+      mx = fmaxf(mx, sc[i]);
+    }
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    // lazy max: p is taken against m_run, which moves (and O is rescaled)
+    // only when a score exceeds it by more than 2^kLazyLog2, so p <= 2^8
+    const bool need = mx > m_run + kLazyLog2;
+    const float m_new = need ? mx : m_run;
+    const float alpha = need ? (m_run == -INFINITY ? 0.f : ex2(m_run - m_new)) : 1.f;
+    float pr[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) pr[i] = (m_new == -INFINITY) ? 0.f : ex2(sc[i] - m_new);
+    l_run = l_run * alpha + (pr[0] + pr[1]) + (pr[2] + pr[3]);
+    m_run = m_new;
+    // V scales of the step, and one exponent for all groups that keeps
+    // p * v_scale * 2^e below 2^15 (p <= 2^8); the accumulator keeps the
+    // smallest exponent seen so far
+    float vsc[NG][4];
+    float vm = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float vs_i[NG];
+      lds_scales<NG>(st + 2 * S::kCodes + S::kScales + col[i] * NG * 4, vs_i);
+#pragma unroll
+      for (int grp = 0; grp < NG; ++grp) vsc[grp][i] = vs_i[grp];
+    }
+#pragma unroll
+    for (int grp = 0; grp < NG; ++grp)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) vm = fmaxf(vm, vis[i] ? vsc[grp][i] : 0.f);
+    vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 1));
+    vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 2));
+    const int e_step = vm > 0.f ? 14 - int(kLazyLog2) - ilog2_floor(vm) : 127;
+    const bool shrink_e = e_step < e_acc;
+    // rescale O (this thread's columns are heads 2t and 2t+1) only when a
+    // head's max moved or the exponent shrank: warp-uniform, and rare
+    if (__any_sync(0xffffffffu, need || shrink_e)) {
+      const float shrink = shrink_e ? (e_acc == 127 ? 0.f : exp2i(e_step - e_acc)) : 1.f;
+      const float f_lo = __shfl_sync(0xffffffffu, alpha, (2 * t) * 4) * shrink;
+      const float f_hi = __shfl_sync(0xffffffffu, alpha, (2 * t + 1) * 4) * shrink;
+#pragma unroll
+      for (int grp = 0; grp < NG; ++grp)
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt) {
+          o[grp][tt][0] *= f_lo;
+          o[grp][tt][1] *= f_hi;
+          o[grp][tt][2] *= f_lo;
+          o[grp][tt][3] *= f_hi;
+        }
+      if (shrink_e) e_acc = e_step;
+    }
+    // (while no scale has been seen, every visible scale is 0 and u is moot)
+    const float u = e_acc == 127 ? 1.f : exp2i(e_acc);
+    float pu[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) pu[i] = vis[i] ? pr[i] * u : 0.f;
+    // ---- PV per group: B = P'^T (slot x head), A = V^T (channel x slot)
+#pragma unroll
+    for (int grp = 0; grp < NG; ++grp) {
+      // masked slots contribute 0 (their scale may be anything, even non-finite)
+      const uint32_t b0 = pack_half2(vis[0] ? pu[0] * vsc[grp][0] : 0.f, vis[1] ? pu[1] * vsc[grp][1] : 0.f);
+      const uint32_t b1 = pack_half2(vis[2] ? pu[2] * vsc[grp][2] : 0.f, vis[3] ? pu[3] * vsc[grp][3] : 0.f);
+      uint32_t vw[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        vw[i] = lds32(st + S::kCodes + swz(uint32_t(col[i] * D + 32 * grp + 4 * g)));
+      const uint32_t x01 = prmt(vw[0], vw[1], 0x5140u) ^ 0x80808080u;
+      const uint32_t x23 = prmt(vw[0], vw[1], 0x7362u) ^ 0x80808080u;
+      const uint32_t y01 = prmt(vw[2], vw[3], 0x5140u) ^ 0x80808080u;
+      const uint32_t y23 = prmt(vw[2], vw[3], 0x7362u) ^ 0x80808080u;
+      // tile 0: rows g <-> channel 4g, rows g+8 <-> channel 4g+1
+      mma_f16_16816(o[grp][0][0], o[grp][0][1], o[grp][0][2], o[grp][0][3],
+                    codes_to_half2(x01, kSelBytes01), codes_to_half2(x01, kSelBytes23),
+                    codes_to_half2(y01, kSelBytes01), codes_to_half2(y01, kSelBytes23), b0, b1);
+      // tile 1: rows g <-> channel 4g+2, rows g+8 <-> channel 4g+3
+      mma_f16_16816(o[grp][1][0], o[grp][1][1], o[grp][1][2], o[grp][1][3],
+                    codes_to_half2(x23, kSelBytes01), codes_to_half2(x23, kSelBytes23),
+                    codes_to_half2(y23, kSelBytes01), codes_to_half2(y23, kSelBytes23), b0, b1);
+    }
     __syncwarp();  // every lane is done with this stage before it is refilled
   }
   cp_async_wait<0>();
@@ -344,13 +496,32 @@ __global__ void __launch_bounds__(NW * 32, D == 128 ? (ST == 4 ? 3 : 2) : (NW ==
   // scheduled from here on; where several CTAs share an SM, early-placed CTAs
   // of the next step crowd unevenly, so there the trigger stays implicit (exit).
   if (D == 64 && NW == 20) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // ---- merge: the warps through shared memory (the stage
+  // ---- merge: quad-sum l, then the warps through shared memory (the stage
   //      buffers are free once every warp is past its loop)
+  l_run += __shfl_xor_sync(0xffffffffu, l_run, 1);
+  l_run += __shfl_xor_sync(0xffffffffu, l_run, 2);
   __syncthreads();
   float *s_o = reinterpret_cast<float *>(smem);  // [NW][8][D]
   float *s_m = s_o + NW * 8 * D;                 // [NW][8]
   float *s_l = s_m + NW * 8;                     // [NW][8]
-  store_state<D>(run, lane, s_o + warp * 8 * D, s_m + warp * 8, s_l + warp * 8);
+  if (t == 0) {
+    s_m[warp * 8 + g] = m_run;
+    s_l[warp * 8 + g] = l_run;
+  }
+  const float down = e_acc == 127 ? 0.f : exp2i(-e_acc);
+#pragma unroll
+  for (int grp = 0; grp < NG; ++grp) {
+#pragma unroll
+    for (int tt = 0; tt < 2; ++tt) {
+      const int ch0 = 32 * grp + 4 * g + 2 * tt;  // row g; row g+8 is ch0 + 1
+      float *w0 = s_o + (warp * 8 + 2 * t) * D;
+      float *w1 = s_o + (warp * 8 + 2 * t + 1) * D;
+      w0[ch0] = o[grp][tt][0] * down;
+      w1[ch0] = o[grp][tt][1] * down;
+      w0[ch0 + 1] = o[grp][tt][2] * down;
+      w1[ch0 + 1] = o[grp][tt][3] * down;
+    }
+  }
   __syncthreads();
   for (int idx = threadIdx.x; idx < G * D; idx += NW * 32) {
     const int h = idx / D, ch = idx % D;

@@ -8,11 +8,14 @@
 //
 // HBM-bound: 2 (D + D/8) bytes per own slot and KV head.  A session's ring is
 // short (256 slots are 73 KB), so a CTA per pair would spend as long starting
-// and ending as reading.  Here a CTA walks several units one after the other,
+// and ending as reading.  Here a warp walks several units one after the other,
 // and its copies run on across the boundary: while a unit is merged and
-// written, the next one's steps are in flight.  The merge needs no memory of
-// its own: of a warp's ST stages ST - 1 are being filled, and the one just
-// read holds its state.
+// written, the next one's steps are in flight.  As many units as make whole
+// rounds of all warps are each one warp's own (sixteen steps per start and end
+// where the four warps of a CTA together would take four); the rest are
+// walked by a CTA's warps together, so the last round is as long as its share.
+// The merge needs no memory of its own: of a warp's ST stages ST - 1 are being
+// filled, and the one just read holds its state.
 //
 // A unit is a (sequence, KV head) pair, or a part of one where the pairs are
 // too few for the SMs; the parts' triples then go to the workspace and a merge
@@ -36,6 +39,7 @@ struct OwnParams {
   nd_kv_cache pre;     // the shared prefix (one row)
   int Hq, G, window;
   int n_split, slots_per_unit, n_units;  // units = pairs * n_split
+  int solo;            // units that every warp takes alone, before those of the whole CTA
   int inline_slots;    // prefix slots walked by every unit (a multiple of kStep), or 0
   uint16_t *out;
   float *lse;
@@ -45,6 +49,227 @@ struct OwnParams {
   int *err;
 };
 
+// ------------------------------------------------------------------ a warp's step
+// Thread (g, t) = (lane / 4, lane % 4).  QK: D[head][slot] = q (fp16, rows =
+// heads) x codes^T per 32-channel group, so that a group's fp32 scale
+// multiplies its own sum; PV: D[channel][head] = codes^T x P'^T with P' = p *
+// v_scale * 2^e; the scores' registers are the weights' (decode.cu has the
+// layout).  What this step does to need about half the instructions of a
+// straightforward one, which bound it (a step of the first form was 750
+// instructions a warp, twice its share of the bytes' time):
+//   - addresses of the swizzled chunks are one XOR from a per-step base;
+//   - the code's bias stays in K's operands (1024 + 128 + code is exact in
+//     fp16) and comes off the sum at once: the accumulator starts at -1152 *
+//     sum q of the group.  (fp32 holds 1152 * 32 |q| to 2^-8 |q| against sums
+//     of about 240 |q|.  V's sums run over all slots, where the same would
+//     cancel away bits, so V's bias comes off each pair of codes.)
+//   - the running maximum and V's exponent are compared without exchange
+//     between lanes; only a step that moves one (rare) reduces and rescales;
+//   - a step whose slots are all visible, the common one, masks nothing.
+template <int D>
+struct HeadQ {
+  uint32_t qa[D / 32][2][2];
+  float bias[D / 32];  // -1152 * the group's sum of q, for head g
+  float coef;          // 2^-Eq * log2(e) / sqrt(D), for head g
+};
+
+// w: thread t's channels 32*grp + 8t .. +7 of head g, bf16
+template <int D>
+__device__ __forceinline__ void make_q(const uint4 (&w)[D / 32], HeadQ<D> &hq) {
+  constexpr int NG = D / 32;
+  float qm = 0.f;
+#pragma unroll
+  for (int grp = 0; grp < NG; ++grp) {
+    const uint32_t ws[4] = {w[grp].x, w[grp].y, w[grp].z, w[grp].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) qm = fmaxf(qm, fmaxf(fabsf(bf16_lo(ws[i])), fabsf(bf16_hi(ws[i]))));
+  }
+  qm = fmaxf(qm, __shfl_xor_sync(0xffffffffu, qm, 1));
+  qm = fmaxf(qm, __shfl_xor_sync(0xffffffffu, qm, 2));
+  const int eq = qm > 0.f ? 14 - ilog2_floor(qm) : 0;
+  const float up = exp2i(eq);
+  hq.coef = exp2i(-eq) * (1.4426950408889634f * rsqrtf(float(D)));
+#pragma unroll
+  for (int grp = 0; grp < NG; ++grp) {
+    const uint32_t ws[4] = {w[grp].x, w[grp].y, w[grp].z, w[grp].w};
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      hq.qa[grp][i >> 1][i & 1] = pack_half2(bf16_lo(ws[i]) * up, bf16_hi(ws[i]) * up);
+      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&hq.qa[grp][i >> 1][i & 1]));
+      sum += f.x + f.y;  // of the rounded values: what the products see
+    }
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    hq.bias[grp] = -1152.f * sum;
+  }
+}
+
+template <int D>
+struct RunState {
+  float o[D / 32][2][4];  // heads 2t, 2t+1; channels 32*grp + 4g + 2*tile (+1)
+  float m, l;             // head g: the max p is taken against (log2 units); this thread's share of the sum
+  int e;                  // power-of-two pre-scale of P' (never increases; 127 = unset)
+  float u, lim;           // 2^e (1 while unset); the v_scale from which e has to shrink
+  __device__ __forceinline__ RunState() {
+#pragma unroll
+    for (int grp = 0; grp < D / 32; ++grp)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[grp][i >> 2][i & 3] = 0.f;
+    m = -INFINITY, l = 0.f, e = 127, u = 1.f, lim = exp2i(-120);
+  }
+};
+
+// fp16 pairs 1152 + code of bytes (0, 1) and (2, 3) of a word of codes
+__device__ __forceinline__ uint32_t biased_half2(uint32_t w_biased, uint32_t sel) {
+  return prmt(w_biased, 0x64646464u, sel);
+}
+
+// The group scales of two neighbouring slots.
+template <int NG>
+__device__ __forceinline__ void lds_scales2(uint32_t a, float (&s0)[NG], float (&s1)[NG]) {
+  const float4 x = lds128f(a);
+  if constexpr (NG == 4) {
+    const float4 y = lds128f(a + 16);
+    s0[0] = x.x, s0[1] = x.y, s0[2] = x.z, s0[3] = x.w;
+    s1[0] = y.x, s1[1] = y.y, s1[2] = y.z, s1[3] = y.w;
+  } else {
+    s0[0] = x.x, s0[1] = x.y, s1[0] = x.z, s1[1] = x.w;
+  }
+}
+
+// One step staged at st (a multiple of 128).  vis_bits: bit i = slot col[i] of
+// this thread counts, col = {2t, 2t+1, 8+2t, 9+2t}; all_vis (the same in the
+// whole warp): every slot does.
+template <int D>
+__device__ __forceinline__ void attend_step(uint32_t st, const HeadQ<D> &hq, bool all_vis, uint32_t vis_bits, int lane,
+                                            RunState<D> &r) {
+  constexpr int NG = D / 32;
+  using S = Stage<D>;
+  const int g = lane >> 2, t = lane & 3;
+  // row 8 lies 8 rows on; at D = 64 (two rows a line) its line's swizzle also
+  // differs in bit 6
+  constexpr uint32_t kRow8 = 8 * D, kFlip8 = D == 64 ? 64u : 0u;
+  const uint32_t kb = st + swz(uint32_t(g * D + 8 * t));
+  const uint32_t vb0 = st + S::kCodes + swz(uint32_t(2 * t * D + 4 * g)),
+                 vb1 = st + S::kCodes + swz(uint32_t((2 * t + 1) * D + 4 * g));
+  const uint32_t sb = st + 2 * S::kCodes + 2 * t * NG * 4;
+  // ---- QK: scores of head g at slots col[0..3]
+  float sc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    float ks0[NG], ks1[NG];
+    lds_scales2<NG>(sb + j * 8 * NG * 4, ks0, ks1);
+#pragma unroll
+    for (int grp = 0; grp < NG; ++grp) {
+      const uint2 kw = lds64((kb ^ (grp * 32 + j * kFlip8)) + j * kRow8);
+      float d0 = hq.bias[grp], d1 = d0, d2 = 0.f, d3 = 0.f;
+      const uint32_t w0 = kw.x ^ 0x80808080u, w1 = kw.y ^ 0x80808080u;
+      mma_f16_16816(d0, d1, d2, d3, hq.qa[grp][0][0], 0u, hq.qa[grp][0][1], 0u, biased_half2(w0, kSelBytes01),
+                    biased_half2(w0, kSelBytes23));
+      mma_f16_16816(d0, d1, d2, d3, hq.qa[grp][1][0], 0u, hq.qa[grp][1][1], 0u, biased_half2(w1, kSelBytes01),
+                    biased_half2(w1, kSelBytes23));
+      sc[2 * j] = fmaf(ks0[grp], d0, sc[2 * j]);
+      sc[2 * j + 1] = fmaf(ks1[grp], d1, sc[2 * j + 1]);
+    }
+  }
+  float vs[4][NG];
+  lds_scales2<NG>(sb + S::kScales, vs[0], vs[1]);
+  lds_scales2<NG>(sb + S::kScales + 8 * NG * 4, vs[2], vs[3]);
+  // ---- online softmax for head g (log2 domain)
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sc[i] *= hq.coef;
+  if (!all_vis) {  // masked slots count 0, whatever their scales are
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (!((vis_bits >> i) & 1u)) {
+        sc[i] = -INFINITY;
+#pragma unroll
+        for (int grp = 0; grp < NG; ++grp) vs[i][grp] = 0.f;
+      }
+  }
+  float mx = fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3])), vm = 0.f;
+#pragma unroll
+  for (int grp = 0; grp < NG; ++grp) vm = fmaxf(vm, fmaxf(fmaxf(vs[0][grp], vs[1][grp]), fmaxf(vs[2][grp], vs[3][grp])));
+  if (__any_sync(0xffffffffu, mx > r.m + kLazyLog2 || vm >= r.lim)) {
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 1));
+    vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 2));
+    const bool need = mx > r.m + kLazyLog2;
+    const float alpha = need ? ex2(r.m - mx) : 1.f;  // 0 from the empty state
+    r.l *= alpha;
+    r.m = need ? mx : r.m;
+    // p * v_scale * 2^e stays below 2^15 (p <= 2^8)
+    float shrink = 1.f;
+    if (vm >= r.lim) {
+      const int e = 14 - int(kLazyLog2) - ilog2_floor(vm);
+      shrink = r.e == 127 ? 0.f : exp2i(e - r.e);
+      r.e = e;
+      r.u = exp2i(e);
+      r.lim = exp2i(7 - e);
+    }
+    const float f_lo = __shfl_sync(0xffffffffu, alpha, (2 * t) * 4) * shrink;
+    const float f_hi = __shfl_sync(0xffffffffu, alpha, (2 * t + 1) * 4) * shrink;
+#pragma unroll
+    for (int grp = 0; grp < NG; ++grp)
+#pragma unroll
+      for (int tt = 0; tt < 2; ++tt) {
+        r.o[grp][tt][0] *= f_lo;
+        r.o[grp][tt][1] *= f_hi;
+        r.o[grp][tt][2] *= f_lo;
+        r.o[grp][tt][3] *= f_hi;
+      }
+  }
+  const float m_ref = r.m == -INFINITY ? 0.f : r.m;
+  float pu[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) pu[i] = ex2(sc[i] - m_ref);
+  r.l += (pu[0] + pu[1]) + (pu[2] + pu[3]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) pu[i] *= r.u;
+  // ---- PV per group: B = P'^T (slot x head), A = V^T (channel x slot)
+#pragma unroll
+  for (int grp = 0; grp < NG; ++grp) {
+    const uint32_t b0 = pack_half2(pu[0] * vs[0][grp], pu[1] * vs[1][grp]);
+    const uint32_t b1 = pack_half2(pu[2] * vs[2][grp], pu[3] * vs[3][grp]);
+    uint32_t vw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      vw[i] = lds32((((i & 1) ? vb1 : vb0) ^ (grp * 32 + (i >> 1) * kFlip8)) + (i >> 1) * kRow8);
+    const uint32_t x01 = prmt(vw[0], vw[1], 0x5140u) ^ 0x80808080u, x23 = prmt(vw[0], vw[1], 0x7362u) ^ 0x80808080u;
+    const uint32_t y01 = prmt(vw[2], vw[3], 0x5140u) ^ 0x80808080u, y23 = prmt(vw[2], vw[3], 0x7362u) ^ 0x80808080u;
+    // tile 0: rows g <-> channel 4g, rows g+8 <-> channel 4g+1; tile 1: 4g+2, 4g+3
+    mma_f16_16816(r.o[grp][0][0], r.o[grp][0][1], r.o[grp][0][2], r.o[grp][0][3], codes_to_half2(x01, kSelBytes01),
+                  codes_to_half2(x01, kSelBytes23), codes_to_half2(y01, kSelBytes01),
+                  codes_to_half2(y01, kSelBytes23), b0, b1);
+    mma_f16_16816(r.o[grp][1][0], r.o[grp][1][1], r.o[grp][1][2], r.o[grp][1][3], codes_to_half2(x23, kSelBytes01),
+                  codes_to_half2(x23, kSelBytes23), codes_to_half2(y23, kSelBytes01),
+                  codes_to_half2(y23, kSelBytes23), b0, b1);
+  }
+}
+
+// The warp's (max, sum, O) of its up to eight heads: o [8][D], m [8], l [8].
+template <int D>
+__device__ __forceinline__ void store_state(RunState<D> &r, int lane, float *o, float *m, float *l) {
+  const int g = lane >> 2, t = lane & 3;
+  r.l += __shfl_xor_sync(0xffffffffu, r.l, 1);
+  r.l += __shfl_xor_sync(0xffffffffu, r.l, 2);
+  if (t == 0) {
+    m[g] = r.m;
+    l[g] = r.l;
+  }
+  const float down = r.e == 127 ? 0.f : exp2i(-r.e);
+  float *w0 = o + (2 * t) * D + 4 * g, *w1 = w0 + D;
+#pragma unroll
+  for (int grp = 0; grp < D / 32; ++grp) {
+    const auto &a = r.o[grp];  // channels 4g .. 4g+3: tile 0 rows g, g+8, tile 1 rows g, g+8
+    *reinterpret_cast<float4 *>(w0 + 32 * grp) = make_float4(a[0][0] * down, a[0][2] * down, a[1][0] * down, a[1][2] * down);
+    *reinterpret_cast<float4 *>(w1 + 32 * grp) = make_float4(a[0][1] * down, a[0][3] * down, a[1][1] * down, a[1][3] * down);
+  }
+}
+
+// ------------------------------------------------------------------ merging
 // The prefix's partials of one row of a KV head: n of them, in adjacent slots.
 struct RowParts {
   const float2 *ml;
@@ -154,54 +379,82 @@ __global__ void __launch_bounds__(NW * 32, kCtas) shared_own_kernel(const __grid
 
   pdl_wait();
 
-  // ---- copies: a cursor (unit, step) that runs ST - 1 steps ahead
-  struct {
-    int unit, step, n, first;  // first: the unit's first virtual slot of this warp
-    size_t own, pre;           // row of the pair's (head's) slot 0
-  } at;
-  auto steps_of = [&](int unit, int &first) {
-    const int v0 = (unit % p.n_split) * p.slots_per_unit, v1 = min(v0 + p.slots_per_unit, v_all);
-    first = v0 + warp * kStep;
-    return v1 > first ? (v1 - first + NW * kStep - 1) / (NW * kStep) : 0;
+  // ---- copies: a cursor that runs ST - 1 steps ahead of the reads
+  // The warp's units in order: solo of its own, then units that the CTA's
+  // warps walk together (every fourth step each).
+  struct Unit {
+    int id, first, n, stride;  // the warp's first virtual slot, steps, slots from one step to its next
+    bool solo;
   };
-  auto enter = [&](int unit) {
-    at.unit = unit;
-    at.step = 0;
-    while (at.unit < p.n_units && (at.n = steps_of(at.unit, at.first)) == 0) at.unit += gridDim.x;
-    if (at.unit < p.n_units) {
-      const int pair = at.unit / p.n_split;
-      at.own = size_t(pair) * nslot;
-      at.pre = size_t(pair % Hkv) * pslot;
+  auto unit_at = [&](int i) {
+    Unit u;
+    u.solo = i < p.solo;
+    u.id = u.solo ? (i * gridDim.x + blockIdx.x) * NW + warp
+                  : (p.solo * NW + i - p.solo) * gridDim.x + blockIdx.x;
+    const int v0 = p.n_split > 1 ? (u.id % p.n_split) * p.slots_per_unit : 0, v1 = min(v0 + p.slots_per_unit, v_all);
+    u.first = u.solo ? v0 : v0 + warp * kStep;
+    u.stride = u.solo ? kStep : NW * kStep;
+    u.n = u.id < p.n_units && v1 > u.first ? (v1 - u.first + u.stride - 1) / u.stride : 0;
+    return u;
+  };
+  // a lane copies 16-byte chunk my_ch of rows my_row0, my_row0 + kRowStride, ..
+  // of K and V, and the scales of one row of K (lanes 0-15) or V
+  constexpr int kPerLane = kStep * D / 16 / 32, kRowStride = 32 * 16 / D;
+  const int my_row0 = lane / (D / 16), my_ch = lane % (D / 16), sc_row = lane & 15;
+  struct Source {  // this lane's first bytes at a pair's (or the prefix's head's) slot 0
+    const int8_t *k, *v;
+    const float *s;
+  };
+  auto source = [&](const nd_kv_cache &from, size_t row) {
+    const size_t at = row * D + my_ch * 16;
+    return Source{from.k_codes + at, from.v_codes + at, (lane < 16 ? from.k_scale : from.v_scale) + row * NG};
+  };
+  Source own_src, pre_src;
+  Unit at;       // the cursor's unit: its next slot, the steps left
+  int at_i = 0;  // its place in the order
+  auto enter = [&]() {
+    // (a warp whose share of a unit is empty goes on to the next one)
+    do at = unit_at(at_i++);
+    while (at.n == 0 && at.id < p.n_units);
+    if (at.n > 0) {
+      const int pair = p.n_split > 1 ? at.id / p.n_split : at.id;
+      own_src = source(c, size_t(pair) * nslot);
+      if (kInline) pre_src = source(p.pre, size_t(pair % Hkv) * pslot);
+      // its query, a unit's time before it is used
+      const int b = pair / Hkv, hkv = pair - b * Hkv;
+      if (lane * 64 < G * D)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q + (size_t(b) * p.Hq + hkv * G) * D + lane * 64));
     }
   };
-  enter(blockIdx.x);
+  enter();
   int in = 0, out = 0;  // stage filled next, stage read next
-  constexpr int kPerLane = kStep * D / 16 / 32, kRowStride = 32 * 16 / D;
-  const int my_row0 = lane / (D / 16), my_ch = lane % (D / 16);
+  const uint32_t off0 = swz(uint32_t(my_row0 * D + my_ch * 16));
+  const uint32_t off_s = 2 * S::kCodes + (lane < 16 ? 0 : S::kScales) + sc_row * NG * 4;
   auto issue = [&]() {
-    if (at.unit < p.n_units) {
-      const int v = at.first + at.step * NW * kStep;
-      const bool pre = kInline && v < v_inline;
-      const nd_kv_cache &src = pre ? p.pre : c;
-      // slots past the region's end read its last one (and are masked)
-      const int base = pre ? v : v - v_inline, last = (pre ? p.pre.sink_cap : nslot) - 1;
-      const size_t row = pre ? at.pre : at.own;
+    if (at.n > 0) {
+      const bool pre = kInline && at.first < v_inline;
+      const Source src = pre ? pre_src : own_src;
+      const int base = pre ? at.first : at.first - v_inline, slots = pre ? p.pre.sink_cap : nslot;
       const uint32_t st = my_stages + in * S::kBytes;
+      const int8_t *k = src.k + size_t(base) * D, *v = src.v + size_t(base) * D;
+      const float *sc = src.s + size_t(base) * NG;
+      const bool whole = base + kStep <= slots;
 #pragma unroll
-      for (int k = 0; k < kPerLane; ++k) {
-        const int r = my_row0 + k * kRowStride;
-        const uint32_t off = swz(uint32_t(r * D + my_ch * 16));
-        const size_t goff = (row + min(base + r, last)) * D + my_ch * 16;
-        cp_async16(st + off, src.k_codes + goff);
-        cp_async16(st + S::kCodes + off, src.v_codes + goff);
+      for (int i = 0; i < kPerLane; ++i) {
+        // (rows kRowStride apart are 512 bytes apart; the swizzle of every
+        // second one differs in bit 6)
+        const uint32_t dst = st + (off0 ^ ((i & 1) * 64)) + i * 512;
+        int r = my_row0 + i * kRowStride;
+        if (!whole) r = min(r, slots - 1 - base);  // past the end: the last slot, masked
+        cp_async16(dst, k + r * D);
+        cp_async16(dst + S::kCodes, v + r * D);
       }
-      const int r = lane & 15, which = lane >> 4;
-      const uint32_t dst = st + 2 * S::kCodes + which * S::kScales + r * NG * 4;
-      const float *sc = (which ? src.v_scale : src.k_scale) + (row + min(base + r, last)) * NG;
-      if constexpr (NG == 4) cp_async16(dst, sc);
-      else cp_async8(dst, sc);
+      const int r = whole ? sc_row : min(sc_row, slots - 1 - base);
+      if constexpr (NG == 4) cp_async16(st + off_s, sc + r * NG);
+      else cp_async8(st + off_s, sc + r * NG);
       if (++in == ST) in = 0;
-      if (++at.step == at.n) enter(at.unit + gridDim.x);
+      at.first += at.stride;
+      if (--at.n == 0) enter();
     }
     cp_async_commit();
   };
@@ -217,10 +470,10 @@ __global__ void __launch_bounds__(NW * 32, kCtas) shared_own_kernel(const __grid
   if (!kInline && p.prefix_grid > 0)
     pl = prefix_plan(p.pre.sink_len[0], p.pre.sink_cap, Hkv, c.batch * G, p.prefix_grid);
 
-  for (int unit = blockIdx.x; unit < p.n_units; unit += gridDim.x) {
-    const int pair = unit / p.n_split, b = pair / Hkv, hkv = pair % Hkv;
-    int first;
-    const int n = steps_of(unit, first);
+  for (int i = 0;; ++i) {
+    const Unit un = unit_at(i);
+    if (un.id >= p.n_units) break;  // (team units: the same for the CTA's warps)
+    const int pair = p.n_split > 1 ? un.id / p.n_split : un.id, b = pair / Hkv, hkv = pair - b * Hkv;
     // ---- the unit's query and metadata
     HeadQ<D> hq;
     {
@@ -242,38 +495,55 @@ __global__ void __launch_bounds__(NW * 32, kCtas) shared_own_kernel(const __grid
     const int rs_eff = c.ring_cap ? (rs + rl - n_vis) % c.ring_cap : 0;  // oldest visible entry
 
     RunState<D> run;
-    for (int s = 0; s < n; ++s) {
+    int v = un.first;
+    for (int s = 0; s < un.n; ++s, v += un.stride) {
       issue();
       cp_async_wait<ST - 1>();
       __syncwarp();
-      const int v = first + s * NW * kStep;
       const bool pre = kInline && v < v_inline;
       const int base = pre ? v : v - v_inline;
       const bool all_vis = pre ? base + kStep <= pre_vis
                                : base + kStep <= nslot &&
                                      (base + kStep <= sl || (base >= c.sink_cap && n_vis == c.ring_cap));
-      bool vis[4];
+      uint32_t vis = 0xfu;
+      if (!all_vis) {
+        vis = 0u;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int ps = base + 2 * t + (i & 1) + 8 * (i >> 1);
-        if (all_vis) vis[i] = true;
-        else if (pre) vis[i] = ps < pre_vis;
-        else if (ps < c.sink_cap) vis[i] = ps < sl;
-        else {
-          int age = ps - c.sink_cap - rs_eff;
-          if (age < 0) age += c.ring_cap;
-          vis[i] = ps < nslot && age < n_vis;
+        for (int i = 0; i < 4; ++i) {
+          const int ps = base + 2 * t + (i & 1) + 8 * (i >> 1);
+          bool on;
+          if (pre) on = ps < pre_vis;
+          else if (ps < c.sink_cap) on = ps < sl;
+          else {
+            int age = ps - c.sink_cap - rs_eff;
+            if (age < 0) age += c.ring_cap;
+            on = ps < nslot && age < n_vis;
+          }
+          vis |= uint32_t(on) << i;
         }
       }
-      attend_step<D>(my_stages + out * S::kBytes, hq, vis, g < G, lane, run);
+      attend_step<D>(my_stages + out * S::kBytes, hq, all_vis, vis, lane, run);
       __syncwarp();  // every lane is done with this stage before it is refilled
       if (++out == ST) out = 0;
     }
 
     // ---- merge.  The stage that the next copy will fill is free until then.
     float *state = reinterpret_cast<float *>(smem + (warp * ST + in) * S::kBytes);  // [8][D], max [8], sum [8]
-    if (lane == 0) s_state[warp] = state;
     store_state<D>(run, lane, state, state + 8 * D, state + 8 * D + 8);
+    if (un.solo) {
+      __syncwarp();
+      for (int h = 0; h < G; ++h) {
+        LaneState<C> st;
+        st.m = state[8 * D + h];
+        st.l = state[8 * D + 8 + h];
+        load_c<C>(state + h * D + C * lane, st.o);
+        if (pl.nt > 0) add_parts<D>(row_parts<D>(p, pl, hkv, b * G + h), 0, 1, lane, st);
+        write_out<C>(p, size_t(b) * p.Hq + hkv * G + h, lane, st);
+      }
+      __syncwarp();
+      continue;
+    }
+    if (lane == 0) s_state[warp] = state;
     __syncthreads();
     for (int h = warp; h < G; h += NW) {
       LaneState<C> st;
@@ -285,7 +555,7 @@ __global__ void __launch_bounds__(NW * 32, kCtas) shared_own_kernel(const __grid
         st.add(sw[8 * D + h], sw[8 * D + 8 + h], x);
       }
       if (p.n_split > 1) {
-        const size_t part = size_t(unit) * G + h;
+        const size_t part = size_t(un.id) * G + h;
         store_c<C>(p.ws_o + part * D + C * lane, st.o);
         if (lane == 0) {
           p.ws_ml[2 * part] = st.m;
@@ -346,7 +616,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __
 }
 
 template <int D, int NW, int ST, int kCtas, bool kInline>
-cudaError_t launch_own(const OwnParams &p, cudaStream_t stream) {
+cudaError_t launch_own(OwnParams &p, cudaStream_t stream) {
   constexpr size_t smem = size_t(NW) * ST * Stage<D>::kBytes;
   auto kern = shared_own_kernel<D, NW, ST, kCtas, kInline>;
   static std::atomic<unsigned long long> smem_set{0};  // the opt-in, once per device
@@ -359,8 +629,12 @@ cudaError_t launch_own(const OwnParams &p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     smem_set.fetch_or(bit, std::memory_order_release);
   }
-  const int most = kPrefixCtas * kCtas;
-  return launch_pdl(kern, dim3(unsigned(p.n_units < most ? p.n_units : most)), dim3(NW * 32), smem, stream, p);
+  const int most = kPrefixCtas * kCtas, grid = p.n_units < most ? p.n_units : most;
+  // whole rounds of the warps take a unit each, the rest is shared: no warp
+  // waits for others while there are units for all (n_split > 1: fewer units
+  // than warps)
+  p.solo = p.n_units / (grid * NW);
+  return launch_pdl(kern, dim3(unsigned(grid)), dim3(NW * 32), smem, stream, p);
 }
 
 // How a call is carried out; the workspace query and the launch agree on it.

@@ -153,7 +153,7 @@ def _stream(stream) -> int:
     # the current stream's handle alone: building the Stream object around it
     # takes longer than a small launch (2.8 us against 0.3 us on the GB300's CPU)
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream
 
 
@@ -211,8 +211,14 @@ class KVCache:
                self.ring_start.data_ptr(), self.ring_len.data_ptr(), self.seq_len.data_ptr())
         if self.__dict__.get("_key") != key:
             self._struct = _Cache(self.batch, self.n_kv_heads, self.head_dim, *key[1:])
+            self._ref = ctypes.byref(self._struct)
             self._key = key
         return self._struct
+
+    def struct_ref(self):
+        """A reference to struct() for ctypes."""
+        self.struct()
+        return self._ref
 
 
 @dataclass
@@ -417,48 +423,47 @@ def nd_swa_sink_decode_noalloc(q: torch.Tensor, cache: KVCache, window: int, out
     return out
 
 
-def _want(cond: bool, what: str) -> None:
-    if not cond:
-        raise ValueError(what)
+# The entry points below sit on a per-token path whose kernels take a few
+# microseconds, about what a handful of attribute look-ups costs on the
+# GB300's CPU: each tensor is looked at once, and addresses go to ctypes as
+# plain integers.
+
+def _here(t: torch.Tensor) -> int:
+    """The index of t's device, which must be the current CUDA device (the
+    library launches there)."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors are on {t.device}; libnd launches on the current CUDA device")
+    return dev
 
 
-def _like(t: Optional[torch.Tensor], name: str, shape, dtype, device, none_ok: bool = False) -> Optional[int]:
-    """The address of a contiguous device tensor of this shape, type and device."""
-    if t is None and none_ok:
-        return None
-    if t is None or t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+def _addr(t: torch.Tensor, name: str, shape, dtype, dev: int) -> int:
+    """The address of a contiguous tensor of this shape, type and device."""
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev}")
     return t.data_ptr()
 
 
-def _rows(t: torch.Tensor, name: str) -> int:
-    """The stride (elements) from one token to the next of [..., heads, d] rows
-    that may lie inside wider ones (a slice of a fused projection)."""
-    *lead, H, d = t.shape
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a CUDA device")
-    if t.numel() == 0:
-        return H * d
-    st = t.stride()
-    ok = st[-1] == 1 and (st[-2] == d or H == 1)
-    step = st[-3]
-    if len(lead) == 2:  # [B, T]: one stride for the tokens of all rows
-        if lead[1] == 1:
-            step = st[-4]
-        elif lead[0] > 1:
-            ok = ok and st[-4] == lead[1] * step
-    elif lead[0] == 1:
-        step = H * d
-    if lead[0] * lead[-1] == 1:
-        step = H * d
+def _step(t: torch.Tensor, name: str) -> int:
+    """The stride (elements) from one token to the next of [B, H, d] or
+    [B, T, H, d] rows that may lie inside wider ones (a slice of a fused
+    projection)."""
+    if t.is_contiguous():
+        return t.shape[-2] * t.shape[-1]
+    shape, st = t.shape, t.stride()
+    H, d = shape[-2:]
+    step, ok = st[0], st[-1] == 1 and (st[-2] == d or H == 1)
+    if len(shape) == 4:  # one stride for the tokens of all rows
+        B, T = shape[:2]
+        if T > 1:
+            ok = ok and (B == 1 or step == T * st[1])
+            step = st[1]
+        B *= T
+    else:
+        B = shape[0]
     if not ok:
         raise ValueError(f"{name}: heads and channels must be contiguous, and the tokens evenly spaced")
-    return step
-
-
-def _on_current(device) -> None:
-    if device.type != "cuda" or device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {device}; libnd launches on the current CUDA device")
+    return step if B > 1 else H * d
 
 
 def nd_kv_cache_read(cache: KVCache, window: int, dtype: torch.dtype = torch.bfloat16,
@@ -469,30 +474,29 @@ def nd_kv_cache_read(cache: KVCache, window: int, dtype: torch.dtype = torch.bfl
     sink_cap + min(ring_cap, window) unless k_out has more.  Rows from
     lengths[b] on keep what k_out / v_out held (nothing in particular when they
     are made here); their positions are -1."""
-    dev = cache.k_codes.device
-    _on_current(dev)
-    B, Hkv, d = cache.batch, cache.n_kv_heads, cache.head_dim
-    if k_out is not None:
-        dtype = k_out.dtype
-        _want(k_out.dim() == 4, "k_out must have shape [B, rows, Hkv, d]")
-    rows = k_out.shape[1] if k_out is not None else cache.sink_cap + min(cache.ring_cap, int(window))
-    code = {torch.float32: ND_F32, torch.bfloat16: ND_BF16}.get(dtype)
-    _want(code is not None, f"unsupported dtype {dtype}")
-    shape = (B, rows, Hkv, d)
+    dev = _here(cache.k_codes)
+    B, Hkv, _, d = cache.k_codes.shape
     if k_out is None:
-        _want(rows >= 0, "window must be at least 1")
-        k_out = torch.empty(shape, dtype=dtype, device=dev)
+        rows = cache.sink_cap + min(cache.ring_cap, window)
+        if window < 1:
+            raise ValueError("window must be at least 1")
+        k_out = torch.empty((B, rows, Hkv, d), dtype=dtype, device=cache.k_codes.device)
+    elif k_out.dim() != 4:
+        raise ValueError("k_out must have shape [B, rows, Hkv, d]")
+    rows = k_out.shape[1]
+    dtype = k_out.dtype
+    code = ND_BF16 if dtype == torch.bfloat16 else _dtype_code(k_out)
+    shape = (B, rows, Hkv, d)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=dtype, device=dev)
+        v_out = torch.empty(shape, dtype=dtype, device=k_out.device)
     if positions is None:
-        positions = torch.empty((B, rows), dtype=torch.int32, device=dev)
+        positions = torch.empty((B, rows), dtype=torch.int32, device=k_out.device)
     if lengths is None:
-        lengths = torch.empty(B, dtype=torch.int32, device=dev)
-    s = cache.struct()
+        lengths = torch.empty((B,), dtype=torch.int32, device=k_out.device)
     _check("nd_kv_cache_read", _lib().nd_kv_cache_read(
-        ctypes.byref(s), int(window), code, rows, _like(k_out, "k_out", shape, dtype, dev),
-        _like(v_out, "v_out", shape, dtype, dev), _like(positions, "positions", (B, rows), torch.int32, dev),
-        _like(lengths, "lengths", (B,), torch.int32, dev), _stream(stream)))
+        cache.struct_ref(), window, code, rows, _addr(k_out, "k_out", shape, dtype, dev),
+        _addr(v_out, "v_out", shape, dtype, dev), _addr(positions, "positions", (B, rows), torch.int32, dev),
+        _addr(lengths, "lengths", (B,), torch.int32, dev), _stream(stream)))
     return k_out, v_out, positions, lengths
 
 
@@ -507,24 +511,30 @@ def nd_shared_prefix_decode(q: torch.Tensor, prefix: KVCache, cache: KVCache, wi
                             workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """nd_swa_sink_decode for sequences that share the sink region of `prefix`
     (a cache of one row) in front of their own cache; returns out."""
-    dev = q.device
-    _on_current(dev)
-    _want(q.dim() == 3, "q must have shape [B, Hq, d]")
-    B, Hq, d = q.shape
-    _want((B, d) == (cache.batch, cache.head_dim), "q and the cache disagree on batch or head_dim")
-    _want(prefix.k_codes.device == dev and cache.k_codes.device == dev, f"the caches must be on {dev}")
+    dev = _here(q)
+    shape = q.shape
+    B, Hq, d = shape
+    k = cache.k_codes
+    if k.shape[0] != B or k.shape[3] != d or k.get_device() != dev or prefix.k_codes.get_device() != dev:
+        raise ValueError("q and the caches must agree on batch, head_dim and device")
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        out = torch.empty_like(q)
     if workspace is None:
-        nbytes = nd_shared_prefix_decode_workspace_size(B, Hq, cache.n_kv_heads, d, prefix.sink_cap,
+        nbytes = nd_shared_prefix_decode_workspace_size(B, Hq, k.shape[1], d, prefix.sink_cap,
                                                         cache.sink_cap + cache.ring_cap)
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
-    ps, cs = prefix.struct(), cache.struct()
+        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
     _check("nd_shared_prefix_decode", _lib().nd_shared_prefix_decode(
-        _like(q, "q", q.shape, torch.bfloat16, dev), ctypes.byref(ps), ctypes.byref(cs), Hq, int(window),
-        _like(out, "out", q.shape, torch.bfloat16, dev), _like(lse, "lse", (B, Hq), torch.float32, dev, True),
-        _ptr(workspace), workspace.nbytes, _stream(stream)))
+        _addr(q, "q", shape, torch.bfloat16, dev), prefix.struct_ref(), cache.struct_ref(), Hq, window,
+        _addr(out, "out", shape, torch.bfloat16, dev),
+        None if lse is None else _addr(lse, "lse", (B, Hq), torch.float32, dev),
+        workspace.data_ptr(), workspace.nbytes, _stream(stream)))
     return out
+
+
+def _weight(w: Optional[torch.Tensor], name: str, d: int, dev: int) -> Optional[int]:
+    return None if w is None else _addr(w, name, (d,), torch.float32, dev)
 
 
 def nd_qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], q_weight: Optional[torch.Tensor] = None,
@@ -536,25 +546,30 @@ def nd_qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], q_weig
     None) with weights fp32 [d], then the rotation at positions int32 [B, T]
     (None: t).  Returns (q_out, k_out), contiguous."""
     one = q if q is not None else k
-    _want(one is not None, "q or k must be given")
-    dev = one.device
-    _on_current(dev)
-    args = []
-    for t, o, name in ((q, q_out, "q"), (k, k_out, "k")):
-        if t is None:
-            args.append((0, 0, None, None, None))
-            continue
-        _want(t.dim() == 4 and t.shape[:2] == one.shape[:2] and t.shape[3] == one.shape[3] and t.dtype == one.dtype
-              and t.device == dev, f"{name} must have shape [B, T, heads, d], q's type and device")
-        if o is None:
-            o = torch.empty(t.shape, dtype=t.dtype, device=dev)
-        args.append((t.shape[2], _rows(t, name), t.data_ptr(), _like(o, name + "_out", t.shape, t.dtype, dev), o))
+    if one is None:
+        raise ValueError("q or k must be given")
+    dev = _here(one)
     B, T, _, d = one.shape
-    (Hq, sq, pq, oq, q_out), (Hk, sk, pk, ok, k_out) = args
+    dtype = one.dtype
+
+    def side(t, out, name):
+        if t is None:
+            return 0, 0, None, None, None
+        shape = t.shape
+        if len(shape) != 4 or shape[0] != B or shape[1] != T or shape[3] != d or t.dtype != dtype or \
+                t.get_device() != dev:
+            raise ValueError(f"{name} must have shape [{B}, {T}, heads, {d}], q's type and device")
+        if out is None:
+            out = torch.empty(shape, dtype=dtype, device=t.device)
+        return shape[2], _step(t, name), t.data_ptr(), _addr(out, name + "_out", shape, dtype, dev), out
+
+    Hq, sq, pq, oq, q_out = side(q, q_out, "q")
+    Hk, sk, pk, ok, k_out = side(k, k_out, "k")
     _check("nd_qk_norm_rope", _lib().nd_qk_norm_rope(
-        pq, pk, _dtype_code(one), B, T, Hq, Hk, d, sq, sk, _like(q_weight, "q_weight", (d,), torch.float32, dev, True),
-        _like(k_weight, "k_weight", (d,), torch.float32, dev, True), float(eps), float(rope_theta),
-        _like(positions, "positions", (B, T), torch.int32, dev, True), oq, ok, _stream(stream)))
+        pq, pk, _dtype_code(one), B, T, Hq, Hk, d, sq, sk, _weight(q_weight, "q_weight", d, dev),
+        _weight(k_weight, "k_weight", d, dev), eps, rope_theta,
+        None if positions is None else _addr(positions, "positions", (B, T), torch.int32, dev), oq, ok,
+        _stream(stream)))
     return q_out, k_out
 
 
@@ -566,28 +581,27 @@ def nd_qk_norm_rope_append(q: torch.Tensor, cache: KVCache, k_new: torch.Tensor,
     slices of a fused projection are taken as they are) are normalised per head
     and rotated at seq_len + pos_base (int32 tensor of one element, or None);
     k_new and v_new are quantised into the cache.  Returns q_out."""
-    dev = q.device
-    _on_current(dev)
-    B, Hkv, d = cache.batch, cache.n_kv_heads, cache.head_dim
-    _want(q.dim() == 3 and q.shape[0] == B and q.shape[2] == d and q.dtype == torch.bfloat16 and
-          cache.k_codes.device == dev, "q must be bf16 [B, Hq, d] on the cache's device")
-    strides = [_rows(q, "q")]
-    for t, name in ((k_new, "k_new"), (v_new, "v_new")):
-        _want(t.shape == (B, Hkv, d) and t.dtype == torch.bfloat16 and t.device == dev,
-              f"{name} must be bf16 [B, Hkv, d] on the cache's device")
-        strides.append(_rows(t, name))
+    dev = _here(q)
+    B, Hkv, _, d = cache.k_codes.shape
+    shape, bf16 = q.shape, torch.bfloat16
+    kv = (B, Hkv, d)
+    if len(shape) != 3 or shape[0] != B or shape[2] != d or k_new.shape != kv or v_new.shape != kv or \
+            q.dtype != bf16 or k_new.dtype != bf16 or v_new.dtype != bf16 or k_new.get_device() != dev or \
+            v_new.get_device() != dev or cache.k_codes.get_device() != dev:
+        raise ValueError(f"q, k_new and v_new must be bf16 [{B}, heads, {d}] (k_new, v_new: {Hkv} heads) on the "
+                         "cache's device")
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        q_out = torch.empty(shape, dtype=bf16, device=q.device)
+    base = None
     if pos_base is not None:
-        _want(pos_base.numel() == 1 and pos_base.dtype == torch.int32 and pos_base.device == dev,
-              "pos_base must be one int32 on the cache's device")
-    s = cache.struct()
+        if pos_base.numel() != 1 or pos_base.dtype != torch.int32 or pos_base.get_device() != dev:
+            raise ValueError("pos_base must be one int32 on the cache's device")
+        base = pos_base.data_ptr()
     _check("nd_qk_norm_rope_append", _lib().nd_qk_norm_rope_append(
-        q.data_ptr(), ctypes.byref(s), k_new.data_ptr(), v_new.data_ptr(), q.shape[1], *strides,
-        _like(q_weight, "q_weight", (d,), torch.float32, dev, True),
-        _like(k_weight, "k_weight", (d,), torch.float32, dev, True), float(eps), float(rope_theta),
-        None if pos_base is None else pos_base.data_ptr(), 1 if to_sink else 0,
-        _like(q_out, "q_out", q.shape, torch.bfloat16, dev), _stream(stream)))
+        q.data_ptr(), cache.struct_ref(), k_new.data_ptr(), v_new.data_ptr(), shape[1], _step(q, "q"),
+        _step(k_new, "k_new"), _step(v_new, "v_new"), _weight(q_weight, "q_weight", d, dev),
+        _weight(k_weight, "k_weight", d, dev), eps, rope_theta, base, 1 if to_sink else 0,
+        _addr(q_out, "q_out", shape, bf16, dev), _stream(stream)))
     return q_out
 
 
