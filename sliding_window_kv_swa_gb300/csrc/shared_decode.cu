@@ -59,8 +59,7 @@ struct OwnParams {
 // instructions a warp, twice its share of the bytes' time):
 //   - addresses of the swizzled chunks are one XOR from a per-step base;
 //   - the code's bias stays in K's operands (1024 + 128 + code is exact in
-//     fp16) and comes off the sum at once: the accumulator starts at -1152 *
-//     sum q of the group.  (fp32 holds 1152 * 32 |q| to 2^-8 |q| against sums
+//     fp16) and comes off the group's sum at once, as 1152 * sum q.  (fp32 holds 1152 * 32 |q| to 2^-8 |q| against sums
 //     of about 240 |q|.  V's sums run over all slots, where the same would
 //     cancel away bits, so V's bias comes off each pair of codes.)
 //   - the running maximum and V's exponent are compared without exchange
@@ -155,7 +154,7 @@ __device__ __forceinline__ void attend_step(uint32_t st, const HeadQ<D> &hq, boo
                  vb1 = st + S::kCodes + swz(uint32_t((2 * t + 1) * D + 4 * g));
   const uint32_t sb = st + 2 * S::kCodes + 2 * t * NG * 4;
   // ---- QK: scores of head g at slots col[0..3]
-  float sc[4] = {0.f, 0.f, 0.f, 0.f};
+  float sc[4];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     float ks0[NG], ks1[NG];
@@ -163,14 +162,16 @@ __device__ __forceinline__ void attend_step(uint32_t st, const HeadQ<D> &hq, boo
 #pragma unroll
     for (int grp = 0; grp < NG; ++grp) {
       const uint2 kw = lds64((kb ^ (grp * 32 + j * kFlip8)) + j * kRow8);
-      float d0 = hq.bias[grp], d1 = d0, d2 = 0.f, d3 = 0.f;
+      float d0 = 0.f, d1 = 0.f, d2 = 0.f, d3 = 0.f;
       const uint32_t w0 = kw.x ^ 0x80808080u, w1 = kw.y ^ 0x80808080u;
       mma_f16_16816(d0, d1, d2, d3, hq.qa[grp][0][0], 0u, hq.qa[grp][0][1], 0u, biased_half2(w0, kSelBytes01),
                     biased_half2(w0, kSelBytes23));
       mma_f16_16816(d0, d1, d2, d3, hq.qa[grp][1][0], 0u, hq.qa[grp][1][1], 0u, biased_half2(w1, kSelBytes01),
                     biased_half2(w1, kSelBytes23));
-      sc[2 * j] = fmaf(ks0[grp], d0, sc[2 * j]);
-      sc[2 * j + 1] = fmaf(ks1[grp], d1, sc[2 * j + 1]);
+      d0 += hq.bias[grp];
+      d1 += hq.bias[grp];
+      sc[2 * j] = grp ? fmaf(ks0[grp], d0, sc[2 * j]) : ks0[grp] * d0;
+      sc[2 * j + 1] = grp ? fmaf(ks1[grp], d1, sc[2 * j + 1]) : ks1[grp] * d1;
     }
   }
   float vs[4][NG];
@@ -282,31 +283,13 @@ template <int D>
 __device__ __forceinline__ RowParts row_parts(const OwnParams &p, const PrefixPlan &pl, int hkv, int row) {
   RowParts r;
   const int rr = row % (2 * kPrefixBlock), item = hkv * pl.pairs + row / (2 * kPrefixBlock);
-  const int c0 = pl.owner((long long)item * pl.nt), c1 = pl.owner((long long)(item + 1) * pl.nt - 1);
+  const int c0 = pl.first_cta(item), c1 = pl.last_cta(item);
   const size_t at = (size_t(c0) + item) * 2 + rr / kPrefixBlock;
   r.ml = p.parts.ml + at * kPrefixBlock + rr % kPrefixBlock;
   r.o = p.parts.o + (at * (D / 4) * kPrefixBlock + rr % kPrefixBlock) * 4;
   r.n = c1 - c0 + 1;
   return r;
 }
-
-// A softmax state of one row, C channels per lane.
-template <int C>
-struct LaneState {
-  float m = -INFINITY, l = 0.f, o[C];
-  __device__ __forceinline__ LaneState() {
-#pragma unroll
-    for (int i = 0; i < C; ++i) o[i] = 0.f;
-  }
-  __device__ __forceinline__ void add(float m2, float l2, const float *o2) {
-    const float mn = fmaxf(m, m2), base = mn == -INFINITY ? 0.f : mn;
-    const float f1 = ex2(m - base), f2 = ex2(m2 - base);
-    l = l * f1 + l2 * f2;
-#pragma unroll
-    for (int i = 0; i < C; ++i) o[i] = o[i] * f1 + o2[i] * f2;
-    m = mn;
-  }
-};
 
 template <int C>
 __device__ __forceinline__ void load_c(const float *p, float *x) {
@@ -324,31 +307,78 @@ __device__ __forceinline__ void store_c(float *p, const float *x) {
   else *reinterpret_cast<float2 *>(p) = make_float2(x[0], x[1]);
 }
 
-// Adds partials first, first + step, .. of the row to the state (four loads in
-// flight).  Lane l holds channels C*l .. (C = D / 32): in a partial's
-// [D/4][128][4] layout, C floats of group C*l/4.
+// A softmax state of one row, C channels per lane.
+template <int C>
+struct LaneState {
+  float m = -INFINITY, l = 0.f, o[C];
+  __device__ __forceinline__ LaneState() {
+#pragma unroll
+    for (int i = 0; i < C; ++i) o[i] = 0.f;
+  }
+  // a warp's state in shared memory: O [8][D], max [8], sum [8]
+  __device__ __forceinline__ void read(const float *s, int h, int lane) {
+    constexpr int D = 32 * C;
+    load_c<C>(s + h * D + C * lane, o);
+    m = s[8 * D + h];
+    l = s[8 * D + 8 + h];
+  }
+  __device__ __forceinline__ void write(float *s, int h, int lane) const {
+    constexpr int D = 32 * C;
+    store_c<C>(s + h * D + C * lane, o);
+    if (lane == 0) s[8 * D + h] = m, s[8 * D + 8 + h] = l;
+  }
+  __device__ __forceinline__ void add(float m2, float l2, const float *o2) {
+    const float mn = fmaxf(m, m2), base = mn == -INFINITY ? 0.f : mn;
+    const float f1 = ex2(m - base), f2 = ex2(m2 - base);
+    l = l * f1 + l2 * f2;
+#pragma unroll
+    for (int i = 0; i < C; ++i) o[i] = o[i] * f1 + o2[i] * f2;
+    m = mn;
+  }
+};
+
+// Adds partials first, first + step, .. of each of a pair's heads h0 .. h0 + 3
+// to that head's state.  The four heads' loads go out together: neighbouring
+// rows share their sectors.  Lane l holds channels C*l .. (C = D / 32): in a
+// partial's [D/4][128][4] layout, C floats of group C*l/4.
+constexpr int kHeads = 4;
 template <int D>
-__device__ __forceinline__ void add_parts(const RowParts &rp, int first, int step, int lane, LaneState<D / 32> &st) {
+__device__ __forceinline__ void add_parts(const OwnParams &p, const PrefixPlan &pl, int b, int hkv, int h0, int first,
+                                          int step, int lane, LaneState<D / 32> (&st)[kHeads]) {
   constexpr int C = D / 32;
-  const size_t o_step = size_t(D) * 2 * kPrefixBlock;
-  const float *o = rp.o + size_t(C * lane / 4) * kPrefixBlock * 4 + (C * lane) % 4;
-  for (int s0 = first; s0 < rp.n; s0 += 4 * step) {
-    float2 ml[4];
-    float x[4][C];
+  constexpr size_t kOStep = size_t(D) * 2 * kPrefixBlock;
+  const size_t lane_off = size_t(C * lane / 4) * kPrefixBlock * 4 + (C * lane) % 4;
+  RowParts rp[kHeads];
+  int n = 0;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int s = s0 + u * step;
-      if (s < rp.n) {
-        ml[u] = rp.ml[s * kMlStep];
-        load_c<C>(o + s * o_step, x[u]);
-      } else {
-        ml[u] = make_float2(-INFINITY, 0.f);
+  for (int i = 0; i < kHeads; ++i) {
+    const int row = b * p.G + h0 + i;
+    if (h0 + i >= p.G) {
+      rp[i] = rp[0];
+      rp[i].n = 0;
+    } else if (i == 0 || row % kPrefixBlock == 0) {
+      rp[i] = row_parts<D>(p, pl, hkv, row);
+    } else {
+      rp[i] = {rp[i - 1].ml + 1, rp[i - 1].o + 4, rp[i - 1].n};
+    }
+    n = max(n, rp[i].n);
+  }
+#pragma unroll 2
+  for (int s = first; s < n; s += step) {
+    float2 ml[kHeads];
+    float x[kHeads][C];
 #pragma unroll
-        for (int i = 0; i < C; ++i) x[u][i] = 0.f;
+    for (int i = 0; i < kHeads; ++i) {
+      ml[i] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int e = 0; e < C; ++e) x[i][e] = 0.f;
+      if (s < rp[i].n) {
+        ml[i] = rp[i].ml[s * kMlStep];
+        load_c<C>(rp[i].o + lane_off + s * kOStep, x[i]);
       }
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) st.add(ml[u].x, ml[u].y, x[u]);
+    for (int i = 0; i < kHeads; ++i) st[i].add(ml[i].x, ml[i].y, x[i]);
   }
 }
 
@@ -401,60 +431,71 @@ __global__ void __launch_bounds__(NW * 32, kCtas) shared_own_kernel(const __grid
   // of K and V, and the scales of one row of K (lanes 0-15) or V
   constexpr int kPerLane = kStep * D / 16 / 32, kRowStride = 32 * 16 / D;
   const int my_row0 = lane / (D / 16), my_ch = lane % (D / 16), sc_row = lane & 15;
-  struct Source {  // this lane's first bytes at a pair's (or the prefix's head's) slot 0
+  struct Source {  // this lane's bytes of a step's rows my_row0 and sc_row
     const int8_t *k, *v;
     const float *s;
   };
   auto source = [&](const nd_kv_cache &from, size_t row) {
-    const size_t at = row * D + my_ch * 16;
-    return Source{from.k_codes + at, from.v_codes + at, (lane < 16 ? from.k_scale : from.v_scale) + row * NG};
+    const size_t at = (row + my_row0) * D + my_ch * 16;
+    return Source{from.k_codes + at, from.v_codes + at,
+                  (lane < 16 ? from.k_scale : from.v_scale) + (row + sc_row) * NG};
   };
-  Source own_src, pre_src;
+  Source src;    // of the cursor's next step
   Unit at;       // the cursor's unit: its next slot, the steps left
   int at_i = 0;  // its place in the order
+  auto seek = [&](int pair) {
+    if (kInline && at.first < v_inline) src = source(p.pre, size_t(pair % Hkv) * pslot + at.first);
+    else src = source(c, size_t(pair) * nslot + (at.first - v_inline));
+  };
   auto enter = [&]() {
     // (a warp whose share of a unit is empty goes on to the next one)
     do at = unit_at(at_i++);
     while (at.n == 0 && at.id < p.n_units);
-    if (at.n > 0) {
-      const int pair = p.n_split > 1 ? at.id / p.n_split : at.id;
-      own_src = source(c, size_t(pair) * nslot);
-      if (kInline) pre_src = source(p.pre, size_t(pair % Hkv) * pslot);
-      // its query, a unit's time before it is used
-      const int b = pair / Hkv, hkv = pair - b * Hkv;
-      if (lane * 64 < G * D)
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q + (size_t(b) * p.Hq + hkv * G) * D + lane * 64));
-    }
+    if (at.n > 0) seek(p.n_split > 1 ? at.id / p.n_split : at.id);
   };
   enter();
   int in = 0, out = 0;  // stage filled next, stage read next
+  // (rows kRowStride apart are 512 bytes apart in the stage; the swizzle of
+  // every second one differs in bit 6)
   const uint32_t off0 = swz(uint32_t(my_row0 * D + my_ch * 16));
   const uint32_t off_s = 2 * S::kCodes + (lane < 16 ? 0 : S::kScales) + sc_row * NG * 4;
   auto issue = [&]() {
     if (at.n > 0) {
       const bool pre = kInline && at.first < v_inline;
-      const Source src = pre ? pre_src : own_src;
       const int base = pre ? at.first : at.first - v_inline, slots = pre ? p.pre.sink_cap : nslot;
       const uint32_t st = my_stages + in * S::kBytes;
-      const int8_t *k = src.k + size_t(base) * D, *v = src.v + size_t(base) * D;
-      const float *sc = src.s + size_t(base) * NG;
-      const bool whole = base + kStep <= slots;
+      const uint32_t d0 = st + off0, d1 = st + (off0 ^ 64u);
+      if (base + kStep <= slots) {
 #pragma unroll
-      for (int i = 0; i < kPerLane; ++i) {
-        // (rows kRowStride apart are 512 bytes apart; the swizzle of every
-        // second one differs in bit 6)
-        const uint32_t dst = st + (off0 ^ ((i & 1) * 64)) + i * 512;
-        int r = my_row0 + i * kRowStride;
-        if (!whole) r = min(r, slots - 1 - base);  // past the end: the last slot, masked
-        cp_async16(dst, k + r * D);
-        cp_async16(dst + S::kCodes, v + r * D);
+        for (int i = 0; i < kPerLane; ++i) {
+          cp_async16((i & 1 ? d1 : d0) + i * 512, src.k + i * kRowStride * D);
+          cp_async16((i & 1 ? d1 : d0) + i * 512 + S::kCodes, src.v + i * kRowStride * D);
+        }
+        if constexpr (NG == 4) cp_async16(st + off_s, src.s);
+        else cp_async8(st + off_s, src.s);
+      } else {  // rows past the end: the last slot, masked
+        const int last = slots - 1 - base;
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) {
+          const int back = (my_row0 + i * kRowStride - min(my_row0 + i * kRowStride, last)) * D;
+          cp_async16((i & 1 ? d1 : d0) + i * 512, src.k + i * kRowStride * D - back);
+          cp_async16((i & 1 ? d1 : d0) + i * 512 + S::kCodes, src.v + i * kRowStride * D - back);
+        }
+        const float *sc = src.s - (sc_row - min(sc_row, last)) * NG;
+        if constexpr (NG == 4) cp_async16(st + off_s, sc);
+        else cp_async8(st + off_s, sc);
       }
-      const int r = whole ? sc_row : min(sc_row, slots - 1 - base);
-      if constexpr (NG == 4) cp_async16(st + off_s, sc + r * NG);
-      else cp_async8(st + off_s, sc + r * NG);
       if (++in == ST) in = 0;
       at.first += at.stride;
-      if (--at.n == 0) enter();
+      if (--at.n == 0) {
+        enter();
+      } else if (pre && at.first >= v_inline) {
+        seek(p.n_split > 1 ? at.id / p.n_split : at.id);
+      } else {
+        src.k += at.stride * D;
+        src.v += at.stride * D;
+        src.s += at.stride * NG;
+      }
     }
     cp_async_commit();
   };
@@ -470,29 +511,36 @@ __global__ void __launch_bounds__(NW * 32, kCtas) shared_own_kernel(const __grid
   if (!kInline && p.prefix_grid > 0)
     pl = prefix_plan(p.pre.sink_len[0], p.pre.sink_cap, Hkv, c.batch * G, p.prefix_grid);
 
-  for (int i = 0;; ++i) {
-    const Unit un = unit_at(i);
-    if (un.id >= p.n_units) break;  // (team units: the same for the CTA's warps)
+  // A unit's query and metadata are loaded while the unit before it is merged.
+  struct {
+    uint4 w[NG];
+    int sl, rl, rs;
+  } next;
+  auto fetch = [&](const Unit &un) {
+    if (un.id >= p.n_units) return;
     const int pair = p.n_split > 1 ? un.id / p.n_split : un.id, b = pair / Hkv, hkv = pair - b * Hkv;
-    // ---- the unit's query and metadata
-    HeadQ<D> hq;
-    {
-      uint4 w[NG];
-      const uint16_t *qh = p.q + (size_t(b) * p.Hq + hkv * G + (g < G ? g : 0)) * D;
+    const uint16_t *qh = p.q + (size_t(b) * p.Hq + hkv * G + (g < G ? g : 0)) * D;
 #pragma unroll
-      for (int grp = 0; grp < NG; ++grp)
-        w[grp] = g < G ? *reinterpret_cast<const uint4 *>(qh + 32 * grp + 8 * t) : make_uint4(0, 0, 0, 0);
-      make_q<D>(w, hq);
-    }
-    int sl = c.sink_len[b], rl = c.ring_len[b], rs = c.ring_start[b];
+    for (int grp = 0; grp < NG; ++grp)
+      next.w[grp] = g < G ? *reinterpret_cast<const uint4 *>(qh + 32 * grp + 8 * t) : make_uint4(0, 0, 0, 0);
+    next.sl = c.sink_len[b], next.rl = c.ring_len[b], next.rs = c.ring_start[b];
+  };
+  Unit un = unit_at(0);
+  fetch(un);
+  for (int i = 1; un.id < p.n_units; ++i) {  // (units of the whole CTA: the same for its warps)
+    const int pair = p.n_split > 1 ? un.id / p.n_split : un.id, b = pair / Hkv, hkv = pair - b * Hkv;
+    HeadQ<D> hq;
+    make_q<D>(next.w, hq);
+    int sl = next.sl, rl = next.rl, rs = next.rs;
     const bool sane = sl >= 0 && sl <= c.sink_cap && rl >= 0 && rl <= c.ring_cap && rs >= 0 &&
                       (c.ring_cap == 0 || rs < c.ring_cap);
     if (!sane) {
-      if (threadIdx.x == 0) raise_device_error(p.err, ND_DEVERR_METADATA);
+      if (lane == 0) raise_device_error(p.err, ND_DEVERR_METADATA);
       sl = rl = rs = 0;
     }
     const int n_vis = min(rl, p.window);
-    const int rs_eff = c.ring_cap ? (rs + rl - n_vis) % c.ring_cap : 0;  // oldest visible entry
+    int rs_eff = rs + rl - n_vis;  // oldest visible entry
+    if (rs_eff >= c.ring_cap) rs_eff -= c.ring_cap;
 
     RunState<D> run;
     int v = un.first;
@@ -530,17 +578,30 @@ __global__ void __launch_bounds__(NW * 32, kCtas) shared_own_kernel(const __grid
     // ---- merge.  The stage that the next copy will fill is free until then.
     float *state = reinterpret_cast<float *>(smem + (warp * ST + in) * S::kBytes);  // [8][D], max [8], sum [8]
     store_state<D>(run, lane, state, state + 8 * D, state + 8 * D + 8);
-    if (un.solo) {
-      __syncwarp();
-      for (int h = 0; h < G; ++h) {
-        LaneState<C> st;
-        st.m = state[8 * D + h];
-        st.l = state[8 * D + 8 + h];
-        load_c<C>(state + h * D + C * lane, st.o);
-        if (pl.nt > 0) add_parts<D>(row_parts<D>(p, pl, hkv, b * G + h), 0, 1, lane, st);
-        write_out<C>(p, size_t(b) * p.Hq + hkv * G + h, lane, st);
+    const Unit un_next = unit_at(i);
+    fetch(un_next);
+    __syncwarp();
+    // the prefix's partials: all of them for a unit of the warp's own, else
+    // this warp's share, folded into its state
+    if (un.solo || (pl.nt > 0 && p.n_split == 1)) {
+      for (int h0 = 0; h0 < G; h0 += kHeads) {
+        LaneState<C> st[kHeads];
+#pragma unroll
+        for (int i = 0; i < kHeads; ++i)
+          if (h0 + i < G) st[i].read(state, h0 + i, lane);
+        if (pl.nt > 0)
+          add_parts<D>(p, pl, b, hkv, h0, un.solo ? 0 : warp, un.solo ? 1 : NW, lane, st);
+#pragma unroll
+        for (int i = 0; i < kHeads; ++i)
+          if (h0 + i < G) {
+            if (un.solo) write_out<C>(p, size_t(b) * p.Hq + hkv * G + h0 + i, lane, st[i]);
+            else st[i].write(state, h0 + i, lane);
+          }
       }
-      __syncwarp();
+    }
+    if (un.solo) {
+      __syncwarp();  // the state is read before its stage is filled again
+      un = un_next;
       continue;
     }
     if (lane == 0) s_state[warp] = state;
@@ -549,10 +610,9 @@ __global__ void __launch_bounds__(NW * 32, kCtas) shared_own_kernel(const __grid
       LaneState<C> st;
 #pragma unroll 4
       for (int w = 0; w < NW; ++w) {
-        const float *sw = s_state[w];
-        float x[C];
-        load_c<C>(sw + h * D + C * lane, x);
-        st.add(sw[8 * D + h], sw[8 * D + 8 + h], x);
+        LaneState<C> other;
+        other.read(s_state[w], h, lane);
+        st.add(other.m, other.l, other.o);
       }
       if (p.n_split > 1) {
         const size_t part = size_t(un.id) * G + h;
@@ -562,11 +622,11 @@ __global__ void __launch_bounds__(NW * 32, kCtas) shared_own_kernel(const __grid
           p.ws_ml[2 * part + 1] = st.l;
         }
       } else {
-        if (pl.nt > 0) add_parts<D>(row_parts<D>(p, pl, hkv, b * G + h), 0, 1, lane, st);
         write_out<C>(p, size_t(b) * p.Hq + hkv * G + h, lane, st);
       }
     }
     __syncthreads();  // the states are read before their stages are filled again
+    un = un_next;
   }
   cp_async_wait<0>();
 }
@@ -587,20 +647,26 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __
   pl.nt = 0;
   if (p.prefix_grid > 0)
     pl = prefix_plan(p.pre.sink_len[0], p.pre.sink_cap, Hkv, p.c.batch * G, p.prefix_grid);
-  for (int h = 0; h < G; ++h) {
-    LaneState<C> st;
-    for (int s = warp; s < p.n_split; s += kMergeWarps) {
-      const size_t part = (size_t(pair) * p.n_split + s) * G + h;
-      float x[C];
-      load_c<C>(p.ws_o + part * D + C * lane, x);
-      st.add(p.ws_ml[2 * part], p.ws_ml[2 * part + 1], x);
-    }
-    // (the first sources go to the warps that the parts left out)
+  for (int h0 = 0; h0 < G; h0 += kHeads) {
+    LaneState<C> st[kHeads];
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i)
+      for (int s = warp; s < p.n_split && h0 + i < G; s += kMergeWarps) {
+        const size_t part = (size_t(pair) * p.n_split + s) * G + h0 + i;
+        float x[C];
+        load_c<C>(p.ws_o + part * D + C * lane, x);
+        st[i].add(p.ws_ml[2 * part], p.ws_ml[2 * part + 1], x);
+      }
+    // (the first partials go to the warps that the parts left out)
     if (pl.nt > 0)
-      add_parts<D>(row_parts<D>(p, pl, hkv, b * G + h), (warp + kMergeWarps - p.n_split % kMergeWarps) % kMergeWarps,
-                   kMergeWarps, lane, st);
-    store_c<C>(&s_o[h][warp][C * lane], st.o);
-    if (lane == 0) s_ml[h][warp][0] = st.m, s_ml[h][warp][1] = st.l;
+      add_parts<D>(p, pl, b, hkv, h0, (warp + kMergeWarps - p.n_split % kMergeWarps) % kMergeWarps, kMergeWarps, lane,
+                   st);
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i)
+      if (h0 + i < G) {
+        store_c<C>(&s_o[h0 + i][warp][C * lane], st[i].o);
+        if (lane == 0) s_ml[h0 + i][warp][0] = st[i].m, s_ml[h0 + i][warp][1] = st[i].l;
+      }
   }
   __syncthreads();
   for (int h = warp; h < G; h += kMergeWarps) {

@@ -31,9 +31,15 @@ __host__ __device__ inline int prefix_pairs(int rows) { return (rows + 2 * kPref
 // one before it in the same CTA with the next item, or in the next CTA.
 struct PrefixPlan {
   int len, nt, pairs, items, ctas;
+  int per_item;  // CTAs of each item where they are the same number, else 0
   bool sane;
   __host__ __device__ long long tiles() const { return (long long)items * nt; }
   __host__ __device__ long long start(int c) const { return tiles() * c / ctas; }
+  // the CTAs of an item's first and last tile
+  __host__ __device__ int first_cta(int item) const { return per_item ? item * per_item : owner((long long)item * nt); }
+  __host__ __device__ int last_cta(int item) const {
+    return per_item ? (item + 1) * per_item - 1 : owner((long long)(item + 1) * nt - 1);
+  }
   // the CTA whose stretch holds tile x
   __host__ __device__ int owner(long long x) const {
     const long long n = tiles(), y = (x + 1) * ctas - 1;
@@ -55,6 +61,7 @@ __host__ __device__ inline PrefixPlan prefix_plan(int sink_len, int sink_cap, in
   // each, 22 us, against 152 of two and more, 26 us).
   const int even = p.items > 0 ? p.ctas / p.items * p.items : 0;
   if (even * 6 >= p.ctas * 5) p.ctas = even;
+  p.per_item = even > 0 && p.ctas == even ? even / p.items : 0;
   return p;
 }
 
