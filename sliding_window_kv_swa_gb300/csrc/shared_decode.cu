@@ -46,6 +46,7 @@ struct OwnParams {
   float *ws_ml, *ws_o; // n_split > 1: [pair][n_split][G][2], [..][G][D]
   PrefixParts parts;   // the prefix's partials, when prefix_grid > 0
   int prefix_grid;
+  bool early;          // the kernel before this one is the call's own prefix kernel: see shared_own_kernel
   int *err;
 };
 
@@ -407,7 +408,12 @@ __global__ void __launch_bounds__(NW * 32, kCtas) shared_own_kernel(const __grid
   const uint32_t my_stages = smem_u32(smem) + warp * ST * S::kBytes;
   const int v_inline = kInline ? p.inline_slots : 0, v_all = v_inline + nslot;
 
-  pdl_wait();
+  // Behind the prefix kernel (p.early) the CTAs may start while it runs: it let
+  // them once what came before it was complete, so the caches and q are final
+  // and only its partials have to be waited for.  What is read before that
+  // wait goes past L1, which may hold an earlier step's lines.
+  bool waited = !p.early;
+  if (waited) pdl_wait();
 
   // ---- copies: a cursor that runs ST - 1 steps ahead of the reads
   // The warp's units in order: solo of its own, then units that the CTA's
@@ -430,7 +436,13 @@ __global__ void __launch_bounds__(NW * 32, kCtas) shared_own_kernel(const __grid
   // a lane copies 16-byte chunk my_ch of rows my_row0, my_row0 + kRowStride, ..
   // of K and V, and the scales of one row of K (lanes 0-15) or V
   constexpr int kPerLane = kStep * D / 16 / 32, kRowStride = 32 * 16 / D;
-  const int my_row0 = lane / (D / 16), my_ch = lane % (D / 16), sc_row = lane & 15;
+  const int my_row0 = lane / (D / 16), my_ch = lane % (D / 16);
+  // scales: a slot's row is 16 bytes, or 8 (D = 64): two slots a copy where a
+  // pair's first row is 16-byte aligned (an even number of slots), by lanes
+  // 0-7 (K) and 8-15 (V), else one slot a lane
+  const bool sc_pairs = D == 64 && !kInline && nslot % 2 == 0;
+  const int sc_row = sc_pairs ? (lane & 7) * 2 : lane & 15;
+  const bool sc_v = sc_pairs ? lane & 8 : lane & 16;
   struct Source {  // this lane's bytes of a step's rows my_row0 and sc_row
     const int8_t *k, *v;
     const float *s;
@@ -438,7 +450,7 @@ __global__ void __launch_bounds__(NW * 32, kCtas) shared_own_kernel(const __grid
   auto source = [&](const nd_kv_cache &from, size_t row) {
     const size_t at = (row + my_row0) * D + my_ch * 16;
     return Source{from.k_codes + at, from.v_codes + at,
-                  (lane < 16 ? from.k_scale : from.v_scale) + (row + sc_row) * NG};
+                  (sc_v ? from.v_scale : from.k_scale) + (row + sc_row) * NG};
   };
   Source src;    // of the cursor's next step
   Unit at;       // the cursor's unit: its next slot, the steps left
@@ -458,7 +470,16 @@ __global__ void __launch_bounds__(NW * 32, kCtas) shared_own_kernel(const __grid
   // (rows kRowStride apart are 512 bytes apart in the stage; the swizzle of
   // every second one differs in bit 6)
   const uint32_t off0 = swz(uint32_t(my_row0 * D + my_ch * 16));
-  const uint32_t off_s = 2 * S::kCodes + (lane < 16 ? 0 : S::kScales) + sc_row * NG * 4;
+  const uint32_t off_s = 2 * S::kCodes + (sc_v ? S::kScales : 0) + sc_row * NG * 4;
+  auto copy_scale = [&](uint32_t dst, const float *from) {
+    if constexpr (NG == 4) {
+      cp_async16(dst, from);
+    } else if (!sc_pairs) {
+      cp_async8(dst, from);
+    } else if (lane < 16) {
+      cp_async16(dst, from);
+    }
+  };
   auto issue = [&]() {
     if (at.n > 0) {
       const bool pre = kInline && at.first < v_inline;
@@ -471,8 +492,7 @@ __global__ void __launch_bounds__(NW * 32, kCtas) shared_own_kernel(const __grid
           cp_async16((i & 1 ? d1 : d0) + i * 512, src.k + i * kRowStride * D);
           cp_async16((i & 1 ? d1 : d0) + i * 512 + S::kCodes, src.v + i * kRowStride * D);
         }
-        if constexpr (NG == 4) cp_async16(st + off_s, src.s);
-        else cp_async8(st + off_s, src.s);
+        copy_scale(st + off_s, src.s);
       } else {  // rows past the end: the last slot, masked
         const int last = slots - 1 - base;
 #pragma unroll
@@ -481,9 +501,8 @@ __global__ void __launch_bounds__(NW * 32, kCtas) shared_own_kernel(const __grid
           cp_async16((i & 1 ? d1 : d0) + i * 512, src.k + i * kRowStride * D - back);
           cp_async16((i & 1 ? d1 : d0) + i * 512 + S::kCodes, src.v + i * kRowStride * D - back);
         }
-        const float *sc = src.s - (sc_row - min(sc_row, last)) * NG;
-        if constexpr (NG == 4) cp_async16(st + off_s, sc);
-        else cp_async8(st + off_s, sc);
+        // (last is odd where slots go in pairs)
+        copy_scale(st + off_s, src.s - (sc_row - min(sc_row, sc_pairs ? last - 1 : last)) * NG);
       }
       if (++in == ST) in = 0;
       at.first += at.stride;
@@ -509,7 +528,7 @@ __global__ void __launch_bounds__(NW * 32, kCtas) shared_own_kernel(const __grid
   PrefixPlan pl;
   pl.nt = 0;
   if (!kInline && p.prefix_grid > 0)
-    pl = prefix_plan(p.pre.sink_len[0], p.pre.sink_cap, Hkv, c.batch * G, p.prefix_grid);
+    pl = prefix_plan(__ldcg(p.pre.sink_len), p.pre.sink_cap, Hkv, c.batch * G, p.prefix_grid);
 
   // A unit's query and metadata are loaded while the unit before it is merged.
   struct {
@@ -522,8 +541,8 @@ __global__ void __launch_bounds__(NW * 32, kCtas) shared_own_kernel(const __grid
     const uint16_t *qh = p.q + (size_t(b) * p.Hq + hkv * G + (g < G ? g : 0)) * D;
 #pragma unroll
     for (int grp = 0; grp < NG; ++grp)
-      next.w[grp] = g < G ? *reinterpret_cast<const uint4 *>(qh + 32 * grp + 8 * t) : make_uint4(0, 0, 0, 0);
-    next.sl = c.sink_len[b], next.rl = c.ring_len[b], next.rs = c.ring_start[b];
+      next.w[grp] = g < G ? __ldcg(reinterpret_cast<const uint4 *>(qh + 32 * grp + 8 * t)) : make_uint4(0, 0, 0, 0);
+    next.sl = __ldcg(c.sink_len + b), next.rl = __ldcg(c.ring_len + b), next.rs = __ldcg(c.ring_start + b);
   };
   Unit un = unit_at(0);
   fetch(un);
@@ -584,6 +603,8 @@ __global__ void __launch_bounds__(NW * 32, kCtas) shared_own_kernel(const __grid
     // the prefix's partials: all of them for a unit of the warp's own, else
     // this warp's share, folded into its state
     if (un.solo || (pl.nt > 0 && p.n_split == 1)) {
+      if (!waited) pdl_wait();
+      waited = true;
       for (int h0 = 0; h0 < G; h0 += kHeads) {
         LaneState<C> st[kHeads];
 #pragma unroll
@@ -629,6 +650,7 @@ __global__ void __launch_bounds__(NW * 32, kCtas) shared_own_kernel(const __grid
     un = un_next;
   }
   cp_async_wait<0>();
+  if (!waited) pdl_wait();  // this kernel is complete only after the one before it
 }
 
 // Joins the parts of each pair and the prefix's partials: a CTA per pair, a
@@ -759,6 +781,8 @@ cudaError_t launch_shared_decode(const void *q, const nd_kv_cache &prefix, const
   p.err = err;
   p.parts = {nullptr, nullptr};
   p.prefix_grid = 0;
+  // (at D = 64 an odd number of slots needs copies that go through L1)
+  p.early = !s.inline_prefix && (d == 128 || (c.sink_cap + c.ring_cap) % 2 == 0);
   float *w = static_cast<float *>(ws);
   cudaError_t e;
   if (!s.inline_prefix) {

@@ -236,6 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Prefix
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   pdl_wait();
+  pdl_trigger();  // the own part reads nothing of this kernel's before it waits
   auto tS = [&](int rb, int buf) { return tmem + (NS * rb + buf) * BN; };
   auto tO = [&](int rb) { return tmem + Y::cO + rb * D; };
 
