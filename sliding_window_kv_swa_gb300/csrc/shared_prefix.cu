@@ -94,7 +94,8 @@ struct Lay {
 struct PrefixParams {
   const uint16_t *q;
   nd_kv_cache c;     // the prefix: one row, its sink region
-  int B, Hq, G, R;
+  int Hq, G, R;
+  unsigned g_magic;  // ceil(2^32 / G): r / G for G >= 2 and r < 2^24
   PrefixParts out;
   int *err;
 };
@@ -537,30 +538,56 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Prefix
       const bool active = s.r0 + rb * BM + (warp & 3) * 32 < p.R;
       float c_row = 0.f;
       if (active) {
-        // Q: this thread's row as fp16 times 2^eq.  The previous segment's
-        // products, the last readers of the buffer, are done: this thread
-        // waited for them before it read O.
-        uint4 w[D / 8];
-        const uint16_t *src = p.q + (size_t(row / p.G) * p.Hq + s.hk * p.G + row % p.G) * D;
-        float qm = 0.f;
+        // Q: the warp's 32 rows as fp16 times 2^eq of the row, D / 8 lanes to
+        // a row (a thread per row would touch 32 lines an instruction: 7000
+        // cycles for the two blocks, in the way of every copy).  The previous
+        // segment's products, the last readers of the buffer, are done: the
+        // warp waited for them before it read O.
+        constexpr int kL = D / 8, kRows = 32 / kL, kIt = 32 / kRows;
+        const int sub = lane / kL, ch = lane % kL;
+        const int first = s.r0 + rb * BM + (warp & 3) * 32 + sub;  // and every kRows-th row after it
+        // (a rolled loop, the next four rows' loads ahead of it: the code runs
+        // once, and unrolled it would wait for its own instructions)
+        auto load_rows = [&](int i0, uint4 (&w)[4]) {
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          w[i] = row < p.R ? reinterpret_cast<const uint4 *>(src)[i] : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+          for (int i = 0; i < 4; ++i) {
+            const int rw = first + (i0 + i) * kRows;
+            const int b = p.G == 1 ? rw : int(__umulhi(unsigned(rw), p.g_magic));
+            const uint16_t *src = p.q + (size_t(b) * p.Hq + s.hk * p.G + (rw - b * p.G)) * D + 8 * ch;
+            w[i] = rw < p.R ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0u, 0u, 0u, 0u);
+          }
+        };
+        uint4 ahead[4];
+        load_rows(0, ahead);
+        int eq_row = 0;
+#pragma unroll 1
+        for (int i0 = 0; i0 < kIt; i0 += 4) {
+          uint4 w[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) qm = fmaxf(qm, fmaxf(fabsf(bf16_lo(u[e])), fabsf(bf16_hi(u[e]))));
+          for (int i = 0; i < 4; ++i) w[i] = ahead[i];
+          if (i0 + 4 < kIt) load_rows(i0 + 4, ahead);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+            float qm = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) qm = fmaxf(qm, fmaxf(fabsf(bf16_lo(u[e])), fabsf(bf16_hi(u[e]))));
+#pragma unroll
+            for (int off = kL / 2; off >= 1; off >>= 1) qm = fmaxf(qm, __shfl_xor_sync(0xffffffffu, qm, off));
+            const int eq = clamp_exp(14 - ilog2(qm));
+            const float up = pow2i(eq);
+            uint32_t h[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[e] = pack_half2(bf16_lo(u[e]) * up, bf16_hi(u[e]) * up);
+            const int rw = (warp & 3) * 32 + sub + (i0 + i) * kRows;  // in the block
+            st_shared_v4(sQ(rb) + (ch / 8) * (BM * 128) + rw * 128 + (((ch & 7) ^ (rw & 7)) << 4), h[0], h[1], h[2],
+                         h[3]);
+            // lane l is row l of the warp: its exponent sits in the lanes of sub l % kRows
+            const int e_l = __shfl_sync(0xffffffffu, eq, (lane % kRows) * kL);
+            if (lane / kRows == i0 + i) eq_row = e_l;
+          }
         }
-        const int eq = clamp_exp(14 - ilog2(qm));
-        const float up = pow2i(eq);
-        c_row = pow2i(-eq) * (1.4426950408889634f * rsqrtf(float(D)));
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-          uint32_t h[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) h[e] = pack_half2(bf16_lo(u[e]) * up, bf16_hi(u[e]) * up);
-          st_shared_v4(sQ(rb) + (i / 8) * (BM * 128) + r * 128 + (((i & 7) ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
-        }
+        c_row = pow2i(-eq_row) * (1.4426950408889634f * rsqrtf(float(D)));
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
       __syncwarp();
@@ -706,10 +733,10 @@ cudaError_t launch_shared_prefix(const void *q, const nd_kv_cache &prefix, int b
   PrefixParams p;
   p.q = static_cast<const uint16_t *>(q);
   p.c = prefix;
-  p.B = batch;
   p.Hq = n_q_heads;
   p.G = n_q_heads / prefix.n_kv_heads;
   p.R = batch * p.G;
+  p.g_magic = p.G > 1 ? unsigned((0x100000000ull + p.G - 1) / p.G) : 0u;
   p.out = out;
   p.err = err;
   const int grid = prefix_grid(prefix.sink_cap, prefix.n_kv_heads, p.R);
