@@ -343,7 +343,7 @@ struct LaneState {
 // rows share their sectors.  Lane l holds channels C*l .. (C = D / 32): in a
 // partial's [D/4][128][4] layout, C floats of group C*l/4.
 constexpr int kHeads = 4;
-template <int D>
+template <int D, int kUnroll>
 __device__ __forceinline__ void add_parts(const OwnParams &p, const PrefixPlan &pl, int b, int hkv, int h0, int first,
                                           int step, int lane, LaneState<D / 32> (&st)[kHeads]) {
   constexpr int C = D / 32;
@@ -364,7 +364,7 @@ __device__ __forceinline__ void add_parts(const OwnParams &p, const PrefixPlan &
     }
     n = max(n, rp[i].n);
   }
-#pragma unroll 2
+#pragma unroll kUnroll
   for (int s = first; s < n; s += step) {
     float2 ml[kHeads];
     float x[kHeads][C];
@@ -425,8 +425,7 @@ __global__ void __launch_bounds__(NW * 32, kCtas) shared_own_kernel(const __grid
   auto unit_at = [&](int i) {
     Unit u;
     u.solo = i < p.solo;
-    u.id = u.solo ? (i * gridDim.x + blockIdx.x) * NW + warp
-                  : (p.solo * NW + i - p.solo) * gridDim.x + blockIdx.x;
+    u.id = ((u.solo ? i * NW + warp : p.solo * NW + i - p.solo)) * gridDim.x + blockIdx.x;
     const int v0 = p.n_split > 1 ? (u.id % p.n_split) * p.slots_per_unit : 0, v1 = min(v0 + p.slots_per_unit, v_all);
     u.first = u.solo ? v0 : v0 + warp * kStep;
     u.stride = u.solo ? kStep : NW * kStep;
@@ -611,7 +610,7 @@ __global__ void __launch_bounds__(NW * 32, kCtas) shared_own_kernel(const __grid
         for (int i = 0; i < kHeads; ++i)
           if (h0 + i < G) st[i].read(state, h0 + i, lane);
         if (pl.nt > 0)
-          add_parts<D>(p, pl, b, hkv, h0, un.solo ? 0 : warp, un.solo ? 1 : NW, lane, st);
+          add_parts<D, 2>(p, pl, b, hkv, h0, un.solo ? 0 : warp, un.solo ? 1 : NW, lane, st);
 #pragma unroll
         for (int i = 0; i < kHeads; ++i)
           if (h0 + i < G) {
@@ -681,7 +680,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __
       }
     // (the first partials go to the warps that the parts left out)
     if (pl.nt > 0)
-      add_parts<D>(p, pl, b, hkv, h0, (warp + kMergeWarps - p.n_split % kMergeWarps) % kMergeWarps, kMergeWarps, lane,
+      add_parts<D, 2>(p, pl, b, hkv, h0, (warp + kMergeWarps - p.n_split % kMergeWarps) % kMergeWarps, kMergeWarps, lane,
                    st);
 #pragma unroll
     for (int i = 0; i < kHeads; ++i)
@@ -718,10 +717,14 @@ cudaError_t launch_own(OwnParams &p, cudaStream_t stream) {
     smem_set.fetch_or(bit, std::memory_order_release);
   }
   const int most = kPrefixCtas * kCtas, grid = p.n_units < most ? p.n_units : most;
-  // whole rounds of the warps take a unit each, the rest is shared: no warp
-  // waits for others while there are units for all (n_split > 1: fewer units
-  // than warps)
-  p.solo = p.n_units / (grid * NW);
+  // Whole rounds of the warps take a unit each.  The rest is one more such
+  // round, or shared: a CTA's warps then need a fourth of the steps, but each
+  // round of theirs has its own start and merge (about seven steps' time; 128
+  // sequences of 256 slots: one round alone 21 us, three together 36 us).
+  const int steps = p.slots_per_unit / kStep, warps = grid * NW, rest = p.n_units % warps;
+  const int rounds = (rest + grid - 1) / grid;
+  p.solo = p.n_units / warps;
+  if (p.n_split == 1 && steps + 7 < rounds * ((steps + NW - 1) / NW + 7)) ++p.solo;
   return launch_pdl(kern, dim3(unsigned(grid)), dim3(NW * 32), smem, stream, p);
 }
 
