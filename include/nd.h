@@ -605,7 +605,7 @@ ND_API int nd_rope_apply(const void *x, void *y, int batch, int T, int n_heads,
  *   q_out, k_out  dtype [batch][T][heads][head_dim], contiguous; may equal q / k
  *      where those are contiguous
  * rope_theta 0 = no rotation.  eps >= 0.  Strides are multiples of 16 bytes.
- * head_dim 32, 64, 128 or 256.  p * theta^(-2i/head_dim) is reduced to a
+ * head_dim 32, 64, 128 or 256; batch * T at most 2^30.  p * theta^(-2i/head_dim) is reduced to a
  * fraction of a turn in 64-bit integers; sine and cosine are fp32.
  */
 ND_API int nd_qk_norm_rope(const void *q, const void *k, nd_dtype dtype, int batch, int T,

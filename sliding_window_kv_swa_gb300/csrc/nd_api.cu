@@ -768,6 +768,7 @@ int nd_qk_norm_rope(const void *q, const void *k, nd_dtype dtype, int batch, int
   if (head_dim != 32 && head_dim != 64 && head_dim != 128 && head_dim != 256) return ND_ERR_UNSUPPORTED;
   if (!norm_args_ok(eps, rope_theta, q_weight, k_weight)) return ND_ERR_INVALID_ARG;
   if (size_t(batch) * T == 0 || n_q_heads + n_k_heads == 0) return ND_OK;
+  if (int64_t(batch) * T > (1 << 30)) return ND_ERR_UNSUPPORTED;
   const int elem = dtype == ND_F32 ? 4 : 2;
   if (n_q_heads && (!q || !q_out || !aligned16(q) || !aligned16(q_out) || !stride_ok(q_stride, n_q_heads, head_dim, elem)))
     return ND_ERR_INVALID_ARG;

@@ -24,6 +24,8 @@
 
 #include <math.h>
 
+#include <atomic>
+
 namespace nd {
 
 namespace {
@@ -64,15 +66,32 @@ __device__ __forceinline__ float2 turn_cs(int pos, unsigned long long f) {
   return make_float2(c, s);
 }
 
-__device__ __forceinline__ void ld8(const uint16_t *p, float *x) {
-  const uint4 w = *reinterpret_cast<const uint4 *>(p);
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+// Eight channels as loaded (bf16: one uint4, fp32: two) and as fp32.
+template <typename E>
+struct Raw8 {
+  uint4 w[sizeof(E) / 2];
+  __device__ __forceinline__ void load(const E *p) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) x[2 * i] = bf16_lo(u[i]), x[2 * i + 1] = bf16_hi(u[i]);
-}
-__device__ __forceinline__ void ld8(const float *p, float *x) {
-  const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    for (int i = 0; i < int(sizeof(E) / 2); ++i) w[i] = reinterpret_cast<const uint4 *>(p)[i];
+  }
+  __device__ __forceinline__ void get(float *x) const {
+    if constexpr (sizeof(E) == 2) {
+      const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[2 * i] = bf16_lo(u[i]), x[2 * i + 1] = bf16_hi(u[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        x[4 * i] = __uint_as_float(w[i].x), x[4 * i + 1] = __uint_as_float(w[i].y),
+              x[4 * i + 2] = __uint_as_float(w[i].z), x[4 * i + 3] = __uint_as_float(w[i].w);
+    }
+  }
+};
+template <typename E>
+__device__ __forceinline__ void ld8(const E *p, float *x) {
+  Raw8<E> r;
+  r.load(p);
+  r.get(x);
 }
 __device__ __forceinline__ void st8(uint16_t *p, const float *x) {
   *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
@@ -81,6 +100,30 @@ __device__ __forceinline__ void st8(uint16_t *p, const float *x) {
 __device__ __forceinline__ void st8(float *p, const float *x) {
   reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
   reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+
+// The eight angles of a lane's channel pairs i0 .. i0 + 7.  The lanes that hold
+// the same pairs of other rows make an eighth to a half of them each.
+template <int D>
+__device__ __forceinline__ void lane_angles(int pos, const unsigned long long *f, int lane, float2 *cs) {
+  constexpr int kLanes = D / 16, kRows = 32 / kLanes, kPer = kRows >= 8 ? 1 : 8 / kRows;
+  float2 mine[kPer];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) mine[j] = turn_cs(pos, f[j]);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int src = (e / kPer) * kLanes + lane % kLanes;
+    cs[e].x = __shfl_sync(0xffffffffu, mine[e % kPer].x, src);
+    cs[e].y = __shfl_sync(0xffffffffu, mine[e % kPer].y, src);
+  }
+}
+// the frequencies of the angles that this lane makes
+template <int D>
+__device__ __forceinline__ void lane_freqs(const Turns &t, int lane, unsigned long long *f) {
+  constexpr int kLanes = D / 16, kRows = 32 / kLanes, kPer = kRows >= 8 ? 1 : 8 / kRows;
+  const int i0 = 8 * (lane % kLanes), e0 = (lane / kLanes) * kPer % 8;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) f[j] = t.f[i0 + e0 + j];
 }
 
 // The row held by D/16 neighbouring lanes: this lane's lo (channels i0..i0+7)
@@ -109,63 +152,125 @@ struct NormRopeParams {
   const float *w[2];   // NULL: ones
   int H[2];
   int64_t stride[2];   // elements from one token to the next in x
-  int T;
-  int64_t tokens;
-  int chunks, per_chunk;  // a warp takes per_chunk heads (of q, then k) of one token
+  int T, tokens;
   float eps;
   const int32_t *pos;
   Turns turns;
 };
 
-// One warp per (token, chunk of heads): its eight angles are made once and
-// serve every head it takes; kU rows' loads go out before any is used.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+
+// A warp takes tokens with the stride of the grid, each as batches of rows (kU
+// * 32 / (D / 16) heads of q, then of k).  HBM-bound: a row in and a row out;
+// what it needs is loads in flight, so each lane copies its own channels kSt -
+// 1 batches ahead into a ring in shared memory (its own slots: nothing to
+// exchange, no barrier), across the end of a token, while the angles -- once
+// per token for all its heads -- and the batches before are computed.
+// At 32768 tokens of 32 + 8 heads of 128 (671 MB): 133 us with plain loads
+// behind the angles, 120 with one batch ahead in registers.
 template <typename E, int D>
-__global__ void __launch_bounds__(256) qk_norm_rope_kernel(const __grid_constant__ NormRopeParams<E> p) {
-  constexpr int kLanes = D / 16, kRows = 32 / kLanes, kU = 2;
-  const int lane = threadIdx.x & 31, i0 = 8 * (lane % kLanes), sub = lane / kLanes;
+struct NormLay {
+  static constexpr int kLanes = D / 16, kRows = 32 / kLanes;
+  static constexpr int kU = sizeof(E) == 2 ? 2 : 1, kBatch = kU * kRows;
+  static constexpr int kSt = 6, kStage = kU * kRows * D * int(sizeof(E));  // 2 KB
+  static constexpr int kWarps = 4, kBytes = kWarps * kSt * kStage;
+};
+
+template <typename E, int D>
+__global__ void __launch_bounds__(128, 4) qk_norm_rope_kernel(const __grid_constant__ NormRopeParams<E> p) {
+  using Y = NormLay<E, D>;
+  constexpr int kLanes = Y::kLanes, kRows = Y::kRows, kU = Y::kU, kSt = Y::kSt, kVec = sizeof(E) / 2;
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, i0 = 8 * (lane % kLanes), sub = lane / kLanes;
+  // a lane's slots: 16 bytes each, 512 apart
+  const uint32_t mine = smem_u32(smem) + warp * kSt * Y::kStage + lane * 16;
   unsigned long long f[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) f[e] = p.turns.f[i0 + e];
+  lane_freqs<D>(p.turns, lane, f);
+  const int stride = gridDim.x * Y::kWarps;
   pdl_wait();
-  const int64_t warps = int64_t(gridDim.x) * (blockDim.x >> 5), n_items = p.tokens * p.chunks;
-  for (int64_t item = int64_t(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); item < n_items; item += warps) {
-    const int64_t tok = item / p.chunks;
-    const int c0 = int(item % p.chunks) * p.per_chunk, c1 = c0 + p.per_chunk;
-    const int pos = p.pos ? p.pos[tok] : int(tok % p.T);
+
+  // the copies' cursor: a token, q (0) or k (1), the batch's first head
+  int c_tok = blockIdx.x * Y::kWarps + warp, c_which = p.H[0] > 0 ? 0 : 1, c_h = 0, in = 0;
+  auto issue = [&]() {
+    if (c_tok < p.tokens) {
+      const int H = c_which ? p.H[1] : p.H[0];
+      const E *x = (c_which ? p.x[1] : p.x[0]) + c_tok * (c_which ? p.stride[1] : p.stride[0]) + i0;
+      const uint32_t dst = mine + in * Y::kStage;
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const E *row = x + min(c_h + u * kRows + sub, H - 1) * D;  // past the end: the last head, not stored
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+          copy16(dst + (u * 2 * kVec + j) * 512, row + j * (16 / sizeof(E)));
+          copy16(dst + (u * 2 * kVec + kVec + j) * 512, row + D / 2 + j * (16 / sizeof(E)));
+        }
+      }
+      if (++in == kSt) in = 0;
+      c_h += Y::kBatch;
+      if (c_h >= H) {
+        c_h = 0;
+        if (c_which == 0 && p.H[1] > 0) {
+          c_which = 1;
+        } else {
+          c_which = p.H[0] > 0 ? 0 : 1;
+          c_tok += stride;
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < kSt - 1; ++i) issue();
+
+  int tok = blockIdx.x * Y::kWarps + warp, out = 0;
+  auto position = [&](int t) { return p.pos ? p.pos[t] : t % p.T; };
+  int pos = tok < p.tokens ? position(tok) : 0;
+  for (; tok < p.tokens; tok += stride) {
     float2 cs[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) cs[e] = turn_cs(pos, f[e]);
-#pragma unroll
+    lane_angles<D>(pos, f, lane, cs);
+    if (tok + stride < p.tokens) pos = position(tok + stride);
+#pragma unroll 1
     for (int which = 0; which < 2; ++which) {
-      // this chunk's heads of q (which 0) or k
-      const int H = p.H[which], off = which ? p.H[0] : 0;
-      const int h0 = max(c0 - off, 0), h1 = min(c1 - off, H);
-      if (h0 >= h1) continue;
+      const int H = which ? p.H[1] : p.H[0];
+      const float *w = which ? p.w[1] : p.w[0];
       float wlo[8], whi[8];
-      if (p.w[which]) {
-        ld8(p.w[which] + i0, wlo);
-        ld8(p.w[which] + D / 2 + i0, whi);
+      if (w) {
+        ld8(w + i0, wlo);
+        ld8(w + D / 2 + i0, whi);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) wlo[e] = whi[e] = 1.f;
       }
-      const E *x = p.x[which] + tok * p.stride[which] + i0;
-      E *y = p.y[which] + tok * H * D + i0;
-      for (int h = h0; h < h1; h += kU * kRows) {
-        float lo[kU][8], hi[kU][8];
+      E *y = (which ? p.y[1] : p.y[0]) + int64_t(tok) * (H * D) + i0;
+#pragma unroll 1
+      for (int h0 = 0; h0 < H; h0 += Y::kBatch) {
+        issue();
+        asm volatile("cp.async.wait_group %0;" ::"n"(kSt - 1) : "memory");
+        const uint32_t src = mine + out * Y::kStage;
+        if (++out == kSt) out = 0;
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
-          const int hh = min(h + u * kRows + sub, h1 - 1);
-          ld8(x + size_t(hh) * D, lo[u]);
-          ld8(x + size_t(hh) * D + D / 2, hi[u]);
-        }
+          Raw8<E> rlo, rhi;
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          const int hh = h + u * kRows + sub;
-          norm_rotate<D>(lo[u], hi[u], wlo, whi, cs, p.eps);
-          if (hh < h1) {
-            st8(y + size_t(hh) * D, lo[u]);
-            st8(y + size_t(hh) * D + D / 2, hi[u]);
+          for (int j = 0; j < kVec; ++j) {
+            rlo.w[j] = lds16(src + (u * 2 * kVec + j) * 512);
+            rhi.w[j] = lds16(src + (u * 2 * kVec + kVec + j) * 512);
+          }
+          float lo[8], hi[8];
+          rlo.get(lo);
+          rhi.get(hi);
+          norm_rotate<D>(lo, hi, wlo, whi, cs, p.eps);
+          const int h = h0 + u * kRows + sub;
+          if (h < H) {
+            st8(y + h * D, lo);
+            st8(y + h * D + D / 2, hi);
           }
         }
       }
@@ -228,7 +333,9 @@ __global__ void __launch_bounds__(512) qk_norm_append_kernel(const __grid_consta
   constexpr int kLanes = D / 16;
   const nd_kv_cache &c = p.c;
   const int b = blockIdx.x, i0 = 8 * (threadIdx.x % kLanes), per = blockDim.x / kLanes;
-  const int Hkv = c.n_kv_heads, nslot = c.sink_cap + c.ring_cap, n_rows = p.Hq + 2 * Hkv;
+  const int Hkv = c.n_kv_heads, nslot = c.sink_cap + c.ring_cap, n_rows = p.Hq + 2 * Hkv, lane = threadIdx.x & 31;
+  unsigned long long f[8];
+  lane_freqs<D>(p.turns, lane, f);
   pdl_wait();
   const int sl = c.sink_len[b], rs = c.ring_start[b], rl = c.ring_len[b], sq = c.seq_len[b];
   const int pos = sq + (p.pos_base ? *p.pos_base : 0);
@@ -244,8 +351,7 @@ __global__ void __launch_bounds__(512) qk_norm_append_kernel(const __grid_consta
     return;
   }
   float2 cs[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) cs[e] = turn_cs(pos, p.turns.f[i0 + e]);
+  lane_angles<D>(pos, f, lane, cs);
   for (int r0 = 0; r0 < n_rows; r0 += per) {
     const int r = r0 + threadIdx.x / kLanes, rr = min(r, n_rows - 1);
     const bool live = r < n_rows;
@@ -293,6 +399,24 @@ __global__ void __launch_bounds__(512) qk_norm_append_kernel(const __grid_consta
   }
 }
 
+template <typename E, int D>
+cudaError_t launch_norm_rope_d(const NormRopeParams<E> &p, cudaStream_t stream) {
+  using Y = NormLay<E, D>;
+  auto kern = qk_norm_rope_kernel<E, D>;
+  static std::atomic<unsigned long long> smem_set{0};  // the opt-in, once per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev >= 0 && dev < 64 ? 1ull << dev : 0ull;
+  if (!bit || !(smem_set.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Y::kBytes);
+    if (e != cudaSuccess) return e;
+    smem_set.fetch_or(bit, std::memory_order_release);
+  }
+  const int blocks = (p.tokens + Y::kWarps - 1) / Y::kWarps, most = 152 * 4;
+  return launch_pdl(kern, dim3(unsigned(blocks < most ? blocks : most)), dim3(32 * Y::kWarps), size_t(Y::kBytes), stream, p);
+}
+
 template <typename E>
 cudaError_t launch_norm_rope_t(const QkNormRope &a, cudaStream_t stream) {
   NormRopeParams<E> p;
@@ -307,21 +431,15 @@ cudaError_t launch_norm_rope_t(const QkNormRope &a, cudaStream_t stream) {
   p.stride[0] = a.q_stride;
   p.stride[1] = a.k_stride;
   p.T = a.T;
-  p.tokens = int64_t(a.batch) * a.T;
+  p.tokens = a.batch * a.T;
   p.eps = a.eps;
   p.pos = a.positions;
   p.turns = make_turns(a.head_dim, a.theta);
-  const int H = a.Hq + a.Hk;
-  p.chunks = 1;
-  p.per_chunk = H;
-  constexpr int kWarps = 8;
-  const int64_t blocks = (p.tokens * p.chunks + kWarps - 1) / kWarps;
-  const dim3 grid(unsigned(blocks < (1 << 30) ? blocks : (1 << 30)));
   switch (a.head_dim) {
-    case 32: return launch_pdl(qk_norm_rope_kernel<E, 32>, grid, dim3(32 * kWarps), 0, stream, p);
-    case 64: return launch_pdl(qk_norm_rope_kernel<E, 64>, grid, dim3(32 * kWarps), 0, stream, p);
-    case 128: return launch_pdl(qk_norm_rope_kernel<E, 128>, grid, dim3(32 * kWarps), 0, stream, p);
-    case 256: return launch_pdl(qk_norm_rope_kernel<E, 256>, grid, dim3(32 * kWarps), 0, stream, p);
+    case 32: return launch_norm_rope_d<E, 32>(p, stream);
+    case 64: return launch_norm_rope_d<E, 64>(p, stream);
+    case 128: return launch_norm_rope_d<E, 128>(p, stream);
+    case 256: return launch_norm_rope_d<E, 256>(p, stream);
   }
   return cudaErrorInvalidValue;
 }
