@@ -5,8 +5,7 @@
 //
 // value = code * scale, one fp32 product, rounded once to the output type.
 // HBM-bound: per (row, KV head) 2 (D + D/8) bytes in, 2 D elements out.
-// A lane moves 16 channels (one 16-byte load of codes); kU rows' loads go out
-// before any is converted.
+// A lane moves 16 channels (one 16-byte load of codes).
 #include "nd_common.cuh"
 #include "nd_internal.h"
 
@@ -41,14 +40,18 @@ __device__ __forceinline__ void store16(float *dst, const uint4 &w, float s) {
                                                      float(int8_t(u[i] >> 16)) * s, float(int8_t(u[i] >> 24)) * s);
 }
 
-constexpr int kRowsPerCta = 8;
+constexpr int kTile = 16;  // output rows per CTA
 
-// grid (row blocks, B): (row, head, K or V) triples of kRowsPerCta output rows.
+// grid (row tiles, B).  A warp takes a (head, K or V) and up to kTile rows of
+// it: the slots of neighbouring rows are neighbours (but for the ring's wrap),
+// so its loads cover 2 KB of codes in one piece, all of them in flight before
+// the first is converted.
 template <typename E, int D>
 __global__ void __launch_bounds__(256) cache_read_kernel(const ReadParams p) {
-  constexpr int kLanes = D / 16, kU = 4;
+  constexpr int kLanes = D / 16, kRows = 32 / kLanes;              // rows per load of the warp
+  constexpr int kU = kTile / kRows < 8 ? kTile / kRows : 8, kGroup = kU * kRows;
   const nd_kv_cache &c = p.c;
-  const int b = blockIdx.y, row0 = blockIdx.x * kRowsPerCta;
+  const int b = blockIdx.y, row0 = blockIdx.x * kTile;
   const int Hkv = c.n_kv_heads, nslot = c.sink_cap + c.ring_cap;
   pdl_wait();
   const int sl = c.sink_len[b], rs = c.ring_start[b], rl = c.ring_len[b], sq = c.seq_len[b];
@@ -59,33 +62,37 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const ReadParams p) {
     if (!sane) raise_device_error(p.err, ND_DEVERR_METADATA);
     if (p.len) p.len[b] = live;
   }
-  if (p.pos && threadIdx.x < kRowsPerCta && row0 + threadIdx.x < p.n_rows) {
+  if (p.pos && threadIdx.x < kTile && row0 + threadIdx.x < p.n_rows) {
     const int r = row0 + threadIdx.x;
     p.pos[size_t(b) * p.n_rows + r] = r >= live ? -1 : (r < sl ? r : sq - n + (r - sl));
   }
-  const int sub = threadIdx.x / kLanes, ch = (threadIdx.x % kLanes) * 16, per = blockDim.x / kLanes;
-  const int rows = min(kRowsPerCta, live - row0), n_items = rows * Hkv * 2;  // none for a block behind the sequence
-  for (int t0 = sub; t0 < n_items; t0 += per * kU) {
+  if (row0 >= live) return;
+  int oldest = rs + rl - n;  // ring slot of the oldest visible entry
+  if (oldest >= c.ring_cap) oldest -= c.ring_cap;
+  const int lane = threadIdx.x & 31, sub = lane / kLanes, ch = (lane % kLanes) * 16;
+  const int rows = min(kTile, live - row0), groups = (rows + kGroup - 1) / kGroup;
+  for (int item = threadIdx.x >> 5; item < 2 * Hkv * groups; item += blockDim.x >> 5) {
+    const int group = item / (2 * Hkv), pair = item - group * 2 * Hkv, h = pair >> 1;
+    const int r0 = row0 + group * kGroup + sub;
+    const size_t base = (size_t(b) * Hkv + h) * nslot;
+    const int8_t *codes = ((pair & 1) ? c.v_codes : c.k_codes) + base * D + ch;
+    const float *scale = ((pair & 1) ? c.v_scale : c.k_scale) + base * (D / 32) + ch / 32;
     uint4 w[kU];
     float s[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const int t = t0 + u * per;
-      if (t >= n_items) continue;
-      const int r = row0 + t / (2 * Hkv), h = (t >> 1) % Hkv;
-      const int slot = r < sl ? r : c.sink_cap + (rs + rl - n + (r - sl)) % c.ring_cap;
-      const size_t row = (size_t(b) * Hkv + h) * nslot + slot;
-      w[u] = *reinterpret_cast<const uint4 *>(((t & 1) ? c.v_codes : c.k_codes) + row * D + ch);
-      s[u] = ((t & 1) ? c.v_scale : c.k_scale)[row * (D / 32) + ch / 32];
+      const int r = r0 + u * kRows;
+      if (r >= live) continue;
+      int ring = oldest + r - sl;
+      if (ring >= c.ring_cap) ring -= c.ring_cap;
+      const int slot = r < sl ? r : c.sink_cap + ring;
+      w[u] = *reinterpret_cast<const uint4 *>(codes + size_t(slot) * D);
+      s[u] = scale[size_t(slot) * (D / 32)];
     }
+    E *out = static_cast<E *>((pair & 1) ? p.v : p.k) + ((size_t(b) * p.n_rows + r0) * Hkv + h) * D + ch;
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int t = t0 + u * per;
-      if (t >= n_items) continue;
-      const int r = row0 + t / (2 * Hkv), h = (t >> 1) % Hkv;
-      E *out = static_cast<E *>((t & 1) ? p.v : p.k);
-      store16(out + ((size_t(b) * p.n_rows + r) * Hkv + h) * D + ch, w[u], s[u]);
-    }
+    for (int u = 0; u < kU; ++u)
+      if (r0 + u * kRows < live) store16(out + size_t(u * kRows) * Hkv * D, w[u], s[u]);
   }
 }
 
@@ -113,7 +120,7 @@ cudaError_t launch_cache_read(const nd_kv_cache &c, int window, bool f32, int n_
   p.pos = positions;
   p.len = lengths;
   p.err = err;
-  const dim3 grid(unsigned((n_rows + kRowsPerCta - 1) / kRowsPerCta), unsigned(c.batch));
+  const dim3 grid(unsigned((n_rows + kTile - 1) / kTile), unsigned(c.batch));
   return f32 ? launch_read_t<float>(p, grid, stream) : launch_read_t<uint16_t>(p, grid, stream);
 }
 

@@ -24,8 +24,6 @@
 
 #include <math.h>
 
-#include <atomic>
-
 namespace nd {
 
 namespace {
@@ -66,13 +64,24 @@ __device__ __forceinline__ float2 turn_cs(int pos, unsigned long long f) {
   return make_float2(c, s);
 }
 
-// Eight channels as loaded (bf16: one uint4, fp32: two) and as fp32.
-template <typename E>
+// Which channels lane j of a row's D / 16 lanes holds in each half: 16 bytes
+// at a time, neighbouring lanes side by side.  bf16: 8j .. 8j + 7; fp32: 4j ..
+// 4j + 3 and D/4 + 4j .. (eight in a row would leave every access half of its
+// sectors).  Element e is channel base + (e % kPiece) + (e / kPiece) * kStep.
+template <typename E, int D>
+struct Chan {
+  static constexpr int kPiece = 16 / sizeof(E), kStep = D / 16 * kPiece, kPieces = 8 / kPiece;
+  __device__ __forceinline__ static int base(int j) { return kPiece * j; }
+  __device__ __forceinline__ static int of(int j, int e) { return kPiece * j + e % kPiece + e / kPiece * kStep; }
+};
+
+// A lane's eight channels of one half as loaded, and as fp32.
+template <typename E, int D>
 struct Raw8 {
   uint4 w[sizeof(E) / 2];
-  __device__ __forceinline__ void load(const E *p) {
+  __device__ __forceinline__ void load(const E *p) {  // p: the half's channel Chan::base
 #pragma unroll
-    for (int i = 0; i < int(sizeof(E) / 2); ++i) w[i] = reinterpret_cast<const uint4 *>(p)[i];
+    for (int i = 0; i < int(sizeof(E) / 2); ++i) w[i] = *reinterpret_cast<const uint4 *>(p + i * Chan<E, D>::kStep);
   }
   __device__ __forceinline__ void get(float *x) const {
     if constexpr (sizeof(E) == 2) {
@@ -87,43 +96,51 @@ struct Raw8 {
     }
   }
 };
-template <typename E>
-__device__ __forceinline__ void ld8(const E *p, float *x) {
-  Raw8<E> r;
-  r.load(p);
-  r.get(x);
+// the weights (fp32) of the lane's channels of one half
+template <typename E, int D>
+__device__ __forceinline__ void load_weights(const float *p, float *x) {
+  constexpr int kStep = Chan<E, D>::kStep, kPiece = Chan<E, D>::kPiece;
+#pragma unroll
+  for (int e = 0; e < 8; e += 4) {
+    const float4 v = *reinterpret_cast<const float4 *>(p + e % kPiece + e / kPiece * kStep);
+    x[e] = v.x, x[e + 1] = v.y, x[e + 2] = v.z, x[e + 3] = v.w;
+  }
 }
-__device__ __forceinline__ void st8(uint16_t *p, const float *x) {
+template <int D>
+__device__ __forceinline__ void store_half(uint16_t *p, const float *x) {
   *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
                                              pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
 }
-__device__ __forceinline__ void st8(float *p, const float *x) {
-  reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-  reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+template <int D>
+__device__ __forceinline__ void store_half(float *p, const float *x) {
+  *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+  *reinterpret_cast<float4 *>(p + Chan<float, D>::kStep) = make_float4(x[4], x[5], x[6], x[7]);
 }
 
-// The eight angles of a lane's channel pairs i0 .. i0 + 7.  The lanes that hold
-// the same pairs of other rows make an eighth to a half of them each.
+// The CTA's copy of the frequencies: indexed by lane, kernel parameters are
+// read one address at a time.
 template <int D>
-__device__ __forceinline__ void lane_angles(int pos, const unsigned long long *f, int lane, float2 *cs) {
+__device__ __forceinline__ void stage_turns(const Turns &t, unsigned long long *s_f) {
+  for (int i = threadIdx.x; i < D / 2; i += blockDim.x) s_f[i] = t.f[i];
+  __syncthreads();
+}
+
+// The angles of a lane's eight channel pairs at the position that all rows of
+// the warp have.  The lanes that hold the same pairs of other rows make an
+// eighth to a half of them each.
+template <typename E, int D>
+__device__ __forceinline__ void shared_angles(int pos, const unsigned long long *s_f, int lane, float2 *cs) {
   constexpr int kLanes = D / 16, kRows = 32 / kLanes, kPer = kRows >= 8 ? 1 : 8 / kRows;
+  const int j = lane % kLanes, e0 = (lane / kLanes) * kPer % 8;
   float2 mine[kPer];
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) mine[j] = turn_cs(pos, f[j]);
+  for (int i = 0; i < kPer; ++i) mine[i] = turn_cs(pos, s_f[Chan<E, D>::of(j, e0 + i)]);
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const int src = (e / kPer) * kLanes + lane % kLanes;
+    const int src = (e / kPer) * kLanes + j;
     cs[e].x = __shfl_sync(0xffffffffu, mine[e % kPer].x, src);
     cs[e].y = __shfl_sync(0xffffffffu, mine[e % kPer].y, src);
   }
-}
-// the frequencies of the angles that this lane makes
-template <int D>
-__device__ __forceinline__ void lane_freqs(const Turns &t, int lane, unsigned long long *f) {
-  constexpr int kLanes = D / 16, kRows = 32 / kLanes, kPer = kRows >= 8 ? 1 : 8 / kRows;
-  const int i0 = 8 * (lane % kLanes), e0 = (lane / kLanes) * kPer % 8;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) f[j] = t.f[i0 + e0 + j];
 }
 
 // The row held by D/16 neighbouring lanes: this lane's lo (channels i0..i0+7)
@@ -167,114 +184,147 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
   return v;
 }
 
-// A warp takes tokens with the stride of the grid, each as batches of rows (kU
-// * 32 / (D / 16) heads of q, then of k).  HBM-bound: a row in and a row out;
-// what it needs is loads in flight, so each lane copies its own channels kSt -
-// 1 batches ahead into a ring in shared memory (its own slots: nothing to
-// exchange, no barrier), across the end of a token, while the angles -- once
-// per token for all its heads -- and the batches before are computed.
-// At 32768 tokens of 32 + 8 heads of 128 (671 MB): 133 us with plain loads
-// behind the angles, 120 with one batch ahead in registers.
+// Many heads: a warp takes a token, as batches of rows (kU * 32 / (D / 16)
+// heads of q, then of k).  HBM-bound: a row in and a row out; what it needs is
+// loads in flight, so each lane copies its own channels kSt - 1 batches ahead
+// into its own slots of shared memory (nothing to exchange, no barrier) while
+// the angles, once per token for all its heads, and the batches before are
+// computed.  One token to a warp: more, with the copies running on across
+// them, spread the accesses of the moment over more of memory (117 us at 13
+// tokens a warp).
+// At 32768 tokens of 32 + 8 heads of 128 (671 MB): 101 us, 6.65 TB/s; 133 us
+// with plain loads behind the angles, 120 with one batch ahead in registers.
 template <typename E, int D>
 struct NormLay {
   static constexpr int kLanes = D / 16, kRows = 32 / kLanes;
   static constexpr int kU = sizeof(E) == 2 ? 2 : 1, kBatch = kU * kRows;
-  static constexpr int kSt = 6, kStage = kU * kRows * D * int(sizeof(E));  // 2 KB
+  static constexpr int kSt = 4, kStage = kU * kRows * D * int(sizeof(E));  // 2 KB
   static constexpr int kWarps = 4, kBytes = kWarps * kSt * kStage;
 };
 
 template <typename E, int D>
-__global__ void __launch_bounds__(128, 4) qk_norm_rope_kernel(const __grid_constant__ NormRopeParams<E> p) {
+__global__ void __launch_bounds__(128, 4) qk_norm_token_kernel(const __grid_constant__ NormRopeParams<E> p) {
   using Y = NormLay<E, D>;
-  constexpr int kLanes = Y::kLanes, kRows = Y::kRows, kU = Y::kU, kSt = Y::kSt, kVec = sizeof(E) / 2;
-  extern __shared__ __align__(16) uint8_t smem[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, i0 = 8 * (lane % kLanes), sub = lane / kLanes;
+  using Ch = Chan<E, D>;
+  constexpr int kRows = Y::kRows, kU = Y::kU, kSt = Y::kSt, kVec = Ch::kPieces;
+  __shared__ __align__(16) uint8_t s_ring[Y::kBytes];
+  __shared__ unsigned long long s_f[D / 2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, i0 = Ch::base(lane % Y::kLanes), sub = lane / Y::kLanes;
   // a lane's slots: 16 bytes each, 512 apart
-  const uint32_t mine = smem_u32(smem) + warp * kSt * Y::kStage + lane * 16;
-  unsigned long long f[8];
-  lane_freqs<D>(p.turns, lane, f);
-  const int stride = gridDim.x * Y::kWarps;
+  const uint32_t mine = smem_u32(s_ring) + warp * kSt * Y::kStage + lane * 16;
+  const int tok = blockIdx.x * Y::kWarps + warp;
+  stage_turns<D>(p.turns, s_f);
   pdl_wait();
+  if (tok >= p.tokens) return;
 
-  // the copies' cursor: a token, q (0) or k (1), the batch's first head
-  int c_tok = blockIdx.x * Y::kWarps + warp, c_which = p.H[0] > 0 ? 0 : 1, c_h = 0, in = 0;
+  // the copies' cursor: q (0), k (1) or the end (2), and the batch's first head
+  int c_which = p.H[0] > 0 ? 0 : 1, c_h = 0, in = 0, out = 0;
   auto issue = [&]() {
-    if (c_tok < p.tokens) {
+    if (c_which < 2) {
       const int H = c_which ? p.H[1] : p.H[0];
-      const E *x = (c_which ? p.x[1] : p.x[0]) + c_tok * (c_which ? p.stride[1] : p.stride[0]) + i0;
+      const E *x = (c_which ? p.x[1] : p.x[0]) + tok * (c_which ? p.stride[1] : p.stride[0]) + i0;
       const uint32_t dst = mine + in * Y::kStage;
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
         const E *row = x + min(c_h + u * kRows + sub, H - 1) * D;  // past the end: the last head, not stored
 #pragma unroll
         for (int j = 0; j < kVec; ++j) {
-          copy16(dst + (u * 2 * kVec + j) * 512, row + j * (16 / sizeof(E)));
-          copy16(dst + (u * 2 * kVec + kVec + j) * 512, row + D / 2 + j * (16 / sizeof(E)));
+          copy16(dst + (u * 2 * kVec + j) * 512, row + j * Ch::kStep);
+          copy16(dst + (u * 2 * kVec + kVec + j) * 512, row + D / 2 + j * Ch::kStep);
         }
       }
       if (++in == kSt) in = 0;
       c_h += Y::kBatch;
-      if (c_h >= H) {
-        c_h = 0;
-        if (c_which == 0 && p.H[1] > 0) {
-          c_which = 1;
-        } else {
-          c_which = p.H[0] > 0 ? 0 : 1;
-          c_tok += stride;
-        }
-      }
+      if (c_h >= H) c_h = 0, c_which += c_which == 0 && p.H[1] == 0 ? 2 : 1;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll
   for (int i = 0; i < kSt - 1; ++i) issue();
 
-  int tok = blockIdx.x * Y::kWarps + warp, out = 0;
-  auto position = [&](int t) { return p.pos ? p.pos[t] : t % p.T; };
-  int pos = tok < p.tokens ? position(tok) : 0;
-  for (; tok < p.tokens; tok += stride) {
-    float2 cs[8];
-    lane_angles<D>(pos, f, lane, cs);
-    if (tok + stride < p.tokens) pos = position(tok + stride);
+  float2 cs[8];
+  shared_angles<E, D>(p.pos ? p.pos[tok] : tok % p.T, s_f, lane, cs);
 #pragma unroll 1
-    for (int which = 0; which < 2; ++which) {
-      const int H = which ? p.H[1] : p.H[0];
-      const float *w = which ? p.w[1] : p.w[0];
-      float wlo[8], whi[8];
-      if (w) {
-        ld8(w + i0, wlo);
-        ld8(w + D / 2 + i0, whi);
-      } else {
+  for (int which = 0; which < 2; ++which) {
+    const int H = which ? p.H[1] : p.H[0];
+    const float *w = which ? p.w[1] : p.w[0];
+    float wlo[8], whi[8];
+    if (w) {
+      load_weights<E, D>(w + i0, wlo);
+      load_weights<E, D>(w + D / 2 + i0, whi);
+    } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) wlo[e] = whi[e] = 1.f;
-      }
-      E *y = (which ? p.y[1] : p.y[0]) + int64_t(tok) * (H * D) + i0;
+      for (int e = 0; e < 8; ++e) wlo[e] = whi[e] = 1.f;
+    }
+    E *y = (which ? p.y[1] : p.y[0]) + int64_t(tok) * (H * D) + i0;
 #pragma unroll 1
-      for (int h0 = 0; h0 < H; h0 += Y::kBatch) {
-        issue();
-        asm volatile("cp.async.wait_group %0;" ::"n"(kSt - 1) : "memory");
-        const uint32_t src = mine + out * Y::kStage;
-        if (++out == kSt) out = 0;
+    for (int h0 = 0; h0 < H; h0 += Y::kBatch) {
+      issue();
+      asm volatile("cp.async.wait_group %0;" ::"n"(kSt - 1) : "memory");
+      const uint32_t src = mine + out * Y::kStage;
+      if (++out == kSt) out = 0;
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          Raw8<E> rlo, rhi;
+      for (int u = 0; u < kU; ++u) {
+        Raw8<E, D> rlo, rhi;
 #pragma unroll
-          for (int j = 0; j < kVec; ++j) {
-            rlo.w[j] = lds16(src + (u * 2 * kVec + j) * 512);
-            rhi.w[j] = lds16(src + (u * 2 * kVec + kVec + j) * 512);
-          }
-          float lo[8], hi[8];
-          rlo.get(lo);
-          rhi.get(hi);
-          norm_rotate<D>(lo, hi, wlo, whi, cs, p.eps);
-          const int h = h0 + u * kRows + sub;
-          if (h < H) {
-            st8(y + h * D, lo);
-            st8(y + h * D + D / 2, hi);
-          }
+        for (int j = 0; j < kVec; ++j) {
+          rlo.w[j] = lds16(src + (u * 2 * kVec + j) * 512);
+          rhi.w[j] = lds16(src + (u * 2 * kVec + kVec + j) * 512);
+        }
+        float lo[8], hi[8];
+        rlo.get(lo);
+        rhi.get(hi);
+        norm_rotate<D>(lo, hi, wlo, whi, cs, p.eps);
+        const int h = h0 + u * kRows + sub;
+        if (h < H) {
+          store_half<D>(y + h * D, lo);
+          store_half<D>(y + h * D + D / 2, hi);
         }
       }
     }
+  }
+}
+
+// Few heads: a token's rows would leave most of a warp's lanes idle and its
+// angles serve hardly any row, so the rows of all tokens lie in one line (of a
+// token q's heads, then k's) and every lane makes the angles of its own.
+template <typename E, int D>
+__global__ void __launch_bounds__(128) qk_norm_rows_kernel(const __grid_constant__ NormRopeParams<E> p) {
+  using Ch = Chan<E, D>;
+  constexpr int kLanes = D / 16, kRows = 32 / kLanes;
+  __shared__ unsigned long long s_f[D / 2];
+  const int lane = threadIdx.x & 31, j = lane % kLanes, i0 = Ch::base(j), H = p.H[0] + p.H[1];
+  stage_turns<D>(p.turns, s_f);
+  pdl_wait();
+  const unsigned n_rows = unsigned(p.tokens) * H;  // below 2^32: see the launch
+  const unsigned row = (blockIdx.x * 4u + (threadIdx.x >> 5)) * kRows + lane / kLanes, rr = min(row, n_rows - 1);
+  const int tok = int(rr / H), hh = int(rr % H);
+  const int which = hh >= p.H[0], h = which ? hh - p.H[0] : hh;
+  const E *x = (which ? p.x[1] : p.x[0]) + tok * (which ? p.stride[1] : p.stride[0]) + h * D + i0;
+  Raw8<E, D> rlo, rhi;
+  rlo.load(x);
+  rhi.load(x + D / 2);
+  const int pos = p.pos ? p.pos[tok] : tok % p.T;
+  const float *w = which ? p.w[1] : p.w[0];
+  float wlo[8], whi[8];
+  if (w) {
+    load_weights<E, D>(w + i0, wlo);
+    load_weights<E, D>(w + D / 2 + i0, whi);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) wlo[e] = whi[e] = 1.f;
+  }
+  float2 cs[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) cs[e] = turn_cs(pos, s_f[Ch::of(j, e)]);
+  float lo[8], hi[8];
+  rlo.get(lo);
+  rhi.get(hi);
+  norm_rotate<D>(lo, hi, wlo, whi, cs, p.eps);
+  if (row < n_rows) {
+    E *y = (which ? p.y[1] : p.y[0]) + (int64_t(tok) * (which ? p.H[1] : p.H[0]) + h) * D + i0;
+    store_half<D>(y, lo);
+    store_half<D>(y + D / 2, hi);
   }
 }
 
@@ -326,68 +376,86 @@ __device__ __forceinline__ void store_codes(const float *lo, const float *hi, in
 }
 
 // One CTA per sequence, D/16 lanes per row: the query heads, then K's, then
-// V's.  Every thread reads the sequence's four metadata words itself, beside
-// its row; the last thing the CTA does is advance them.
+// V's.  A step is a chain of latencies, so all loads go out at once: every
+// thread reads the sequence's four metadata words itself, beside its row and
+// weights; the last thing the CTA does is advance them.
 template <int D>
-__global__ void __launch_bounds__(512) qk_norm_append_kernel(const __grid_constant__ NormAppendParams p) {
+__global__ void __launch_bounds__(192, 4) qk_norm_append_kernel(const __grid_constant__ NormAppendParams p) {
   constexpr int kLanes = D / 16;
+  using Ch = Chan<uint16_t, D>;
   const nd_kv_cache &c = p.c;
-  const int b = blockIdx.x, i0 = 8 * (threadIdx.x % kLanes), per = blockDim.x / kLanes;
-  const int Hkv = c.n_kv_heads, nslot = c.sink_cap + c.ring_cap, n_rows = p.Hq + 2 * Hkv, lane = threadIdx.x & 31;
-  unsigned long long f[8];
-  lane_freqs<D>(p.turns, lane, f);
+  const int b = blockIdx.x, j = threadIdx.x % kLanes, i0 = Ch::base(j), per = blockDim.x / kLanes;
+  const int Hkv = c.n_kv_heads, n_rows = p.Hq + 2 * Hkv, lane = threadIdx.x & 31;
+  __shared__ unsigned long long s_f[D / 2];
+  stage_turns<D>(p.turns, s_f);
   pdl_wait();
+  Raw8<uint16_t, D> rlo, rhi;
+  auto load = [&](int r) {
+    const uint16_t *x = r < p.Hq         ? p.q + b * p.q_stride + r * D
+                        : r < p.Hq + Hkv ? p.k + b * p.k_stride + (r - p.Hq) * D
+                                         : p.v + b * p.v_stride + (r - p.Hq - Hkv) * D;
+    rlo.load(x + i0);
+    rhi.load(x + D / 2 + i0);
+  };
+  load(min(int(threadIdx.x) / kLanes, n_rows - 1));
   const int sl = c.sink_len[b], rs = c.ring_start[b], rl = c.ring_len[b], sq = c.seq_len[b];
   const int pos = sq + (p.pos_base ? *p.pos_base : 0);
   const bool sane = sl >= 0 && sl <= c.sink_cap && rl >= 0 && rl <= c.ring_cap && rs >= 0 &&
                     rs < (c.ring_cap > 0 ? c.ring_cap : 1);
   int slot = -1;
   if (sane) {
-    if (p.to_sink) slot = rl == 0 && sl < c.sink_cap ? sl : -1;
-    else if (c.ring_cap > 0) slot = c.sink_cap + (rl < c.ring_cap ? (rs + rl) % c.ring_cap : rs);
+    if (p.to_sink) {
+      slot = rl == 0 && sl < c.sink_cap ? sl : -1;
+    } else if (c.ring_cap > 0) {
+      int r = rl < c.ring_cap ? rs + rl : rs;
+      if (r >= c.ring_cap) r -= c.ring_cap;
+      slot = c.sink_cap + r;
+    }
   }
   if (slot < 0) {  // the same for the whole CTA
     if (threadIdx.x == 0) raise_device_error(p.err, ND_DEVERR_METADATA);
     return;
   }
   float2 cs[8];
-  lane_angles<D>(pos, f, lane, cs);
+  shared_angles<uint16_t, D>(pos, s_f, lane, cs);
   for (int r0 = 0; r0 < n_rows; r0 += per) {
-    const int r = r0 + threadIdx.x / kLanes, rr = min(r, n_rows - 1);
-    const bool live = r < n_rows;
-    const int kind = rr < p.Hq ? 0 : (rr < p.Hq + Hkv ? 1 : 2);  // q, k, v
-    const int h = rr - (kind == 0 ? 0 : (kind == 1 ? p.Hq : p.Hq + Hkv));
-    const uint16_t *x = kind == 0 ? p.q + b * p.q_stride : (kind == 1 ? p.k + b * p.k_stride : p.v + b * p.v_stride);
+    const int r = r0 + threadIdx.x / kLanes;
+    const bool live = r < n_rows, is_v = r >= p.Hq + Hkv;
+    if (r0 > 0) load(min(r, n_rows - 1));
     float lo[8], hi[8];
-    ld8(x + size_t(h) * D + i0, lo);
-    ld8(x + size_t(h) * D + D / 2 + i0, hi);
-    const float *w = kind == 0 ? p.wq : p.wk;
-    float wlo[8], whi[8];
-    if (w && kind < 2) {
-      ld8(w + i0, wlo);
-      ld8(w + D / 2 + i0, whi);
-    } else {
+    rlo.get(lo);
+    rhi.get(hi);
+    if (__any_sync(0xffffffffu, !is_v)) {  // (a warp may hold rows of K and of V)
+      const float *w = r < p.Hq ? p.wq : p.wk;
+      float wlo[8], whi[8];
+      if (w) {
+        load_weights<uint16_t, D>(w + i0, wlo);
+        load_weights<uint16_t, D>(w + D / 2 + i0, whi);
+      } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) wlo[e] = whi[e] = 1.f;
-    }
-    float zlo[8], zhi[8];
+        for (int e = 0; e < 8; ++e) wlo[e] = whi[e] = 1.f;
+      }
+      float zlo[8], zhi[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) zlo[e] = lo[e], zhi[e] = hi[e];
-    norm_rotate<D>(zlo, zhi, wlo, whi, cs, p.eps);
-    if (kind < 2) {
+      for (int e = 0; e < 8; ++e) zlo[e] = lo[e], zhi[e] = hi[e];
+      norm_rotate<D>(zlo, zhi, wlo, whi, cs, p.eps);
       // the key is rounded to bf16 before it is quantised, so a token that a
       // step appends has the codes of one that a prefill (which writes bf16
       // keys) and the handoff put there
 #pragma unroll
-      for (int e = 0; e < 8; ++e) lo[e] = round_bf16(zlo[e]), hi[e] = round_bf16(zhi[e]);
+      for (int e = 0; e < 8; ++e)
+        if (!is_v) lo[e] = round_bf16(zlo[e]), hi[e] = round_bf16(zhi[e]);
     }
-    const size_t row = (size_t(b) * Hkv + h) * nslot + slot;
-    store_codes<D>(lo, hi, i0, live && kind > 0, (kind == 2 ? c.v_codes : c.k_codes) + row * D,
-                   (kind == 2 ? c.v_scale : c.k_scale) + row * (D / 32));
-    if (live && kind == 0) {
-      uint16_t *y = p.q_out + (size_t(b) * p.Hq + h) * D + i0;
-      st8(y, lo);
-      st8(y + D / 2, hi);
+    if (__any_sync(0xffffffffu, live && r >= p.Hq)) {
+      const int h = is_v ? r - p.Hq - Hkv : r - p.Hq;
+      const size_t row = (size_t(b) * Hkv + h) * (c.sink_cap + c.ring_cap) + slot;
+      store_codes<D>(lo, hi, i0, live && r >= p.Hq, (is_v ? c.v_codes : c.k_codes) + row * D,
+                     (is_v ? c.v_scale : c.k_scale) + row * (D / 32));
+    }
+    if (r < p.Hq) {
+      uint16_t *y = p.q_out + (size_t(b) * p.Hq + r) * D + i0;
+      store_half<D>(y, lo);
+      store_half<D>(y + D / 2, hi);
     }
   }
   __syncthreads();  // every thread has read the metadata
@@ -399,22 +467,20 @@ __global__ void __launch_bounds__(512) qk_norm_append_kernel(const __grid_consta
   }
 }
 
+// A warp to a token where its heads fill two row sets (8 + 2 heads of 64, just
+// more than one: 33 us as rows, 34 as a token; 16 + 2: 56 against 37) and the
+// rows are many (40 heads of 128: 250 tokens 4.0 us as rows, 4.5 as tokens;
+// 400: 5.3 against 4.5).
+constexpr int kMinSets = 2, kFewSets = 2600;
 template <typename E, int D>
 cudaError_t launch_norm_rope_d(const NormRopeParams<E> &p, cudaStream_t stream) {
   using Y = NormLay<E, D>;
-  auto kern = qk_norm_rope_kernel<E, D>;
-  static std::atomic<unsigned long long> smem_set{0};  // the opt-in, once per device
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const unsigned long long bit = dev >= 0 && dev < 64 ? 1ull << dev : 0ull;
-  if (!bit || !(smem_set.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Y::kBytes);
-    if (e != cudaSuccess) return e;
-    smem_set.fetch_or(bit, std::memory_order_release);
-  }
-  const int blocks = (p.tokens + Y::kWarps - 1) / Y::kWarps, most = 152 * 4;
-  return launch_pdl(kern, dim3(unsigned(blocks < most ? blocks : most)), dim3(32 * Y::kWarps), size_t(Y::kBytes), stream, p);
+  const int64_t H = p.H[0] + p.H[1], rows = H * p.tokens;
+  if ((H >= kMinSets * Y::kRows && rows > kFewSets * Y::kRows) || rows >= (int64_t(1) << 32) - 4 * Y::kRows)
+    return launch_pdl(qk_norm_token_kernel<E, D>, dim3(unsigned((p.tokens + Y::kWarps - 1) / Y::kWarps)),
+                      dim3(32 * Y::kWarps), 0, stream, p);
+  return launch_pdl(qk_norm_rows_kernel<E, D>, dim3(unsigned((rows + 4 * Y::kRows - 1) / (4 * Y::kRows))), dim3(128), 0,
+                    stream, p);
 }
 
 template <typename E>
@@ -470,7 +536,9 @@ cudaError_t launch_qk_norm_append(const nd_kv_cache &c, const QkNormRope &a, con
   p.err = err;
   p.turns = make_turns(c.head_dim, a.theta);
   const int lanes = (a.Hq + 2 * c.n_kv_heads) * (c.head_dim / 16);
-  const int threads = lanes >= 512 ? 512 : (lanes + 31) / 32 * 32;
+  // (192 threads at most, four CTAs to an SM and the rows in passes: 512 tokens
+  // of 48 rows 6.5 us, against 9 with a thread group per row)
+  const int threads = lanes >= 192 ? 192 : (lanes + 31) / 32 * 32;
   const dim3 grid(c.batch), blk(threads);
   switch (c.head_dim) {
     case 32: return launch_pdl(qk_norm_append_kernel<32>, grid, blk, 0, stream, p);
