@@ -38,12 +38,15 @@
 //   warps 0-3, 4-7 : softmax of row block 0, 1 (thread = row = TMEM lane):
 //                    stage Q; per tile read S, write P over it; at a segment's
 //                    end read O and write the partials
+//                    (with up to 128 rows there is one block, and warps 4-7
+//                    turn codes)
 //   warps 8-9, 10-11 : codes of the staged tile -> fp16 K, V operands in shared
 //                    memory
 //   warp 12        : copies codes (bulk) and scales of the tiles ahead
 //   warp 15        : the staged tile's scales -> its exponents, fp16 scales
-//   warps 13, 14   : MMA issuer of row block 0, 1: S(g) = Q K(g)^T, then
-//                    O += P(g-1) V(g-1)
+//   warps 13, 14   : MMA issuers: S(g) = Q K(g)^T; O += P(g) V(g).  (One issuer
+//                    per block for both had to go through every wait of a tile
+//                    one after the other, 1100 cycles with all of them met.)
 // Every wait is bounded: one that gives up raises the device error flag and
 // the abort flag, and all roles leave through the common exit.
 #include <atomic>
@@ -61,7 +64,7 @@ namespace {
 constexpr int BM = kPrefixBlock;   // rows per block = TMEM lanes
 constexpr int BN = kPrefixTile;    // keys per tile
 constexpr int kThreads = 16 * 32;
-constexpr int kWarpDeq0 = 8, kDeqWarps = 4, kWarpLoad = 12, kWarpMma0 = 13, kWarpScan = 15;
+constexpr int kWarpDeq0 = 8, kWarpLoad = 12, kWarpS = 13, kWarpPV = 14, kWarpScan = 15;
 // Register split (setmaxnreg, per warpgroup) of the 128 a thread at launch:
 // the softmax holds a 64-score row per thread.  (Four more warps for the
 // conversion, on alternate tiles, measured slower -- 63 against 60 us at 4
@@ -73,7 +76,8 @@ constexpr float kLazyLog2 = 8.f;   // the maximum used may lag the true one by 2
 constexpr float kPBias = 7.f;      // P is scaled by 2^7
 constexpr int kInfo = 16;          // tile records in flight
 
-template <int D>
+// NB: row blocks a CTA holds
+template <int D, int NB>
 struct Lay {
   static constexpr int NG = D / 32;
   static constexpr int kBoxes = D / 64;
@@ -81,8 +85,8 @@ struct Lay {
   static constexpr int kKV = kBoxes * BN * 128;         // one K or V operand tile, fp16
   static constexpr int kCodes = BN * D, kScales = BN * NG * 4;
   static constexpr int kRaw = 2 * kCodes + 2 * kScales; // K codes, V codes, K scales, V scales
-  static constexpr int NK = D == 128 ? 2 : 3, NV = 3, NR = D == 128 ? 4 : 6;
-  static constexpr int oQ = 0, oK = 2 * kQ, oV = oK + NK * kKV, oR = oV + NV * kKV;
+  static constexpr int NK = D == 128 && NB == 2 ? 2 : 3, NV = 3, NR = D == 64 ? 6 : (NB == 2 ? 4 : 5);
+  static constexpr int oQ = 0, oK = NB * kQ, oV = oK + NK * kKV, oR = oV + NV * kKV;
   static constexpr int kBytes = oR + NR * kRaw + 1024;  // + alignment slack
   static_assert(kBytes <= 227 * 1024, "shared memory");
   static constexpr int NS = D == 64 ? 3 : 2;            // S buffers per block
@@ -182,9 +186,11 @@ __device__ __forceinline__ bool ring_wait(uint64_t *bar, uint32_t parity, int *e
   return __all_sync(0xffffffffu, ok);
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const PrefixParams p) {
-  using Y = Lay<D>;
+template <int D, int NB>
+__global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid_constant__ PrefixParams p) {
+  using Y = Lay<D, NB>;
+  // warps that turn codes: 8-11, with one row block also 4-7; half of them K, half V
+  constexpr int kTurn = NB == 2 ? 2 : 4, kTurnRows = BN / kTurn;
   constexpr int NK = Y::NK, NV = Y::NV, NR = Y::NR, NS = Y::NS, NG = Y::NG;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t raw_full[NR], raw_empty[NR], scan_full[NR], k_full[NK], k_empty[NK], v_full[NV], v_empty[NV],
@@ -193,7 +199,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Prefix
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be the same in the warp
   volatile int *abort_flag = &s_abort;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   auto sQ = [&](int rb) { return base + Y::oQ + rb * Y::kQ; };
@@ -204,16 +211,16 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Prefix
   if (tid == 0) {
     for (int s = 0; s < NR; ++s) {
       mbar_init(&raw_full[s], 33);          // the bulk copies' transaction and 32 lanes' scale copies
-      mbar_init(&raw_empty[s], 4 + 1);  // the four warps that turn the tile, and the scan
+      mbar_init(&raw_empty[s], 2 * kTurn + 1);  // the warps that turn the tile, and the scan
       mbar_init(&scan_full[s], 1);
     }
     for (int s = 0; s < NK; ++s) {
-      mbar_init(&k_full[s], 2);
-      mbar_init(&k_empty[s], 2);            // one arrival per row block
+      mbar_init(&k_full[s], kTurn);
+      mbar_init(&k_empty[s], 1);
     }
     for (int s = 0; s < NV; ++s) {
-      mbar_init(&v_full[s], 2);
-      mbar_init(&v_empty[s], 2);
+      mbar_init(&v_full[s], kTurn);
+      mbar_init(&v_empty[s], 1);
     }
     for (int r = 0; r < 2; ++r) {
       for (int u = 0; u < NS; ++u) {
@@ -226,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Prefix
     s_abort = 0;
     fence_barrier_init();
   }
-  if (warp == kWarpMma0) {
+  if (warp == kWarpS) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
                  "r"(Y::kTmemCols)
                  : "memory");
@@ -235,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Prefix
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
   pdl_wait();
   pdl_trigger();  // the own part reads nothing of this kernel's before it waits
   auto tS = [&](int rb, int buf) { return tmem + (NS * rb + buf) * BN; };
@@ -255,13 +262,13 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Prefix
     s.t0 = int(x - (long long)s.item * pl.nt);
     s.n = int(min((long long)(pl.nt - s.t0), x1 - x));
     s.hk = s.item / pl.pairs;
-    s.r0 = (s.item % pl.pairs) * 2 * BM;
-    s.nb = p.R - s.r0 > BM ? 2 : 1;
+    s.r0 = NB == 1 ? 0 : (s.item % pl.pairs) * 2 * BM;
+    s.nb = NB == 2 && p.R - s.r0 > BM ? 2 : 1;
     return s;
   };
   bool fail = false;
 
-  if (warp >= 8) {
+  if (warp >= 4 * NB) {
     regs_dec<kRegsOther>();
     if (warp == kWarpLoad) {
       // ------------------------------------------------ loader
@@ -306,13 +313,14 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Prefix
         }
         x += s.n;
       }
-    } else if (warp < kWarpDeq0 + kDeqWarps) {
+    } else if (warp < kWarpLoad) {
       // ------------------------------------------------ codes -> fp16 operands
-      // two warps turn K, two turn V, 32 rows each: neither operand waits
-      // behind the other's stages
-      const int half = warp & 1;
+      // half of the warps turn K, half V, so that neither operand waits behind
+      // the other's stages
+      const int row_w = ((warp & 1) + (warp < kWarpDeq0 ? 2 : 0)) * kTurnRows;  // the warp's first row
       const bool is_v = warp & 2;
-      constexpr int kPieces = D / 16, kRowsIt = 32 / kPieces, kIts = 32 / kRowsIt, kU = 2;
+      constexpr int kPieces = D / 16, kRowsIt = 32 / kPieces, kIts = kTurnRows / kRowsIt, kU = 2;
+      static_assert(kIts % kU == 0, "rows of a warp");
       const int piece = lane % kPieces, row_l = lane / kPieces;
       // K-major (and for V MN-major) 128-byte swizzle: row * 128 + 16-byte
       // chunk ^ (row & 7) inside a box of 64 channels; a lane's two chunks.
@@ -322,9 +330,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Prefix
       const uint32_t odd_first = box == 1 ? 1u : 0u;
       uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
       const int n_st = is_v ? NV : NK;
-      const uint32_t codes_off = (is_v ? Y::kCodes : 0) + (32 * half + row_l) * D + piece * 16 + 8 * odd_first;
-      const uint32_t scale_off = 2 * Y::kCodes + (is_v ? Y::kScales : 0) + 4 * ((32 * half + row_l) * NG + piece / 2);
-      const uint32_t row_off = (is_v ? sV(0) : sK(0)) + (32 * half + row_l) * 128 + box * (BN * 128);
+      const uint32_t codes_off = (is_v ? Y::kCodes : 0) + (row_w + row_l) * D + piece * 16 + 8 * odd_first;
+      const uint32_t scale_off = 2 * Y::kCodes + (is_v ? Y::kScales : 0) + 4 * ((row_w + row_l) * NG + piece / 2);
+      const uint32_t row_off = (is_v ? sV(0) : sK(0)) + (row_w + row_l) * 128 + box * (BN * 128);
       // a lane's rows are kRowsIt (4 or 8) apart: the swizzle of the second of
       // a pair differs from the first's in one bit at most
       const uint32_t first_c = ((c0 + odd_first) ^ (row_l & 7)) << 4;  // and the other chunk: ^ 16
@@ -445,76 +453,91 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Prefix
         }
         x += s.n;
       }
-    } else if (warp == kWarpMma0 || warp == kWarpMma0 + 1) {
-      // ------------------------------------------------ MMA issuers, one per block
-      const int rb = warp - kWarpMma0;
+    } else if (warp == kWarpS) {
+      // ------------------------------------------------ S(g) = Q K(g)^T of every block
       const uint32_t leader = elect_one();
       constexpr uint32_t kIdS = idesc_f16(BM, BN, 0);
-      constexpr uint32_t kIdPV = idesc_f16(BM, D, 1);
       Ring<NK> kr;
-      Ring<NV> vr;
-      Ring<NS> sr, pr;  // S buffers by the order of S and of PV
-      uint32_t q_phase = 0;
-      // descriptors of the first stage's first 16 channels (or keys)
-      const uint64_t dq = sdesc_sw128(sQ(rb), 16, 1024), dk = sdesc_sw128(sK(0), 16, 1024),
-                     dv = sdesc_sw128(sV(0), BN * 128, 1024);
+      Ring<NS> sr[NB];  // a buffer is free once PV has read the P in it
+      uint32_t q_phase[NB];
+#pragma unroll
+      for (int rb = 0; rb < NB; ++rb) sr[rb].phase = 1, q_phase[rb] = 0;
+      // descriptors of the first stage's first 16 channels
+      const uint64_t dq = sdesc_sw128(sQ(0), 16, 1024), dk = sdesc_sw128(sK(0), 16, 1024);
       for (long long x = x0; x < x1 && !fail;) {
         const Seg s = seg_at(x);
         x += s.n;
-        if (rb >= s.nb) {
-          // no rows: only the hand-back of the operand stages
-#pragma unroll 1
-          for (int j = 0; j < s.n && !fail; ++j, kr.next(), vr.next()) {
-            fail = !ring_wait(&k_full[kr.i], kr.phase, p.err, abort_flag) ||
-                   !ring_wait(&v_full[vr.i], vr.phase, p.err, abort_flag);
-            if (lane == 0 && !fail) {
-              mbar_arrive(&k_empty[kr.i]);
-              mbar_arrive(&v_empty[vr.i]);
-            }
-            __syncwarp();
+#pragma unroll
+        for (int rb = 0; rb < NB; ++rb)
+          if (rb < s.nb && !fail) {
+            fail = !ring_wait(&q_full[rb], q_phase[rb], p.err, abort_flag);
+            q_phase[rb] ^= 1u;
           }
-          continue;
-        }
-        fail = !ring_wait(&q_full[rb], q_phase, p.err, abort_flag);
-        q_phase ^= 1u;
-        // step j: S(j), then PV(j - 1).  S(j) goes over the P that PV(j - NS)
-        // read: this thread issued that product earlier, and one thread's MMAs
-        // run in order
 #pragma unroll 1
-        for (int j = 0; j <= s.n && !fail; ++j) {
-          if (j < s.n) {
-            if (!ring_wait(&k_full[kr.i], kr.phase, p.err, abort_flag)) {
+        for (int j = 0; j < s.n && !fail; ++j) {
+          if (!ring_wait(&k_full[kr.i], kr.phase, p.err, abort_flag)) {
+            fail = true;
+            break;
+          }
+          const uint64_t kd = dk + uint64_t(kr.i * (Y::kKV >> 4));
+#pragma unroll
+          for (int rb = 0; rb < NB; ++rb) {
+            if (rb >= s.nb) break;
+            const int u = sr[rb].i;
+            if (!ring_wait(&pv_done[rb][u], sr[rb].phase, p.err, abort_flag)) {
               fail = true;
               break;
             }
             tc_fence_after();
-            const uint64_t kd = dk + uint64_t(kr.i * (Y::kKV >> 4));
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
-              mma_ss(tS(rb, sr.i), dq + (kk >> 2) * (BM * 128 >> 4) + (kk & 3) * 2,
+              mma_ss(tS(rb, u), dq + rb * (Y::kQ >> 4) + (kk >> 2) * (BM * 128 >> 4) + (kk & 3) * 2,
                      kd + (kk >> 2) * (BN * 128 >> 4) + (kk & 3) * 2, kIdS, kk > 0 ? 1u : 0u, leader);
-            mma_commit(&s_full[rb][sr.i], leader);
-            mma_commit(&k_empty[kr.i], leader);
-            kr.next();
-            sr.next();
+            mma_commit(&s_full[rb][u], leader);
+            sr[rb].next();
           }
-          if (j > 0) {
-            if (!ring_wait(&p_full[rb][pr.i], pr.phase, p.err, abort_flag) ||
-                !ring_wait(&v_full[vr.i], vr.phase, p.err, abort_flag)) {
+          if (fail) break;
+          mma_commit(&k_empty[kr.i], leader);
+          kr.next();
+        }
+      }
+    } else if (warp == kWarpPV) {
+      // ------------------------------------------------ O += P(g) V(g) of every block
+      // (a segment's first product overwrites O: its P exists only once the
+      // block's softmax warps have read the segment before out of it)
+      const uint32_t leader = elect_one();
+      constexpr uint32_t kIdPV = idesc_f16(BM, D, 1);
+      Ring<NV> vr;
+      Ring<NS> pr[NB];
+      const uint64_t dv = sdesc_sw128(sV(0), BN * 128, 1024);
+      for (long long x = x0; x < x1 && !fail;) {
+        const Seg s = seg_at(x);
+        x += s.n;
+#pragma unroll 1
+        for (int j = 0; j < s.n && !fail; ++j) {
+          if (!ring_wait(&v_full[vr.i], vr.phase, p.err, abort_flag)) {
+            fail = true;
+            break;
+          }
+          const uint64_t vd = dv + uint64_t(vr.i * (Y::kKV >> 4));
+#pragma unroll
+          for (int rb = 0; rb < NB; ++rb) {
+            if (rb >= s.nb) break;
+            const int u = pr[rb].i;
+            if (!ring_wait(&p_full[rb][u], pr[rb].phase, p.err, abort_flag)) {
               fail = true;
               break;
             }
             tc_fence_after();
-            const uint64_t vd = dv + uint64_t(vr.i * (Y::kKV >> 4));
 #pragma unroll
             for (int kk = 0; kk < BN / 16; ++kk)  // 16 keys = 8 TMEM columns of fp16 pairs
-              mma_ts(tO(rb), tS(rb, pr.i) + kk * 8, vd + kk * (16 * 128 >> 4), kIdPV, (j > 1 || kk > 0) ? 1u : 0u,
-                     leader);
-            mma_commit(&pv_done[rb][pr.i], leader);
-            mma_commit(&v_empty[vr.i], leader);
-            vr.next();
-            pr.next();
+              mma_ts(tO(rb), tS(rb, u) + kk * 8, vd + kk * (16 * 128 >> 4), kIdPV, (j > 0 || kk > 0) ? 1u : 0u, leader);
+            mma_commit(&pv_done[rb][u], leader);
+            pr[rb].next();
           }
+          if (fail) break;
+          mma_commit(&v_empty[vr.i], leader);
+          vr.next();
         }
       }
     }
@@ -704,26 +727,26 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const Prefix
   if (__syncthreads_or(fail || *abort_flag))
     for (int i = 0; i < 2000; ++i) __nanosleep(1000);
   __syncthreads();
-  if (warp == kWarpMma0) {
+  if (warp == kWarpS) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(Y::kTmemCols) : "memory");
   }
 }
 
-template <int D>
+template <int D, int NB>
 cudaError_t launch_d(const PrefixParams &p, int grid, cudaStream_t stream) {
-  auto kern = shared_prefix_kernel<D>;
+  auto kern = shared_prefix_kernel<D, NB>;
   static std::atomic<unsigned long long> smem_set{0};  // the opt-in, once per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const unsigned long long bit = dev >= 0 && dev < 64 ? 1ull << dev : 0ull;
   if (!bit || !(smem_set.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::kBytes);
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D, NB>::kBytes);
     if (e != cudaSuccess) return e;
     smem_set.fetch_or(bit, std::memory_order_release);
   }
-  return launch_pdl(kern, dim3(grid), dim3(kThreads), size_t(Lay<D>::kBytes), stream, p);
+  return launch_pdl(kern, dim3(grid), dim3(kThreads), size_t(Lay<D, NB>::kBytes), stream, p);
 }
 
 }  // namespace
@@ -740,8 +763,9 @@ cudaError_t launch_shared_prefix(const void *q, const nd_kv_cache &prefix, int b
   p.out = out;
   p.err = err;
   const int grid = prefix_grid(prefix.sink_cap, prefix.n_kv_heads, p.R);
-  if (prefix.head_dim == 128) return launch_d<128>(p, grid, stream);
-  if (prefix.head_dim == 64) return launch_d<64>(p, grid, stream);
+  const bool one = p.R <= BM;
+  if (prefix.head_dim == 128) return one ? launch_d<128, 1>(p, grid, stream) : launch_d<128, 2>(p, grid, stream);
+  if (prefix.head_dim == 64) return one ? launch_d<64, 1>(p, grid, stream) : launch_d<64, 2>(p, grid, stream);
   return cudaErrorInvalidValue;
 }
 
