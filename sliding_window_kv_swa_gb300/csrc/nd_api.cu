@@ -841,7 +841,11 @@ int nd_shared_prefix_decode(const void *q, const nd_kv_cache *prefix, const nd_k
       prefix->head_dim != cache->head_dim)
     return ND_ERR_INVALID_ARG;
   if (cache->batch == 0) return ND_OK;
-  if (int64_t(cache->batch) * n_q_heads > (1 << 24)) return ND_ERR_UNSUPPORTED;
+  // (rows of a KV head stay below 2^24, key tiles of all row pairs below 2^30)
+  const int64_t rows = int64_t(cache->batch) * (n_q_heads / cache->n_kv_heads);
+  if (int64_t(cache->batch) * n_q_heads > (1 << 24) ||
+      (int64_t(prefix->sink_cap) / 64 + 1) * (rows / 256 + 1) * cache->n_kv_heads >= (1 << 30))
+    return ND_ERR_UNSUPPORTED;
   const size_t need = nd_shared_prefix_decode_workspace_size(cache->batch, n_q_heads, cache->n_kv_heads, cache->head_dim,
                                                              prefix->sink_cap, cache->sink_cap + cache->ring_cap);
   if (need && (!workspace || workspace_bytes < need || !aligned16(workspace))) return ND_ERR_WORKSPACE;

@@ -45,6 +45,7 @@ struct OwnParams {
   float *lse;
   float *ws_ml, *ws_o; // n_split > 1: [pair][n_split][G][2], [..][G][D]
   PrefixParts parts;   // the prefix's partials, when prefix_grid > 0
+  int streams;         // prefix_streams
   int prefix_grid;
   bool early;          // the kernel before this one is the call's own prefix kernel: see shared_own_kernel
   int *err;
@@ -272,13 +273,13 @@ __device__ __forceinline__ void store_state(RunState<D> &r, int lane, float *o, 
 }
 
 // ------------------------------------------------------------------ merging
-// The prefix's partials of one row of a KV head: n of them, in adjacent slots.
+// The prefix's partials of one row of a KV head: n of them, evenly spaced (a
+// slot apart, or half a slot with two streams).
 struct RowParts {
   const float2 *ml;
   const float *o;
   int n;
 };
-constexpr size_t kMlStep = 2 * kPrefixBlock;  // from one slot's (max, sum) to the next one's
 
 template <int D>
 __device__ __forceinline__ RowParts row_parts(const OwnParams &p, const PrefixPlan &pl, int hkv, int row) {
@@ -288,7 +289,7 @@ __device__ __forceinline__ RowParts row_parts(const OwnParams &p, const PrefixPl
   const size_t at = (size_t(c0) + item) * 2 + rr / kPrefixBlock;
   r.ml = p.parts.ml + at * kPrefixBlock + rr % kPrefixBlock;
   r.o = p.parts.o + (at * (D / 4) * kPrefixBlock + rr % kPrefixBlock) * 4;
-  r.n = c1 - c0 + 1;
+  r.n = (c1 - c0 + 1) * p.streams;
   return r;
 }
 
@@ -347,7 +348,8 @@ template <int D, int kUnroll>
 __device__ __forceinline__ void add_parts(const OwnParams &p, const PrefixPlan &pl, int b, int hkv, int h0, int first,
                                           int step, int lane, LaneState<D / 32> (&st)[kHeads]) {
   constexpr int C = D / 32;
-  constexpr size_t kOStep = size_t(D) * 2 * kPrefixBlock;
+  const int ml_step = 2 * kPrefixBlock / p.streams;
+  const size_t o_step = size_t(D) * ml_step;
   const size_t lane_off = size_t(C * lane / 4) * kPrefixBlock * 4 + (C * lane) % 4;
   RowParts rp[kHeads];
   int n = 0;
@@ -374,12 +376,17 @@ __device__ __forceinline__ void add_parts(const OwnParams &p, const PrefixPlan &
 #pragma unroll
       for (int e = 0; e < C; ++e) x[i][e] = 0.f;
       if (s < rp[i].n) {
-        ml[i] = rp[i].ml[s * kMlStep];
-        load_c<C>(rp[i].o + lane_off + s * kOStep, x[i]);
+        ml[i] = rp[i].ml[s * ml_step];
+        load_c<C>(rp[i].o + lane_off + s * o_step, x[i]);
       }
     }
 #pragma unroll
-    for (int i = 0; i < kHeads; ++i) st[i].add(ml[i].x, ml[i].y, x[i]);
+    for (int i = 0; i < kHeads; ++i) {
+      // (a stream without a tile wrote no O)
+#pragma unroll
+      for (int e = 0; e < C; ++e) x[i][e] = ml[i].x == -INFINITY ? 0.f : x[i][e];
+      st[i].add(ml[i].x, ml[i].y, x[i]);
+    }
   }
 }
 
@@ -784,6 +791,7 @@ cudaError_t launch_shared_decode(const void *q, const nd_kv_cache &prefix, const
   p.err = err;
   p.parts = {nullptr, nullptr};
   p.prefix_grid = 0;
+  p.streams = prefix_streams(rows);
   // (at D = 64 an odd number of slots needs copies that go through L1)
   p.early = !s.inline_prefix && (d == 128 || (c.sink_cap + c.ring_cap) % 2 == 0);
   float *w = static_cast<float *>(ws);

@@ -38,8 +38,7 @@
 //   warps 0-3, 4-7 : softmax of row block 0, 1 (thread = row = TMEM lane):
 //                    stage Q; per tile read S, write P over it; at a segment's
 //                    end read O and write the partials
-//                    (with up to 128 rows there is one block, and warps 4-7
-//                    turn codes)
+//                    (fewer rows: see Mode)
 //   warps 8-9, 10-11 : codes of the staged tile -> fp16 K, V operands in shared
 //                    memory
 //   warp 12        : copies codes (bulk) and scales of the tiles ahead
@@ -76,23 +75,38 @@ constexpr float kLazyLog2 = 8.f;   // the maximum used may lag the true one by 2
 constexpr float kPBias = 7.f;      // P is scaled by 2^7
 constexpr int kInfo = 16;          // tile records in flight
 
-// NB: row blocks a CTA holds
-template <int D, int NB>
+// What a CTA's two softmax warpgroups hold:
+//   kPair    two row blocks (more than 128 rows)
+//   kSingle  one row block; the other warpgroup turns codes
+//   kStreams one half block (up to 64 rows) twice: the warpgroups take every
+//            other key tile each, with sums and an O of their own, so a tile
+//            has two tiles' time for the latencies of its softmax, which
+//            bound a single warp; the four idle warps turn codes
+enum Mode { kPair, kSingle, kStreams };
+
+template <int D, Mode M>
 struct Lay {
+  static constexpr int NB = M == kSingle ? 1 : 2;       // S and O sets
   static constexpr int NG = D / 32;
   static constexpr int kBoxes = D / 64;
-  static constexpr int kQ = kBoxes * BM * 128;          // one block's Q, fp16
+  // Q, fp16: rows staged per set, and from one 64-channel box to the next.  (A
+  // half block's MMA also reads the rows behind it, whatever they are, into
+  // rows of S that nobody reads.)
+  static constexpr int kQRows = M == kStreams ? 64 : BM;
+  static constexpr int kQBox = kQRows * 128, kQ = kBoxes * kQBox;
   static constexpr int kKV = kBoxes * BN * 128;         // one K or V operand tile, fp16
   static constexpr int kCodes = BN * D, kScales = BN * NG * 4;
   static constexpr int kRaw = 2 * kCodes + 2 * kScales; // K codes, V codes, K scales, V scales
-  static constexpr int NK = D == 128 && NB == 2 ? 2 : 3, NV = 3, NR = D == 64 ? 6 : (NB == 2 ? 4 : 5);
+  static constexpr int NK = D == 128 && M == kPair ? 2 : 3, NV = 3, NR = D == 64 ? 6 : (M == kPair ? 4 : 5);
   static constexpr int oQ = 0, oK = NB * kQ, oV = oK + NK * kKV, oR = oV + NV * kKV;
   static constexpr int kBytes = oR + NR * kRaw + 1024;  // + alignment slack
   static_assert(kBytes <= 227 * 1024, "shared memory");
-  static constexpr int NS = D == 64 ? 3 : 2;            // S buffers per block
+  static constexpr int NS = D == 64 ? 3 : 2;            // S buffers per set
   static constexpr int cO = 2 * NS * BN;                // TMEM columns: S[2][NS], O[2]
   static constexpr int kTmemCols = 512;
   static_assert(cO + 2 * D <= kTmemCols, "TMEM");
+  static constexpr int kSoft = M == kStreams ? 2 : 4;   // softmax warps per set
+  static constexpr int kTurn = M == kPair ? 2 : 4;      // warps that turn K, and V
 };
 
 struct PrefixParams {
@@ -186,11 +200,10 @@ __device__ __forceinline__ bool ring_wait(uint64_t *bar, uint32_t parity, int *e
   return __all_sync(0xffffffffu, ok);
 }
 
-template <int D, int NB>
+template <int D, Mode M>
 __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid_constant__ PrefixParams p) {
-  using Y = Lay<D, NB>;
-  // warps that turn codes: 8-11, with one row block also 4-7; half of them K, half V
-  constexpr int kTurn = NB == 2 ? 2 : 4, kTurnRows = BN / kTurn;
+  using Y = Lay<D, M>;
+  constexpr int NB = Y::NB, kTurn = Y::kTurn, kTurnRows = BN / kTurn;
   constexpr int NK = Y::NK, NV = Y::NV, NR = Y::NR, NS = Y::NS, NG = Y::NG;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t raw_full[NR], raw_empty[NR], scan_full[NR], k_full[NK], k_empty[NK], v_full[NV], v_empty[NV],
@@ -225,10 +238,10 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
     for (int r = 0; r < 2; ++r) {
       for (int u = 0; u < NS; ++u) {
         mbar_init(&s_full[r][u], 1);
-        mbar_init(&p_full[r][u], 4);
+        mbar_init(&p_full[r][u], Y::kSoft);
         mbar_init(&pv_done[r][u], 1);
       }
-      mbar_init(&q_full[r], 4);
+      mbar_init(&q_full[r], Y::kSoft);
     }
     s_abort = 0;
     fence_barrier_init();
@@ -252,31 +265,33 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
   const PrefixPlan pl = prefix_plan(p.c.sink_len[0], p.c.sink_cap, p.c.n_kv_heads, p.R, gridDim.x);
   if (!pl.sane && blockIdx.x == 0 && tid == 0) raise_device_error(p.err, ND_DEVERR_METADATA);
   const bool has_work = int(blockIdx.x) < pl.ctas;
-  const long long x0 = has_work ? pl.start(blockIdx.x) : 0, x1 = has_work ? pl.start(blockIdx.x + 1) : 0;
+  const int x0 = has_work ? pl.start(blockIdx.x) : 0, x1 = has_work ? pl.start(blockIdx.x + 1) : 0;
   struct Seg {
-    int item, t0, n, hk, r0, nb;
+    int item, t0, n, hk, r0, nb;  // nb: sets at work
   };
-  auto seg_at = [&](long long x) {
+  auto seg_at = [&](int x) {
     Seg s;
-    s.item = int(x / pl.nt);
-    s.t0 = int(x - (long long)s.item * pl.nt);
-    s.n = int(min((long long)(pl.nt - s.t0), x1 - x));
+    s.item = x / pl.nt;
+    s.t0 = x - s.item * pl.nt;
+    s.n = min(pl.nt - s.t0, x1 - x);
     s.hk = s.item / pl.pairs;
-    s.r0 = NB == 1 ? 0 : (s.item % pl.pairs) * 2 * BM;
-    s.nb = NB == 2 && p.R - s.r0 > BM ? 2 : 1;
+    s.r0 = M == kPair ? (s.item % pl.pairs) * 2 * BM : 0;
+    s.nb = M == kSingle ? 1 : M == kStreams ? min(s.n, 2) : p.R - s.r0 > BM ? 2 : 1;
     return s;
   };
   bool fail = false;
 
-  if (warp >= 4 * NB) {
-    regs_dec<kRegsOther>();
+  const bool soft = warp < 4 * NB && (warp & 3) < Y::kSoft;
+  if (warp < 4 * NB) regs_inc<kRegsSoftmax>();
+  else regs_dec<kRegsOther>();
+  if (!soft) {
     if (warp == kWarpLoad) {
       // ------------------------------------------------ loader
       const uint32_t leader = elect_one();
       const size_t nslot = size_t(p.c.sink_cap) + p.c.ring_cap;
       Ring<NR> raw;
       raw.phase = 1;  // the first round of an empty ring does not wait
-      for (long long x = x0; x < x1 && !fail;) {
+      for (int x = x0; x < x1 && !fail;) {
         const Seg s = seg_at(x);
         const size_t slot0 = s.hk * nslot + size_t(s.t0) * BN;
         const int8_t *kc = p.c.k_codes + slot0 * D, *vc = p.c.v_codes + slot0 * D;
@@ -317,8 +332,11 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
       // ------------------------------------------------ codes -> fp16 operands
       // half of the warps turn K, half V, so that neither operand waits behind
       // the other's stages
-      const int row_w = ((warp & 1) + (warp < kWarpDeq0 ? 2 : 0)) * kTurnRows;  // the warp's first row
-      const bool is_v = warp & 2;
+      // (warps 8-11; with one block also 4-7, with two streams 2, 3, 6 and 7)
+      const int turn = M == kStreams ? (warp < kWarpDeq0 ? (warp & 1) + (warp >> 2) * 2 : warp - 4)
+                                     : warp - (M == kSingle ? 4 : kWarpDeq0);
+      const int row_w = (turn >> 1) * kTurnRows;  // the warp's first row
+      const bool is_v = turn & 1;
       constexpr int kPieces = D / 16, kRowsIt = 32 / kPieces, kIts = kTurnRows / kRowsIt, kU = 2;
       static_assert(kIts % kU == 0, "rows of a warp");
       const int piece = lane % kPieces, row_l = lane / kPieces;
@@ -339,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
       Ring<NR> raw;
       int so = 0;
       uint32_t so_phase = 1;
-      for (long long x = x0; x < x1 && !fail;) {
+      for (int x = x0; x < x1 && !fail;) {
         const Seg s = seg_at(x);
 #pragma unroll 1
         for (int j = 0; j < s.n; ++j, raw.next()) {
@@ -395,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
       // fp16 pairs that multiply the codes, in place
       Ring<NR> raw;
       int g = 0;
-      for (long long x = x0; x < x1 && !fail;) {
+      for (int x = x0; x < x1 && !fail;) {
         const Seg s = seg_at(x);
         int e_v = INT_MAX;  // the exponent that V's operands have in O (unset)
         int left = pl.len - s.t0 * BN;
@@ -418,11 +436,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
             km = fmaxf(km, fabsf(ksc[i]));
             vm = fmaxf(vm, fabsf(vsc[i]));
           }
-#pragma unroll
-          for (int off = 16; off >= 1; off >>= 1) {
-            km = fmaxf(km, __shfl_xor_sync(0xffffffffu, km, off));
-            vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, off));
-          }
+          // (of values >= 0 the bits order as the values do)
+          km = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(km)));
+          vm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vm)));
           // |code * scale| < 2^(ilog2 + 8): K below 2^15, V first below 2^12
           const int e_k = clamp_exp(7 - ilog2(km));
           float fix = 1.f;
@@ -464,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
       for (int rb = 0; rb < NB; ++rb) sr[rb].phase = 1, q_phase[rb] = 0;
       // descriptors of the first stage's first 16 channels
       const uint64_t dq = sdesc_sw128(sQ(0), 16, 1024), dk = sdesc_sw128(sK(0), 16, 1024);
-      for (long long x = x0; x < x1 && !fail;) {
+      for (int x = x0; x < x1 && !fail;) {
         const Seg s = seg_at(x);
         x += s.n;
 #pragma unroll
@@ -482,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
           const uint64_t kd = dk + uint64_t(kr.i * (Y::kKV >> 4));
 #pragma unroll
           for (int rb = 0; rb < NB; ++rb) {
-            if (rb >= s.nb) break;
+            if (M == kStreams ? (j & 1) != rb : rb >= s.nb) continue;
             const int u = sr[rb].i;
             if (!ring_wait(&pv_done[rb][u], sr[rb].phase, p.err, abort_flag)) {
               fail = true;
@@ -491,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
             tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
-              mma_ss(tS(rb, u), dq + rb * (Y::kQ >> 4) + (kk >> 2) * (BM * 128 >> 4) + (kk & 3) * 2,
+              mma_ss(tS(rb, u), dq + rb * (Y::kQ >> 4) + (kk >> 2) * (Y::kQBox >> 4) + (kk & 3) * 2,
                      kd + (kk >> 2) * (BN * 128 >> 4) + (kk & 3) * 2, kIdS, kk > 0 ? 1u : 0u, leader);
             mma_commit(&s_full[rb][u], leader);
             sr[rb].next();
@@ -510,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
       Ring<NV> vr;
       Ring<NS> pr[NB];
       const uint64_t dv = sdesc_sw128(sV(0), BN * 128, 1024);
-      for (long long x = x0; x < x1 && !fail;) {
+      for (int x = x0; x < x1 && !fail;) {
         const Seg s = seg_at(x);
         x += s.n;
 #pragma unroll 1
@@ -522,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
           const uint64_t vd = dv + uint64_t(vr.i * (Y::kKV >> 4));
 #pragma unroll
           for (int rb = 0; rb < NB; ++rb) {
-            if (rb >= s.nb) break;
+            if (M == kStreams ? (j & 1) != rb : rb >= s.nb) continue;
             const int u = pr[rb].i;
             if (!ring_wait(&p_full[rb][u], pr[rb].phase, p.err, abort_flag)) {
               fail = true;
@@ -531,7 +547,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
             tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < BN / 16; ++kk)  // 16 keys = 8 TMEM columns of fp16 pairs
-              mma_ts(tO(rb), tS(rb, u) + kk * 8, vd + kk * (16 * 128 >> 4), kIdPV, (j > 0 || kk > 0) ? 1u : 0u, leader);
+              mma_ts(tO(rb), tS(rb, u) + kk * 8, vd + kk * (16 * 128 >> 4), kIdPV,
+                     (j >= (M == kStreams ? 2 : 1) || kk > 0) ? 1u : 0u, leader);
             mma_commit(&pv_done[rb][u], leader);
             pr[rb].next();
           }
@@ -542,23 +559,25 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
       }
     }
   } else {
-    // ------------------------------------------------ softmax warpgroups
-    regs_inc<kRegsSoftmax>();
+    // ------------------------------------------------ softmax warps
     const int rb = warp >> 2, r = tid & (BM - 1);
     const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
     int g = 0;
     Ring<NS> sr;
-    for (long long x = x0; x < x1 && !fail;) {
+    for (int x = x0; x < x1 && !fail;) {
       const Seg s = seg_at(x);
       x += s.n;
       if (rb >= s.nb) {
+        // a stream without a tile: its partials count nothing
+        if (M == kStreams && r < p.R)
+          p.out.ml[((size_t(blockIdx.x) + s.item) * 2 + rb) * BM + r] = make_float2(-INFINITY, 0.f);
         g += s.n;
         continue;
       }
-      const int row = s.r0 + rb * BM + r;
+      const int row0 = M == kPair ? s.r0 + rb * BM : 0, row = row0 + r;
       // a warp none of whose rows exists keeps the handshakes only; its part
       // of P is whatever TMEM holds, which reaches no other row
-      const bool active = s.r0 + rb * BM + (warp & 3) * 32 < p.R;
+      const bool active = row0 + (warp & 3) * 32 < p.R;
       float c_row = 0.f;
       if (active) {
         // Q: the warp's 32 rows as fp16 times 2^eq of the row, D / 8 lanes to
@@ -568,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
         // warp waited for them before it read O.
         constexpr int kL = D / 8, kRows = 32 / kL, kIt = 32 / kRows;
         const int sub = lane / kL, ch = lane % kL;
-        const int first = s.r0 + rb * BM + (warp & 3) * 32 + sub;  // and every kRows-th row after it
+        const int first = row0 + (warp & 3) * 32 + sub;  // and every kRows-th row after it
         // (a rolled loop, the next four rows' loads ahead of it: the code runs
         // once, and unrolled it would wait for its own instructions)
         auto load_rows = [&](int i0, uint4 (&w)[4]) {
@@ -603,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
 #pragma unroll
             for (int e = 0; e < 4; ++e) h[e] = pack_half2(bf16_lo(u[e]) * up, bf16_hi(u[e]) * up);
             const int rw = (warp & 3) * 32 + sub + (i0 + i) * kRows;  // in the block
-            st_shared_v4(sQ(rb) + (ch / 8) * (BM * 128) + rw * 128 + (((ch & 7) ^ (rw & 7)) << 4), h[0], h[1], h[2],
+            st_shared_v4(sQ(rb) + (ch / 8) * Y::kQBox + rw * 128 + (((ch & 7) ^ (rw & 7)) << 4), h[0], h[1], h[2],
                          h[3]);
             // lane l is row l of the warp: its exponent sits in the lanes of sub l % kRows
             const int e_l = __shfl_sync(0xffffffffu, eq, (lane % kRows) * kL);
@@ -617,11 +636,13 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
       if (lane == 0) mbar_arrive(&q_full[rb]);
 
       float m_used = -INFINITY, l = 0.f, down = 1.f;
-      int left = pl.len - s.t0 * BN;
+      constexpr int kEvery = M == kStreams ? 2 : 1;  // the set's tiles: every one, or every other
+      const int j0 = M == kStreams ? rb : 0;
+      int left = pl.len - (s.t0 + j0) * BN;
       uint64_t *pv_last = nullptr;  // PV of the tile before: its barrier and parity
       uint32_t pv_phase = 0;
 #pragma unroll 1
-      for (int j = 0; j < s.n; ++j, ++g, sr.next(), left -= BN) {
+      for (int j = j0; j < s.n; j += kEvery, sr.next(), left -= kEvery * BN) {
         const int u = sr.i;
         if (!fail) fail = !ring_wait(&s_full[rb][u], sr.phase, p.err, abort_flag);
         tc_fence_after();
@@ -633,7 +654,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
           if (lane == 0) mbar_arrive(&p_full[rb][u]);
           continue;
         }
-        const float4 info = s_info[g % kInfo];
+        float4 info = s_info[(g + j) % kInfo];
+        // the tile in between may have changed V's exponent too
+        if (M == kStreams && j >= 2) info.y *= s_info[(g + j - 1) % kInfo].y;
         uint32_t v[BN];
         tmem_ld32(tS(rb, u) + lane_base, v);
         tmem_ld32(tS(rb, u) + lane_base + 32, v + 32);
@@ -676,8 +699,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
           v[i / 2] = pack_half2(a, b);
         }
         l += (rsp[0] + rsp[1]) + (rsp[2] + rsp[3]);
-        if (j >= 1 && __any_sync(0xffffffffu, alpha != 1.f)) {
-          // O once PV(j-1) has landed
+        if (j >= kEvery && __any_sync(0xffffffffu, alpha != 1.f)) {
+          // O once the set's PV before has landed
           if (!fail) fail = !ring_wait(pv_prev, pv_prev_phase, p.err, abort_flag);
           tc_fence_after();
 #pragma unroll 1
@@ -696,6 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[rb][u]);
       }
+      g += s.n;
       // ---- the segment's partials
       if (!fail) fail = !ring_wait(pv_last, pv_phase, p.err, abort_flag);
       tc_fence_after();
@@ -733,20 +757,26 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
   }
 }
 
-template <int D, int NB>
-cudaError_t launch_d(const PrefixParams &p, int grid, cudaStream_t stream) {
-  auto kern = shared_prefix_kernel<D, NB>;
+template <int D, Mode M>
+cudaError_t launch_m(const PrefixParams &p, int grid, cudaStream_t stream) {
+  auto kern = shared_prefix_kernel<D, M>;
   static std::atomic<unsigned long long> smem_set{0};  // the opt-in, once per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const unsigned long long bit = dev >= 0 && dev < 64 ? 1ull << dev : 0ull;
   if (!bit || !(smem_set.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D, NB>::kBytes);
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D, M>::kBytes);
     if (e != cudaSuccess) return e;
     smem_set.fetch_or(bit, std::memory_order_release);
   }
-  return launch_pdl(kern, dim3(grid), dim3(kThreads), size_t(Lay<D, NB>::kBytes), stream, p);
+  return launch_pdl(kern, dim3(grid), dim3(kThreads), size_t(Lay<D, M>::kBytes), stream, p);
+}
+
+template <int D>
+cudaError_t launch_d(const PrefixParams &p, int grid, cudaStream_t stream) {
+  if (prefix_streams(p.R) == 2) return launch_m<D, kStreams>(p, grid, stream);
+  return p.R <= BM ? launch_m<D, kSingle>(p, grid, stream) : launch_m<D, kPair>(p, grid, stream);
 }
 
 }  // namespace
@@ -763,9 +793,8 @@ cudaError_t launch_shared_prefix(const void *q, const nd_kv_cache &prefix, int b
   p.out = out;
   p.err = err;
   const int grid = prefix_grid(prefix.sink_cap, prefix.n_kv_heads, p.R);
-  const bool one = p.R <= BM;
-  if (prefix.head_dim == 128) return one ? launch_d<128, 1>(p, grid, stream) : launch_d<128, 2>(p, grid, stream);
-  if (prefix.head_dim == 64) return one ? launch_d<64, 1>(p, grid, stream) : launch_d<64, 2>(p, grid, stream);
+  if (prefix.head_dim == 128) return launch_d<128>(p, grid, stream);
+  if (prefix.head_dim == 64) return launch_d<64>(p, grid, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -147,12 +147,13 @@ def test_slots_that_are_not_visible_may_hold_anything():
 
 
 @pytest.mark.parametrize("Hq,Hkv,d", [(8, 2, 64), (8, 2, 128)])
+@pytest.mark.parametrize("B", [3, 20, 70])   # rows of a KV head: up to 64, up to 128, more
 @pytest.mark.parametrize("kind", ["large", "tiny", "mixed", "rising", "zero_v"])
-def test_scales_of_any_size(Hq, Hkv, d, kind):
+def test_scales_of_any_size(Hq, Hkv, d, kind, B):
     """The power-of-two scaling of keys and values follows the data: large and tiny tokens, magnitudes that differ by
     2^40 within the prefix, values that grow along it, all-zero values."""
     rng = philox(10400 + d)
-    B, L, W = 20, 330, 16
+    L, W = 330, 16
     prefix = random_cache(rng, 1, Hkv, d, L, 0, [(L, 0)])
     own = random_cache(rng, B, Hkv, d, 0, W)
     kmul, vmul = np.ones(L), np.ones(L)
@@ -183,8 +184,8 @@ def test_scales_of_any_size(Hq, Hkv, d, kind):
 def test_scores_that_grow_along_the_prefix():
     """The running maximum moves by far more than a lazy rescale allows, in both directions."""
     rng = philox(10500)
-    Hq, Hkv, d, B, L = 8, 2, 64, 18, 400
-    for order in (1, -1):
+    Hq, Hkv, d, L = 8, 2, 64, 400
+    for order, B in ((1, 18), (-1, 18), (1, 4), (-1, 4), (1, 40), (-1, 40)):
         prefix = random_cache(rng, 1, Hkv, d, L, 0, [(L, 0)])
         ramp = np.linspace(0.01, 8.0, L)[::order]
         prefix.k_scale *= ramp[None, None, :, None].astype(np.float32)
