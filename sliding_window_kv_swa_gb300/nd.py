@@ -474,29 +474,41 @@ def nd_kv_cache_read(cache: KVCache, window: int, dtype: torch.dtype = torch.bfl
     sink_cap + min(ring_cap, window) unless k_out has more.  Rows from
     lengths[b] on keep what k_out / v_out held (nothing in particular when they
     are made here); their positions are -1."""
-    dev = _here(cache.k_codes)
-    B, Hkv, _, d = cache.k_codes.shape
+    codes = cache.k_codes
+    dev = _here(codes)
+    B, Hkv, _, d = codes.shape
     if k_out is None:
-        rows = cache.sink_cap + min(cache.ring_cap, window)
         if window < 1:
             raise ValueError("window must be at least 1")
-        k_out = torch.empty((B, rows, Hkv, d), dtype=dtype, device=cache.k_codes.device)
-    elif k_out.dim() != 4:
-        raise ValueError("k_out must have shape [B, rows, Hkv, d]")
-    rows = k_out.shape[1]
-    dtype = k_out.dtype
-    code = ND_BF16 if dtype == torch.bfloat16 else _dtype_code(k_out)
-    shape = (B, rows, Hkv, d)
+        rows = cache.sink_cap + min(cache.ring_cap, window)
+        shape = (B, rows, Hkv, d)
+        k_out = torch.empty(shape, dtype=dtype, device=codes.device)
+        at_k = k_out.data_ptr()
+    else:
+        if k_out.dim() != 4:
+            raise ValueError("k_out must have shape [B, rows, Hkv, d]")
+        rows = k_out.shape[1]
+        dtype = k_out.dtype
+        shape = (B, rows, Hkv, d)
+        at_k = _addr(k_out, "k_out", shape, dtype, dev)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=dtype, device=k_out.device)
+        v_out = torch.empty_like(k_out)
+        at_v = v_out.data_ptr()
+    else:
+        at_v = _addr(v_out, "v_out", shape, dtype, dev)
     if positions is None:
-        positions = torch.empty((B, rows), dtype=torch.int32, device=k_out.device)
+        positions = torch.empty((B, rows), dtype=torch.int32, device=codes.device)
+        at_p = positions.data_ptr()
+    else:
+        at_p = _addr(positions, "positions", (B, rows), torch.int32, dev)
     if lengths is None:
-        lengths = torch.empty((B,), dtype=torch.int32, device=k_out.device)
+        lengths = torch.empty((B,), dtype=torch.int32, device=codes.device)
+        at_n = lengths.data_ptr()
+    else:
+        at_n = _addr(lengths, "lengths", (B,), torch.int32, dev)
+    code = ND_BF16 if dtype == torch.bfloat16 else _dtype_code(k_out)
     _check("nd_kv_cache_read", _lib().nd_kv_cache_read(
-        cache.struct_ref(), window, code, rows, _addr(k_out, "k_out", shape, dtype, dev),
-        _addr(v_out, "v_out", shape, dtype, dev), _addr(positions, "positions", (B, rows), torch.int32, dev),
-        _addr(lengths, "lengths", (B,), torch.int32, dev), _stream(stream)))
+        cache.struct_ref(), window, code, rows, at_k, at_v, at_p, at_n, _stream(stream)))
     return k_out, v_out, positions, lengths
 
 
@@ -517,8 +529,12 @@ def nd_shared_prefix_decode(q: torch.Tensor, prefix: KVCache, cache: KVCache, wi
     k = cache.k_codes
     if k.shape[0] != B or k.shape[3] != d or k.get_device() != dev or prefix.k_codes.get_device() != dev:
         raise ValueError("q and the caches must agree on batch, head_dim and device")
+    at_q = _addr(q, "q", shape, torch.bfloat16, dev)
     if out is None:
         out = torch.empty_like(q)
+        at_out = out.data_ptr()
+    else:
+        at_out = _addr(out, "out", shape, torch.bfloat16, dev)
     if workspace is None:
         nbytes = nd_shared_prefix_decode_workspace_size(B, Hq, k.shape[1], d, prefix.sink_cap,
                                                         cache.sink_cap + cache.ring_cap)
@@ -526,8 +542,7 @@ def nd_shared_prefix_decode(q: torch.Tensor, prefix: KVCache, cache: KVCache, wi
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
     _check("nd_shared_prefix_decode", _lib().nd_shared_prefix_decode(
-        _addr(q, "q", shape, torch.bfloat16, dev), prefix.struct_ref(), cache.struct_ref(), Hq, window,
-        _addr(out, "out", shape, torch.bfloat16, dev),
+        at_q, prefix.struct_ref(), cache.struct_ref(), Hq, window, at_out,
         None if lse is None else _addr(lse, "lse", (B, Hq), torch.float32, dev),
         workspace.data_ptr(), workspace.nbytes, _stream(stream)))
     return out
@@ -559,9 +574,11 @@ def nd_qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], q_weig
         if len(shape) != 4 or shape[0] != B or shape[1] != T or shape[3] != d or t.dtype != dtype or \
                 t.get_device() != dev:
             raise ValueError(f"{name} must have shape [{B}, {T}, heads, {d}], q's type and device")
+        step = _step(t, name)
         if out is None:
             out = torch.empty(shape, dtype=dtype, device=t.device)
-        return shape[2], _step(t, name), t.data_ptr(), _addr(out, name + "_out", shape, dtype, dev), out
+            return shape[2], step, t.data_ptr(), out.data_ptr(), out
+        return shape[2], step, t.data_ptr(), _addr(out, name + "_out", shape, dtype, dev), out
 
     Hq, sq, pq, oq, q_out = side(q, q_out, "q")
     Hk, sk, pk, ok, k_out = side(k, k_out, "k")
@@ -592,6 +609,9 @@ def nd_qk_norm_rope_append(q: torch.Tensor, cache: KVCache, k_new: torch.Tensor,
                          "cache's device")
     if q_out is None:
         q_out = torch.empty(shape, dtype=bf16, device=q.device)
+        at_out = q_out.data_ptr()
+    else:
+        at_out = _addr(q_out, "q_out", shape, bf16, dev)
     base = None
     if pos_base is not None:
         if pos_base.numel() != 1 or pos_base.dtype != torch.int32 or pos_base.get_device() != dev:
@@ -601,7 +621,7 @@ def nd_qk_norm_rope_append(q: torch.Tensor, cache: KVCache, k_new: torch.Tensor,
         q.data_ptr(), cache.struct_ref(), k_new.data_ptr(), v_new.data_ptr(), shape[1], _step(q, "q"),
         _step(k_new, "k_new"), _step(v_new, "v_new"), _weight(q_weight, "q_weight", d, dev),
         _weight(k_weight, "k_weight", d, dev), eps, rope_theta, base, 1 if to_sink else 0,
-        _addr(q_out, "q_out", shape, bf16, dev), _stream(stream)))
+        at_out, _stream(stream)))
     return q_out
 
 
