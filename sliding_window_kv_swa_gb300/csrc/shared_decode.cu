@@ -288,7 +288,7 @@ __device__ __forceinline__ RowParts row_parts(const OwnParams &p, const PrefixPl
   const int c0 = pl.first_cta(item), c1 = pl.last_cta(item);
   const size_t at = (size_t(c0) + item) * 2 + rr / kPrefixBlock;
   r.ml = p.parts.ml + at * kPrefixBlock + rr % kPrefixBlock;
-  r.o = p.parts.o + (at * (D / 4) * kPrefixBlock + rr % kPrefixBlock) * 4;
+  r.o = p.parts.o + (at * kPrefixBlock + rr % kPrefixBlock / 4 * 4) * D + rr % 4 * 4;
   r.n = (c1 - c0 + 1) * p.streams;
   return r;
 }
@@ -324,11 +324,6 @@ struct LaneState {
     m = s[8 * D + h];
     l = s[8 * D + 8 + h];
   }
-  __device__ __forceinline__ void write(float *s, int h, int lane) const {
-    constexpr int D = 32 * C;
-    store_c<C>(s + h * D + C * lane, o);
-    if (lane == 0) s[8 * D + h] = m, s[8 * D + 8 + h] = l;
-  }
   __device__ __forceinline__ void add(float m2, float l2, const float *o2) {
     const float mn = fmaxf(m, m2), base = mn == -INFINITY ? 0.f : mn;
     const float f1 = ex2(m - base), f2 = ex2(m2 - base);
@@ -339,54 +334,74 @@ struct LaneState {
   }
 };
 
-// Adds partials first, first + step, .. of each of a pair's heads h0 .. h0 + 3
-// to that head's state.  The four heads' loads go out together: neighbouring
-// rows share their sectors.  Lane l holds channels C*l .. (C = D / 32): in a
-// partial's [D/4][128][4] layout, C floats of group C*l/4.
+// Four rows' softmax states across a warp, as a partial's layout has them: lane
+// l holds channels 4 (l/4 + 8i) .. + 3 of row l % 4.
 constexpr int kHeads = 4;
-template <int D, int kUnroll>
-__device__ __forceinline__ void add_parts(const OwnParams &p, const PrefixPlan &pl, int b, int hkv, int h0, int first,
-                                          int step, int lane, LaneState<D / 32> (&st)[kHeads]) {
-  constexpr int C = D / 32;
+template <int D>
+struct RowState {
+  static constexpr int I = D / 32;
+  float m = -INFINITY, l = 0.f, o[I][4];
+  __device__ __forceinline__ RowState() {
+#pragma unroll
+    for (int i = 0; i < I; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+  }
+  __device__ __forceinline__ static int channel(int lane, int i) { return 4 * (lane / 4 + 8 * i); }
+  // a warp's state in shared memory: O [8][D], max [8], sum [8]
+  __device__ __forceinline__ void read(const float *s, int h, int lane) {
+#pragma unroll
+    for (int i = 0; i < I; ++i) load_c<4>(s + h * D + channel(lane, i), o[i]);
+    m = s[8 * D + h];
+    l = s[8 * D + 8 + h];
+  }
+  __device__ __forceinline__ void write(float *s, int h, int lane) const {
+#pragma unroll
+    for (int i = 0; i < I; ++i) store_c<4>(s + h * D + channel(lane, i), o[i]);
+    if (lane < 4) s[8 * D + h] = m, s[8 * D + 8 + h] = l;
+  }
+  __device__ __forceinline__ void add(float m2, float l2, const float (&o2)[I][4]) {
+    const float mn = fmaxf(m, m2), base = mn == -INFINITY ? 0.f : mn;
+    const float f1 = ex2(m - base), f2 = ex2(m2 - base);
+    l = l * f1 + l2 * f2;
+#pragma unroll
+    for (int i = 0; i < I; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][e] = o[i][e] * f1 + o2[i][e] * f2;
+    m = mn;
+  }
+  __device__ __forceinline__ void write_out(const OwnParams &p, size_t row, int lane) const {
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+    for (int i = 0; i < I; ++i)
+      *reinterpret_cast<uint2 *>(p.out + row * D + channel(lane, i)) =
+          make_uint2(pack_bf16x2(o[i][0] * inv, o[i][1] * inv), pack_bf16x2(o[i][2] * inv, o[i][3] * inv));
+    if (lane < 4 && p.lse) p.lse[row] = l > 0.f ? (m + __log2f(l)) * 0.6931471805599453f : -INFINITY;
+  }
+};
+
+// Adds partials first, first + step, .. of the lane's row (a KV head's row) to
+// its state.
+template <int D>
+__device__ __forceinline__ void add_parts(const OwnParams &p, const PrefixPlan &pl, int hkv, int row, int first,
+                                          int step, int lane, RowState<D> &st) {
+  constexpr int I = D / 32;
   const int ml_step = 2 * kPrefixBlock / p.streams;
   const size_t o_step = size_t(D) * ml_step;
-  const size_t lane_off = size_t(C * lane / 4) * kPrefixBlock * 4 + (C * lane) % 4;
-  RowParts rp[kHeads];
-  int n = 0;
+  const RowParts rp = row_parts<D>(p, pl, hkv, row);
+  const float *o = rp.o + lane / 4 * 16;
+#pragma unroll 3
+  for (int s = first; s < rp.n; s += step) {
+    const float2 ml = rp.ml[s * ml_step];
+    float x[I][4];
 #pragma unroll
-  for (int i = 0; i < kHeads; ++i) {
-    const int row = b * p.G + h0 + i;
-    if (h0 + i >= p.G) {
-      rp[i] = rp[0];
-      rp[i].n = 0;
-    } else if (i == 0 || row % kPrefixBlock == 0) {
-      rp[i] = row_parts<D>(p, pl, hkv, row);
-    } else {
-      rp[i] = {rp[i - 1].ml + 1, rp[i - 1].o + 4, rp[i - 1].n};
-    }
-    n = max(n, rp[i].n);
-  }
-#pragma unroll kUnroll
-  for (int s = first; s < n; s += step) {
-    float2 ml[kHeads];
-    float x[kHeads][C];
+    for (int i = 0; i < I; ++i) load_c<4>(o + s * o_step + i * 128, x[i]);
+    // (a stream without a tile wrote no O)
 #pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
-      ml[i] = make_float2(-INFINITY, 0.f);
+    for (int i = 0; i < I; ++i)
 #pragma unroll
-      for (int e = 0; e < C; ++e) x[i][e] = 0.f;
-      if (s < rp[i].n) {
-        ml[i] = rp[i].ml[s * ml_step];
-        load_c<C>(rp[i].o + lane_off + s * o_step, x[i]);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
-      // (a stream without a tile wrote no O)
-#pragma unroll
-      for (int e = 0; e < C; ++e) x[i][e] = ml[i].x == -INFINITY ? 0.f : x[i][e];
-      st[i].add(ml[i].x, ml[i].y, x[i]);
-    }
+      for (int e = 0; e < 4; ++e) x[i][e] = ml.x == -INFINITY ? 0.f : x[i][e];
+    st.add(ml.x, ml.y, x);
   }
 }
 
@@ -612,18 +627,13 @@ __global__ void __launch_bounds__(NW * 32, kCtas) shared_own_kernel(const __grid
       if (!waited) pdl_wait();
       waited = true;
       for (int h0 = 0; h0 < G; h0 += kHeads) {
-        LaneState<C> st[kHeads];
-#pragma unroll
-        for (int i = 0; i < kHeads; ++i)
-          if (h0 + i < G) st[i].read(state, h0 + i, lane);
-        if (pl.nt > 0)
-          add_parts<D, 2>(p, pl, b, hkv, h0, un.solo ? 0 : warp, un.solo ? 1 : NW, lane, st);
-#pragma unroll
-        for (int i = 0; i < kHeads; ++i)
-          if (h0 + i < G) {
-            if (un.solo) write_out<C>(p, size_t(b) * p.Hq + hkv * G + h0 + i, lane, st[i]);
-            else st[i].write(state, h0 + i, lane);
-          }
+        const int h = h0 + lane % kHeads;
+        if (h >= G) continue;
+        RowState<D> st;
+        st.read(state, h, lane);
+        if (pl.nt > 0) add_parts<D>(p, pl, hkv, b * G + h, un.solo ? 0 : warp, un.solo ? 1 : NW, lane, st);
+        if (un.solo) st.write_out(p, size_t(b) * p.Hq + hkv * G + h, lane);
+        else st.write(state, h, lane);
       }
     }
     if (un.solo) {
@@ -676,25 +686,23 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __
   if (p.prefix_grid > 0)
     pl = prefix_plan(p.pre.sink_len[0], p.pre.sink_cap, Hkv, p.c.batch * G, p.prefix_grid);
   for (int h0 = 0; h0 < G; h0 += kHeads) {
-    LaneState<C> st[kHeads];
+    const int h = h0 + lane % kHeads;
+    if (h >= G) continue;
+    RowState<D> st;
+    for (int s = warp; s < p.n_split; s += kMergeWarps) {
+      const size_t part = (size_t(pair) * p.n_split + s) * G + h;
+      float x[C][4];
 #pragma unroll
-    for (int i = 0; i < kHeads; ++i)
-      for (int s = warp; s < p.n_split && h0 + i < G; s += kMergeWarps) {
-        const size_t part = (size_t(pair) * p.n_split + s) * G + h0 + i;
-        float x[C];
-        load_c<C>(p.ws_o + part * D + C * lane, x);
-        st[i].add(p.ws_ml[2 * part], p.ws_ml[2 * part + 1], x);
-      }
+      for (int i = 0; i < C; ++i) load_c<4>(p.ws_o + part * D + RowState<D>::channel(lane, i), x[i]);
+      st.add(p.ws_ml[2 * part], p.ws_ml[2 * part + 1], x);
+    }
     // (the first partials go to the warps that the parts left out)
     if (pl.nt > 0)
-      add_parts<D, 2>(p, pl, b, hkv, h0, (warp + kMergeWarps - p.n_split % kMergeWarps) % kMergeWarps, kMergeWarps, lane,
+      add_parts<D>(p, pl, hkv, b * G + h, (warp + kMergeWarps - p.n_split % kMergeWarps) % kMergeWarps, kMergeWarps, lane,
                    st);
 #pragma unroll
-    for (int i = 0; i < kHeads; ++i)
-      if (h0 + i < G) {
-        store_c<C>(&s_o[h0 + i][warp][C * lane], st[i].o);
-        if (lane == 0) s_ml[h0 + i][warp][0] = st[i].m, s_ml[h0 + i][warp][1] = st[i].l;
-      }
+    for (int i = 0; i < C; ++i) store_c<4>(&s_o[h][warp][RowState<D>::channel(lane, i)], st.o[i]);
+    if (lane < 4) s_ml[h][warp][0] = st.m, s_ml[h][warp][1] = st.l;
   }
   __syncthreads();
   for (int h = warp; h < G; h += kMergeWarps) {

@@ -725,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
       tc_fence_after();
       if (active && !fail) {
         const size_t slot = size_t(blockIdx.x) + s.item;
-        float4 *o = reinterpret_cast<float4 *>(p.out.o) + (slot * 2 + rb) * (D / 4) * BM + r;
+        float4 *o = reinterpret_cast<float4 *>(p.out.o) + (slot * 2 + rb) * (D / 4) * BM + r / 4 * D + r % 4;
 #pragma unroll 1
         for (int ch = 0; ch < D; ch += 32) {
           uint32_t ov[32];
@@ -734,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
           if (row < p.R) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
-              o[size_t(ch + i) / 4 * BM] =
+              o[ch + i] =
                   make_float4(__uint_as_float(ov[i]) * down, __uint_as_float(ov[i + 1]) * down,
                               __uint_as_float(ov[i + 2]) * down, __uint_as_float(ov[i + 3]) * down);
           }

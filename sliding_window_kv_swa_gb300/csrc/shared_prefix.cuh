@@ -20,8 +20,12 @@ constexpr int kPrefixMinTiles = 2; // fewest tiles worth a CTA
 // softmax warps, and each half has partials of its own.
 __host__ __device__ inline int prefix_streams(int rows) { return rows <= kPrefixBlock / 2 ? 2 : 1; }
 
-// Partials: slot s holds a row pair's O [2][D/4][128][4] and (max, sum)
+// Partials: slot s holds a row pair's O [2][32][D/4][4 rows][4] and (max, sum)
 // [2][128], maxima in log2 units; with two streams, theirs of the one block.
+// (The prefix kernel has a row per thread and stores four channels of 32 rows
+// at once, the merge reads all channels of the four heads of a group: in this
+// order both touch whole sectors.  With O [D/4][128][4] the merge's loads went
+// to 32 lines each.)
 struct PrefixParts {
   float *o;
   float2 *ml;
