@@ -551,7 +551,11 @@ __global__ void __launch_bounds__(NW * 32, kCtas) shared_own_kernel(const __grid
   if (!kInline && p.prefix_grid > 0)
     pl = prefix_plan(__ldcg(p.pre.sink_len), p.pre.sink_cap, Hkv, c.batch * G, p.prefix_grid);
 
-  // A unit's query and metadata are loaded while the unit before it is merged.
+  // A unit's query and metadata are loaded while the unit before it is walked,
+  // or where that costs the walk registers it lacks or a launch is one unit
+  // per warp, while it is merged (512 sequences at D = 128: 81.4 us against
+  // 83.5; 64 at D = 64: 13.7 against 13.4).
+  constexpr bool kEarly = D == 128 && kCtas > 1;
   struct {
     uint4 w[NG];
     int sl, rl, rs;
@@ -582,6 +586,8 @@ __global__ void __launch_bounds__(NW * 32, kCtas) shared_own_kernel(const __grid
     int rs_eff = rs + rl - n_vis;  // oldest visible entry
     if (rs_eff >= c.ring_cap) rs_eff -= c.ring_cap;
 
+    const Unit un_next = unit_at(i);
+    if (kEarly) fetch(un_next);
     RunState<D> run;
     int v = un.first;
     for (int s = 0; s < un.n; ++s, v += un.stride) {
@@ -618,8 +624,7 @@ __global__ void __launch_bounds__(NW * 32, kCtas) shared_own_kernel(const __grid
     // ---- merge.  The stage that the next copy will fill is free until then.
     float *state = reinterpret_cast<float *>(smem + (warp * ST + in) * S::kBytes);  // [8][D], max [8], sum [8]
     store_state<D>(run, lane, state, state + 8 * D, state + 8 * D + 8);
-    const Unit un_next = unit_at(i);
-    fetch(un_next);
+    if (!kEarly) fetch(un_next);
     __syncwarp();
     // the prefix's partials: all of them for a unit of the warp's own, else
     // this warp's share, folded into its state
