@@ -4,8 +4,11 @@
 // oldest first.  The inverse of the handoff from a prefill.
 //
 // value = code * scale, one fp32 product, rounded once to the output type.
-// HBM-bound: per (row, KV head) 2 (D + D/8) bytes in, 2 D elements out.
-// A lane moves 16 channels (one 16-byte load of codes).
+// HBM-bound: per (row, KV head) 2 (D + D/8) bytes in, 2 D elements out, most
+// of it the output's writes: a lane moves 8 channels, so that a warp's store
+// of bf16 covers whole lines (with 16 channels to a lane, two stores of half a
+// sector each: 18.9 us against 15.7 for 36 rows of 384 slots, 8 heads, D =
+// 128; the bytes take 13 us).
 #include "nd_common.cuh"
 #include "nd_internal.h"
 
@@ -21,35 +24,33 @@ struct ReadParams {
   int *err;
 };
 
-__device__ __forceinline__ void store16(uint16_t *dst, const uint4 &w, float s) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-  uint32_t o[8];
+__device__ __forceinline__ void store8(uint16_t *dst, const uint2 &w, float s) {
+  const uint32_t u[2] = {w.x, w.y};
+  uint32_t o[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 2; ++i) {
     o[2 * i] = pack_bf16x2(float(int8_t(u[i])) * s, float(int8_t(u[i] >> 8)) * s);
     o[2 * i + 1] = pack_bf16x2(float(int8_t(u[i] >> 16)) * s, float(int8_t(u[i] >> 24)) * s);
   }
-  reinterpret_cast<uint4 *>(dst)[0] = make_uint4(o[0], o[1], o[2], o[3]);
-  reinterpret_cast<uint4 *>(dst)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
 }
-__device__ __forceinline__ void store16(float *dst, const uint4 &w, float s) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+__device__ __forceinline__ void store8(float *dst, const uint2 &w, float s) {
+  const uint32_t u[2] = {w.x, w.y};
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 2; ++i)
     reinterpret_cast<float4 *>(dst)[i] = make_float4(float(int8_t(u[i])) * s, float(int8_t(u[i] >> 8)) * s,
                                                      float(int8_t(u[i] >> 16)) * s, float(int8_t(u[i] >> 24)) * s);
 }
 
-constexpr int kTile = 16;  // output rows per CTA
+constexpr int kTile = 8;  // output rows per CTA (16: 16.4 us; 32: 18.5)
 
-// grid (row tiles, B).  A warp takes a (head, K or V) and up to kTile rows of
-// it: the slots of neighbouring rows are neighbours (but for the ring's wrap),
-// so its loads cover 2 KB of codes in one piece, all of them in flight before
-// the first is converted.
+// grid (row tiles, B).  A warp takes a (head, K or V) and its kTile rows: the
+// slots of neighbouring rows are neighbours (but for the ring's wrap), so its
+// loads cover 8 D bytes of codes in one piece, all of them in flight before the
+// first is converted.
 template <typename E, int D>
 __global__ void __launch_bounds__(256) cache_read_kernel(const ReadParams p) {
-  constexpr int kLanes = D / 16, kRows = 32 / kLanes;              // rows per load of the warp
-  constexpr int kU = kTile / kRows < 8 ? kTile / kRows : 8, kGroup = kU * kRows;
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes, kU = kTile / kRows;  // rows per load of the warp, loads
   const nd_kv_cache &c = p.c;
   const int b = blockIdx.y, row0 = blockIdx.x * kTile;
   const int Hkv = c.n_kv_heads, nslot = c.sink_cap + c.ring_cap;
@@ -69,15 +70,14 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const ReadParams p) {
   if (row0 >= live) return;
   int oldest = rs + rl - n;  // ring slot of the oldest visible entry
   if (oldest >= c.ring_cap) oldest -= c.ring_cap;
-  const int lane = threadIdx.x & 31, sub = lane / kLanes, ch = (lane % kLanes) * 16;
-  const int rows = min(kTile, live - row0), groups = (rows + kGroup - 1) / kGroup;
-  for (int item = threadIdx.x >> 5; item < 2 * Hkv * groups; item += blockDim.x >> 5) {
-    const int group = item / (2 * Hkv), pair = item - group * 2 * Hkv, h = pair >> 1;
-    const int r0 = row0 + group * kGroup + sub;
+  const int lane = threadIdx.x & 31, sub = lane / kLanes, ch = (lane % kLanes) * 8;
+  const int r0 = row0 + sub;
+  for (int pair = threadIdx.x >> 5; pair < 2 * Hkv; pair += blockDim.x >> 5) {
+    const int h = pair >> 1;
     const size_t base = (size_t(b) * Hkv + h) * nslot;
     const int8_t *codes = ((pair & 1) ? c.v_codes : c.k_codes) + base * D + ch;
     const float *scale = ((pair & 1) ? c.v_scale : c.k_scale) + base * (D / 32) + ch / 32;
-    uint4 w[kU];
+    uint2 w[kU];
     float s[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
@@ -86,13 +86,13 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const ReadParams p) {
       int ring = oldest + r - sl;
       if (ring >= c.ring_cap) ring -= c.ring_cap;
       const int slot = r < sl ? r : c.sink_cap + ring;
-      w[u] = *reinterpret_cast<const uint4 *>(codes + size_t(slot) * D);
+      w[u] = *reinterpret_cast<const uint2 *>(codes + size_t(slot) * D);
       s[u] = scale[size_t(slot) * (D / 32)];
     }
     E *out = static_cast<E *>((pair & 1) ? p.v : p.k) + ((size_t(b) * p.n_rows + r0) * Hkv + h) * D + ch;
 #pragma unroll
     for (int u = 0; u < kU; ++u)
-      if (r0 + u * kRows < live) store16(out + size_t(u * kRows) * Hkv * D, w[u], s[u]);
+      if (r0 + u * kRows < live) store8(out + size_t(u * kRows) * Hkv * D, w[u], s[u]);
   }
 }
 
