@@ -75,6 +75,27 @@ def test_norm_rope_matches_the_formula(d, f32, B, T, Hq, Hk):
     check(host(ko), formula(kf, wk, pos, 1e-6, 10000.0), not f32, what="k")
 
 
+@pytest.mark.parametrize("d,Hq,Hk", [(32, 33, 4), (64, 13, 4), (128, 7, 2), (256, 3, 2)])
+@pytest.mark.parametrize("f32", [False, True])
+def test_many_tokens(d, Hq, Hk, f32):
+    """Enough rows that a warp takes a token; heads that do not fill its last batch; slices, positions, in place."""
+    rng = philox(9050 + d)
+    B, T = 3, 433
+    x, xf = draw(rng, (B, T, Hq + Hk + 1, d), f32)
+    q, k = x[:, :, :Hq], x[:, :, Hq:Hq + Hk]
+    wq, wk = (rng.uniform(0.5, 1.5, d).astype(np.float32) for _ in range(2))
+    pos = rng.integers(-5, 100000, (B, T)).astype(np.int32)
+    qo, ko = nd().nd_qk_norm_rope(q, k, dev(wq), dev(wk), 1e-6, 10000.0, positions=dev(pos))
+    far = 1e5 * 2.0 ** -49
+    check(host(qo), formula(xf[:, :, :Hq], wq, pos, 1e-6, 10000.0), not f32, far, "q")
+    check(host(ko), formula(xf[:, :, Hq:Hq + Hk], wk, pos, 1e-6, 10000.0), not f32, far, "k")
+    qc, kc = q.contiguous(), k.contiguous()
+    nd().nd_qk_norm_rope(qc, kc, dev(wq), dev(wk), 1e-6, 10000.0, positions=dev(pos), q_out=qc, k_out=kc)
+    assert torch.equal(qc, qo) and torch.equal(kc, ko)
+    _, k2 = nd().nd_qk_norm_rope(None, q, None, dev(wq), 1e-6, 10000.0, positions=dev(pos))
+    assert torch.equal(k2, qo)
+
+
 def test_without_weights_without_rotation_and_one_tensor():
     rng = philox(9100)
     q, qf = draw(rng, (2, 5, 3, 64), False)

@@ -181,6 +181,33 @@ def test_scales_of_any_size(Hq, Hkv, d, kind, B):
     assert_close_bf16(out / top, want / top, kind)
 
 
+@pytest.mark.parametrize("B", [3, 20, 70])
+def test_slots_behind_a_long_prefix_may_hold_anything(B):
+    rng = philox(10350 + B)
+    Hq, Hkv, d, L, W = 8, 2, 128, 601, 24
+    prefix = random_cache(rng, 1, Hkv, d, 900, 4, [(L, 0)])
+    own = random_cache(rng, B, Hkv, d, 3, W, [(3, 2 * W + 5), (1, 7), (0, 0)])
+    clean = prefix.copy()
+    for f in ("k_scale", "v_scale"):
+        getattr(prefix, f)[:, :, L:] = np.array([np.nan, np.inf, -np.inf, 3e38], np.float32)
+    qb, q = normal_bf16(rng, (B, Hq, d))
+    got, want = run(prefix, own, qb, W), run(clean, own, qb, W)
+    for g, w in zip(got, want):
+        np.testing.assert_array_equal(g, w)
+    check(prefix, own, qb, q, W)
+
+
+@pytest.mark.parametrize("d,W", [(128, 40), (64, 41)])
+def test_more_pairs_than_warps(d, W):
+    """Several units to a warp one after the other, and a last round that a CTA's warps share."""
+    rng = philox(10360 + d)
+    Hq, Hkv, B, L = 16, 8, 480, 70
+    prefix = random_cache(rng, 1, Hkv, d, L, 0, [(L, 0)])
+    own = random_cache(rng, B, Hkv, d, 1, W, [(1, 2 * W), (0, 5), (0, 0), (1, W), (0, W + 1)])
+    qb, q = normal_bf16(rng, (B, Hq, d))
+    check(prefix, own, qb, q, W - 3)
+
+
 def test_scores_that_grow_along_the_prefix():
     """The running maximum moves by far more than a lazy rescale allows, in both directions."""
     rng = philox(10500)
@@ -255,6 +282,36 @@ def test_captured_replayed_and_on_two_streams():
     torch.cuda.synchronize()
     for o in out:
         assert torch.equal(o, first)
+
+
+def test_two_graphs_share_a_workspace():
+    """Replayed in turn, as any two users of one workspace have to be."""
+    rng = philox(10750)
+    Hq, Hkv, d, B = 32, 8, 128, 12
+    own = random_cache(rng, B, Hkv, d, 0, 32)
+    qb, q = normal_bf16(rng, (B, Hq, d))
+    c, qd = device_cache(own), dev_bf16(qb)
+    prefixes = [random_cache(rng, 1, Hkv, d, L, 0, [(L, 0)]) for L in (700, 1900)]
+    devs = [device_cache(p) for p in prefixes]
+    size = max(nd().nd_shared_prefix_decode_workspace_size(B, Hq, Hkv, d, p.sink_cap, 32) for p in prefixes)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    out = [torch.empty(B, Hq, d, dtype=torch.bfloat16, device="cuda") for _ in prefixes]
+    graphs = []
+    for p, o in zip(devs, out):
+        nd().nd_shared_prefix_decode(qd, p, c, 32, out=o, workspace=ws)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            nd().nd_shared_prefix_decode(qd, p, c, 32, out=o, workspace=ws)
+        graphs.append(g)
+    for o in out:
+        o.zero_()
+    for _ in range(5):
+        for g in graphs:
+            g.replay()
+    for p, o in zip(prefixes, out):
+        want, _ = oracle.decode(q, joined(p, own), 32)
+        assert_close_bf16(host(o), want)
 
 
 def test_outputs_and_workspace_stay_inside_their_buffers():
