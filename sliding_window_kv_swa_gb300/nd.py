@@ -204,21 +204,20 @@ class KVCache:
         return self.k_codes.shape[3]
 
     def struct(self) -> _Cache:
-        # (built again only when a tensor or a size changed: half the time of
-        # a call on a per-token path)
+        return _Cache(self.batch, self.n_kv_heads, self.head_dim, self.sink_cap, self.ring_cap,
+                      *(t.data_ptr() for t in (self.k_codes, self.v_codes, self.k_scale, self.v_scale,
+                                               self.sink_len, self.ring_start, self.ring_len,
+                                               self.seq_len)))
+
+    def struct_ref(self):
+        """A reference to the struct for ctypes, made again only when a tensor or a size changed (half the time)."""
         key = (self.k_codes.shape, self.sink_cap, self.ring_cap, self.k_codes.data_ptr(), self.v_codes.data_ptr(),
                self.k_scale.data_ptr(), self.v_scale.data_ptr(), self.sink_len.data_ptr(),
                self.ring_start.data_ptr(), self.ring_len.data_ptr(), self.seq_len.data_ptr())
-        if self.__dict__.get("_key") != key:
-            self._struct = _Cache(self.batch, self.n_kv_heads, self.head_dim, *key[1:])
-            self._ref = ctypes.byref(self._struct)
-            self._key = key
-        return self._struct
-
-    def struct_ref(self):
-        """A reference to struct() for ctypes."""
-        self.struct()
-        return self._ref
+        kept = self.__dict__.get("_kept")
+        if kept is None or kept[0] != key:
+            self._kept = kept = (key, ctypes.byref(self.struct()))
+        return kept[1]
 
 
 @dataclass
@@ -437,6 +436,11 @@ def _here(t: torch.Tensor) -> int:
     return dev
 
 
+def _on(stream, dev: int) -> int:
+    """_stream() where the current device is known."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
 def _addr(t: torch.Tensor, name: str, shape, dtype, dev: int) -> int:
     """The address of a contiguous tensor of this shape, type and device."""
     if t.shape != shape or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
@@ -502,13 +506,13 @@ def nd_kv_cache_read(cache: KVCache, window: int, dtype: torch.dtype = torch.bfl
     else:
         at_p = _addr(positions, "positions", (B, rows), torch.int32, dev)
     if lengths is None:
-        lengths = torch.empty((B,), dtype=torch.int32, device=codes.device)
+        lengths = torch.empty_like(cache.seq_len)
         at_n = lengths.data_ptr()
     else:
         at_n = _addr(lengths, "lengths", (B,), torch.int32, dev)
     code = ND_BF16 if dtype == torch.bfloat16 else _dtype_code(k_out)
     _check("nd_kv_cache_read", _lib().nd_kv_cache_read(
-        cache.struct_ref(), window, code, rows, at_k, at_v, at_p, at_n, _stream(stream)))
+        cache.struct_ref(), window, code, rows, at_k, at_v, at_p, at_n, _on(stream, dev)))
     return k_out, v_out, positions, lengths
 
 
@@ -544,7 +548,7 @@ def nd_shared_prefix_decode(q: torch.Tensor, prefix: KVCache, cache: KVCache, wi
     _check("nd_shared_prefix_decode", _lib().nd_shared_prefix_decode(
         at_q, prefix.struct_ref(), cache.struct_ref(), Hq, window, at_out,
         None if lse is None else _addr(lse, "lse", (B, Hq), torch.float32, dev),
-        workspace.data_ptr(), workspace.nbytes, _stream(stream)))
+        workspace.data_ptr(), workspace.nbytes, _on(stream, dev)))
     return out
 
 
@@ -576,7 +580,7 @@ def nd_qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], q_weig
             raise ValueError(f"{name} must have shape [{B}, {T}, heads, {d}], q's type and device")
         step = _step(t, name)
         if out is None:
-            out = torch.empty(shape, dtype=dtype, device=t.device)
+            out = torch.empty_like(t, memory_format=torch.contiguous_format)
             return shape[2], step, t.data_ptr(), out.data_ptr(), out
         return shape[2], step, t.data_ptr(), _addr(out, name + "_out", shape, dtype, dev), out
 
@@ -586,7 +590,7 @@ def nd_qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], q_weig
         pq, pk, _dtype_code(one), B, T, Hq, Hk, d, sq, sk, _weight(q_weight, "q_weight", d, dev),
         _weight(k_weight, "k_weight", d, dev), eps, rope_theta,
         None if positions is None else _addr(positions, "positions", (B, T), torch.int32, dev), oq, ok,
-        _stream(stream)))
+        _on(stream, dev)))
     return q_out, k_out
 
 
@@ -608,7 +612,7 @@ def nd_qk_norm_rope_append(q: torch.Tensor, cache: KVCache, k_new: torch.Tensor,
         raise ValueError(f"q, k_new and v_new must be bf16 [{B}, heads, {d}] (k_new, v_new: {Hkv} heads) on the "
                          "cache's device")
     if q_out is None:
-        q_out = torch.empty(shape, dtype=bf16, device=q.device)
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
         at_out = q_out.data_ptr()
     else:
         at_out = _addr(q_out, "q_out", shape, bf16, dev)
@@ -621,7 +625,7 @@ def nd_qk_norm_rope_append(q: torch.Tensor, cache: KVCache, k_new: torch.Tensor,
         q.data_ptr(), cache.struct_ref(), k_new.data_ptr(), v_new.data_ptr(), shape[1], _step(q, "q"),
         _step(k_new, "k_new"), _step(v_new, "v_new"), _weight(q_weight, "q_weight", d, dev),
         _weight(k_weight, "k_weight", d, dev), eps, rope_theta, base, 1 if to_sink else 0,
-        at_out, _stream(stream)))
+        at_out, _on(stream, dev)))
     return q_out
 
 
