@@ -753,15 +753,27 @@ struct SharedPlan {
   bool inline_prefix;
   int n_split, slots_per_unit, inline_slots;
   bool wide;  // more warps per unit: few units
+  int ctas;   // of the prefix kernel, at most
 };
 
-SharedPlan shared_plan(int batch, int n_kv_heads, int head_dim, int prefix_cap, int max_slots) {
+constexpr int kSpareTiles = 6;  // see below
+
+SharedPlan shared_plan(int batch, int G, int n_kv_heads, int head_dim, int prefix_cap, int max_slots) {
   SharedPlan s;
   const long long pairs = (long long)batch * n_kv_heads;
-  // A prefix of up to 256 slots for up to 152 pairs is read again by each.
-  s.inline_prefix = pairs <= kPrefixCtas && prefix_cap <= 256;
+  // A prefix of up to 512 slots for up to 152 pairs is read again by each of
+  // them (2 heads of 64: 64 slots 5.6 us against 10.2; 152 pairs of 128: 256
+  // slots 8.2 against 13.7, 512 slots 10.0 against 13.9; 64 pairs of 64: 512
+  // slots 7.3 against 8.7, 768 slots 9.3 against 8.7.  256 pairs of 128: 256
+  // slots 13.9 against 11.1).
+  s.inline_prefix = pairs <= kPrefixCtas && prefix_cap <= 512;
   s.inline_slots = s.inline_prefix ? (prefix_cap + kStep - 1) / kStep * kStep : 0;
-  s.wide = pairs <= kPrefixCtas;
+  // One CTA of more warps to an SM where the pairs are few, and up to twice
+  // the SMs where a pair's walk is long (64 pairs of 128 over 256 slots 16.5 us
+  // against 21.5 with three CTAs of four; 192 pairs of 64 over 1024 slots 23.3
+  // against 33.6, over 512 20.2 against 23.8, over 256 18.8 against 18.9; 456
+  // of 128 over 512 35.7 against 29.7).
+  s.wide = pairs <= kPrefixCtas || (pairs <= 2 * kPrefixCtas && max_slots >= 512);
   const int warps = s.wide ? (head_dim == 64 ? 16 : 8) : 4;
   const int steps = (s.inline_slots + max_slots + kStep - 1) / kStep;
   // parts of a pair where the pairs leave SMs idle, each at least two steps
@@ -771,6 +783,18 @@ SharedPlan shared_plan(int batch, int n_kv_heads, int head_dim, int prefix_cap, 
   s.n_split = n > 1 ? int(n) : 1;
   s.slots_per_unit = (steps + s.n_split - 1) / s.n_split * kStep;
   s.n_split = (steps * kStep + s.slots_per_unit - 1) / s.slots_per_unit;
+  // The own part starts beside the prefix kernel where that leaves it SMs: a
+  // CTA walks its unit meanwhile and waits only to merge, which saves 3 to 4
+  // us.  Worth six more tiles per CTA of the prefix, at 0.45 (D = 64) to 0.55
+  // us each (32 pairs of 128 over 4096 slots 12.6 us against 16.2; 16 over
+  // 32768, 5 tiles: 27.6 against 29.1; 64 over 32768, 8 tiles: 31.0 against
+  // 29.7).
+  const long long own = pairs * s.n_split, tiles = (long long)n_kv_heads * prefix_pairs(batch * G) *
+                                                   ((prefix_cap + kPrefixTile - 1) / kPrefixTile);
+  s.ctas = kPrefixCtas;
+  if (own <= kPrefixCtas / 2 &&
+      (tiles + kPrefixCtas - own - 1) / (kPrefixCtas - own) <= (tiles + kPrefixCtas - 1) / kPrefixCtas + kSpareTiles)
+    s.ctas = int(kPrefixCtas - own);
   return s;
 }
 
@@ -778,16 +802,17 @@ SharedPlan shared_plan(int batch, int n_kv_heads, int head_dim, int prefix_cap, 
 
 size_t shared_decode_workspace_bytes(int batch, int n_q_heads, int n_kv_heads, int head_dim, int prefix_cap,
                                      int max_slots) {
-  const SharedPlan s = shared_plan(batch, n_kv_heads, head_dim, prefix_cap, max_slots);
+  const int G = n_q_heads / n_kv_heads;
+  const SharedPlan s = shared_plan(batch, G, n_kv_heads, head_dim, prefix_cap, max_slots);
   size_t rows = s.n_split > 1 ? size_t(batch) * n_q_heads * s.n_split : 0;
-  if (!s.inline_prefix) rows += prefix_slots(prefix_cap, n_kv_heads, batch * (n_q_heads / n_kv_heads)) * 2 * kPrefixBlock;
+  if (!s.inline_prefix) rows += prefix_slots(prefix_cap, n_kv_heads, batch * G, s.ctas) * 2 * kPrefixBlock;
   return rows * (head_dim + 2) * sizeof(float);
 }
 
 cudaError_t launch_shared_decode(const void *q, const nd_kv_cache &prefix, const nd_kv_cache &c, int n_q_heads,
                                  int window, void *out, float *lse, void *ws, int *err, cudaStream_t stream) {
   const int d = c.head_dim, G = n_q_heads / c.n_kv_heads, rows = c.batch * G;
-  const SharedPlan s = shared_plan(c.batch, c.n_kv_heads, d, prefix.sink_cap, c.sink_cap + c.ring_cap);
+  const SharedPlan s = shared_plan(c.batch, G, c.n_kv_heads, d, prefix.sink_cap, c.sink_cap + c.ring_cap);
   OwnParams p;
   p.q = static_cast<const uint16_t *>(q);
   p.c = c;
@@ -810,12 +835,12 @@ cudaError_t launch_shared_decode(const void *q, const nd_kv_cache &prefix, const
   float *w = static_cast<float *>(ws);
   cudaError_t e;
   if (!s.inline_prefix) {
-    const size_t pre_rows = prefix_slots(prefix.sink_cap, c.n_kv_heads, rows) * 2 * kPrefixBlock;
+    const size_t pre_rows = prefix_slots(prefix.sink_cap, c.n_kv_heads, rows, s.ctas) * 2 * kPrefixBlock;
     p.parts.o = w;
     p.parts.ml = reinterpret_cast<float2 *>(w + pre_rows * d);
-    p.prefix_grid = prefix_grid(prefix.sink_cap, c.n_kv_heads, rows);
+    p.prefix_grid = prefix_grid(prefix.sink_cap, c.n_kv_heads, rows, s.ctas);
     w += pre_rows * (d + 2);
-    e = launch_shared_prefix(q, prefix, c.batch, n_q_heads, p.parts, err, stream);
+    e = launch_shared_prefix(q, prefix, c.batch, n_q_heads, p.prefix_grid, p.parts, err, stream);
     if (e != cudaSuccess) return e;
   }
   p.ws_o = w;

@@ -781,7 +781,7 @@ cudaError_t launch_d(const PrefixParams &p, int grid, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_shared_prefix(const void *q, const nd_kv_cache &prefix, int batch, int n_q_heads,
+cudaError_t launch_shared_prefix(const void *q, const nd_kv_cache &prefix, int batch, int n_q_heads, int grid,
                                  const PrefixParts &out, int *err, cudaStream_t stream) {
   PrefixParams p;
   p.q = static_cast<const uint16_t *>(q);
@@ -792,7 +792,6 @@ cudaError_t launch_shared_prefix(const void *q, const nd_kv_cache &prefix, int b
   p.g_magic = p.G > 1 ? unsigned((0x100000000ull + p.G - 1) / p.G) : 0u;
   p.out = out;
   p.err = err;
-  const int grid = prefix_grid(prefix.sink_cap, prefix.n_kv_heads, p.R);
   if (prefix.head_dim == 128) return launch_d<128>(p, grid, stream);
   if (prefix.head_dim == 64) return launch_d<64>(p, grid, stream);
   return cudaErrorInvalidValue;

@@ -78,16 +78,17 @@ __host__ __device__ inline PrefixPlan prefix_plan(int sink_len, int sink_cap, in
   return p;
 }
 
-// Blocks to launch for a prefix of up to sink_cap slots, and partial slots.
-inline int prefix_grid(int sink_cap, int n_kv_heads, int rows) {
-  const int c = prefix_plan(sink_cap, sink_cap, n_kv_heads, rows, kPrefixCtas).ctas;
+// Blocks to launch (up to `most`) for a prefix of up to sink_cap slots, and
+// partial slots.
+inline int prefix_grid(int sink_cap, int n_kv_heads, int rows, int most) {
+  const int c = prefix_plan(sink_cap, sink_cap, n_kv_heads, rows, most).ctas;
   return c > 0 ? c : 1;
 }
-inline size_t prefix_slots(int sink_cap, int n_kv_heads, int rows) {
-  return size_t(prefix_grid(sink_cap, n_kv_heads, rows)) + size_t(n_kv_heads) * prefix_pairs(rows);
+inline size_t prefix_slots(int sink_cap, int n_kv_heads, int rows, int most) {
+  return size_t(prefix_grid(sink_cap, n_kv_heads, rows, most)) + size_t(n_kv_heads) * prefix_pairs(rows);
 }
 
-cudaError_t launch_shared_prefix(const void *q, const nd_kv_cache &prefix, int batch, int n_q_heads,
+cudaError_t launch_shared_prefix(const void *q, const nd_kv_cache &prefix, int batch, int n_q_heads, int grid,
                                  const PrefixParts &out, int *err, cudaStream_t stream);
 
 }  // namespace nd

@@ -146,14 +146,9 @@ def test_slots_that_are_not_visible_may_hold_anything():
         np.testing.assert_array_equal(g, w)
 
 
-@pytest.mark.parametrize("Hq,Hkv,d", [(8, 2, 64), (8, 2, 128)])
-@pytest.mark.parametrize("B", [3, 20, 70])   # rows of a KV head: up to 64, up to 128, more
-@pytest.mark.parametrize("kind", ["large", "tiny", "mixed", "rising", "zero_v"])
-def test_scales_of_any_size(Hq, Hkv, d, kind, B):
-    """The power-of-two scaling of keys and values follows the data: large and tiny tokens, magnitudes that differ by
-    2^40 within the prefix, values that grow along it, all-zero values."""
+def scales_of_any_size(Hq, Hkv, d, kind, B, L):
     rng = philox(10400 + d)
-    L, W = 330, 16
+    W = 16
     prefix = random_cache(rng, 1, Hkv, d, L, 0, [(L, 0)])
     own = random_cache(rng, B, Hkv, d, 0, W)
     kmul, vmul = np.ones(L), np.ones(L)
@@ -179,6 +174,65 @@ def test_scales_of_any_size(Hq, Hkv, d, kind, B):
     want, _ = oracle.decode(q, joined(prefix, own), W)
     top = np.abs(want).max()
     assert_close_bf16(out / top, want / top, kind)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(8, 2, 64), (8, 2, 128)])
+@pytest.mark.parametrize("B", [3, 20, 70])   # rows of a KV head: up to 64, up to 128, more
+@pytest.mark.parametrize("kind", ["large", "tiny", "mixed", "rising", "zero_v"])
+def test_scales_of_any_size(Hq, Hkv, d, kind, B):
+    """The power-of-two scaling of keys and values follows the data: large and tiny tokens, magnitudes that differ by
+    2^40 within the prefix, values that grow along it, all-zero values."""
+    scales_of_any_size(Hq, Hkv, d, kind, B, 330)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(8, 2, 64), (8, 2, 128)])
+@pytest.mark.parametrize("B", [3, 20, 70])
+@pytest.mark.parametrize("kind", ["large", "tiny", "mixed", "rising", "zero_v"])
+def test_scales_of_any_size_along_a_long_prefix(Hq, Hkv, d, kind, B):
+    """The same past the lengths that every pair reads for itself."""
+    scales_of_any_size(Hq, Hkv, d, kind, B, 830)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", LAYOUTS)
+@pytest.mark.parametrize("B,L,cap,S,W,window", [
+    (2, 576, 576, 0, 16, 16),        # whole tiles
+    (5, 639, 700, 3, 20, 11),        # ends inside a tile, a hole behind it, a narrower window
+    (9, 1025, 1025, 0, 33, 64),
+    (3, 2000, 5000, 2, 600, 590),    # a long ring
+    (40, 513, 900, 0, 520, 600)])    # more pairs than SMs, each with a long walk
+def test_matches_the_joined_caches_past_short_prefixes(Hq, Hkv, d, B, L, cap, S, W, window):
+    rng = philox(10050 + 7 * L + d + B)
+    prefix = random_cache(rng, 1, Hkv, d, cap, 4, [(L, 0)])
+    lens = None if B < 5 else [(S, 3 * W + 1), (S, W // 2), (0, 0), (S // 2, W)]
+    own = random_cache(rng, B, Hkv, d, S, W, lens)
+    qb, q = normal_bf16(rng, (B, Hq, d))
+    check(prefix, own, qb, q, window)
+
+
+def test_the_own_part_beside_the_prefix_kernel():
+    """Few pairs: the own part's CTAs run while the prefix is multiplied, also with parts of a pair; a captured call
+    follows a prefix that grows from nothing to its capacity."""
+    rng = philox(10060)
+    for Hq, Hkv, d, B, cap, W in ((8, 2, 128, 1, 6000, 24), (16, 8, 64, 2, 9000, 40), (4, 1, 64, 2, 3000, 2048)):
+        prefix = random_cache(rng, 1, Hkv, d, cap, 0, [(cap, 0)])
+        own = random_cache(rng, B, Hkv, d, 0, W)
+        qb, q = normal_bf16(rng, (B, Hq, d))
+        p, c, qd = device_cache(prefix), device_cache(own), dev_bf16(qb)
+        ws = torch.empty(nd().nd_shared_prefix_decode_workspace_size(B, Hq, Hkv, d, cap, W), dtype=torch.uint8, device="cuda")
+        out = torch.empty(B, Hq, d, dtype=torch.bfloat16, device="cuda")
+        nd().nd_shared_prefix_decode(qd, p, c, W, out=out, workspace=ws)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            nd().nd_shared_prefix_decode(qd, p, c, W, out=out, workspace=ws)
+            nd().nd_shared_prefix_decode(qd, p, c, W, out=out, workspace=ws)
+        for length in (0, 1, 130, 2500, cap):
+            p.sink_len.fill_(length)
+            prefix.sink_len[0] = length
+            for _ in range(3):
+                g.replay()
+            want, _ = oracle.decode(q, joined(prefix, own), W)
+            assert_close_bf16(host(out), want, f"prefix of {length} of {cap}")
 
 
 @pytest.mark.parametrize("B", [3, 20, 70])
