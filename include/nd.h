@@ -327,9 +327,9 @@ ND_API int nd_swa_sink_decode_noalloc(const void *q, const nd_kv_cache *cache,
 /*
  * Reads a cache back: every sequence's visible keys and values, dequantised
  * (the fp32 product code * scale, then rounded to dtype), in position order
- * and in the layout a prefill has them -- the way back from nd_kv_cache_from_prefill, e.g. to
- * move a session to a cache of another shape, to prefill after it, or to
- * inspect it.
+ * and in the layout a prefill has them -- the way back from
+ * nd_kv_cache_from_prefill, e.g. to move a session to a cache of another
+ * shape, to prefill after it, or to inspect it.
  *   row r of sequence b, r < lengths[b] = sink_len + min(ring_len, window):
  *     r < sink_len: sink slot r (position r); then the newest
  *     min(ring_len, window) ring entries, oldest first (positions ending at
@@ -363,8 +363,10 @@ ND_API int nd_kv_cache_read(const nd_kv_cache *cache, int window, nd_dtype dtype
  *   q, out, lse, window, n_q_heads  as nd_swa_sink_decode; batch * n_q_heads at
  *           most 2^24
  * A sequence that sees no key gets out = 0, lse = -inf.  The prefix's keys
- * and values are taken as fp16 after a power-of-two scaling (each within
- * 2^-11 of code * scale, relative), products and sums in fp32.
+ * and values are taken as fp16 after a power-of-two scaling (each within 2^-10
+ * of code * scale, relative; a prefix that is short and shared by few
+ * sequences exactly, as nd_swa_sink_decode takes its slots), products and sums
+ * in fp32.
  * Partial results go to the workspace (device, 16-byte aligned) of
  * nd_shared_prefix_decode_workspace_size(batch, n_q_heads, n_kv_heads,
  * head_dim, prefix->sink_cap, cache->sink_cap + cache->ring_cap) bytes (0: none
@@ -605,8 +607,9 @@ ND_API int nd_rope_apply(const void *x, void *y, int batch, int T, int n_heads,
  *   q_out, k_out  dtype [batch][T][heads][head_dim], contiguous; may equal q / k
  *      where those are contiguous
  * rope_theta 0 = no rotation.  eps >= 0.  Strides are multiples of 16 bytes.
- * head_dim 32, 64, 128 or 256; batch * T at most 2^30.  p * theta^(-2i/head_dim) is reduced to a
- * fraction of a turn in 64-bit integers; sine and cosine are fp32.
+ * head_dim 32, 64, 128 or 256; batch * T at most 2^30.  p *
+ * theta^(-2i/head_dim) is reduced to a fraction of a turn in 64-bit integers;
+ * sine and cosine are fp32.
  */
 ND_API int nd_qk_norm_rope(const void *q, const void *k, nd_dtype dtype, int batch, int T,
                            int n_q_heads, int n_k_heads, int head_dim, int64_t q_stride,

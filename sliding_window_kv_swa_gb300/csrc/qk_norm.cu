@@ -192,7 +192,7 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
 // computed.  One token to a warp: more, with the copies running on across
 // them, spread the accesses of the moment over more of memory (117 us at 13
 // tokens a warp).
-// At 32768 tokens of 32 + 8 heads of 128 (671 MB): 101 us, 6.65 TB/s; 133 us
+// At 32768 tokens of 32 + 8 heads of 128 (671 MB): 99.8 us, 6.72 TB/s; 133 us
 // with plain loads behind the angles, 120 with one batch ahead in registers.
 template <typename E, int D>
 struct NormLay {

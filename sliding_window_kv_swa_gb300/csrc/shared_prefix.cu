@@ -8,7 +8,7 @@
 //   m = max_j s_j,  l = sum_j 2^(s_j - m),  O = sum_j 2^(s_j - m) v_j,
 //   s_j = (q . k_j) log2(e) / sqrt(D),
 // taken in one pass over the keys; triples of different key ranges, and of the
-// sequence's own slots, merge exactly (decode.cu).
+// sequence's own slots, merge exactly (shared_decode.cu).
 //
 // Types.  The tensor cores multiply fp16 with fp32 sums.  q (bf16) becomes
 // fp16 exactly after a power-of-two scaling per row (channels 2^-28 below the
@@ -21,11 +21,17 @@
 // all of it scaled by 2^7, so it stays below 2^15 and keys 2^-21 below the
 // maximum still have all bits.  Sums, maxima and partials are fp32.
 //
-// What bounds it.  4 R D flops per key and KV head on the tensor cores, and as
-// many exponentials as scores (16 per clock and SM: at D = 128 as long as the
-// products); below about 40 rows per KV head the read of the codes (2 (D +
-// D/8) bytes per key).  Each CTA therefore keeps two 128-row blocks and turns
-// a tile's codes into fp16 once for both.
+// What bounds it.  4 R D flops per key and KV head on the tensor cores, or
+// below about 40 rows per KV head the read of the codes (2 (D + D/8) bytes per
+// key); a CTA keeps two 128-row blocks and turns a tile's codes into fp16 once
+// for both.  Measured (ncu, D = 128): 512 rows over 32768 keys of 8 heads 58
+// us, the products' pipe 72 % active: S = Q K^T of 128 x 64 reads Q from shared
+// memory for every tile and runs at half the rate (N = 128 would not, but its
+// scores, two blocks and O are all of TMEM with no second buffer).  16 rows
+// over 65536 keys: 42 us for 151 MB, 22 us of it the bytes; a tile costs 0.55
+// us of the chain copy - scales - turn - S - softmax - PV, in which no role is
+// busy for much more than half of it (Q from TMEM, other waits, deeper rings:
+// no change), and 6 us go before the first product.
 //
 // Work split.  The (KV head, 256-row pair, 64-key tile) triples, key tiles
 // fastest, form one line that is cut into equal stretches, one per CTA (one

@@ -1,6 +1,6 @@
 // shared_prefix.cuh -- how the shared prefix's work is split, and where its
 // partial results lie: used by the kernel that makes them (shared_prefix.cu)
-// and by the one that merges them (decode.cu).
+// and by the ones that merge them (shared_decode.cu).
 #pragma once
 
 #include <cuda_runtime.h>
