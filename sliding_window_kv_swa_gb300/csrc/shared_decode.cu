@@ -792,13 +792,13 @@ SharedPlan shared_plan(int batch, int G, int n_kv_heads, int head_dim, int prefi
   // The own part starts beside the prefix kernel where that leaves it SMs: a
   // CTA walks its unit meanwhile and waits only to merge, which saves 3 to 4
   // us.  Worth six more tiles per CTA of the prefix, at 0.45 (D = 64) to 0.55
-  // us each (32 pairs of 128 over 4096 slots 12.6 us against 16.2; 16 over
-  // 32768, 5 tiles: 27.6 against 29.1; 64 over 32768, 8 tiles: 31.0 against
-  // 29.7).
+  // us each (32 pairs of 128 over 4096 slots 12.6 us against 16.2; 128 of 64
+  // over 4096, 5 tiles: 12.6 against 13.6; 64 of 128 over 32768, 8 tiles: 31.0
+  // against 29.7).
   const long long own = pairs * s.n_split, tiles = (long long)n_kv_heads * prefix_pairs(batch * G) *
                                                    ((prefix_cap + kPrefixTile - 1) / kPrefixTile);
   s.ctas = kPrefixCtas;
-  if (own <= kPrefixCtas / 2 &&
+  if (own <= kPrefixCtas - 8 &&
       (tiles + kPrefixCtas - own - 1) / (kPrefixCtas - own) <= (tiles + kPrefixCtas - 1) / kPrefixCtas + kSpareTiles)
     s.ctas = int(kPrefixCtas - own);
   return s;
