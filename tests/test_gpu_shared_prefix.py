@@ -419,3 +419,32 @@ def test_a_prompt_served_to_many_sessions():
     for i in range(2):
         assert torch.equal(a[i], b[i][:, L:]) and torch.equal(b[i][:, :L], p[i][:, :L].expand(B, -1, -1, -1))
     np.testing.assert_array_equal(host(a[2]) + L, host(b[2])[:, L:])
+
+
+def test_caches_whose_offsets_pass_32_bits():
+    """A prefix region and own rings of more than 2^32 bytes of codes: the last head and sequence lie behind it."""
+    rng = philox(10950)
+    n, Hq, Hkv, d, B, L, steps = nd(), 8, 2, 128, 2, 600, 5
+    far, near = n.KVCache.empty(1, Hkv, d, 34_000_000, 0), n.KVCache.empty(1, Hkv, d, L, 0)
+    ref = random_cache(rng, 1, Hkv, d, L, 0, [(L, 0)])
+    for f in ("k_codes", "v_codes", "k_scale", "v_scale"):
+        getattr(near, f).copy_(dev(getattr(ref, f)))
+        getattr(far, f)[:, :, :L].copy_(getattr(near, f))
+    own, ring = n.KVCache.empty(B, Hkv, d, 0, 8), n.KVCache.empty(B, Hkv, d, 0, 12_000_000)
+    for c, length in ((near, L), (far, L)):
+        c.sink_len.fill_(length)
+        c.seq_len.fill_(length)
+    assert ring.k_codes[0].numel() * (B - 1) + 12_000_000 * d > 1 << 32 and far.k_codes[0, 0].numel() > 1 << 32
+    for _ in range(steps):
+        x = dev_bf16(normal_bf16(rng, (B, Hq + 2 * Hkv, d))[0])
+        parts = x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:]
+        q = [n.nd_qk_norm_rope_append(parts[0], c, parts[1], parts[2], rope_theta=10000.0, pos_base=near.seq_len)
+             for c in (own, ring)]
+    assert torch.equal(*q)
+    for a, b in zip(n.nd_kv_cache_read(own, 8), n.nd_kv_cache_read(ring, 8)):
+        rows = (slice(None), slice(0, steps)) if a.dim() > 1 else slice(None)
+        assert torch.equal(a[rows], b[rows])
+    want = host(n.nd_shared_prefix_decode(q[0], near, own, 8))
+    for prefix, cache in ((far, own), (near, ring), (far, ring)):
+        # (two results, each as far from the exact one as any: twice the tolerance, as halves)
+        assert_close_bf16(host(n.nd_shared_prefix_decode(q[0], prefix, cache, 8)) / 2, want / 2)
