@@ -639,12 +639,20 @@ __global__ void __launch_bounds__(NW * 32, kCtas) shared_own_kernel(const __grid
       waited = true;
       for (int h0 = 0; h0 < G; h0 += kHeads) {
         const int h = h0 + lane % kHeads;
-        if (h >= G) continue;
+        const bool live = h < G;
         RowState<D> st;
-        st.read(state, h, lane);
-        if (pl.nt > 0) add_parts<D>(p, pl, hkv, b * G + h, un.solo ? 0 : warp, un.solo ? 1 : NW, lane, st);
-        if (un.solo) st.write_out(p, size_t(b) * p.Hq + hkv * G + h, lane);
-        else st.write(state, h, lane);
+        if (live) {
+          st.read(state, h, lane);
+          if (pl.nt > 0) add_parts<D>(p, pl, hkv, b * G + h, un.solo ? 0 : warp, un.solo ? 1 : NW, lane, st);
+          if (un.solo) st.write_out(p, size_t(b) * p.Hq + hkv * G + h, lane);
+        }
+        if (!un.solo) {
+          // eight lanes read a head's (max, sum) and one of them writes it back;
+          // the rows of a group may have different numbers of partials, so the
+          // lanes need not come out of the loop above together
+          __syncwarp();
+          if (live) st.write(state, h, lane);
+        }
       }
     }
     if (un.solo) {
