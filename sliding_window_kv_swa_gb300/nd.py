@@ -157,6 +157,35 @@ def _stream(stream) -> int:
     return stream.cuda_stream
 
 
+# Tensors that a call makes belong to the stream it runs on: memory that the
+# caching allocator gave out for another stream may still be in use there, and a
+# workspace, which is let go when the call returns, would be handed to that
+# stream's next tensor while the call's kernels are yet to run.
+
+def _pool(stream):
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    return torch.cuda.stream(stream)
+
+
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _pool(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _like(t: torch.Tensor, stream, memory_format=torch.preserve_format) -> torch.Tensor:
+    if stream is None:
+        return torch.empty_like(t, memory_format=memory_format)
+    with _pool(stream):
+        return torch.empty_like(t, memory_format=memory_format)
+
+
+def _scratch(nbytes: int, device, stream) -> torch.Tensor:
+    return _empty((max(nbytes, 16),), torch.uint8, device, stream)
+
+
 def _dtype_code(t: torch.Tensor) -> int:
     if t.dtype == torch.float32:
         return ND_F32
@@ -297,7 +326,7 @@ def nd_kv_cache_from_prefill(cache: KVCache, k: torch.Tensor, v: torch.Tensor, s
     B, T = k.shape[:2]
     if workspace is None:
         nbytes = nd_kv_cache_from_prefill_workspace_size(cache.batch, cache.sink_cap, cache.ring_cap)
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=cache.k_codes.device)
+        workspace = _scratch(nbytes, cache.k_codes.device, stream)
     s = cache.struct()
     _check("nd_kv_cache_from_prefill", _lib().nd_kv_cache_from_prefill(
         ctypes.byref(s), _ptr(k), _ptr(v), B, T, _ptr(seg_ids), _ptr(sink), _ptr(src_row), _ptr(src_seg),
@@ -314,11 +343,11 @@ def nd_swa_sink_decode(q: torch.Tensor, cache: KVCache, window: int, out: Option
                        stream=None) -> torch.Tensor:
     B, Hq, d = q.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _like(q, stream)
     if workspace is None:
         max_slots = cache.sink_cap + cache.ring_cap
         nbytes = nd_swa_sink_decode_workspace_size(B, Hq, cache.n_kv_heads, d, max_slots)
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(nbytes, q.device, stream)
     s = cache.struct()
     _check("nd_swa_sink_decode", _lib().nd_swa_sink_decode(
         _ptr(q), ctypes.byref(s), Hq, int(window), _ptr(out), _ptr(lse), _ptr(workspace),
@@ -334,10 +363,10 @@ def nd_swa_sink_decode_step(q: torch.Tensor, cache: KVCache, k_new: torch.Tensor
     in one launch when the sequence's CTAs fit a thread-block cluster."""
     B, Hq, d = q.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _like(q, stream)
     if workspace is None:
         nbytes = nd_swa_sink_decode_workspace_size(B, Hq, cache.n_kv_heads, d, cache.sink_cap + cache.ring_cap)
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(nbytes, q.device, stream)
     s = cache.struct()
     _check("nd_swa_sink_decode_step", _lib().nd_swa_sink_decode_step(
         _ptr(q), ctypes.byref(s), _ptr(k_new), _ptr(v_new), Hq, int(window), _ptr(out), _ptr(lse),
@@ -372,7 +401,7 @@ def nd_swa_sink_decode_step_host(q_host: torch.Tensor, cache: KVCache, k_new_hos
     if workspace is None:
         nbytes = nd_swa_sink_decode_step_host_workspace_size(B, Hq, cache.n_kv_heads, d,
                                                              cache.sink_cap + cache.ring_cap)
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=cache.k_codes.device)
+        workspace = _scratch(nbytes, cache.k_codes.device, stream)
     s = cache_struct if cache_struct is not None else cache.struct()
     _check("nd_swa_sink_decode_step_host", _lib().nd_swa_sink_decode_step_host(
         q_host.data_ptr(), ctypes.byref(s), k_new_host.data_ptr(), v_new_host.data_ptr(), Hq, int(window),
@@ -400,7 +429,7 @@ def nd_swa_sink_decode_step_host_packed(in_host: torch.Tensor, cache: KVCache, n
         raise ValueError(f"out_host must be a contiguous host tensor of at least {nout} bytes")
     if workspace is None:
         nbytes = nd_swa_sink_decode_step_host_workspace_size(B, n_q_heads, Hkv, d, s.sink_cap + s.ring_cap)
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=cache.k_codes.device)
+        workspace = _scratch(nbytes, cache.k_codes.device, stream)
     _check("nd_swa_sink_decode_step_host_packed", _lib().nd_swa_sink_decode_step_host_packed(
         in_host.data_ptr(), ctypes.byref(s), n_q_heads, window, out_host.data_ptr(),
         1 if with_lse else 0, workspace.data_ptr(), workspace.nbytes, _stream(stream)))
@@ -486,7 +515,7 @@ def nd_kv_cache_read(cache: KVCache, window: int, dtype: torch.dtype = torch.bfl
             raise ValueError("window must be at least 1")
         rows = cache.sink_cap + min(cache.ring_cap, window)
         shape = (B, rows, Hkv, d)
-        k_out = torch.empty(shape, dtype=dtype, device=codes.device)
+        k_out = _empty(shape, dtype, codes.device, stream)
         at_k = k_out.data_ptr()
     else:
         if k_out.dim() != 4:
@@ -496,17 +525,17 @@ def nd_kv_cache_read(cache: KVCache, window: int, dtype: torch.dtype = torch.bfl
         shape = (B, rows, Hkv, d)
         at_k = _addr(k_out, "k_out", shape, dtype, dev)
     if v_out is None:
-        v_out = torch.empty_like(k_out)
+        v_out = _like(k_out, stream)
         at_v = v_out.data_ptr()
     else:
         at_v = _addr(v_out, "v_out", shape, dtype, dev)
     if positions is None:
-        positions = torch.empty((B, rows), dtype=torch.int32, device=codes.device)
+        positions = _empty((B, rows), torch.int32, codes.device, stream)
         at_p = positions.data_ptr()
     else:
         at_p = _addr(positions, "positions", (B, rows), torch.int32, dev)
     if lengths is None:
-        lengths = torch.empty_like(cache.seq_len)
+        lengths = _like(cache.seq_len, stream)
         at_n = lengths.data_ptr()
     else:
         at_n = _addr(lengths, "lengths", (B,), torch.int32, dev)
@@ -535,14 +564,14 @@ def nd_shared_prefix_decode(q: torch.Tensor, prefix: KVCache, cache: KVCache, wi
         raise ValueError("q and the caches must agree on batch, head_dim and device")
     at_q = _addr(q, "q", shape, torch.bfloat16, dev)
     if out is None:
-        out = torch.empty_like(q)
+        out = _like(q, stream)
         at_out = out.data_ptr()
     else:
         at_out = _addr(out, "out", shape, torch.bfloat16, dev)
     if workspace is None:
         nbytes = nd_shared_prefix_decode_workspace_size(B, Hq, k.shape[1], d, prefix.sink_cap,
                                                         cache.sink_cap + cache.ring_cap)
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(nbytes, q.device, stream)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
     _check("nd_shared_prefix_decode", _lib().nd_shared_prefix_decode(
@@ -580,7 +609,7 @@ def nd_qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], q_weig
             raise ValueError(f"{name} must have shape [{B}, {T}, heads, {d}], q's type and device")
         step = _step(t, name)
         if out is None:
-            out = torch.empty_like(t, memory_format=torch.contiguous_format)
+            out = _like(t, stream, torch.contiguous_format)
             return shape[2], step, t.data_ptr(), out.data_ptr(), out
         return shape[2], step, t.data_ptr(), _addr(out, name + "_out", shape, dtype, dev), out
 
@@ -612,7 +641,7 @@ def nd_qk_norm_rope_append(q: torch.Tensor, cache: KVCache, k_new: torch.Tensor,
         raise ValueError(f"q, k_new and v_new must be bf16 [{B}, heads, {d}] (k_new, v_new: {Hkv} heads) on the "
                          "cache's device")
     if q_out is None:
-        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        q_out = _like(q, stream, torch.contiguous_format)
         at_out = q_out.data_ptr()
     else:
         at_out = _addr(q_out, "q_out", shape, bf16, dev)
@@ -642,11 +671,11 @@ def nd_compressed_decode_step(q: torch.Tensor, cache: CompressedCache, k_new: to
     to the compressed cache and attend with it; returns out."""
     B, Hq, d = q.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _like(q, stream)
     kv = cache.kv
     if workspace is None:
         nbytes = nd_compressed_decode_step_workspace_size(B, Hq, kv.n_kv_heads, d, kv.sink_cap + kv.ring_cap)
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(nbytes, q.device, stream)
     s = cache_struct if cache_struct is not None else cache.struct()
     _check("nd_compressed_decode_step", _lib().nd_compressed_decode_step(
         _ptr(q), ctypes.byref(s), _ptr(k_new), _ptr(v_new), Hq, int(window), float(rope_theta), _ptr(out),
@@ -671,10 +700,10 @@ def nd_swa_sink_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     Hkv = k.shape[2]
     dt = _dtype_code(q)
     if out is None:
-        out = torch.empty_like(q)
+        out = _like(q, stream)
     if workspace is None:
         nbytes = nd_swa_sink_prefill_workspace_size(dt, B, T, Hq, Hkv, d, rope_theta, block)
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(nbytes, q.device, stream)
     _check("nd_swa_sink_prefill", _lib().nd_swa_sink_prefill(
         _ptr(q), _ptr(k), _ptr(v), dt, B, T, Hq, Hkv, d, _ptr(seg_ids), _ptr(sink), int(window),
         float(rope_theta), _ptr(pooled_k), _ptr(pooled_v), int(block), _ptr(out), _ptr(lse),
@@ -707,10 +736,10 @@ def nd_compressed_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, win
     B, T, Hq, d = q.shape
     Hkv = k.shape[2]
     if out is None:
-        out = torch.empty_like(q)
+        out = _like(q, stream)
     if workspace is None:
         nbytes = nd_compressed_prefill_workspace_size(B, T, Hq, Hkv, d, rope_theta, block)
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(nbytes, q.device, stream)
     _check("nd_compressed_prefill", _lib().nd_compressed_prefill(
         _ptr(q), _ptr(k), _ptr(v), B, T, Hq, Hkv, d, int(window), int(block), int(n_pinned), float(rope_theta),
         _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), _stream(stream)))
@@ -730,11 +759,11 @@ def nd_swa_sink_chunk_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     against the cache, then ring-append the chunk to it; returns out."""
     B, Tc, Hq, d = q.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _like(q, stream)
     if workspace is None:
         nbytes = nd_swa_sink_chunk_prefill_workspace_size(B, Tc, Hq, cache.n_kv_heads, d, cache.sink_cap,
                                                           cache.ring_cap, window)
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(nbytes, q.device, stream)
     s = cache.struct()
     _check("nd_swa_sink_chunk_prefill", _lib().nd_swa_sink_chunk_prefill(
         _ptr(q), _ptr(k), _ptr(v), Tc, ctypes.byref(s), Hq, int(window), _ptr(out), _ptr(lse), _ptr(workspace),
@@ -755,7 +784,7 @@ def nd_rope_apply(x: torch.Tensor, y: Optional[torch.Tensor] = None, rope_theta:
                   stream=None) -> torch.Tensor:
     B, T, H, d = x.shape
     if y is None:
-        y = torch.empty_like(x)
+        y = _like(x, stream)
     _check("nd_rope_apply", _lib().nd_rope_apply(_ptr(x), _ptr(y), B, T, H, d, float(rope_theta),
                                                  _stream(stream)))
     return y
@@ -767,9 +796,9 @@ def nd_kv_compress_pool(k: torch.Tensor, v: torch.Tensor, block: int, rope_theta
     B, T, H, d = k.shape
     nb = T // block
     if pooled_k is None:
-        pooled_k = torch.empty((B, nb, H, d), dtype=k.dtype, device=k.device)
+        pooled_k = _empty((B, nb, H, d), k.dtype, k.device, stream)
     if pooled_v is None:
-        pooled_v = torch.empty((B, nb, H, d), dtype=v.dtype, device=v.device)
+        pooled_v = _empty((B, nb, H, d), v.dtype, v.device, stream)
     _check("nd_kv_compress_pool", _lib().nd_kv_compress_pool(
         _ptr(k), _ptr(v), B, T, H, d, int(block), float(rope_theta), _ptr(pooled_k), _ptr(pooled_v),
         _stream(stream)))
@@ -789,14 +818,13 @@ def nd_kv_compress_pool_rope(k: torch.Tensor, v: torch.Tensor, block: int, rope_
     B, T, H, d = k.shape
     nb = T // block
     if k_rot is None and rope_theta:
-        k_rot = torch.empty_like(k)
+        k_rot = _like(k, stream)
     if pooled_k is None:
-        pooled_k = torch.empty((B, nb, H, d), dtype=k.dtype, device=k.device)
+        pooled_k = _empty((B, nb, H, d), k.dtype, k.device, stream)
     if pooled_v is None:
-        pooled_v = torch.empty((B, nb, H, d), dtype=v.dtype, device=v.device)
+        pooled_v = _empty((B, nb, H, d), v.dtype, v.device, stream)
     if workspace is None:
-        workspace = torch.empty(max(nd_kv_compress_pool_rope_workspace_size(T, d, rope_theta), 16),
-                                dtype=torch.uint8, device=k.device)
+        workspace = _scratch(nd_kv_compress_pool_rope_workspace_size(T, d, rope_theta), k.device, stream)
     _check("nd_kv_compress_pool_rope", _lib().nd_kv_compress_pool_rope(
         _ptr(k), _ptr(v), B, T, H, d, int(block), float(rope_theta), _ptr(k_rot), _ptr(pooled_k), _ptr(pooled_v),
         _ptr(workspace), workspace.numel(), _stream(stream)))

@@ -1,0 +1,78 @@
+"""The binding's own work, without a GPU: what it allocates and where."""
+import contextlib
+
+import pytest
+import torch
+
+import sliding_window_kv_swa_gb300 as nd
+
+
+class FakeLibrary:
+    """Sizes are 4096, statuses ND_OK; nothing is launched."""
+    def __getattr__(self, name):
+        return lambda *a: 4096 if name.endswith("_size") else 0
+
+
+class OtherStream(torch.cuda.Stream if torch.cuda.is_available() else object):
+    cuda_stream = 77
+
+
+def calls(stream):
+    """Every entry point that makes a workspace or an output when it is given none."""
+    B, T, Hq, Hkv, d = 2, 16, 4, 2, 64
+    x = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    cache, prefix = nd.KVCache.empty(B, Hkv, d, 4, 8, device="cpu"), nd.KVCache.empty(1, Hkv, d, 600, 0, device="cpu")
+    comp = nd.CompressedCache.empty(B, Hkv, d, 4, 8, 4, device="cpu")
+    q, k, Q, K = x(B, Hq, d), x(B, Hkv, d), x(B, T, Hq, d), x(B, T, Hkv, d)
+    kw = dict(stream=stream)
+    return {
+        "nd_kv_cache_from_prefill": lambda: nd.nd_kv_cache_from_prefill(cache, K, K, i32(B), **kw),
+        "nd_swa_sink_decode": lambda: nd.nd_swa_sink_decode(q, cache, 8, **kw),
+        "nd_swa_sink_decode_step": lambda: nd.nd_swa_sink_decode_step(q, cache, k, k, 8, **kw),
+        "nd_swa_sink_decode_step_host": lambda: nd.nd_swa_sink_decode_step_host(q, cache, k, k, 8, x(B, Hq, d), **kw),
+        "nd_swa_sink_decode_step_host_packed":
+            lambda: nd.nd_swa_sink_decode_step_host_packed(x(B * (Hq + 2 * Hkv) * d), cache, Hq, 8, x(B, Hq, d), **kw),
+        "nd_kv_cache_read": lambda: nd.nd_kv_cache_read(cache, 8, **kw),
+        "nd_shared_prefix_decode": lambda: nd.nd_shared_prefix_decode(q, prefix, cache, 8, **kw),
+        "nd_qk_norm_rope": lambda: nd.nd_qk_norm_rope(Q, K, **kw),
+        "nd_qk_norm_rope_append": lambda: nd.nd_qk_norm_rope_append(q, cache, k, k, **kw),
+        "nd_compressed_decode_step": lambda: nd.nd_compressed_decode_step(q, comp, k, k, 8, **kw),
+        "nd_swa_sink_prefill": lambda: nd.nd_swa_sink_prefill(Q, K, K, **kw),
+        "nd_compressed_prefill": lambda: nd.nd_compressed_prefill(Q, K, K, 8, 4, **kw),
+        "nd_swa_sink_chunk_prefill": lambda: nd.nd_swa_sink_chunk_prefill(Q, K, K, cache, 8, **kw),
+        "nd_rope_apply": lambda: nd.nd_rope_apply(Q, **kw),
+        "nd_kv_compress_pool": lambda: nd.nd_kv_compress_pool(K, K, 4, **kw),
+        "nd_kv_compress_pool_rope": lambda: nd.nd_kv_compress_pool_rope(K, K, 4, 1e4, **kw),
+    }
+
+
+@pytest.mark.parametrize("name", sorted(calls(None)))
+def test_what_a_call_makes_belongs_to_the_stream_it_runs_on(name, monkeypatch):
+    """A workspace from another stream's memory would be handed on, when the call returns, to that stream's next tensor
+    while the call's kernels still use it."""
+    stream, inside, made = OtherStream.__new__(OtherStream), [], []
+
+    @contextlib.contextmanager
+    def on(s):
+        inside.append(s)
+        yield
+        inside.pop()
+
+    def watched(fn):
+        def make(*a, **kw):
+            made.append(bool(inside) and inside[-1].cuda_stream == stream.cuda_stream)
+            return fn(*a, **kw)
+        return make
+
+    m = nd.nd
+    call = calls(stream)[name]
+    monkeypatch.setattr(m, "_lib", FakeLibrary)
+    monkeypatch.setattr(m, "_ptr", lambda t: None if t is None else t.data_ptr())
+    monkeypatch.setattr(m, "_here", lambda t: -1)   # the index that a host tensor gives
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle: stream)
+    monkeypatch.setattr(torch, "empty", watched(torch.empty))
+    monkeypatch.setattr(torch, "empty_like", watched(torch.empty_like))
+    call()
+    assert made and all(made), f"{made.count(False)} of {len(made)} tensors made on the current stream"

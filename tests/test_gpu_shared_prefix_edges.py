@@ -1,5 +1,6 @@
 """Shared-prefix decode where the rest of the suite does not look: groups of
-query heads that lie across two row pairs of the prefix kernel.  Tolerances as
+query heads that lie across two row pairs of the prefix kernel, and a call on a
+stream that is not the current one.  Tolerances as
 in test_gpu_shared_prefix.py."""
 import pytest
 import torch
@@ -34,3 +35,25 @@ def test_a_group_whose_heads_have_different_numbers_of_partials(Hq, Hkv, d, L):
     first = host(nd().nd_shared_prefix_decode(qd, p, c, W, workspace=ws))
     for _ in range(20):
         assert (host(nd().nd_shared_prefix_decode(qd, p, c, W, workspace=ws)) == first).all()
+
+
+def test_a_call_on_another_stream_keeps_its_workspace():
+    """The call's stream is held up behind a timed wait; meanwhile the current stream asks for memory of every size
+    that the call used, and fills it."""
+    rng = philox(11100)
+    Hq, Hkv, d, B, L, W = 32, 8, 128, 20, 900, 32
+    prefix = random_cache(rng, 1, Hkv, d, L, 0, [(L, 0)])
+    own = random_cache(rng, B, Hkv, d, 0, W)
+    p, c, qd = device_cache(prefix), device_cache(own), dev_bf16(normal_bf16(rng, (B, Hq, d))[0])
+    size = nd().nd_shared_prefix_decode_workspace_size(B, Hq, Hkv, d, L, W)
+    assert size > 0
+    want = nd().nd_shared_prefix_decode(qd, p, c, W).clone()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(50_000_000)
+        out = nd().nd_shared_prefix_decode(qd, p, c, W, stream=s)
+        filled = [torch.full((n,), 0x7F, dtype=torch.uint8, device="cuda") for n in (size, size, out.nbytes, out.nbytes)]
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and all((f == 0x7F).all() for f in filled)
