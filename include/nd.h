@@ -601,7 +601,7 @@ ND_API int nd_rope_apply(const void *x, void *y, int batch, int T, int n_heads,
  *      to the next (token b*T + t; n_q_heads*head_dim when q is contiguous,
  *      the row length of a fused projection when q is a slice of one)
  *   k  likewise with n_k_heads and k_stride; either of q, k may have 0 heads
- *      (its pointers are then not read)
+ *      (its pointers, the weight among them, are then neither read nor checked)
  *   q_weight, k_weight  fp32 [head_dim], 16-byte aligned, or NULL (ones)
  *   positions  int32 [batch][T], or NULL (position t); any int32
  *   q_out, k_out  dtype [batch][T][heads][head_dim], contiguous; may equal q / k

@@ -766,6 +766,9 @@ int nd_qk_norm_rope(const void *q, const void *k, nd_dtype dtype, int batch, int
   if (batch < 0 || T < 0 || n_q_heads < 0 || n_k_heads < 0 || n_q_heads + int64_t(n_k_heads) > 65536) return ND_ERR_INVALID_ARG;
   if (head_dim <= 0 || head_dim % 32) return ND_ERR_INVALID_ARG;
   if (head_dim != 32 && head_dim != 64 && head_dim != 128 && head_dim != 256) return ND_ERR_UNSUPPORTED;
+  // what belongs to a side without heads is neither read nor checked
+  if (!n_q_heads) q_weight = nullptr;
+  if (!n_k_heads) k_weight = nullptr;
   if (!norm_args_ok(eps, rope_theta, q_weight, k_weight)) return ND_ERR_INVALID_ARG;
   if (size_t(batch) * T == 0 || n_q_heads + n_k_heads == 0) return ND_OK;
   if (int64_t(batch) * T > (1 << 30)) return ND_ERR_UNSUPPORTED;
