@@ -671,7 +671,10 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
 #pragma unroll
           for (int i = 0; i < BN; ++i) v[i] = i < left ? v[i] : 0xff800000u;
         }
-        const float ct = c_row * info.x;
+        // never 0, which would make NaN of the -inf of a slot behind the prefix:
+        // |S| < 2^37, so at 2^-126 and below a score is 2^-89 at most and its
+        // weight 1 to every bit, whatever the factor
+        const float ct = fmaxf(c_row * info.x, 1.1754943508222875e-38f);
         down = info.z;
         float mxp[8];
 #pragma unroll

@@ -1,13 +1,16 @@
 """Shared-prefix decode where the rest of the suite does not look: groups of
-query heads that lie across two row pairs of the prefix kernel, and a call on a
-stream that is not the current one.  Tolerances as
-in test_gpu_shared_prefix.py."""
+query heads that lie across two row pairs of the prefix kernel, calls on a
+stream that is not the current one, scores that vanish.  Tolerances as in
+test_gpu_shared_prefix.py."""
+import math
+
+import numpy as np
 import pytest
 import torch
 
 from gpu_util import dev_bf16, host, need_gpu, no_device_errors
 from test_gpu_shared_prefix import check, device_cache, nd, random_cache
-from workloads import normal_bf16, philox
+from workloads import normal_bf16, philox, to_bf16_bits
 
 pytestmark = pytest.mark.gpu
 
@@ -57,3 +60,36 @@ def test_a_call_on_another_stream_keeps_its_workspace():
         filled = [torch.full((n,), 0x7F, dtype=torch.uint8, device="cuda") for n in (size, size, out.nbytes, out.nbytes)]
         torch.cuda.synchronize()
         assert torch.equal(out, want) and all((f == 0x7F).all() for f in filled)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(8, 2, 64), (8, 2, 128)])
+@pytest.mark.parametrize("B", [3, 20, 70])   # rows of a KV head: up to 64, up to 128, more
+@pytest.mark.parametrize("L", [601, 1])      # the last tile is partly behind the prefix
+@pytest.mark.parametrize("keys", ["normal", "tiny", "zero"])
+def test_queries_and_keys_that_are_zero_or_tiny(Hq, Hkv, d, B, L, keys):
+    """Scores that are 0, or too small to be seen in fp32: the weights of all keys are then the same, and nothing that
+    stands behind the prefix counts."""
+    rng = philox(11200 + B + L + d)
+    prefix = random_cache(rng, 1, Hkv, d, 900, 0, [(L, 0)])
+    prefix.k_scale *= np.float32({"normal": 1.0, "tiny": 2.0 ** -30, "zero": 0.0}[keys])
+    own = random_cache(rng, B, Hkv, d, 0, 16, [(0, 0), (0, 5), (0, 40)])
+    q = normal_bf16(rng, (B, Hq, d))[1]
+    q[:, 0] = 0.0
+    q[:, 1] *= 2.0 ** -30
+    q[0] = 0.0
+    q[1] *= 2.0 ** -100
+    check(prefix, own, to_bf16_bits(q), q, 16, f"{keys} keys")
+
+
+def test_a_zeroed_prefix_and_a_zero_query():
+    """What a warm-up or a padded session gives: uniform weights over values that are all 0."""
+    n = nd()
+    for B in (3, 20, 70):
+        prefix, own = n.KVCache.empty(1, 2, 64, 900, 0), n.KVCache.empty(B, 2, 64, 0, 16)
+        prefix.sink_len.fill_(601)
+        lse = torch.empty(B, 8, device="cuda")
+        out = n.nd_shared_prefix_decode(torch.zeros(B, 8, 64, dtype=torch.bfloat16, device="cuda"), prefix, own, 16, lse=lse)
+        assert (out == 0).all()
+        # the sum, 601 * 2^7, is exact; its log2 (16.2) within 2 ulp of 2^-19, the sum with the maximum and the product
+        # with log 2 within half an ulp each: below 6e-6
+        torch.testing.assert_close(lse, torch.full_like(lse, math.log(601.0)), rtol=0, atol=1e-5)
