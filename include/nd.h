@@ -362,7 +362,8 @@ ND_API int nd_kv_cache_read(const nd_kv_cache *cache, int window, nd_dtype dtype
  *           position fills it from a prefill of the prompt.
  *   q, out, lse, window, n_q_heads  as nd_swa_sink_decode; batch * n_q_heads at
  *           most 2^24
- * A sequence that sees no key gets out = 0, lse = -inf.  The prefix's keys
+ * A sequence that sees no key gets out = 0, lse = -inf, and so does a query
+ * head with a NaN or an infinity, as in nd_swa_sink_decode.  The prefix's keys
  * and values are taken as fp16 after a power-of-two scaling (each within 2^-10
  * of code * scale, relative; a prefix that is short and shared by few
  * sequences exactly, as nd_swa_sink_decode takes its slots), products and sums

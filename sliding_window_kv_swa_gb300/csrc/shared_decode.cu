@@ -377,12 +377,16 @@ struct RowState {
     m = mn;
   }
   __device__ __forceinline__ void write_out(const OwnParams &p, size_t row, int lane) const {
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    // no key seen, or a query with a NaN or an infinity, whose sum is NaN: 0,
+    // whatever O holds
+    const bool seen = l > 0.f;
+    const float inv = 1.f / l;
 #pragma unroll
     for (int i = 0; i < I; ++i)
       *reinterpret_cast<uint2 *>(p.out + row * D + channel(lane, i)) =
-          make_uint2(pack_bf16x2(o[i][0] * inv, o[i][1] * inv), pack_bf16x2(o[i][2] * inv, o[i][3] * inv));
-    if (lane < 4 && p.lse) p.lse[row] = l > 0.f ? (m + __log2f(l)) * 0.6931471805599453f : -INFINITY;
+          seen ? make_uint2(pack_bf16x2(o[i][0] * inv, o[i][1] * inv), pack_bf16x2(o[i][2] * inv, o[i][3] * inv))
+               : make_uint2(0u, 0u);
+    if (lane < 4 && p.lse) p.lse[row] = seen ? (m + __log2f(l)) * 0.6931471805599453f : -INFINITY;
   }
 };
 
@@ -413,14 +417,16 @@ __device__ __forceinline__ void add_parts(const OwnParams &p, const PrefixPlan &
 
 template <int C>
 __device__ __forceinline__ void write_out(const OwnParams &p, size_t row, int lane, const LaneState<C> &st) {
-  const float inv = st.l > 0.f ? 1.f / st.l : 0.f;
+  const bool seen = st.l > 0.f;  // else 0, whatever O holds (see RowState)
+  const float inv = 1.f / st.l;
   uint16_t *out = p.out + row * (32 * C) + C * lane;
   if constexpr (C == 4)
-    *reinterpret_cast<uint2 *>(out) = make_uint2(pack_bf16x2(st.o[0] * inv, st.o[1] * inv),
-                                                 pack_bf16x2(st.o[2] * inv, st.o[3] * inv));
+    *reinterpret_cast<uint2 *>(out) = seen ? make_uint2(pack_bf16x2(st.o[0] * inv, st.o[1] * inv),
+                                                        pack_bf16x2(st.o[2] * inv, st.o[3] * inv))
+                                           : make_uint2(0u, 0u);
   else
-    *reinterpret_cast<uint32_t *>(out) = pack_bf16x2(st.o[0] * inv, st.o[1] * inv);
-  if (lane == 0 && p.lse) p.lse[row] = st.l > 0.f ? (st.m + __log2f(st.l)) * 0.6931471805599453f : -INFINITY;
+    *reinterpret_cast<uint32_t *>(out) = seen ? pack_bf16x2(st.o[0] * inv, st.o[1] * inv) : 0u;
+  if (lane == 0 && p.lse) p.lse[row] = seen ? (st.m + __log2f(st.l)) * 0.6931471805599453f : -INFINITY;
 }
 
 template <int D, int NW, int ST, int kCtas, bool kInline>

@@ -9,7 +9,7 @@ import pytest
 import torch
 
 from gpu_util import dev_bf16, host, need_gpu, no_device_errors
-from test_gpu_shared_prefix import check, device_cache, nd, random_cache
+from test_gpu_shared_prefix import check, device_cache, joined, nd, random_cache
 from workloads import normal_bf16, philox, to_bf16_bits
 
 pytestmark = pytest.mark.gpu
@@ -93,3 +93,37 @@ def test_a_zeroed_prefix_and_a_zero_query():
         # the sum, 601 * 2^7, is exact; its log2 (16.2) within 2 ulp of 2^-19, the sum with the maximum and the product
         # with log 2 within half an ulp each: below 6e-6
         torch.testing.assert_close(lse, torch.full_like(lse, math.log(601.0)), rtol=0, atol=1e-5)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,B,cap,L,W", [
+    (8, 2, 64, 2, 64, 64, 16),        # a short prefix, read by each pair
+    (8, 2, 128, 1, 300, 290, 600),    # the same in parts that a merge kernel joins
+    (8, 2, 128, 1, 900, 900, 600),    # parts, and a prefix of its own kernel: two streams
+    (8, 2, 64, 3, 900, 601, 24),      # two streams, a unit for a CTA
+    (8, 2, 64, 20, 900, 601, 24),     # one row block
+    (8, 2, 128, 70, 900, 601, 24),    # two row blocks
+    (16, 8, 128, 480, 600, 600, 40),  # more pairs than warps
+    (16, 8, 64, 480, 600, 601, 41)])
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+def test_queries_that_are_not_finite(Hq, Hkv, d, B, cap, L, W, value):
+    """As in nd_swa_sink_decode, out = 0 and lse = -inf for such a head, with and without own slots; the heads beside it
+    keep their bits."""
+    rng = philox(11300 + d + B)
+    L = min(L, cap)
+    prefix = random_cache(rng, 1, Hkv, d, cap, 0, [(L, 0)])
+    own = random_cache(rng, B, Hkv, d, 0, W, [(0, W), (0, 0), (0, 2 * W)])
+    q = dev_bf16(normal_bf16(rng, (B, Hq, d))[0])
+    bad = torch.zeros(B, Hq, dtype=torch.bool, device="cuda")
+    bad[:, 1] = bad[0, Hq - 1] = bad[B - 1, 0] = True
+    qbad = q.clone()
+    qbad[:, 1, 5] = qbad[0, Hq - 1, d - 1] = value
+    qbad[B - 1, 0] = value
+    p, c = device_cache(prefix), device_cache(own)
+    lse, want_lse = torch.empty(B, Hq, device="cuda"), torch.empty(B, Hq, device="cuda")
+    out = nd().nd_shared_prefix_decode(qbad, p, c, W, lse=lse)
+    want = nd().nd_shared_prefix_decode(q, p, c, W, lse=want_lse)
+    assert torch.equal(out[~bad], want[~bad]) and torch.equal(lse[~bad], want_lse[~bad])
+    assert (out[bad] == 0).all() and (lse[bad] == -math.inf).all()
+    whole = device_cache(joined(prefix, own))
+    plain = nd().nd_swa_sink_decode(qbad, whole, W, lse=lse)
+    assert (plain[bad] == 0).all() and (lse[bad] == -math.inf).all()
