@@ -248,6 +248,12 @@ class KVCache:
             self._kept = kept = (key, ctypes.byref(self.struct()))
         return kept[1]
 
+    def __getstate__(self):
+        # copies and pickles take the fields alone: the kept reference is to this cache's struct, and cannot be pickled
+        state = self.__dict__.copy()
+        state.pop("_kept", None)
+        return state
+
 
 @dataclass
 class CompressedCache:

@@ -1,5 +1,9 @@
-"""The binding's own work, without a GPU: what it allocates and where."""
+"""The binding's own work, without a GPU: what it allocates and where, and what
+it keeps in a cache."""
 import contextlib
+import copy
+import io
+import pickle
 
 import pytest
 import torch
@@ -76,3 +80,26 @@ def test_what_a_call_makes_belongs_to_the_stream_it_runs_on(name, monkeypatch):
     monkeypatch.setattr(torch, "empty_like", watched(torch.empty_like))
     call()
     assert made and all(made), f"{made.count(False)} of {len(made)} tensors made on the current stream"
+
+
+def test_a_cache_that_a_call_has_seen_can_be_copied_and_saved():
+    """deepcopy, pickle and torch.save of a cache after its address was kept for the calls; the copy's own address."""
+    cache = nd.KVCache.empty(2, 2, 64, 4, 8, device="cpu")
+    cache.k_codes.random_(-127, 128)
+    before = set(vars(cache))
+    cache.struct_ref()
+    for copied in (copy.deepcopy(cache), pickle.loads(pickle.dumps(cache)), copy.copy(cache), saved(cache)):
+        assert set(vars(copied)) == before and (copied.sink_cap, copied.ring_cap) == (4, 8)
+        assert torch.equal(copied.k_codes, cache.k_codes)
+        s = copied.struct_ref()._obj
+        assert s.k_codes == copied.k_codes.data_ptr() and s.seq_len == copied.seq_len.data_ptr()
+    assert cache.struct_ref() is cache.struct_ref()
+    comp = nd.CompressedCache.empty(2, 2, 64, 4, 8, 4, device="cpu")
+    comp.kv.struct_ref()
+    copy.deepcopy(comp), pickle.dumps(comp)
+
+
+def saved(cache):
+    f = io.BytesIO()
+    torch.save(cache, f)
+    return torch.load(io.BytesIO(f.getvalue()), weights_only=False)
