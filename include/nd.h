@@ -363,11 +363,15 @@ ND_API int nd_kv_cache_read(const nd_kv_cache *cache, int window, nd_dtype dtype
  *   q, out, lse, window, n_q_heads  as nd_swa_sink_decode; batch * n_q_heads at
  *           most 2^24
  * A sequence that sees no key gets out = 0, lse = -inf, and so does a query
- * head with a NaN or an infinity, as in nd_swa_sink_decode.  The prefix's keys
- * and values are taken as fp16 after a power-of-two scaling (each within 2^-10
- * of code * scale, relative; a prefix that is short and shared by few
- * sequences exactly, as nd_swa_sink_decode takes its slots), products and sums
- * in fp32.
+ * head with a NaN or an infinity, as in nd_swa_sink_decode.
+ * Precision: a prefix that is short and shared by few sequences is taken as
+ * nd_swa_sink_decode takes its slots.  Otherwise its keys and values become
+ * fp16 after a power-of-two scaling, one of each 64 keys and one that follows
+ * the largest value of the KV head's prefix: a key is within 2^-10 of
+ * code * scale or 2^-31 of the largest among its 64, whichever is more, a
+ * value within 2^-10 of itself or 2^-28 of the largest of the KV head's prefix
+ * (values that are smaller than that beside it count as 0).  A weight is
+ * within 2^-11 of itself or 2^-32 of the largest; products and sums are fp32.
  * Partial results go to the workspace (device, 16-byte aligned) of
  * nd_shared_prefix_decode_workspace_size(batch, n_q_heads, n_kv_heads,
  * head_dim, prefix->sink_cap, cache->sink_cap + cache->ring_cap) bytes (0: none

@@ -17,7 +17,12 @@
 // operands would cost.  e is chosen per 64-key tile for K (its inverse is one
 // factor of the tile's scores) and follows the largest value scale seen for V,
 // with 4 bits of headroom, so that O is rescaled for it only where scales grow
-// by more than 2^3.  P is fp16 with the running maximum up to 2^8 behind and
+// by more than 2^3.  Far below the largest the operands are subnormal and off
+// by 2^-25 in place of 2^-11 of themselves: with the tile's largest key scale
+// in [2^7, 2^8), 127 * 2^-25 of a code's scale and 2^-25 of the product are
+// below 2^-31 of the tile's largest key; with the largest value scale at 2^4
+// or more, below 2^-28 of the largest value, under what an fp32 sum that holds
+// both can tell apart.  P is fp16 with the running maximum up to 2^8 behind and
 // all of it scaled by 2^7, so it stays below 2^15 and keys 2^-21 below the
 // maximum still have all bits.  Sums, maxima and partials are fp32.
 //

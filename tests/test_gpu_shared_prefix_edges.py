@@ -1,15 +1,17 @@
 """Shared-prefix decode where the rest of the suite does not look: groups of
 query heads that lie across two row pairs of the prefix kernel, calls on a
-stream that is not the current one, scores that vanish.  Tolerances as in
-test_gpu_shared_prefix.py."""
+stream that is not the current one, scores that vanish, queries that are not
+finite, values far smaller than others.  Tolerances as in
+test_gpu_shared_prefix.py where nothing else is said."""
 import math
 
 import numpy as np
 import pytest
 import torch
 
+import oracle
 from gpu_util import dev_bf16, host, need_gpu, no_device_errors
-from test_gpu_shared_prefix import check, device_cache, joined, nd, random_cache
+from test_gpu_shared_prefix import check, device_cache, joined, nd, random_cache, run
 from workloads import normal_bf16, philox, to_bf16_bits
 
 pytestmark = pytest.mark.gpu
@@ -127,3 +129,30 @@ def test_queries_that_are_not_finite(Hq, Hkv, d, B, cap, L, W, value):
     whole = device_cache(joined(prefix, own))
     plain = nd().nd_swa_sink_decode(qbad, whole, W, lse=lse)
     assert (plain[bad] == 0).all() and (lse[bad] == -math.inf).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B", [3, 20, 70])
+@pytest.mark.parametrize("at", [0, 300, 600])
+@pytest.mark.parametrize("far", [12, 20, 28])
+def test_small_values_beside_one_large_value(d, B, at, far):
+    """A query that attends to small values only, with one key of the prefix, far from the query, whose value is 2^far
+    times as large: each value is within 2^-10 of itself or 2^-28 of the largest.  All keys but the far one are the
+    same, so their weights are, and the far one's is e^-64.  Compared head by head: the values' bound over their mean
+    magnitude, the weights' rounding 2^-11 and the fp32 sums' 2^-14 likewise, and the output's own half step."""
+    Hq, Hkv, L = 8, 2, 601
+    rng = philox(11400 + d + at)
+    prefix, own = random_cache(rng, 1, Hkv, d, 700, 0, [(L, 0)]), random_cache(rng, B, Hkv, d, 0, 8, [(0, 0)])
+    prefix.k_codes[...] = 127
+    prefix.k_codes[:, :, at] = -127
+    prefix.k_scale[...] = 4.0 / 127 / np.sqrt(d / 64)     # score 4 * 8 or -4 * 8 for a query of ones
+    prefix.v_scale[:, :, at] *= np.float32(2.0 ** far)
+    q = np.ones((B, Hq, d), np.float32)
+    out, _ = run(prefix, own, to_bf16_bits(q), 8)
+    want, _ = oracle.decode(q[:1], joined(prefix, random_cache(rng, 1, Hkv, d, 0, 8, [(0, 0)])), 8)
+    v = prefix.v_codes[0, :, :L].astype(np.float64) * np.repeat(prefix.v_scale[0, :, :L].astype(np.float64), 32, -1)
+    small = np.delete(np.abs(v), at, 1).mean(1)            # [Hkv][d]
+    largest = np.abs(v).max((1, 2))                        # [Hkv]
+    tol = (2.0 ** -10 + 2.0 ** -11 + 2.0 ** -14) * small + 2.0 ** -28 * largest[:, None]
+    err = np.abs(out - want)
+    assert (err <= np.repeat(tol, Hq // Hkv, 0)[None] + 2.0 ** -8 * np.abs(want)).all(), err.max()
