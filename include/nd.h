@@ -362,6 +362,7 @@ ND_API int nd_kv_cache_read(const nd_kv_cache *cache, int window, nd_dtype dtype
  *           position fills it from a prefill of the prompt.
  *   q, out, lse, window, n_q_heads  as nd_swa_sink_decode; batch * n_q_heads at
  *           most 2^24
+ *   slots   sink_cap + ring_cap of either at most 2^31 - 4097
  * A sequence that sees no key gets out = 0, lse = -inf, and so does a query
  * head with a NaN or an infinity, as in nd_swa_sink_decode.
  * Precision: a prefix that is short and shared by few sequences is taken as
@@ -634,6 +635,7 @@ ND_API int nd_qk_norm_rope(const void *q, const void *k, nd_dtype dtype, int bat
  *   pos_base  device int32, or NULL (0): what stands before the cache's first
  *          token, e.g. the seq_len of a shared prefix
  *   q_out  bf16 [batch][n_q_heads][head_dim], contiguous
+ * At most 65536 heads of either kind.
  * A rejected sink append writes nothing for that sequence, q_out included, and
  * sets device error flag 2.
  */

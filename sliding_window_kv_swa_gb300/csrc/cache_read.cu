@@ -120,7 +120,7 @@ cudaError_t launch_cache_read(const nd_kv_cache &c, int window, bool f32, int n_
   p.pos = positions;
   p.len = lengths;
   p.err = err;
-  const dim3 grid(unsigned((n_rows + kTile - 1) / kTile), unsigned(c.batch));
+  const dim3 grid(unsigned((n_rows - 1) / kTile + 1), unsigned(c.batch));  // (n_rows may be the largest int)
   return f32 ? launch_read_t<float>(p, grid, stream) : launch_read_t<uint16_t>(p, grid, stream);
 }
 

@@ -3,6 +3,7 @@
 // Nothing here allocates memory; nothing here synchronises except
 // nd_device_errors().
 #include <cuda_runtime.h>
+#include <limits.h>
 #include <stdint.h>
 
 #include <mutex>
@@ -791,7 +792,7 @@ int nd_qk_norm_rope_append(const void *q, const nd_kv_cache *cache, const void *
   int st = validate_cache(cache);
   if (st != ND_OK) return st;
   const int d = cache->head_dim, Hkv = cache->n_kv_heads;
-  if (n_q_heads <= 0 || n_q_heads > 65536) return ND_ERR_INVALID_ARG;
+  if (n_q_heads <= 0 || n_q_heads > 65536 || Hkv > 65536) return ND_ERR_INVALID_ARG;
   if (!to_sink && cache->ring_cap <= 0) return ND_ERR_INVALID_ARG;
   if (to_sink && cache->sink_cap <= 0) return ND_ERR_INVALID_ARG;
   if (d != 32 && d != 64 && d != 128 && d != 256) return ND_ERR_UNSUPPORTED;
@@ -826,10 +827,14 @@ int nd_kv_cache_read(const nd_kv_cache *cache, int window, nd_dtype dtype, int n
                                   device_error_word(), reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// Slots of a region that the shared-prefix decode walks, by steps and tiles
+// that may end behind the last one: below the end of the int range.
+static constexpr int kMostSlots = INT_MAX - 4096;
+
 size_t nd_shared_prefix_decode_workspace_size(int batch, int n_q_heads, int n_kv_heads, int head_dim,
                                               int prefix_cap, int max_slots) {
   if (batch <= 0 || n_q_heads <= 0 || n_kv_heads <= 0 || n_q_heads % n_kv_heads || head_dim <= 0 || prefix_cap <= 0 ||
-      max_slots <= 0)
+      max_slots <= 0 || prefix_cap > kMostSlots || max_slots > kMostSlots)
     return 0;
   return round_up(shared_decode_workspace_bytes(batch, n_q_heads, n_kv_heads, head_dim, prefix_cap, max_slots), 256);
 }
@@ -837,9 +842,12 @@ size_t nd_shared_prefix_decode_workspace_size(int batch, int n_q_heads, int n_kv
 int nd_shared_prefix_decode(const void *q, const nd_kv_cache *prefix, const nd_kv_cache *cache, int n_q_heads,
                             int window, void *out, float *lse, void *workspace, size_t workspace_bytes,
                             nd_stream_t stream) {
-  int st = validate_decode(q, cache, n_q_heads, window, out);
+  int st = validate_cache(cache);
   if (st != ND_OK) return st;
   if ((st = validate_cache(prefix)) != ND_OK) return st;
+  if (int64_t(prefix->sink_cap) + prefix->ring_cap > kMostSlots || int64_t(cache->sink_cap) + cache->ring_cap > kMostSlots)
+    return ND_ERR_UNSUPPORTED;
+  if ((st = validate_decode(q, cache, n_q_heads, window, out)) != ND_OK) return st;
   if (prefix->batch != 1 || prefix->sink_cap < 1 || prefix->n_kv_heads != cache->n_kv_heads ||
       prefix->head_dim != cache->head_dim)
     return ND_ERR_INVALID_ARG;
