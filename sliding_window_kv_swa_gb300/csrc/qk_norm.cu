@@ -16,9 +16,11 @@
 // 1, is one 64-bit integer product: the host scales freq / (2 pi) to 2^64 and
 // the wrap-around of the multiply is the reduction.  Its upper 32 bits give
 // the angle to 2^-32 of a turn at any 32-bit position (the fp64 frequency
-// itself limits that to 2^-53 p turns); the pair of a 64-bit multiply and
-// sincospif costs no fp64 instruction, of which this part issues two per
-// clock and SM.
+// itself limits that to 2^-53 p turns); as the fp32 argument of sincospif it
+// keeps 24 bits of up to half a turn, so it is within 2^-26 of a turn, 9.4e-8
+// radians: a rounding or two more of the fp32 result.  The pair of a 64-bit
+// multiply and sincospif costs no fp64 instruction, of which this part issues
+// two per clock and SM.
 #include "nd_common.cuh"
 #include "nd_internal.h"
 

@@ -1,5 +1,5 @@
-"""The per-head norm with rotation where one side is absent.  Results are compared bit for bit with the
-same side's in a call that has both."""
+"""The per-head norm with rotation where one side is absent, and the rotation's
+angles by themselves."""
 import numpy as np
 import pytest
 import torch
@@ -35,3 +35,24 @@ def test_weights_of_a_side_that_is_absent(B, T):
         assert none is None and torch.equal(one, both_q)
         none, one = nd().nd_qk_norm_rope(None, q, other, wk, 1e-6, 10000.0)
         assert none is None and torch.equal(one, both_k)
+
+
+@pytest.mark.parametrize("d,theta", [(32, 10000.0), (128, 500000.0), (256, 2.0)])
+def test_angles(d, theta):
+    """A row of ones and zeros comes out as r (cos a, sin a).  The angle is rounded to fp32 in half turns, 24 bits of up
+    to one: 2 pi 2^-26 off; its frequency by 2^-49 of the position; sine and cosine by 2 ulp, 2^-22; the norm's 17
+    additions at D = 256, halved by the root, the root's and the two products' roundings, 12 of 2^-24.  Angles just
+    beside half a turn, where the first of these is largest, are sought out among the positions."""
+    rng = philox(9260 + d)
+    top = 1 << 22
+    freq = np.float64(theta) ** (-2.0 * np.arange(d // 2) / d)
+    pos = rng.integers(-top, top, 200000)
+    half = np.abs(np.abs(np.remainder(pos[:, None] * freq[:4] / (2 * np.pi), 1.0)) - 0.5).min(1)
+    pos = np.concatenate([pos[np.argsort(half)[:1000]], pos[:1000], [0, 1, -1, top]]).astype(np.int32)
+    x = torch.zeros(1, len(pos), 1, d, device="cuda")
+    x[..., : d // 2] = 1.0
+    _, y = nd().nd_qk_norm_rope(None, x, eps=0.0, rope_theta=theta, positions=dev(pos[None]))
+    a = pos.astype(np.float64)[:, None] * freq
+    want = np.concatenate([np.cos(a), np.sin(a)], -1) * np.sqrt(2.0)
+    err = np.abs(y[0, :, 0].double().cpu().numpy() - want)
+    assert err.max() <= np.sqrt(2.0) * (2 * np.pi * 2.0 ** -26 + top * 2.0 ** -49 + 2.0 ** -22 + 12 * 2.0 ** -24), err.max()
