@@ -156,3 +156,48 @@ def test_small_values_beside_one_large_value(d, B, at, far):
     tol = (2.0 ** -10 + 2.0 ** -11 + 2.0 ** -14) * small + 2.0 ** -28 * largest[:, None]
     err = np.abs(out - want)
     assert (err <= np.repeat(tol, Hq // Hkv, 0)[None] + 2.0 ** -8 * np.abs(want)).all(), err.max()
+
+
+def parts_of(cache, b, window):
+    """Sequence b's visible keys and values in fp64: [Hkv][keys][d] each, and the keys' scales [Hkv][keys][d/32]."""
+    kpos, sink = oracle.slot_positions(cache, b)
+    keep = oracle.decode_keep(int(cache.seq_len[b]) - 1, kpos, sink, window).astype(bool) & (kpos >= 0)
+    k, v = (c[b][:, keep] * np.repeat(s[b][:, keep].astype(np.float64), 32, -1)
+            for c, s in ((cache.k_codes, cache.k_scale), (cache.v_codes, cache.v_scale)))
+    return k, v, cache.k_scale[b][:, keep].astype(np.float64)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B", [4, 18, 40])        # rows of a KV head: up to 64, up to 128, more
+@pytest.mark.parametrize("L", [400, 830])         # read by each pair; by the prefix kernel
+@pytest.mark.parametrize("order", [1, -1])
+def test_scores_that_grow_or_fall_along_the_prefix_row_by_row(d, B, L, order):
+    """The running maximum moves by far more than a lazy rescale allows.  Every channel of every head is held to a bound
+    from its own keys.  A key's score is off by at most e = 2^-10 sum |q_i k_i| / sqrt(d) in the prefix kernel, or where
+    a pair walks it by the fp32 sums that carry 1152 sum q (four roundings of 2^-24 each): the larger, and 2^-20 for the
+    scores' own fp32.  Weights p_j then become p_j exp(+-2e_j) after the division by their sum, at most, so the output
+    moves by sum p_j (exp(2 e_j) - 1) |v_j - o|; the weights' and values' fp16 add 2^-11 and 2^-10, the sums 2^-14, of
+    sum p_j |v_j|, and the output its half step.  lse moves by at most the weighted e."""
+    Hq, Hkv, W = 8, 2, 8
+    rng = philox(11500 + d + B + L)
+    prefix, own = random_cache(rng, 1, Hkv, d, L, 0, [(L, 0)]), random_cache(rng, B, Hkv, d, 0, W)
+    prefix.k_scale *= np.linspace(0.01, 8.0, L)[::order][None, None, :, None].astype(np.float32)
+    qb, q = normal_bf16(rng, (B, Hq, d))
+    out, lse = run(prefix, own, qb, W)
+    whole = joined(prefix, own)
+    want, wlse = oracle.decode(q, whole, W)
+    for b in range(B):
+        k, v, scale = parts_of(whole, b, W)
+        k, v, scale = (np.repeat(x, Hq // Hkv, 0) for x in (k, v, scale))
+        qh = q[b].astype(np.float64)
+        s = np.einsum("hc,hjc->hj", qh, k) / np.sqrt(d)
+        p = np.exp(s - s.max(-1, keepdims=True))
+        p /= p.sum(-1, keepdims=True)
+        e16 = 2.0 ** -10 * np.einsum("hc,hjc->hj", np.abs(qh), np.abs(k))
+        e32 = 4 * 2.0 ** -24 * 1152 * np.einsum("hg,hjg->hj", np.abs(qh).reshape(Hq, -1, 32).sum(-1), scale)
+        e = np.maximum(e16, e32) / np.sqrt(d) + 2.0 ** -20 * np.abs(s).max(-1, keepdims=True)
+        tol = np.einsum("hj,hjc->hc", p * np.expm1(2 * e), np.abs(v - want[b][:, None]))
+        tol += (2.0 ** -11 + 2.0 ** -10 + 2.0 ** -14) * np.einsum("hj,hjc->hc", p, np.abs(v)) + 2.0 ** -8 * np.abs(want[b])
+        err = np.abs(out[b] - want[b])
+        assert (err <= tol).all(), (b, err.max(), (err / tol).max())
+        assert (np.abs(lse[b] - wlse[b]) <= (p * np.expm1(e)).sum(-1) + 2.0 ** -20 * np.abs(s).max(-1)).all()
