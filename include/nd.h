@@ -355,11 +355,14 @@ ND_API int nd_kv_cache_read(const nd_kv_cache *cache, int window, nd_dtype dtype
  * query attends one softmax over [the prefix's sink slots, its own sequence's
  * sink slots, its ring entries within `window`]; otherwise as
  * nd_swa_sink_decode, whose result on caches that each hold a copy of the
- * prefix in front of their own sinks this equals up to rounding.
+ * prefix in front of their own sinks this equals within the precision below.
  *   prefix  batch 1, sink_cap >= 1, the n_kv_heads and head_dim of cache.
  *           sink_len may be anything from 0 to sink_cap; the prefix's ring is
  *           not read.  nd_kv_cache_from_prefill with a sink flag on every
- *           position fills it from a prefill of the prompt.
+ *           position fills it from a prefill of the prompt (that call wants a
+ *           ring_cap of at least 1).  How the call is carried out, and so its
+ *           speed and precision, goes by batch and sink_cap, not by sink_len:
+ *           a region not much longer than its prefix is the faster one.
  *   q, out, lse, window, n_q_heads  as nd_swa_sink_decode; batch * n_q_heads at
  *           most 2^24
  *   slots   sink_cap + ring_cap of either at most 2^31 - 4097
@@ -615,7 +618,9 @@ ND_API int nd_rope_apply(const void *x, void *y, int batch, int T, int n_heads,
  * rope_theta 0 = no rotation.  eps >= 0.  Strides are multiples of 16 bytes.
  * head_dim 32, 64, 128 or 256; batch * T at most 2^30.  p *
  * theta^(-2i/head_dim) is reduced to a fraction of a turn in 64-bit integers;
- * sine and cosine are fp32.
+ * sine and cosine are fp32.  A row whose squares overflow fp32 (beyond 2^64)
+ * comes out 0; with eps = 0, a row whose squares vanish in fp32 (a zero row,
+ * all below 2^-75) is not finite.
  */
 ND_API int nd_qk_norm_rope(const void *q, const void *k, nd_dtype dtype, int batch, int T,
                            int n_q_heads, int n_k_heads, int head_dim, int64_t q_stride,

@@ -378,9 +378,11 @@ __device__ __forceinline__ void store_codes(const float *lo, const float *hi, in
 }
 
 // One CTA per sequence, D/16 lanes per row: the query heads, then K's, then
-// V's.  A step is a chain of latencies, so all loads go out at once: every
-// thread reads the sequence's four metadata words itself, beside its row and
-// weights; the last thing the CTA does is advance them.
+// V's.  A step is a chain of latencies, so the loads of the first pass go out
+// at once: every thread reads the sequence's four metadata words itself, beside
+// its row and weights; the last thing the CTA does is advance them.  Above 192
+// lanes the rows take further passes (32 + 8 + 8 heads of 128: two), whose
+// loads follow the pass before: 6.5 us for 512 sequences, the bytes 1.9.
 template <int D>
 __global__ void __launch_bounds__(192, 4) qk_norm_append_kernel(const __grid_constant__ NormAppendParams p) {
   constexpr int kLanes = D / 16;

@@ -16,12 +16,18 @@
 // walked by a CTA's warps together, so the last round is as long as its share.
 // The merge needs no memory of its own: of a warp's ST stages ST - 1 are being
 // filled, and the one just read holds its state.
-// 512 sequences of 256 slots, 8 heads of 128 (302 MB): 66 us, of which the
-// bytes take 44.  A warp's step takes 2000 cycles, three warps to a scheduler
-// whose issue slots it fills to 70 % (400 instructions of the products, their
-// operands and the softmax, 100 of the copies), and a quarter of the time goes
-// between units.  Copies by one lane and a tensor map, two steps to a softmax
-// update, and four CTAs to an SM (128 registers a thread spill) were no faster.
+// 512 sequences of 256 slots, 8 heads of 128 (302 MB): 66 us (4.6 TB/s), of
+// which the bytes take 44; the decode kernel, on walks of 1280 slots, moves the
+// same format at 5.5 TB/s.  While a warp walks, a step takes 2000 cycles, three
+// warps to a scheduler whose issue slots they fill to 70 % (400 instructions of
+// the products, their operands and the softmax, 100 of the copies); a walk is
+// 16 steps, and about a quarter of a warp's time goes between walks (metadata,
+// query, the merge, and the loads of the prefix's partials, which are asked for
+// only there), so over the whole kernel the slots are 41 % used and loads are
+// the longest stall.  Copies by one lane and a tensor map, two steps to a
+// softmax update, and four CTAs to an SM were no faster.  At 168 registers the
+// kernel spills 66 bytes a thread (82 at D = 64, at 96 registers), at the 128
+// of four CTAs more.
 //
 // A unit is a (sequence, KV head) pair, or a part of one where the pairs are
 // too few for the SMs; the parts' triples then go to the workspace and a merge
@@ -781,6 +787,10 @@ constexpr int kSpareTiles = 6;  // see below
 SharedPlan shared_plan(int batch, int G, int n_kv_heads, int head_dim, int prefix_cap, int max_slots) {
   SharedPlan s;
   const long long pairs = (long long)batch * n_kv_heads;
+  // The grids and the workspace have to be, so the path is chosen from the
+  // prefix's capacity; a short prefix in a long region takes the path of the
+  // long one (128 pairs of 128, 300 slots: in a region of 300 8.4 us, of 512
+  // 9.9, of 600 to 65536 13.6; 512 pairs 25.8, 25.6 and 25.8 to 26.7).
   // A prefix of up to 512 slots for up to 152 pairs is read again by each of
   // them (2 heads of 64: 64 slots 5.6 us against 10.2; 152 pairs of 128: 256
   // slots 8.2 against 13.7, 512 slots 10.0 against 13.9; 64 pairs of 64: 512

@@ -31,8 +31,10 @@
 // key); a CTA keeps two 128-row blocks and turns a tile's codes into fp16 once
 // for both.  Measured (ncu, D = 128): 512 rows over 32768 keys of 8 heads 58
 // us, the products' pipe 72 % active: S = Q K^T of 128 x 64 reads Q from shared
-// memory for every tile and runs at half the rate (N = 128 would not, but its
-// scores, two blocks and O are all of TMEM with no second buffer).  16 rows
+// memory for every tile and runs at half the rate (N = 128 would not, but the
+// scores of two blocks and O are all of one CTA's TMEM with no second buffer;
+// two CTAs with a block each would have the room, which has not been tried).
+// 16 rows
 // over 65536 keys: 42 us for 151 MB, 22 us of it the bytes; a tile costs 0.55
 // us of the chain copy - scales - turn - S - softmax - PV, in which no role is
 // busy for much more than half of it (Q from TMEM, other waits, deeper rings:
