@@ -245,8 +245,24 @@ class KVCache:
                self.ring_start.data_ptr(), self.ring_len.data_ptr(), self.seq_len.data_ptr())
         kept = self.__dict__.get("_kept")
         if kept is None or kept[0] != key:
+            self._check_layout()
             self._kept = kept = (key, ctypes.byref(self.struct()))
         return kept[1]
+
+    def _check_layout(self):
+        # the kernels go by the sizes: what is shorter would be read past its end
+        codes = self.k_codes
+        if codes.dim() != 4 or self.sink_cap < 0 or self.ring_cap < 0 or codes.shape[2] != self.sink_cap + self.ring_cap:
+            raise ValueError("KVCache.k_codes must have shape [B, Hkv, sink_cap + ring_cap, d]")
+        scales, rows = (*codes.shape[:3], codes.shape[3] // 32), codes.shape[:1]
+        for name, shape, dtype in (("k_codes", codes.shape, torch.int8), ("v_codes", codes.shape, torch.int8),
+                                   ("k_scale", scales, torch.float32), ("v_scale", scales, torch.float32),
+                                   ("sink_len", rows, torch.int32), ("ring_start", rows, torch.int32),
+                                   ("ring_len", rows, torch.int32), ("seq_len", rows, torch.int32)):
+            t = getattr(self, name)
+            if t.shape != shape or t.dtype != dtype or t.device != codes.device or not t.is_contiguous():
+                raise ValueError(f"KVCache.{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                                 f"{codes.device}")
 
     def __getstate__(self):
         # copies and pickles take the fields alone: the kept reference is to this cache's struct, and cannot be pickled

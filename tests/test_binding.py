@@ -103,3 +103,30 @@ def saved(cache):
     f = io.BytesIO()
     torch.save(cache, f)
     return torch.load(io.BytesIO(f.getvalue()), weights_only=False)
+
+
+@pytest.mark.parametrize("field", ["k_codes", "v_codes", "k_scale", "v_scale", "sink_len", "ring_start", "ring_len", "seq_len"])
+def test_a_cache_whose_tensors_are_not_in_the_layout_is_refused(field):
+    """The kernels go by the sizes alone: a tensor that is shorter would be read past its end, one with other strides
+    or another type read wrongly."""
+    def changed(make):
+        cache = nd.KVCache.empty(2, 2, 64, 4, 8, device="cpu")
+        setattr(cache, field, make(getattr(cache, field)))
+        return cache
+
+    wrong = [lambda t: t[:1], lambda t: t.repeat_interleave(2, -1)[..., ::2], lambda t: t.double(), lambda t: t.to("meta")]
+    for make in wrong:
+        with pytest.raises(ValueError):
+            changed(make).struct_ref()
+    assert changed(torch.clone).struct_ref()._obj.batch == 2
+
+
+def test_a_cache_whose_capacities_are_not_its_tensors_is_refused():
+    for sinks, ring in ((5, 8), (4, 7), (8, 4), (12, 0), (13, -1)):
+        cache = nd.KVCache.empty(2, 2, 64, 4, 8, device="cpu")
+        cache.sink_cap, cache.ring_cap = sinks, ring
+        if sinks + ring == 12 and ring >= 0:
+            assert cache.struct_ref()._obj.sink_cap == sinks
+        else:
+            with pytest.raises(ValueError):
+                cache.struct_ref()
