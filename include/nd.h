@@ -389,6 +389,110 @@ ND_API int nd_shared_prefix_decode(const void *q, const nd_kv_cache *prefix,
                                    size_t workspace_bytes, nd_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* Trees of drafted tokens                                                   */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * A step that verifies drafted tokens: each sequence has up to n nodes, node i
+ * continues the path of its parent parents[i] < i, and a root (parent -1)
+ * continues the cache.  The step is nd_tree_layout once, then per layer
+ * nd_rope_positions and nd_tree_decode, then nd_tree_accept once and
+ * nd_tree_commit per layer.  A node at depth t sits at position seq_len + t.
+ * n is at most ND_TREE_MAX_NODES.  Nodes from n_nodes[b] on are padding.
+ */
+#define ND_TREE_MAX_NODES 256
+
+/*
+ * Depths, positions and masks of trees from their parents.
+ *   parents    int32 [batch][n]: the parent's number, below the node's own, or -1
+ *   n_nodes    int32 [batch], or NULL (n each)
+ *   seq_len    int32 [batch], or NULL (0): the caches' seq_len
+ *   pos_base   device int32, or NULL (0): what stands before the caches' first token
+ *   window     >= 1: a node sees itself and its ancestors less than window above it
+ *   depth      int32 [batch][n]: 0 for a root, the parent's + 1 otherwise
+ *   positions  int32 [batch][n], or NULL: seq_len + *pos_base + depth
+ *   mask       uint32 [batch][n][ceil(n/32)]: bit j % 32 of word j / 32 of row i
+ *              is set iff node i sees node j
+ * Padding has depth -1, position -1 and an empty mask.  A parent that is
+ * neither -1 nor an earlier node sets device error flag 2 and makes padding of
+ * its node and that node's descendants; n_nodes[b] outside 0..n does so of the
+ * whole sequence.
+ */
+ND_API int nd_tree_layout(const int32_t *parents, const int32_t *n_nodes, const int32_t *seq_len,
+                          const int32_t *pos_base, int batch, int n, int window, int32_t *depth,
+                          int32_t *positions, uint32_t *mask, nd_stream_t stream);
+
+/*
+ * Attention of a tree's nodes: node i of sequence b, at position p = seq_len +
+ * depth[b][i], attends one softmax over the filled sink slots, the ring entries
+ * within `window` of p (p - position < window), and the nodes that its mask
+ * row names.  Nothing is appended.  For a chain (parents i - 1) this is
+ * nd_swa_sink_chunk_prefill without its append; for one node it is
+ * nd_swa_sink_decode with the node's key in place of its appended codes.
+ *   q      bf16 [batch][n][n_q_heads][head_dim]  (rotated at the positions, if
+ *          the model rotates)
+ *   k_new, v_new  bf16, rows of [n_kv_heads][head_dim], k_stride / v_stride
+ *          elements from one node to the next (node b*n + i), multiples of 8
+ *   depth  int32 [batch][n]; a negative one marks padding, whose row of q is not
+ *          used and whose key no node sees
+ *   mask   uint32 [batch][n][ceil(n/32)]: any set of nodes, as nd_tree_layout
+ *          lays it out; it alone decides which nodes are seen, and bits from n on
+ *          count nothing
+ *   out    bf16 [batch][n][n_q_heads][head_dim]
+ *   lse    fp32 [batch][n_q_heads][n] natural-log softmax denominator, or NULL
+ *   window >= 1; n_q_heads / n_kv_heads 1..8; head_dim 64 or 128; n 1..256;
+ *   batch * n_kv_heads at most 2^20; 1 <= sink_cap + ring_cap <= 2^31 - 4097
+ * A row that sees no key, and padding, get out = 0, lse = -inf, and so does a
+ * query head with a NaN or an infinity, as in nd_swa_sink_decode.
+ * Partial results go to the workspace (device, 16-byte aligned) of
+ * nd_tree_decode_workspace_size(batch, n, n_q_heads, n_kv_heads, head_dim,
+ * sink_cap + ring_cap) bytes (0: none is needed, NULL allowed).
+ */
+ND_API size_t nd_tree_decode_workspace_size(int batch, int n, int n_q_heads, int n_kv_heads,
+                                            int head_dim, int max_slots);
+ND_API int nd_tree_decode(const void *q, const nd_kv_cache *cache, const void *k_new,
+                          const void *v_new, int64_t k_stride, int64_t v_stride,
+                          const int32_t *depth, const uint32_t *mask, int n, int n_q_heads,
+                          int window, void *out, float *lse, void *workspace,
+                          size_t workspace_bytes, nd_stream_t stream);
+
+/*
+ * The longest path of drafted tokens that the model's own choices agree with
+ * (greedy verification).  A node holds iff its parent holds and its token is
+ * the parent's target; a root holds iff its token is root_target[b], or always
+ * when root_target is NULL (the root is then a token already decided).  Of the
+ * nodes that hold at depth < max_path the deepest is taken, the lowest number
+ * among equals.
+ *   parents, n_nodes  as nd_tree_layout
+ *   tokens     int32 [batch][n]: the drafted tokens
+ *   target     int32 [batch][n]: the model's choice behind each node
+ *   root_target  int32 [batch]: the model's choice behind the cache, or NULL
+ *   path       int32 [batch][max_path]: the nodes from the root down, -1 behind
+ *   path_len   int32 [batch]: how many (0: none holds)
+ *   next       int32 [batch], or NULL: the target of the path's last node, of an
+ *              empty path root_target (-1 if that is NULL)
+ * max_path >= 1.  Bad parents and n_nodes are handled as by nd_tree_layout.
+ */
+ND_API int nd_tree_accept(const int32_t *parents, const int32_t *n_nodes, const int32_t *tokens,
+                          const int32_t *target, const int32_t *root_target, int batch, int n,
+                          int max_path, int32_t *path, int32_t *path_len, int32_t *next,
+                          nd_stream_t stream);
+
+/*
+ * Appends a path of nodes to each sequence's ring: exactly as path_len[b] calls
+ * of nd_kv_append_quant with to_sink = 0 on the keys and values of nodes
+ * path[b][0], path[b][1], ...  Afterwards seq_len has advanced by path_len[b].
+ *   k_new, v_new, k_stride, v_stride, n  as nd_tree_decode
+ *   path      int32 [batch][max_path]; path_len int32 [batch], 0..max_path
+ * Requires ring_cap > 0, max_path >= 1, head_dim 32, 64, 128 or 256.  A
+ * path_len outside its range, or a node outside 0..n-1 among the first
+ * path_len, sets device error flag 2 and leaves the sequence untouched.
+ */
+ND_API int nd_tree_commit(const nd_kv_cache *cache, const void *k_new, const void *v_new,
+                          int64_t k_stride, int64_t v_stride, int n, const int32_t *path,
+                          const int32_t *path_len, int max_path, nd_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* Compressed-attention decode                                               */
 /* ------------------------------------------------------------------------ */
 
@@ -650,6 +754,47 @@ ND_API int nd_qk_norm_rope_append(const void *q, const nd_kv_cache *cache, const
                                   const float *k_weight, float eps, float rope_theta,
                                   const int32_t *pos_base, int to_sink, void *q_out,
                                   nd_stream_t stream);
+
+/*
+ * Rotary embedding of query and key heads at given positions, in the layouts
+ * and with the frequency scalings that models use, or its gradient.  For a
+ * token at position p, pair i of the first rotary_dim = r channels of each head
+ * is turned by the angle p * f_i and multiplied by `magnitude`; the channels
+ * from r on are copied.
+ *   interleaved = 0: pair i is channels (i, i + r/2); 1: (2i, 2i + 1)
+ *   f_i = theta^(-2i/r), and with scaling
+ *     ND_ROPE_LINEAR    f_i / factor
+ *     ND_ROPE_BY_PARTS  (1 - g) f_i / factor + g f_i, g = clamp((orig_len f_i /
+ *                       2 pi - low) / (high - low), 0, 1): a pair that turns
+ *                       more than `high` times over orig_len positions keeps
+ *                       its frequency, one that turns less than `low` times
+ *                       has it divided
+ *   inverse = 1: turned by -p * f_i instead (times magnitude): the gradient
+ *     with respect to the unrotated heads, given the one of the rotated
+ * r is a multiple of 16, at most head_dim; theta, factor, orig_len and
+ * magnitude are finite and > 0 and 0 <= low < high (the fields that a scaling does not use
+ * are not checked).
+ * q, k, strides, positions, q_out, k_out, dtype, head_dim and the sizes as
+ * nd_qk_norm_rope (either side may have 0 heads).  The angle is reduced to a
+ * fraction of a turn in 64-bit integers, within 2^-53 |p| turns and an fp32
+ * rounding; sine, cosine and the rotation are fp32, rounded once to dtype.
+ */
+typedef enum { ND_ROPE_PLAIN = 0, ND_ROPE_LINEAR = 1, ND_ROPE_BY_PARTS = 2 } nd_rope_scaling;
+typedef struct {
+  int rotary_dim;
+  int interleaved;
+  int inverse;
+  int scaling; /* nd_rope_scaling */
+  float theta;
+  float factor;
+  float low, high;
+  float orig_len;
+  float magnitude;
+} nd_rope_cfg;
+ND_API int nd_rope_positions(const void *q, const void *k, nd_dtype dtype, int batch, int T,
+                             int n_q_heads, int n_k_heads, int head_dim, int64_t q_stride,
+                             int64_t k_stride, const nd_rope_cfg *cfg, const int32_t *positions,
+                             void *q_out, void *k_out, nd_stream_t stream);
 
 /*
  * Block pooling with midpoint rotation ([C3] "Pool before rotating, not

@@ -6,7 +6,7 @@ The Python names mirror the C entry points (every name in EXPORTED); see nd.py.
 """
 from . import nd as _nd
 from .nd import (  # noqa: F401
-    CompressedCache, EXPORTED, KVCache, ND_BF16, ND_F32, NDError, library_path)
+    CompressedCache, EXPORTED, KVCache, ND_BF16, ND_F32, NDError, RopeConfig, library_path)
 
 for _name in EXPORTED:
     globals()[_name] = getattr(_nd, _name)

@@ -865,6 +865,128 @@ int nd_shared_prefix_decode(const void *q, const nd_kv_cache *prefix, const nd_k
                                      reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// finite and > 0 (NaN fails every comparison)
+static bool positive(float x) { return x > 0.f && x < 1e30f; }
+
+static int validate_rope(const nd_rope_cfg *c, int head_dim) {
+  if (!c || c->rotary_dim <= 0 || c->rotary_dim > head_dim) return ND_ERR_INVALID_ARG;
+  if ((c->interleaved != 0 && c->interleaved != 1) || (c->inverse != 0 && c->inverse != 1)) return ND_ERR_INVALID_ARG;
+  if (!positive(c->theta) || !positive(c->magnitude)) return ND_ERR_INVALID_ARG;
+  if (c->scaling != ND_ROPE_PLAIN && c->scaling != ND_ROPE_LINEAR && c->scaling != ND_ROPE_BY_PARTS) return ND_ERR_INVALID_ARG;
+  if (c->scaling != ND_ROPE_PLAIN && !positive(c->factor)) return ND_ERR_INVALID_ARG;
+  if (c->scaling == ND_ROPE_BY_PARTS && !(positive(c->orig_len) && c->low >= 0.f && c->low < c->high && c->high < 1e30f))
+    return ND_ERR_INVALID_ARG;
+  return c->rotary_dim % 16 ? ND_ERR_UNSUPPORTED : ND_OK;
+}
+
+int nd_rope_positions(const void *q, const void *k, nd_dtype dtype, int batch, int T, int n_q_heads, int n_k_heads,
+                      int head_dim, int64_t q_stride, int64_t k_stride, const nd_rope_cfg *cfg,
+                      const int32_t *positions, void *q_out, void *k_out, nd_stream_t stream) {
+  if (dtype != ND_F32 && dtype != ND_BF16) return ND_ERR_INVALID_ARG;
+  if (batch < 0 || T < 0 || n_q_heads < 0 || n_k_heads < 0 || n_q_heads + int64_t(n_k_heads) > 65536) return ND_ERR_INVALID_ARG;
+  if (head_dim <= 0 || head_dim % 32) return ND_ERR_INVALID_ARG;
+  if (head_dim != 32 && head_dim != 64 && head_dim != 128 && head_dim != 256) return ND_ERR_UNSUPPORTED;
+  int st = validate_rope(cfg, head_dim);
+  if (st != ND_OK) return st;
+  if (size_t(batch) * T == 0 || n_q_heads + n_k_heads == 0) return ND_OK;
+  if (int64_t(batch) * T > (1 << 30)) return ND_ERR_UNSUPPORTED;
+  const int elem = dtype == ND_F32 ? 4 : 2;
+  if (n_q_heads && (!q || !q_out || !aligned16(q) || !aligned16(q_out) || !stride_ok(q_stride, n_q_heads, head_dim, elem)))
+    return ND_ERR_INVALID_ARG;
+  if (n_k_heads && (!k || !k_out || !aligned16(k) || !aligned16(k_out) || !stride_ok(k_stride, n_k_heads, head_dim, elem)))
+    return ND_ERR_INVALID_ARG;
+  if ((st = check_device(nullptr)) != ND_OK) return st;
+  QkNormRope a = {q, k, q_stride, k_stride, batch, T, n_q_heads, n_k_heads, head_dim, nullptr, nullptr, 0.f,
+                  cfg->theta, positions, q_out, k_out};
+  return finish(launch_rope_positions(a, *cfg, dtype == ND_F32, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// Sequences of one launch of the tree operators (a grid's x and room for the
+// offsets of their nodes in 64 bits).
+static constexpr int kMostTrees = 1 << 24;
+
+static int validate_tree(int batch, int n) {
+  if (batch < 0 || n < 0) return ND_ERR_INVALID_ARG;
+  return n > ND_TREE_MAX_NODES || batch > kMostTrees ? ND_ERR_UNSUPPORTED : ND_OK;
+}
+
+int nd_tree_layout(const int32_t *parents, const int32_t *n_nodes, const int32_t *seq_len, const int32_t *pos_base,
+                   int batch, int n, int window, int32_t *depth, int32_t *positions, uint32_t *mask,
+                   nd_stream_t stream) {
+  int st = validate_tree(batch, n);
+  if (st != ND_OK) return st;
+  if (window < 1) return ND_ERR_INVALID_ARG;
+  if (batch == 0 || n == 0) return ND_OK;
+  if (!parents || !depth || !mask) return ND_ERR_INVALID_ARG;
+  if ((st = check_device(nullptr)) != ND_OK) return st;
+  return finish(launch_tree_layout(parents, n_nodes, seq_len, pos_base, batch, n, window, depth, positions, mask,
+                                   device_error_word(), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int nd_tree_accept(const int32_t *parents, const int32_t *n_nodes, const int32_t *tokens, const int32_t *target,
+                   const int32_t *root_target, int batch, int n, int max_path, int32_t *path, int32_t *path_len,
+                   int32_t *next, nd_stream_t stream) {
+  int st = validate_tree(batch, n);
+  if (st != ND_OK) return st;
+  if (max_path < 1) return ND_ERR_INVALID_ARG;
+  if (batch == 0) return ND_OK;
+  if ((n > 0 && (!parents || !tokens || !target)) || !path || !path_len) return ND_ERR_INVALID_ARG;
+  if ((st = check_device(nullptr)) != ND_OK) return st;
+  return finish(launch_tree_accept(parents, n_nodes, tokens, target, root_target, batch, n, max_path, path, path_len,
+                                   next, device_error_word(), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int nd_tree_commit(const nd_kv_cache *cache, const void *k_new, const void *v_new, int64_t k_stride, int64_t v_stride,
+                   int n, const int32_t *path, const int32_t *path_len, int max_path, nd_stream_t stream) {
+  int st = validate_cache(cache);
+  if (st != ND_OK) return st;
+  if ((st = validate_tree(cache->batch, n)) != ND_OK) return st;
+  const int d = cache->head_dim, Hkv = cache->n_kv_heads;
+  if (max_path < 1 || cache->ring_cap <= 0 || Hkv > 65536) return ND_ERR_INVALID_ARG;
+  if (d != 32 && d != 64 && d != 128 && d != 256) return ND_ERR_UNSUPPORTED;
+  if (cache->batch == 0) return ND_OK;
+  if (!path || !path_len) return ND_ERR_INVALID_ARG;
+  if (n > 0 && (!k_new || !v_new || !aligned16(k_new) || !aligned16(v_new) || !stride_ok(k_stride, Hkv, d, 2) ||
+                !stride_ok(v_stride, Hkv, d, 2)))
+    return ND_ERR_INVALID_ARG;
+  if ((st = check_device(nullptr)) != ND_OK) return st;
+  return finish(launch_tree_commit(*cache, k_new, v_new, k_stride, v_stride, n, path, path_len, max_path,
+                                   device_error_word(), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+static bool tree_sizes_ok(int64_t batch, int n_kv_heads, int64_t slots) {
+  return batch * n_kv_heads <= (1 << 20) && slots <= kMostSlots;
+}
+
+size_t nd_tree_decode_workspace_size(int batch, int n, int n_q_heads, int n_kv_heads, int head_dim, int max_slots) {
+  if (batch <= 0 || n <= 0 || n > ND_TREE_MAX_NODES || n_q_heads <= 0 || n_kv_heads <= 0 || n_q_heads % n_kv_heads ||
+      head_dim <= 0 || max_slots <= 0 || !tree_sizes_ok(batch, n_kv_heads, max_slots))
+    return 0;
+  return round_up(tree_decode_workspace_bytes(batch, n, n_q_heads, n_kv_heads, head_dim, max_slots), 256);
+}
+
+int nd_tree_decode(const void *q, const nd_kv_cache *cache, const void *k_new, const void *v_new, int64_t k_stride,
+                   int64_t v_stride, const int32_t *depth, const uint32_t *mask, int n, int n_q_heads, int window,
+                   void *out, float *lse, void *workspace, size_t workspace_bytes, nd_stream_t stream) {
+  int st = validate_cache(cache);
+  if (st != ND_OK) return st;
+  const int d = cache->head_dim, Hkv = cache->n_kv_heads;
+  if (n < 0 || window < 1 || n_q_heads <= 0 || n_q_heads % Hkv) return ND_ERR_INVALID_ARG;
+  if (n > ND_TREE_MAX_NODES || n_q_heads / Hkv > 8 || (d != 64 && d != 128)) return ND_ERR_UNSUPPORTED;
+  if (cache->batch == 0 || n == 0) return ND_OK;
+  if (!q || !k_new || !v_new || !out || !depth || !mask) return ND_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(out)) return ND_ERR_INVALID_ARG;
+  if (!stride_ok(k_stride, Hkv, d, 2) || !stride_ok(v_stride, Hkv, d, 2)) return ND_ERR_INVALID_ARG;
+  const int64_t slots = int64_t(cache->sink_cap) + cache->ring_cap;
+  if (slots < 1) return ND_ERR_INVALID_ARG;
+  if (!tree_sizes_ok(cache->batch, Hkv, slots)) return ND_ERR_UNSUPPORTED;
+  const size_t need = nd_tree_decode_workspace_size(cache->batch, n, n_q_heads, Hkv, d, int(slots));
+  if (need && (!workspace || workspace_bytes < need || !aligned16(workspace))) return ND_ERR_WORKSPACE;
+  if ((st = check_device(nullptr)) != ND_OK) return st;
+  const TreeDecodeArgs a = {q, k_new, v_new, k_stride, v_stride, depth, mask, n, n_q_heads, window, out, lse};
+  return finish(launch_tree_decode(a, *cache, workspace, device_error_word(), reinterpret_cast<cudaStream_t>(stream)));
+}
+
 int nd_kv_compress_pool(const void *k, const void *v, int batch, int T, int n_heads, int head_dim,
                         int block, float rope_theta, void *pooled_k, void *pooled_v,
                         nd_stream_t stream) {

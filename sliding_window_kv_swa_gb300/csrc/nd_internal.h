@@ -128,6 +128,31 @@ cudaError_t launch_qk_norm_rope(const QkNormRope &a, bool f32, cudaStream_t stre
 cudaError_t launch_qk_norm_append(const nd_kv_cache &c, const QkNormRope &a, const void *v, int64_t v_stride,
                                   const int32_t *pos_base, int to_sink, int *err, cudaStream_t stream);
 
+// The rotation alone, at given positions (weights and eps of `a` are not used).
+cudaError_t launch_rope_positions(const QkNormRope &a, const nd_rope_cfg &c, bool f32, cudaStream_t stream);
+
+// Trees of drafted tokens (tree.cu, tree_decode.cu).
+cudaError_t launch_tree_layout(const int32_t *parents, const int32_t *n_nodes, const int32_t *seq_len,
+                               const int32_t *pos_base, int batch, int n, int window, int32_t *depth,
+                               int32_t *positions, uint32_t *mask, int *err, cudaStream_t stream);
+cudaError_t launch_tree_accept(const int32_t *parents, const int32_t *n_nodes, const int32_t *tokens,
+                               const int32_t *target, const int32_t *root_target, int batch, int n, int max_path,
+                               int32_t *path, int32_t *path_len, int32_t *next, int *err, cudaStream_t stream);
+cudaError_t launch_tree_commit(const nd_kv_cache &c, const void *k, const void *v, int64_t k_stride, int64_t v_stride,
+                               int n, const int32_t *path, const int32_t *path_len, int max_path, int *err,
+                               cudaStream_t stream);
+struct TreeDecodeArgs {
+  const void *q, *k, *v;
+  int64_t k_stride, v_stride;  // elements from one node to the next
+  const int32_t *depth;
+  const uint32_t *mask;
+  int n, n_q_heads, window;
+  void *out;
+  float *lse;  // may be NULL
+};
+size_t tree_decode_workspace_bytes(int batch, int n, int n_q_heads, int n_kv_heads, int head_dim, int max_slots);
+cudaError_t launch_tree_decode(const TreeDecodeArgs &a, const nd_kv_cache &c, void *ws, int *err, cudaStream_t stream);
+
 // Reads the cache back in position order into [B][n_rows][Hkv][d].
 cudaError_t launch_cache_read(const nd_kv_cache &c, int window, bool f32, int n_rows, void *k, void *v,
                               int32_t *positions, int32_t *lengths, int *err, cudaStream_t stream);

@@ -12,28 +12,14 @@
 // rotation partners D/2 + 8j..; the norm's sum is then log2(D/16) shuffles
 // and the rotation stays inside the lane.
 //
-// Angles: the fraction of a turn that position p makes, p * freq / (2 pi) mod
-// 1, is one 64-bit integer product: the host scales freq / (2 pi) to 2^64 and
-// the wrap-around of the multiply is the reduction.  Its upper 32 bits give
-// the angle to 2^-32 of a turn at any 32-bit position (the fp64 frequency
-// itself limits that to 2^-53 p turns); as the fp32 argument of sincospif it
-// keeps 24 bits of up to half a turn, so it is within 2^-26 of a turn, 9.4e-8
-// radians: a rounding or two more of the fp32 result.  The pair of a 64-bit
-// multiply and sincospif costs no fp64 instruction, of which this part issues
-// two per clock and SM.
+// Angles: turns.cuh.
 #include "nd_common.cuh"
 #include "nd_internal.h"
-
-#include <math.h>
+#include "turns.cuh"
 
 namespace nd {
 
 namespace {
-
-// freq_i / (2 pi) mod 1, in units of 2^-64
-struct Turns {
-  unsigned long long f[kMaxHalf];
-};
 
 // The table of a model's head_dim and theta, kept per host thread: building it
 // takes a pow per channel pair, about as long as a decode step's kernel.
@@ -43,27 +29,10 @@ const Turns &make_turns(int head_dim, float theta) {
   static thread_local float t_theta = 0.f;
   if (t_dim == head_dim && t_theta == theta) return t;
   const Freqs fr = make_freqs(head_dim, theta);
-  for (int i = 0; i < kMaxHalf; ++i) {
-    double turn = 0.0;
-    if (theta != 0.f && i < head_dim / 2) {
-      turn = fr.f[i] * 0.15915494309189533576888376337251;
-      turn -= floor(turn);
-    }
-    // turn < 1, so the product is below 2^64 (it may only reach it by the
-    // rounding of the subtraction above, where the wrap to 0 is the same angle)
-    const double scaled = turn * 18446744073709551616.0;
-    t.f[i] = scaled >= 18446744073709551616.0 ? 0ull : (unsigned long long)scaled;
-  }
+  for (int i = 0; i < kMaxHalf; ++i) t.f[i] = turn_of(theta != 0.f && i < head_dim / 2 ? fr.f[i] : 0.0);
   t_dim = head_dim;
   t_theta = theta;
   return t;
-}
-
-__device__ __forceinline__ float2 turn_cs(int pos, unsigned long long f) {
-  const long long turn = (long long)((unsigned long long)(long long)pos * f);
-  float s, c;
-  sincospif(float(int(turn >> 32)) * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
-  return make_float2(c, s);
 }
 
 // Which channels lane j of a row's D / 16 lanes holds in each half: 16 bytes
@@ -119,14 +88,6 @@ __device__ __forceinline__ void store_half(float *p, const float *x) {
   *reinterpret_cast<float4 *>(p + Chan<float, D>::kStep) = make_float4(x[4], x[5], x[6], x[7]);
 }
 
-// The CTA's copy of the frequencies: indexed by lane, kernel parameters are
-// read one address at a time.
-template <int D>
-__device__ __forceinline__ void stage_turns(const Turns &t, unsigned long long *s_f) {
-  for (int i = threadIdx.x; i < D / 2; i += blockDim.x) s_f[i] = t.f[i];
-  __syncthreads();
-}
-
 // The angles of a lane's eight channel pairs at the position that all rows of
 // the warp have.  The lanes that hold the same pairs of other rows make an
 // eighth to a half of them each.
@@ -176,15 +137,6 @@ struct NormRopeParams {
   const int32_t *pos;
   Turns turns;
 };
-
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ uint4 lds16(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-  return v;
-}
 
 // Many heads: a warp takes a token, as batches of rows (kU * 32 / (D / 16)
 // heads of q, then of k).  HBM-bound: a row in and a row out; what it needs is

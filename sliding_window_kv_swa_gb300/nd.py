@@ -53,6 +53,13 @@ class _ModelCfg(ctypes.Structure):
                                              "kv_window")]
 
 
+class _RopeCfg(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("inverse", ctypes.c_int),
+                ("scaling", ctypes.c_int), ("theta", ctypes.c_float), ("factor", ctypes.c_float),
+                ("low", ctypes.c_float), ("high", ctypes.c_float), ("orig_len", ctypes.c_float),
+                ("magnitude", ctypes.c_float)]
+
+
 _LIB = None
 
 
@@ -97,6 +104,12 @@ def _lib():
             "nd_shared_prefix_decode": (I, [P, P, P, I, I, P, P, P, S, P]),
             "nd_qk_norm_rope": (I, [P, P, I, I, I, I, I, I, L, L, P, P, F, F, P, P, P, P]),
             "nd_qk_norm_rope_append": (I, [P, P, P, P, I, L, L, L, P, P, F, F, P, I, P, P]),
+            "nd_tree_layout": (I, [P, P, P, P, I, I, I, P, P, P, P]),
+            "nd_tree_decode_workspace_size": (S, [I, I, I, I, I, I]),
+            "nd_tree_decode": (I, [P, P, P, P, L, L, P, P, I, I, I, P, P, P, S, P]),
+            "nd_tree_accept": (I, [P, P, P, P, P, I, I, I, P, P, P, P]),
+            "nd_tree_commit": (I, [P, P, P, L, L, I, P, P, I, P]),
+            "nd_rope_positions": (I, [P, P, I, I, I, I, I, I, L, L, P, P, P, P, P]),
             "nd_rope_apply": (I, [P, P, I, I, I, I, F, P]),
             "nd_kv_compress_pool": (I, [P, P, I, I, I, I, I, F, P, P, P]),
             "nd_kv_compress_pool_rope_workspace_size": (S, [I, I, F]),
@@ -129,7 +142,8 @@ EXPORTED = ("nd_version", "nd_status_string", "nd_last_cuda_error", "nd_device_e
             "nd_swa_sink_chunk_prefill_workspace_size", "nd_swa_sink_chunk_prefill",
             "nd_swa_sink_chunk_prefill_tiles",
             "nd_kv_cache_read", "nd_shared_prefix_decode_workspace_size", "nd_shared_prefix_decode",
-            "nd_qk_norm_rope", "nd_qk_norm_rope_append",
+            "nd_tree_layout", "nd_tree_decode_workspace_size", "nd_tree_decode", "nd_tree_accept", "nd_tree_commit",
+            "nd_qk_norm_rope", "nd_qk_norm_rope_append", "nd_rope_positions",
             "nd_rope_apply", "nd_kv_compress_pool", "nd_kv_compress_pool_rope_workspace_size",
             "nd_kv_compress_pool_rope", "nd_kv_budget_window")
 
@@ -607,6 +621,21 @@ def _weight(w: Optional[torch.Tensor], name: str, d: int, dev: int) -> Optional[
     return None if w is None else _addr(w, name, (d,), torch.float32, dev)
 
 
+def _heads(t: Optional[torch.Tensor], out: Optional[torch.Tensor], name: str, B, T, d, dtype, dev: int, stream):
+    """(heads, token stride, address, output's address, output) of q or k [B, T, heads, d]; None: no heads."""
+    if t is None:
+        return 0, 0, None, None, None
+    shape = t.shape
+    if len(shape) != 4 or shape[0] != B or shape[1] != T or shape[3] != d or t.dtype != dtype or \
+            t.get_device() != dev:
+        raise ValueError(f"{name} must have shape [{B}, {T}, heads, {d}], q's type and device")
+    step = _step(t, name)
+    if out is None:
+        out = _like(t, stream, torch.contiguous_format)
+        return shape[2], step, t.data_ptr(), out.data_ptr(), out
+    return shape[2], step, t.data_ptr(), _addr(out, name + "_out", shape, dtype, dev), out
+
+
 def nd_qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], q_weight: Optional[torch.Tensor] = None,
                     k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, rope_theta: float = 0.0,
                     positions: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
@@ -622,21 +651,8 @@ def nd_qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], q_weig
     B, T, _, d = one.shape
     dtype = one.dtype
 
-    def side(t, out, name):
-        if t is None:
-            return 0, 0, None, None, None
-        shape = t.shape
-        if len(shape) != 4 or shape[0] != B or shape[1] != T or shape[3] != d or t.dtype != dtype or \
-                t.get_device() != dev:
-            raise ValueError(f"{name} must have shape [{B}, {T}, heads, {d}], q's type and device")
-        step = _step(t, name)
-        if out is None:
-            out = _like(t, stream, torch.contiguous_format)
-            return shape[2], step, t.data_ptr(), out.data_ptr(), out
-        return shape[2], step, t.data_ptr(), _addr(out, name + "_out", shape, dtype, dev), out
-
-    Hq, sq, pq, oq, q_out = side(q, q_out, "q")
-    Hk, sk, pk, ok, k_out = side(k, k_out, "k")
+    Hq, sq, pq, oq, q_out = _heads(q, q_out, "q", B, T, d, dtype, dev, stream)
+    Hk, sk, pk, ok, k_out = _heads(k, k_out, "k", B, T, d, dtype, dev, stream)
     _check("nd_qk_norm_rope", _lib().nd_qk_norm_rope(
         pq, pk, _dtype_code(one), B, T, Hq, Hk, d, sq, sk, _weight(q_weight, "q_weight", d, dev),
         _weight(k_weight, "k_weight", d, dev), eps, rope_theta,
@@ -678,6 +694,203 @@ def nd_qk_norm_rope_append(q: torch.Tensor, cache: KVCache, k_new: torch.Tensor,
         _weight(k_weight, "k_weight", d, dev), eps, rope_theta, base, 1 if to_sink else 0,
         at_out, _on(stream, dev)))
     return q_out
+
+
+TREE_MAX_NODES = 256                # ND_TREE_MAX_NODES in nd.h
+ROPE_SCALINGS = {"none": 0, "linear": 1, "by_parts": 2}
+
+
+@dataclass(frozen=True)
+class RopeConfig:
+    """How nd_rope_positions turns a head (nd_rope_cfg): its first rotary_dim
+    channels (0: all), paired across halves or as neighbours, with the plain
+    frequencies or scaled ones; inverse: the gradient's direction."""
+    theta: float = 10000.0
+    rotary_dim: int = 0
+    interleaved: bool = False
+    inverse: bool = False
+    scaling: str = "none"            # "none", "linear" or "by_parts"
+    factor: float = 1.0
+    low: float = 1.0
+    high: float = 32.0
+    orig_len: float = 4096.0
+    magnitude: float = 1.0
+
+    def struct(self, head_dim: int) -> _RopeCfg:
+        if self.scaling not in ROPE_SCALINGS:
+            raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}")
+        return _RopeCfg(self.rotary_dim or head_dim, int(self.interleaved), int(self.inverse), ROPE_SCALINGS[self.scaling],
+                        self.theta, self.factor, self.low, self.high, self.orig_len, self.magnitude)
+
+    def struct_ref(self, head_dim: int):
+        """A reference to the struct for ctypes, made once per head_dim (the fields are frozen)."""
+        kept = self.__dict__.get("_kept")
+        if kept is None or kept[0] != head_dim:
+            kept = (head_dim, ctypes.byref(self.struct(head_dim)))
+            object.__setattr__(self, "_kept", kept)
+        return kept[1]
+
+    def __getstate__(self):
+        state = self.__dict__.copy()  # (the kept reference cannot be pickled)
+        state.pop("_kept", None)
+        return state
+
+
+def nd_rope_positions(q: Optional[torch.Tensor], k: Optional[torch.Tensor], rope: RopeConfig = RopeConfig(),
+                      positions: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                      k_out: Optional[torch.Tensor] = None, stream=None):
+    """The heads of q [B, T, Hq, d] and k [B, T, Hk, d] (bf16 or fp32; slices of
+    a fused projection are taken as they are; either may be None) rotated at
+    positions int32 [B, T] (None: t) as `rope` says.  Returns (q_out, k_out),
+    contiguous.  For the gradient of the unrotated heads call it on the rotated
+    heads' gradient with inverse=True."""
+    one = q if q is not None else k
+    if one is None:
+        raise ValueError("q or k must be given")
+    dev = _here(one)
+    B, T, _, d = one.shape
+    dtype = one.dtype
+    Hq, sq, pq, oq, q_out = _heads(q, q_out, "q", B, T, d, dtype, dev, stream)
+    Hk, sk, pk, ok, k_out = _heads(k, k_out, "k", B, T, d, dtype, dev, stream)
+    _check("nd_rope_positions", _lib().nd_rope_positions(
+        pq, pk, _dtype_code(one), B, T, Hq, Hk, d, sq, sk, rope.struct_ref(d),
+        None if positions is None else _addr(positions, "positions", (B, T), torch.int32, dev), oq, ok,
+        _on(stream, dev)))
+    return q_out, k_out
+
+
+def _ints(t: Optional[torch.Tensor], name: str, shape, dev: int) -> Optional[int]:
+    return None if t is None else _addr(t, name, shape, torch.int32, dev)
+
+
+def _parents(parents: torch.Tensor):
+    dev = _here(parents)
+    if parents.dim() != 2:
+        raise ValueError("parents must have shape [B, n]")
+    return dev, parents.shape[0], parents.shape[1], _addr(parents, "parents", parents.shape, torch.int32, dev)
+
+
+def _one(t: Optional[torch.Tensor], name: str, dev: int) -> Optional[int]:
+    if t is None:
+        return None
+    if t.numel() != 1 or t.dtype != torch.int32 or t.get_device() != dev:
+        raise ValueError(f"{name} must be one int32 on cuda:{dev}")
+    return t.data_ptr()
+
+
+def _made(t: Optional[torch.Tensor], name: str, shape, dev: int, like: torch.Tensor, stream):
+    """(tensor, address) of an int32 output, made here when it is not given."""
+    if t is None:
+        t = _empty(shape, torch.int32, like.device, stream)
+        return t, t.data_ptr()
+    return t, _addr(t, name, shape, torch.int32, dev)
+
+
+def nd_tree_layout(parents: torch.Tensor, seq_len: Optional[torch.Tensor], window: int,
+                   n_nodes: Optional[torch.Tensor] = None, pos_base: Optional[torch.Tensor] = None,
+                   depth: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                   mask: Optional[torch.Tensor] = None, stream=None):
+    """Trees of drafted tokens from their parents (int32 [B, n], an earlier node
+    or -1): (depth int32 [B, n], positions int32 [B, n] = seq_len + pos_base +
+    depth, mask int32 [B, n, ceil(n/32)], the bits of the ancestors less than
+    window above each node, itself among them).  Nodes from n_nodes[b] on are
+    padding: depth and position -1, mask 0."""
+    dev, B, n, at = _parents(parents)
+    words = (n + 31) // 32
+    depth, at_d = _made(depth, "depth", (B, n), dev, parents, stream)
+    positions, at_p = _made(positions, "positions", (B, n), dev, parents, stream)
+    mask, at_m = _made(mask, "mask", (B, n, words), dev, parents, stream)
+    _check("nd_tree_layout", _lib().nd_tree_layout(
+        at, _ints(n_nodes, "n_nodes", (B,), dev), _ints(seq_len, "seq_len", (B,), dev), _one(pos_base, "pos_base", dev),
+        B, n, window, at_d, at_p, at_m, _on(stream, dev)))
+    return depth, positions, mask
+
+
+def nd_tree_accept(parents: torch.Tensor, tokens: torch.Tensor, target: torch.Tensor, max_path: int,
+                   n_nodes: Optional[torch.Tensor] = None, root_target: Optional[torch.Tensor] = None,
+                   path: Optional[torch.Tensor] = None, path_len: Optional[torch.Tensor] = None,
+                   next: Optional[torch.Tensor] = None, stream=None):
+    """The longest path of drafted tokens (int32 [B, n]) that the model's choices
+    behind the nodes (target, int32 [B, n]) agree with: (path int32
+    [B, max_path], -1 behind its end, path_len int32 [B], next int32 [B], the
+    choice behind the path).  root_target: the choice behind the cache, which
+    roots have to equal; None: roots hold."""
+    dev, B, n, at = _parents(parents)
+    if path is None and max_path < 1:
+        raise ValueError("max_path must be at least 1")
+    path, at_p = _made(path, "path", (B, max_path), dev, parents, stream)
+    path_len, at_l = _made(path_len, "path_len", (B,), dev, parents, stream)
+    next, at_n = _made(next, "next", (B,), dev, parents, stream)
+    _check("nd_tree_accept", _lib().nd_tree_accept(
+        at, _ints(n_nodes, "n_nodes", (B,), dev), _addr(tokens, "tokens", (B, n), torch.int32, dev),
+        _addr(target, "target", (B, n), torch.int32, dev), _ints(root_target, "root_target", (B,), dev), B, n, max_path,
+        at_p, at_l, at_n, _on(stream, dev)))
+    return path, path_len, next
+
+
+def _node_rows(k_new: torch.Tensor, v_new: torch.Tensor, cache: KVCache, dev: int):
+    """n and the strides of the nodes' keys and values [B, n, Hkv, d]."""
+    B, Hkv, _, d = cache.k_codes.shape
+    shape = k_new.shape
+    if len(shape) != 4 or shape[0] != B or shape[2] != Hkv or shape[3] != d or v_new.shape != shape or \
+            k_new.dtype != torch.bfloat16 or v_new.dtype != torch.bfloat16 or k_new.get_device() != dev or \
+            v_new.get_device() != dev or cache.k_codes.get_device() != dev:
+        raise ValueError(f"k_new and v_new must be bf16 [{B}, n, {Hkv}, {d}] on the cache's device")
+    return shape[1], _step(k_new, "k_new"), _step(v_new, "v_new")
+
+
+def nd_tree_commit(cache: KVCache, k_new: torch.Tensor, v_new: torch.Tensor, path: torch.Tensor,
+                   path_len: torch.Tensor, stream=None) -> None:
+    """Append nodes path[b, :path_len[b]] (of k_new, v_new bf16 [B, n, Hkv, d])
+    to each sequence's ring, as single appends in order would."""
+    dev = _here(k_new)
+    n, ks, vs = _node_rows(k_new, v_new, cache, dev)
+    B = k_new.shape[0]
+    if path.dim() != 2:
+        raise ValueError("path must have shape [B, max_path]")
+    m = path.shape[1]
+    _check("nd_tree_commit", _lib().nd_tree_commit(
+        cache.struct_ref(), k_new.data_ptr(), v_new.data_ptr(), ks, vs, n, _addr(path, "path", (B, m), torch.int32, dev),
+        _addr(path_len, "path_len", (B,), torch.int32, dev), m, _on(stream, dev)))
+
+
+def nd_tree_decode_workspace_size(batch: int, n: int, n_q_heads: int, n_kv_heads: int, head_dim: int,
+                                  max_slots: int) -> int:
+    return int(_lib().nd_tree_decode_workspace_size(batch, n, n_q_heads, n_kv_heads, head_dim, max_slots))
+
+
+def nd_tree_decode(q: torch.Tensor, cache: KVCache, k_new: torch.Tensor, v_new: torch.Tensor, depth: torch.Tensor,
+                   mask: torch.Tensor, window: int, out: Optional[torch.Tensor] = None,
+                   lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                   stream=None) -> torch.Tensor:
+    """Attention of a tree's nodes (q bf16 [B, n, Hq, d]; k_new, v_new bf16
+    [B, n, Hkv, d], slices of a fused projection are taken as they are) over the
+    cache and the nodes that mask (nd_tree_layout's) names; returns out."""
+    dev = _here(q)
+    shape = q.shape
+    if len(shape) != 4:
+        raise ValueError("q must have shape [B, n, Hq, d]")
+    n, ks, vs = _node_rows(k_new, v_new, cache, dev)
+    B, _, Hq, d = shape
+    if B != k_new.shape[0] or shape[1] != n or d != k_new.shape[3]:
+        raise ValueError("q, k_new and v_new must agree on batch, nodes and head_dim")
+    at_q = _addr(q, "q", shape, torch.bfloat16, dev)
+    if out is None:
+        out = _like(q, stream)
+        at_out = out.data_ptr()
+    else:
+        at_out = _addr(out, "out", shape, torch.bfloat16, dev)
+    if workspace is None:
+        nbytes = nd_tree_decode_workspace_size(B, n, Hq, k_new.shape[2], d, cache.sink_cap + cache.ring_cap)
+        workspace = _scratch(nbytes, q.device, stream)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
+    _check("nd_tree_decode", _lib().nd_tree_decode(
+        at_q, cache.struct_ref(), k_new.data_ptr(), v_new.data_ptr(), ks, vs,
+        _addr(depth, "depth", (B, n), torch.int32, dev), _addr(mask, "mask", (B, n, (n + 31) // 32), torch.int32, dev), n,
+        Hq, window, at_out, None if lse is None else _addr(lse, "lse", (B, Hq, n), torch.float32, dev),
+        workspace.data_ptr(), workspace.nbytes, _on(stream, dev)))
+    return out
 
 
 def nd_compressed_decode_step_workspace_size(batch: int, n_q_heads: int, n_kv_heads: int, head_dim: int,

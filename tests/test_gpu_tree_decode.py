@@ -1,0 +1,244 @@
+"""Attention of a tree of drafted tokens against the fp64 softmax over each
+node's slots and nodes; outputs within the bf16 tolerance of every attention
+here (max-abs 2e-2, mean-abs 2e-3).  lse: a score is off by at most 2^-10 sum
+|q_i k_i| / sqrt(d) (two fp16 roundings, 2^-11 each, of every key channel) plus
+the fp32 sums' roundings; with N(0,1) values the sum stays below 1.5 sqrt(d) for
+d >= 64: 2^-10 * 1.5 * sqrt(128) < 2e-2."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import tree_util as tu
+from gpu_util import assert_close_bf16, dev_bf16, host, need_gpu, no_device_errors
+from tree_util import i32
+from workloads import normal_bf16, philox
+
+pytestmark = pytest.mark.gpu
+LSE_TOL = 2e-2
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    need_gpu()
+    yield
+    no_device_errors()
+
+
+def nd():
+    import sliding_window_kv_swa_gb300 as m
+    return m
+
+
+def nodes(rng, B, n, Hq, Hkv, d):
+    bits, x = normal_bf16(rng, (B, n, Hq + 2 * Hkv, d))
+    t = dev_bf16(bits)
+    return (t[:, :, :Hq].contiguous(), t[:, :, Hq:Hq + Hkv], t[:, :, Hq + Hkv:]), \
+        (x[:, :, :Hq], x[:, :, Hq:Hq + Hkv], x[:, :, Hq + Hkv:])
+
+
+def check(ref, dev_qkv, qkv, depth, see, mask, window, what=""):
+    q, k, v = dev_qkv
+    B, n, Hq, d = q.shape
+    lse = torch.empty((B, Hq, n), dtype=torch.float32, device="cuda")
+    out = nd().nd_tree_decode(q, tu.device_cache(ref), k, v, i32(depth), i32(mask), window, lse=lse)
+    want, wlse = tu.decode_rows(*qkv[:1], ref, *qkv[1:], depth, see, window)
+    got, glse = host(out), host(lse)
+    assert_close_bf16(got, want, what)
+    seen = np.isfinite(wlse)
+    np.testing.assert_array_equal(np.isfinite(glse), seen)
+    assert (glse[~seen] == -np.inf).all() and (got.transpose(0, 2, 1, 3)[~seen] == 0).all()
+    if seen.any():
+        np.testing.assert_allclose(glse[seen], wlse[seen], atol=LSE_TOL, rtol=0)
+    return out
+
+
+LAYOUTS = [(8, 2, 64), (4, 4, 64), (8, 1, 64), (32, 8, 128), (3, 1, 128), (16, 2, 128), (5, 1, 64), (7, 1, 128)]
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", LAYOUTS)
+@pytest.mark.parametrize("B,n,S,W,window", [
+    (1, 1, 0, 1, 1),           # one node, nothing of the cache inside its window
+    (2, 4, 64, 64, 64),        # whole tiles
+    (3, 13, 5, 40, 17),        # ragged, a narrower window
+    (2, 33, 63, 65, 500),      # more than a word of nodes, tiles that end inside the sinks and the ring
+    (1, 100, 200, 100, 30),    # deeper than the window
+    (2, 70, 0, 7, 7)])
+def test_matches_the_softmax(Hq, Hkv, d, B, n, S, W, window):
+    rng = philox(22000 + 7 * n + d + Hq)
+    lens = None if B == 1 else [(S, 3 * W + 1), (S // 2, W // 2), (0, 0)]
+    ref = tu.random_cache(rng, B, Hkv, d, S, W, lens)
+    parents = tu.random_parents(rng, B, n, reach=3)
+    counts = np.maximum(n - np.arange(B) * (n // 3), 0).astype(np.int32)
+    depth, _, mask, see = tu.layout(parents, counts, ref.seq_len, 0, window)
+    a, b = nodes(rng, B, n, Hq, Hkv, d)
+    check(ref, a, b, depth, see, mask, window)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,B,n,S,W", [(8, 2, 64, 1, 256, 300, 100), (32, 8, 128, 1, 256, 100, 256), (32, 8, 128, 20, 16, 1024, 256),
+                                              (8, 2, 64, 200, 5, 10, 30), (16, 16, 64, 37, 13, 48, 200), (8, 1, 128, 2, 64, 3000, 0),
+                                              (4, 1, 64, 1, 8, 20000, 64), (8, 8, 64, 1, 3, 9000, 128)])
+def test_larger_ones(Hq, Hkv, d, B, n, S, W):
+    rng = philox(22100 + n + S)
+    ref = tu.random_cache(rng, B, Hkv, d, S, W)
+    depth, _, mask, see = tu.layout(tu.random_parents(rng, B, n), None, ref.seq_len, 0, 64)
+    a, b = nodes(rng, B, n, Hq, Hkv, d)
+    check(ref, a, b, depth, see, mask, 64)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(8, 2, 64), (32, 8, 128)])
+def test_without_a_cache_and_with_arbitrary_masks(Hq, Hkv, d):
+    rng = philox(22200)
+    B, n = 3, 45
+    for S, W in ((0, 8), (9, 0)):
+        ref = tu.random_cache(rng, B, Hkv, d, S, W, [(S, W), (0, 0)])
+        see = rng.random((B, n, n)) < 0.2
+        see[:, 7] = False                          # nothing: empty where the cache is
+        see[:, 11] = True
+        depth = rng.integers(0, 5, (B, n)).astype(np.int32)
+        depth[:, 20] = -1                          # padding in the middle
+        depth[0, 3] = -7
+        bits = np.zeros((B, n, 64), np.uint64)
+        bits[..., :n] = see
+        bits[:, 5, n:] = 1                         # bits from n on count nothing
+        mask = (bits.reshape(B, n, 2, 32) << np.arange(32, dtype=np.uint64)).sum(-1).astype(np.uint32)
+        a, b = nodes(rng, B, n, Hq, Hkv, d)
+        check(ref, a, b, depth, see, mask, 6)
+
+
+def test_depths_far_beyond_the_window():
+    rng = philox(22250)
+    B, n, Hq, Hkv, d = 1, 6, 8, 2, 64
+    ref = tu.random_cache(rng, B, Hkv, d, 0, 20)
+    depth = np.array([[0, 19, 20, 2 ** 31 - 1, 1000, 5]], np.int32)
+    see = np.eye(n, dtype=bool)[None]
+    mask = (1 << np.arange(n, dtype=np.uint32)).astype(np.uint32).reshape(1, n, 1)
+    a, b = nodes(rng, B, n, Hq, Hkv, d)
+    for window in (1, 20, 2 ** 31 - 1):
+        check(ref, a, b, depth, see, mask, window)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(8, 2, 64), (32, 8, 128)])
+def test_a_chain_is_a_chunk_and_one_node_a_decode(Hq, Hkv, d):
+    """The chunk prefill rounds cached keys to bf16, this to fp16 or not at all: the two are within the sum of their tolerances."""
+    rng = philox(22300)
+    B, n, S, W, window = 3, 24, 30, 64, 50
+    ref = tu.random_cache(rng, B, Hkv, d, S, W, [(S, 2 * W), (S // 2, W // 2), (0, 3)])
+    parents = np.tile(np.arange(n, dtype=np.int32) - 1, (B, 1))
+    depth, _, mask, _ = tu.layout(parents, None, ref.seq_len, 0, window)
+    (q, k, v), _ = nodes(rng, B, n, Hq, Hkv, d)
+    out = nd().nd_tree_decode(q, tu.device_cache(ref), k, v, i32(depth), i32(mask), window)
+    want = nd().nd_swa_sink_chunk_prefill(q, k.contiguous(), v.contiguous(), tu.device_cache(ref), window)
+    err = np.abs(host(out) - host(want))
+    assert err.max() <= 4e-2 and err.mean() <= 4e-3
+
+
+def test_padding_and_masked_keys_may_hold_anything():
+    """Keys, values and queries of padding, slots that the metadata hides and nodes that nobody sees reach no output."""
+    rng = philox(22400)
+    B, n, Hq, Hkv, d, S, W, window = 2, 20, 8, 2, 64, 40, 50, 30
+    ref = tu.random_cache(rng, B, Hkv, d, S, W, [(13, 2 * W), (S, W // 3)])
+    counts = np.array([12, 7], np.int32)
+    depth, _, mask, see = tu.layout(tu.random_parents(rng, B, n), counts, ref.seq_len, 0, window)
+    (q, k, v), x = nodes(rng, B, n, Hq, Hkv, d)
+    cache = tu.device_cache(ref)
+    args = (i32(depth), i32(mask), window)
+    want = nd().nd_tree_decode(q, cache, k, v, *args)
+    k2, v2, q2 = k.clone(), v.clone(), q.clone()
+    for b in range(B):
+        for t, bad in ((k2, float("nan")), (v2, float("inf")), (q2, float("nan"))):
+            t[b, counts[b]:] = bad
+    for scale in (cache.k_scale, cache.v_scale):
+        scale[0, :, 13:S] = float("nan")
+        scale[1, :, S + W // 3:] = float("inf")
+    got = nd().nd_tree_decode(q2, cache, k2, v2, *args)
+    assert torch.equal(got, want)
+
+
+def test_a_row_with_a_nan_or_an_infinity_leaves_the_others():
+    rng = philox(22450)
+    B, n, Hq, Hkv, d, S, W = 1, 10, 8, 2, 64, 40, 50
+    ref = tu.random_cache(rng, B, Hkv, d, S, W)
+    depth, _, mask, _ = tu.layout(tu.random_parents(rng, B, n), None, ref.seq_len, 0, 99)
+    (q, k, v), _ = nodes(rng, B, n, Hq, Hkv, d)
+    cache = tu.device_cache(ref)
+    want = nd().nd_tree_decode(q, cache, k, v, i32(depth), i32(mask), 99)
+    q2 = q.clone()
+    q2[0, 3, 1, 5], q2[0, 4, 6, 0] = float("nan"), float("inf")
+    got = nd().nd_tree_decode(q2, cache, k, v, i32(depth), i32(mask), 99)
+    same = torch.ones(n, Hq, dtype=torch.bool, device="cuda")
+    same[3, 1] = same[4, 6] = False
+    assert torch.equal(got[0][same], want[0][same])
+
+
+def test_large_and_small_values():
+    """Keys and values of very different sizes: scores up to a few hundred, values down to 2^-20 of the largest."""
+    rng = philox(22500)
+    B, n, Hq, Hkv, d, S, W = 1, 18, 8, 2, 128, 150, 60
+    ref = tu.random_cache(rng, B, Hkv, d, S, W)
+    ref.k_scale *= np.exp2(rng.integers(-6, 3, ref.k_scale.shape)).astype(np.float32)
+    ref.v_scale *= np.exp2(rng.integers(-12, 5, ref.v_scale.shape)).astype(np.float32)
+    depth, _, mask, see = tu.layout(tu.random_parents(rng, B, n), None, ref.seq_len, 0, 99)
+    (q, k, v), x = nodes(rng, B, n, Hq, Hkv, d)
+    lse = torch.empty((B, Hq, n), dtype=torch.float32, device="cuda")
+    out = host(nd().nd_tree_decode(q, tu.device_cache(ref), k, v, i32(depth), i32(mask), 99, lse=lse))
+    want, wlse = tu.decode_rows(x[0], ref, x[1], x[2], depth, see, 99)
+    # a score: 2^-10 sum |q_i k_i| / sqrt(d), so a weight is off by that, and an output by twice that of sum p |v|, plus its rounding
+    most = max(np.abs(oracle.dequant_g32(ref.k_codes, ref.k_scale)).max(), 5.0)
+    reach = 2.0 ** -10 * most * np.abs(x[0]).sum(-1).max() / np.sqrt(d)
+    top = max(np.abs(oracle.dequant_g32(ref.v_codes, ref.v_scale)).max(), np.abs(x[2]).max())
+    assert np.abs(host(lse) - wlse).max() <= reach
+    assert np.abs(out - want).max() <= 2 * reach * top + 2.0 ** -8 * top
+
+
+def test_repeats_itself_in_a_graph_on_another_stream_and_with_a_workspace():
+    rng = philox(22600)
+    for B, n, Hq, Hkv, d, S, W in ((2, 20, 8, 2, 64, 700, 64), (1, 64, 32, 8, 128, 2000, 64), (40, 5, 8, 2, 64, 30, 30)):
+        ref = tu.random_cache(rng, B, Hkv, d, S, W)
+        depth, _, mask, _ = tu.layout(tu.random_parents(rng, B, n), None, ref.seq_len, 0, 99)
+        (q, k, v), _ = nodes(rng, B, n, Hq, Hkv, d)
+        cache = tu.device_cache(ref)
+        size = nd().nd_tree_decode_workspace_size(B, n, Hq, Hkv, d, S + W)
+        ws = torch.full((max(size, 16),), 255, dtype=torch.uint8, device="cuda")
+        dd, dm = i32(depth), i32(mask)
+        want = nd().nd_tree_decode(q, cache, k, v, dd, dm, 99)
+        assert torch.equal(nd().nd_tree_decode(q, cache, k, v, dd, dm, 99, workspace=ws), want)
+        out = torch.empty_like(q)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            nd().nd_tree_decode(q, cache, k, v, dd, dm, 99, out=out, workspace=ws)
+        for _ in range(3):
+            out.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want)
+
+
+def test_the_whole_step():
+    """Draft, lay out, rotate, attend, accept, commit, and draft again: the cache after two steps is that of single appends, and
+    each step's attention the fp64 one."""
+    rng = philox(22700)
+    B, n, Hq, Hkv, d, S, W, window, m = 4, 17, 8, 2, 64, 6, 24, 20, 5
+    ref = tu.random_cache(rng, B, Hkv, d, S, W, [(S, 2 * W), (S, 3), (0, 0), (S, W)])
+    cache = tu.device_cache(ref)
+    for step in range(2):
+        parents = tu.random_parents(rng, B, n, roots=0)
+        counts = rng.integers(1, n + 1, B).astype(np.int32)
+        dp, dc = i32(parents), i32(counts)
+        depth, pos, mask = nd().nd_tree_layout(dp, cache.seq_len, window, n_nodes=dc)
+        (q, k, v), x = nodes(rng, B, n, Hq, Hkv, d)
+        qr, kr = nd().nd_rope_positions(q, k, nd().RopeConfig(), positions=pos)
+        out = nd().nd_tree_decode(qr, cache, kr, v, depth, mask, window)
+        wd, _, _, see = tu.layout(parents, counts, ref.seq_len, 0, window)
+        want, _ = tu.decode_rows(host(qr), ref, host(kr), x[2], wd, see, window)
+        assert_close_bf16(host(out), want, f"step {step}")
+        tokens, target = (rng.integers(0, 2, (B, n)).astype(np.int32) for _ in range(2))
+        path, length, _ = nd().nd_tree_accept(dp, i32(tokens), i32(target), m, n_nodes=dc)
+        nd().nd_tree_commit(cache, kr, v, path, length)
+        wp, wl, _ = tu.accept(parents, counts, tokens, target, None, m)
+        np.testing.assert_array_equal(host(path), wp)
+        tu.commit(ref, host(kr).astype(np.float32), x[2], wp, wl)
+        for f in tu.FIELDS:
+            np.testing.assert_array_equal(host(getattr(cache, f)), getattr(ref, f), err_msg=f)
