@@ -960,7 +960,8 @@ static bool tree_sizes_ok(int64_t batch, int n_kv_heads, int64_t slots) {
 
 size_t nd_tree_decode_workspace_size(int batch, int n, int n_q_heads, int n_kv_heads, int head_dim, int max_slots) {
   if (batch <= 0 || n <= 0 || n > ND_TREE_MAX_NODES || n_q_heads <= 0 || n_kv_heads <= 0 || n_q_heads % n_kv_heads ||
-      head_dim <= 0 || max_slots <= 0 || !tree_sizes_ok(batch, n_kv_heads, max_slots))
+      head_dim <= 0 || max_slots <= 0 || !tree_sizes_ok(batch, n_kv_heads, max_slots) ||
+      !tree_decode_fits(batch, n, n_kv_heads, max_slots, 1))
     return 0;
   return round_up(tree_decode_workspace_bytes(batch, n, n_q_heads, n_kv_heads, head_dim, max_slots), 256);
 }
@@ -979,7 +980,8 @@ int nd_tree_decode(const void *q, const nd_kv_cache *cache, const void *k_new, c
   if (!stride_ok(k_stride, Hkv, d, 2) || !stride_ok(v_stride, Hkv, d, 2)) return ND_ERR_INVALID_ARG;
   const int64_t slots = int64_t(cache->sink_cap) + cache->ring_cap;
   if (slots < 1) return ND_ERR_INVALID_ARG;
-  if (!tree_sizes_ok(cache->batch, Hkv, slots)) return ND_ERR_UNSUPPORTED;
+  if (!tree_sizes_ok(cache->batch, Hkv, slots) || !tree_decode_fits(cache->batch, n, Hkv, cache->sink_cap, cache->ring_cap))
+    return ND_ERR_UNSUPPORTED;
   const size_t need = nd_tree_decode_workspace_size(cache->batch, n, n_q_heads, Hkv, d, int(slots));
   if (need && (!workspace || workspace_bytes < need || !aligned16(workspace))) return ND_ERR_WORKSPACE;
   if ((st = check_device(nullptr)) != ND_OK) return st;

@@ -150,6 +150,8 @@ struct TreeDecodeArgs {
   void *out;
   float *lse;  // may be NULL
 };
+// Fewer than 2^30 tiles.
+bool tree_decode_fits(int batch, int n, int n_kv_heads, int sink_cap, int ring_cap);
 size_t tree_decode_workspace_bytes(int batch, int n, int n_q_heads, int n_kv_heads, int head_dim, int max_slots);
 cudaError_t launch_tree_decode(const TreeDecodeArgs &a, const nd_kv_cache &c, void *ws, int *err, cudaStream_t stream);
 
