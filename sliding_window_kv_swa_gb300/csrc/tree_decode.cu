@@ -41,18 +41,20 @@
 // tree_merge_kernel.  The line counts the tiles that the caches have room for;
 // those that hold nothing are skipped.
 //
-// Roles (16 warps):
-//   warps 0-3   : softmax (thread = TMEM lane): stage Q; per tile read S, write
-//                 P over it; at a segment's end read O and write it
-//   warps 4-11  : codes (or nodes' bf16) of the staged tile -> K, V operands in
+// Roles (20 warps):
+//   warps 0-7   : softmax (two threads to a TMEM lane, for half of its columns
+//                 each): stage Q; per tile read S, write P; at a segment's end
+//                 read O and write it
+//   warps 8-15  : codes (or nodes' bf16) of the staged tile -> K, V operands in
 //                 shared memory, half of them K, half V
-//   warp 12     : copies the tiles ahead
-//   warp 15     : the staged tile's scales -> exponents, fp16 scales
-//   warps 13, 14: MMA issuers: S = Q K^T; O += P V
+//   warp 16     : copies the tiles ahead
+//   warp 19     : the staged tile's scales -> exponents, fp16 scales
+//   warps 17, 18: MMA issuers: S = Q K^T; O += P V
 // Every wait is bounded: one that gives up raises the device error flag and the
 // abort flag, and all roles leave through the common exit.
 #include <atomic>
 #include <climits>
+#include <type_traits>
 
 #include "nd_common.cuh"
 #include "nd_internal.h"
@@ -65,16 +67,19 @@ namespace {
 constexpr int BM = 128;        // rows of a product = TMEM lanes
 constexpr int BN = 128;        // cached keys per tile
 constexpr int kNodes = 64;     // nodes per tile
-constexpr int kThreads = 16 * 32;
-constexpr int kWarpTurn = 4, kWarpLoad = 12, kWarpS = 13, kWarpPV = 14, kWarpScan = 15;
-// Register split (setmaxnreg, per warpgroup) of the 128 a thread at launch: a
-// softmax thread holds up to 128 scores.
-constexpr int kRegsSoftmax = 232, kRegsOther = 88;
-static_assert(128 * kRegsSoftmax + 3 * 128 * kRegsOther <= kThreads * 128, "register split");
+constexpr int kThreads = 20 * 32;
+constexpr int kWarpTurn = 8, kWarpFeedK = 16, kWarpFeedV = 17, kWarpS = 18;
+// Register split (setmaxnreg, per warpgroup) of the 96 a thread at launch: a
+// softmax thread holds up to 64 scores.
+constexpr int kRegsLaunch = 96, kRegsSoftmax = 144, kRegsOther = 64;
+static_assert(2 * 128 * kRegsSoftmax + 3 * 128 * kRegsOther <= kThreads * kRegsLaunch, "register split");
+constexpr int kAhead = 4;         // tiles that are asked into L2 ahead of their copies
+constexpr int kKf = 8;            // node tiles' key factors in flight: more than the tiles between operand and softmax
 constexpr float kLazyLog2 = 8.f;  // the maximum used may lag the true one by 2^8
 constexpr float kPBias = 7.f;     // P is scaled by 2^7
-constexpr int kInfo = 16;         // tile records in flight: more than the tiles between copy and softmax
-constexpr int kMostUp = 64;       // V's largest exponent: a node's value times 2^(64 + 15) stays finite up to 2^48
+constexpr int kCodeBits = 24;     // operands made of codes hold 2^-24 of code * scale * 2^e
+constexpr int kMostUp = 88;       // V's largest e: a node's value times 2^(88 - 24 + 15) stays finite up to 2^48
+constexpr float kUnits = 16777216.f;  // 2^24
 constexpr int kCtas = 152;        // one per SM
 
 // ------------------------------------------------------------ the split
@@ -86,12 +91,15 @@ struct TreePlan {
   int even, odd;       // units / ctas and units % ctas
   bool whole;          // a unit is a pair (nothing is split), else a tile
   __host__ __device__ int start(int c) const {
-    const int u = even * c + int((long long)odd * c / ctas);
+    const int u = even * c + odd * c / ctas;  // = units * c / ctas
     return whole ? u * t : u;
   }
   // the stretch that holds tile x of the line
-  __host__ __device__ int owner(int x) const {
-    return int(((long long)(x + 1) * ctas - 1) / ((long long)pairs * t));
+  __device__ int owner(int x) const {
+    int c = min(ctas - 1, int(float(x) * float(ctas) / (float(pairs) * float(t))));
+    while (start(c) > x) --c;
+    while (start(c + 1) <= x) ++c;
+    return c;
   }
   int rows_of_lanes() const { return rb <= 32 ? 32 : rb <= 64 ? 64 : 128; }
 };
@@ -125,21 +133,43 @@ __host__ __device__ constexpr size_t part_floats() {
 }
 
 // ------------------------------------------------------------ the kernel
+// A tile's record: what it is made of, whether its segment begins or ends with
+// it and the stretch ends, keys (bits 8-15) and those in the first piece (16-23).
+constexpr int kKindRing = 1, kKindNodes = 2, kFresh = 4, kEnd = 8, kLast = 16;
+
 template <int D>
 struct Lay {
   static constexpr int NG = D / 32, kBoxes = D / 64;
   static constexpr int kKV = kBoxes * BN * 128;          // one K or V operand tile
   static constexpr int kCodes = BN * D, kScales = BN * NG * 4;
-  static constexpr int kRaw = 2 * kCodes + 2 * kScales;  // K codes, V codes, K scales, V scales; or nodes' K, V
   static_assert(kNodes * D * 2 == kCodes, "a node tile's rows take the codes' place");
-  static constexpr int NK = D == 128 ? 2 : 3, NV = NK, NR = D == 128 ? 2 : 5;
-  static constexpr int kRow = 144, kT = 4 * 32 * kRow;   // a softmax warp's 32 rows of 64 channels, padded
-  static constexpr int oK = 0, oV = oK + NK * kKV, oR = oV + NV * kKV, oT = oR + NR * kRaw;
-  static constexpr int kBytes = oT + kT + 1024;          // + alignment slack
-  static_assert(kBytes + 6 * 1024 <= 227 * 1024, "shared memory");
-  // TMEM columns: S[2], O, Q
-  static constexpr int cO = 2 * BN, cQ = cO + D, kTmemCols = 512;
-  static_assert(cQ + D / 2 <= kTmemCols, "TMEM");
+  // stages: operands of K and of V, staged codes (or nodes' rows) of either, staged scales of either
+  static constexpr int NK = D == 128 ? 2 : 3, NR = D == 128 ? 2 : 5, NS = NR + 1;
+  static constexpr int kInfo = 16;                       // tile records in flight
+  static_assert(kInfo > NS + NK + 2 + kAhead, "tile records");
+  static constexpr int kT1 = 2048, kT = 8 * kT1;         // a softmax warp's turning buffer
+  static constexpr int oK = 0, oV = oK + NK * kKV, oR = oV + NK * kKV, oS = oR + 2 * NR * kCodes, oT = oS + 2 * NS * kScales,
+                       oSmall = oT + kT;
+  // barriers; [2]: K, V
+  struct Small {
+    uint64_t raw_full[2][NR], raw_empty[2][NR], sc_full[2][NS], sc_empty[2][NS], op_full[2][NK], op_empty[2][NK];
+    uint64_t s_full[2], s_empty[2], p_full, pv_done, q_full;  // s_: score buffers
+    int4 rec[2][kInfo];       // tiles, as the feeders see them ahead: flags (kFresh ...), first key, pair, slot
+    float4 info[kInfo];       // for the softmax: the factor that O needs before the tile's V; 2^-e of V; e - 24
+    float down_k[kInfo];      // 2^-e of K
+    uint2 live[2][kInfo];     // node tiles: nodes that are not padding
+    uint32_t bad[2][kInfo][2];  // and those whose key, value is not finite
+    float kf[kKf][kNodes];    // and 2^-e of their keys
+    float mx[2][2][BM];       // what the two halves of a row's columns tell each other, in turns
+    float2 ml[BM];            // and its copies
+    uint32_t tmem;
+    int abort;
+  };
+  static constexpr int kBytes = oSmall + int(sizeof(Small));
+  static_assert(kBytes <= 227 * 1024, "shared memory");
+  // TMEM columns: S[2], O, Q, P
+  static constexpr int cO = 2 * BN, cQ = cO + D, cP = cQ + D / 2, kTmemCols = 512;
+  static_assert(cP + BN / 2 <= kTmemCols, "TMEM");
 };
 
 struct TreeParams {
@@ -168,30 +198,62 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_
                "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
                : "memory");
 }
+// Asks memory into L2.
+__device__ __forceinline__ void bulk_l2(const void *src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(reinterpret_cast<uint64_t>(src)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void prefetch_l2(const void *src) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<uint64_t>(src)) : "memory");
+}
 __device__ __forceinline__ void cp_async8(uint32_t dst, const void *src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ float lds_f32(uint32_t a) {
-  float v;
-  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-  return v;
+// A row's NG scales; and put back as pairs of fp16, times a power of two.
+template <int NG>
+__device__ __forceinline__ void lds_row(uint32_t a, float *x) {
+  if constexpr (NG == 4)
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]) : "r"(a) : "memory");
+  else
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(x[0]), "=f"(x[1]) : "r"(a) : "memory");
+}
+template <int NG>
+__device__ __forceinline__ void sts_row(uint32_t a, const float *x, float up) {
+  uint32_t h[NG];
+#pragma unroll
+  for (int i = 0; i < NG; ++i) {
+    const float y = x[i] * up;
+    h[i] = pack_half2(y, y);
+  }
+  if constexpr (NG == 4) st_shared_v4(a, h[0], h[1], h[2], h[3]);
+  else asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(a), "r"(h[0]), "r"(h[1]) : "memory");
 }
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t v;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
 }
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
-  return v;
+// Two codes times a scale, in fp16 and rounded once.  A code biased to unsigned
+// (xor 0x80) in the low byte of an fp16 is the subnormal (code + 128) 2^-24, and
+// code * s 2^-24 = (code + 128) 2^-24 * s - s 2^-17, a fused multiply and add of
+// exact operands (off = s * -2^-17 is exact down to s = 2^3, below that off by
+// 2^-25).  One instruction less per pair than subtracting the bias first.
+constexpr uint32_t kMinus128 = 0x80808080u;  // two fp16 -2^-17
+constexpr uint32_t kBytes01 = 0x4140u, kBytes23 = 0x4342u;  // [b0, 0, b1, 0], [b2, 0, b3, 0]
+__device__ __forceinline__ uint32_t scaled_codes(uint32_t biased, uint32_t sel, uint32_t s, uint32_t off) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(prmt(biased, 0u, sel)), "r"(s), "r"(off));
+  return r;
 }
-__device__ __forceinline__ void sts32(uint32_t a, uint32_t v) {
-  asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
-}
+
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 
@@ -207,9 +269,15 @@ struct Ring {
   }
 };
 
-// A bounded wait of a whole warp that sleeps between polls (up to 2 us each).
-__device__ __forceinline__ bool ring_wait(uint64_t *bar, uint32_t parity, int *err, volatile int *abort_flag) {
+// A bounded wait of a whole warp that sleeps between polls (up to 2 us each).  One
+// that gives up sets the abort flag, and the common exit raises the device's.
+// All roles' loops together have to stay small enough for the SM's instruction
+// cache: with 160 KB of code, a walk over the tiles in every role, the fetches
+// from the cache behind it bounded the kernel (85 % of their rate; 210 us at 128
+// sessions of 16 nodes).
+__device__ __forceinline__ bool ring_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
   bool ok = mbar_test_wait(bar, parity);
+#pragma unroll 1
   for (uint32_t i = 0; i < kWaitLimit / 64 && !ok; ++i) {
     uint32_t r;
     asm volatile(
@@ -221,18 +289,15 @@ __device__ __forceinline__ bool ring_wait(uint64_t *bar, uint32_t parity, int *e
     ok = r != 0;
     if (!ok && *abort_flag) break;
   }
-  if (!ok && !*abort_flag) {
-    raise_device_error(err, ND_DEVERR_TIMEOUT);
-    *abort_flag = 1;
-  }
+  if (!ok) *abort_flag = 1;
   return __all_sync(0xffffffffu, ok);
 }
 
-// Whether any thread of the four softmax warps says so; a barrier of theirs.
+// Whether any thread of the eight softmax warps says so; a barrier of theirs.
 __device__ __forceinline__ bool softmax_any(bool x) {
   uint32_t r;
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, 256, p;\n selp.u32 %0, 1, 0, q;\n}\n"
       : "=r"(r)
       : "r"(uint32_t(x))
       : "memory");
@@ -276,50 +341,45 @@ __device__ __forceinline__ int live_tile(const TreePlan &pl, const Seg &s, int t
 template <int D, int REP>
 __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_constant__ TreeParams p) {
   using Y = Lay<D>;
-  constexpr int NK = Y::NK, NV = Y::NV, NR = Y::NR, NG = Y::NG;
-  constexpr int kLanes = BM / REP;  // rows, and lanes of a copy of them
-  constexpr int kCols = BN / REP;   // a thread's columns of a tile
+  constexpr int NK = Y::NK, NR = Y::NR, NS = Y::NS, NG = Y::NG, kInfo = Y::kInfo;
+  constexpr int kLanes = BM / REP;     // rows, and lanes of a copy of them
+  constexpr int kCols = BN / REP / 2;  // a thread's columns of a tile
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t raw_full[NR], raw_empty[NR], scan_full[NR], k_full[NK], k_empty[NK], v_full[NV], v_empty[NV],
-      s_full[2], p_full[2], pv_done[2], q_full;
-  __shared__ float4 s_info[kInfo];           // per tile, for the softmax
-  __shared__ uint2 s_live[kInfo];            // node tiles: nodes that are not padding
-  __shared__ uint32_t s_bad[kInfo][2];       // and those that are not finite
-  __shared__ float s_kf[kInfo][kNodes];      // and 2^-e of their keys
-  __shared__ uint32_t s_tmem;
-  __shared__ int s_abort;
-  __shared__ float2 s_ml[BM];
+  typename Y::Small &sm = *reinterpret_cast<typename Y::Small *>(smem_raw + Y::oSmall);
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be the same in the warp
-  volatile int *abort_flag = &s_abort;
-  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  volatile int *abort_flag = &sm.abort;
+  const uint32_t base = smem_u32(smem_raw);
   const uint32_t sK = base + Y::oK, sV = base + Y::oV, sT = base + Y::oT;
-  auto sR = [&](int st) { return base + Y::oR + st * Y::kRaw; };
+  auto sR = [&](int kv, int st) { return base + Y::oR + (kv * NR + st) * Y::kCodes; };
+  auto sS = [&](int kv, int st) { return base + Y::oS + (kv * NS + st) * Y::kScales; };
 
   if (tid == 0) {
-    for (int s = 0; s < NR; ++s) {
-      mbar_init(&raw_full[s], 33);  // the bulk copies' transaction and 32 lanes' scale copies
-      mbar_init(&raw_empty[s], 9);  // the warps that turn the tile, and the scan
-      mbar_init(&scan_full[s], 1);
+    for (int kv = 0; kv < 2; ++kv) {
+      for (int s = 0; s < NR; ++s) {
+        mbar_init(&sm.raw_full[kv][s], 1);   // the copies' transaction
+        mbar_init(&sm.raw_empty[kv][s], 4);  // the warps that turn it
+      }
+      for (int s = 0; s < NS; ++s) {
+        mbar_init(&sm.sc_full[kv][s], 1);
+        mbar_init(&sm.sc_empty[kv][s], 4);
+      }
+      for (int s = 0; s < NK; ++s) {
+        mbar_init(&sm.op_full[kv][s], 4);
+        mbar_init(&sm.op_empty[kv][s], 1);
+      }
+      mbar_init(&sm.s_full[kv], 1);
+      mbar_init(&sm.s_empty[kv], 8);
     }
-    for (int s = 0; s < NK; ++s) {
-      mbar_init(&k_full[s], 4);
-      mbar_init(&k_empty[s], 1);
-      mbar_init(&v_full[s], 4);
-      mbar_init(&v_empty[s], 1);
-    }
-    for (int u = 0; u < 2; ++u) {
-      mbar_init(&s_full[u], 1);
-      mbar_init(&p_full[u], 4);
-      mbar_init(&pv_done[u], 1);
-    }
-    mbar_init(&q_full, 4);
-    s_abort = 0;
+    mbar_init(&sm.p_full, 8);
+    mbar_init(&sm.pv_done, 1);
+    mbar_init(&sm.q_full, 8);
+    sm.abort = 0;
     fence_barrier_init();
   }
   if (warp == kWarpS) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem)),
                  "r"(Y::kTmemCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -327,10 +387,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0);
   pdl_wait();
   pdl_trigger();  // the merge reads nothing of this kernel's before it waits
-  const uint32_t tO = tmem + Y::cO, tQ = tmem + Y::cQ;
+  const uint32_t tO = tmem + Y::cO, tQ = tmem + Y::cQ, tP = tmem + Y::cP;
 
   const TreePlan &pl = p.plan;
   const int stretch = blockIdx.x / pl.nb, blk = blockIdx.x % pl.nb;
@@ -339,281 +399,292 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
 
   // (each side of the split has its setmaxnreg to itself: behind a common one the
   // compiler takes the smaller bound for all roles)
-  if (warp >= 4) {
+  if (warp >= kWarpTurn) {
   regs_dec<kRegsOther>();
-  if (warp == kWarpLoad) {
-    // -------------------------------------------------- loader
+  if (warp == kWarpFeedK || warp == kWarpFeedV) {
+    // -------------------------------------------------- feeders, one for K and one for V
+    // Per round i: note tile i + kAhead and ask its codes into L2 (two staged
+    // tiles are too few bytes in flight for memory's latency), copy tile i + 1's
+    // scales, turn tile i's scales into fp16 pairs and its exponent, copy its
+    // codes.
+    const int kv = warp == kWarpFeedV;
     const uint32_t leader = elect_one();
-    const int nslot = p.c.sink_cap + p.c.ring_cap;
+    const int8_t *const codes = kv ? p.c.v_codes : p.c.k_codes;
+    const float *const scales = kv ? p.c.v_scale : p.c.k_scale;
+    const size_t nslot = size_t(p.c.sink_cap) + p.c.ring_cap;
+    auto node_row = [&](int pair, int j) {
+      const int b = pair / p.c.n_kv_heads;
+      return (kv ? p.v : p.k) + (int64_t(b) * p.n + j) * (kv ? p.v_stride : p.k_stride) + (pair - b * p.c.n_kv_heads) * D;
+    };
     Ring<NR> raw;
-    raw.phase = 1;  // the first round of an empty ring does not wait
-    for (int x = x0; x < x1 && !fail;) {
-      const Seg s = seg_at(p, x, x1);
-      x += s.t1 - s.t0;
-      if (!s.sane && lane == 0) raise_device_error(p.err, ND_DEVERR_METADATA);
-      const size_t slot0 = size_t(s.pair) * nslot;
-      const int hk = s.pair - s.b * p.c.n_kv_heads;
+    Ring<NS> sc, sc_in;
+    raw.phase = sc_in.phase = 1;  // the first round of an empty ring does not wait
+    int noted = 0, x = x0, t = 0, e_v = INT_MAX;  // e_v: the exponent that V's operands have in O (unset)
+    bool fresh = true;
+    Seg s = {};
 #pragma unroll 1
-      for (int t = live_tile(pl, s, s.t0); t < s.t1; t = live_tile(pl, s, t + 1), raw.next()) {
-        if (!ring_wait(&raw_empty[raw.i], raw.phase, p.err, abort_flag)) {
-          fail = true;
-          break;
+    for (int i = -kAhead;; ++i) {
+      if (!fresh || x < x1) {
+        if (fresh) {
+          s = seg_at(p, x, x1);
+          x += s.t1 - s.t0;
+          // at least one tile, though it may hold nothing
+          t = min(live_tile(pl, s, s.t0), s.t1 - 1);
+          if (!kv && !s.sane && lane == 0) raise_device_error(p.err, ND_DEVERR_METADATA);
+          if (kv) {  // ask for its queries
+            const int hk = s.pair - s.b * p.c.n_kv_heads, r1 = min(p.n * p.G, (blk + 1) * pl.rb);
+            constexpr int kLines = D * 2 / 128;
+#pragma unroll 1
+            for (int k = lane; k < (r1 - blk * pl.rb) * kLines; k += 32) {
+              const int r = blk * pl.rb + k / kLines, nd = p.G == 1 ? r : int(__umulhi(unsigned(r), p.g_magic));
+              prefetch_l2(p.q + ((int64_t(s.b) * p.n + nd) * p.Hq + hk * p.G + (r - nd * p.G)) * D + k % kLines * 64);
+            }
+          }
         }
-        uint64_t *bar = &raw_full[raw.i];
-        const uint32_t dst = sR(raw.i);
+        int4 rec = make_int4(fresh ? kFresh : 0, 0, s.pair, 0);
         if (t < pl.ts + pl.tr) {
-          // up to two pieces: a ring tile may wrap
           const bool ring = t >= pl.ts;
-          const int first = (ring ? t - pl.ts : t) * BN;
-          const int cnt = min(BN, (ring ? s.nv : s.sl) - first);
-          int at = first, c1 = cnt;
+          rec.y = (ring ? t - pl.ts : t) * BN;
+          const int cnt = max(0, min(BN, (ring ? s.nv : s.sl) - rec.y));
+          int c1 = cnt;
+          rec.w = rec.y;
           if (ring) {
-            unsigned w = unsigned(s.ring0) + unsigned(first);
+            // two pieces where it wraps
+            unsigned w = unsigned(s.ring0) + unsigned(rec.y);
             if (w >= unsigned(p.c.ring_cap)) w -= unsigned(p.c.ring_cap);
             c1 = min(cnt, p.c.ring_cap - int(w));
-            at = p.c.sink_cap + int(w);
+            rec.w = p.c.sink_cap + int(w);
+            rec.x |= kKindRing;
           }
-          expect_tx(bar, 2 * cnt * D, leader);
-          if (leader) {
-            const size_t a = (slot0 + at) * D;
-            bulk_copy(dst, p.c.k_codes + a, c1 * D, bar);
-            bulk_copy(dst + Y::kCodes, p.c.v_codes + a, c1 * D, bar);
-            if (c1 < cnt) {
-              const size_t w = (slot0 + p.c.sink_cap) * D;
-              bulk_copy(dst + c1 * D, p.c.k_codes + w, (cnt - c1) * D, bar);
-              bulk_copy(dst + Y::kCodes + c1 * D, p.c.v_codes + w, (cnt - c1) * D, bar);
-            }
-          }
-          __syncwarp();
-          // scales: a slot's row is 16 (D = 128) or 8 bytes, and a head's first
-          // one aligned to no more than that
-#pragma unroll
-          for (int i = 0; i < BN / 32; ++i) {
-            const int r = lane + 32 * i;
-            if (r < cnt) {
-              const size_t w = (slot0 + (r < c1 ? at + r : p.c.sink_cap + r - c1)) * NG;
-              const uint32_t sd = dst + 2 * Y::kCodes + r * (NG * 4);
-              if constexpr (NG == 4) {
-                cp_async16(sd, p.c.k_scale + w);
-                cp_async16(sd + Y::kScales, p.c.v_scale + w);
-              } else {
-                cp_async8(sd, p.c.k_scale + w);
-                cp_async8(sd + Y::kScales, p.c.v_scale + w);
-              }
-            }
-          }
+          rec.x |= cnt << 8 | c1 << 16;
+          if (leader && c1 > 0) bulk_l2(codes + (s.pair * nslot + rec.w) * D, c1 * D);
         } else {
-          const int j0 = (t - pl.ts - pl.tr) * kNodes, cnt = min(kNodes, p.n - j0);
-          expect_tx(bar, 2 * cnt * (2 * D), leader);
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < kNodes / 32; ++i) {
-            const int r = lane + 32 * i;
-            if (r < cnt) {
-              const int64_t node = int64_t(s.b) * p.n + j0 + r;
-              bulk_copy(dst + r * (2 * D), p.k + node * p.k_stride + hk * D, 2 * D, bar);
-              bulk_copy(dst + Y::kCodes + r * (2 * D), p.v + node * p.v_stride + hk * D, 2 * D, bar);
-            }
+          rec.y = (t - pl.ts - pl.tr) * kNodes;
+          const int cnt = min(kNodes, p.n - rec.y);
+          rec.x |= kKindNodes | cnt << 8;
+#pragma unroll 1
+          for (int r = lane; r < cnt; r += 32) {
+            const uint16_t *row = node_row(s.pair, rec.y + r);
+            prefetch_l2(row);
+            if (D == 128) prefetch_l2(row + 64);
           }
         }
-        cp_async_arrive(bar);
+        t = live_tile(pl, s, t + 1);
+        fresh = t >= s.t1;
+        if (fresh) rec.x |= kEnd;
+        if (fresh && x >= x1) rec.x |= kLast;
+        if (lane == 0) sm.rec[kv][noted % kInfo] = rec;
+        ++noted;
         __syncwarp();
       }
-    }
-  } else if (warp >= kWarpTurn && warp < kWarpLoad) {
-    // -------------------------------------------------- operands
-    const int turn = warp - kWarpTurn;
-    const bool is_v = turn & 1;
-    constexpr int kTurnRows = BN / 4;
-    const int row_w = (turn >> 1) * kTurnRows;  // the warp's first row
-    constexpr int kPieces = D / 16, kRowsIt = 32 / kPieces, kIts = kTurnRows / kRowsIt, kU = 2;
-    static_assert(kIts % kU == 0, "rows of a warp");
-    const int piece = lane % kPieces, row_l = lane / kPieces;
-    // K-major (and for V MN-major) 128-byte swizzle: row * 128 + 16-byte chunk ^
-    // (row & 7) inside a box of 64 channels; a lane's two chunks.  The upper
-    // box's lanes store their odd chunk first, so the eight lanes of a row cover
-    // the eight chunk positions (all banks) at once.
-    const int box = piece / 4, c0 = (2 * piece) & 7;
-    const uint32_t odd_first = box == 1 ? 1u : 0u;
-    uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
-    const uint32_t codes_off = (is_v ? Y::kCodes : 0) + (row_w + row_l) * D + piece * 16 + 8 * odd_first;
-    const uint32_t scale_off = 2 * Y::kCodes + (is_v ? Y::kScales : 0) + 4 * ((row_w + row_l) * NG + piece / 2);
-    const uint32_t operand = is_v ? sV : sK;
-    const uint32_t row_off = operand + (row_w + row_l) * 128 + box * (BN * 128);
-    const uint32_t first_c = ((c0 + odd_first) ^ (row_l & 7)) << 4;  // and the other chunk: ^ 16
-    Ring<NR> raw;
-    Ring<NK> op;
-    op.phase = 1;
-    int g = 0;
-    for (int x = x0; x < x1 && !fail;) {
-      const Seg s = seg_at(p, x, x1);
-      x += s.t1 - s.t0;
-#pragma unroll 1
-      for (int t = live_tile(pl, s, s.t0); t < s.t1; t = live_tile(pl, s, t + 1), ++g, raw.next(), op.next()) {
-        // the scan waited for the tile's copies before it arrived
-        if (!ring_wait(&scan_full[raw.i], raw.phase, p.err, abort_flag) ||
-            !ring_wait(&empty[op.i], op.phase, p.err, abort_flag)) {
+      if (i + 1 >= 0 && i + 1 < noted) {
+        const int4 rec = sm.rec[kv][(i + 1) % kInfo];
+        if (!ring_wait(&sm.sc_empty[kv][sc_in.i], sc_in.phase, abort_flag)) {
           fail = true;
           break;
         }
-        if (t < pl.ts + pl.tr) {
-          const uint32_t raw_at = sR(raw.i) + codes_off, sc_at = sR(raw.i) + scale_off;
-          const uint32_t dst = row_off + op.i * Y::kKV;
-#pragma unroll 1
-          for (int i0 = 0; i0 < kIts; i0 += kU) {
-            uint2 w[kU][2];
-            uint32_t s2[kU];
+        if (!(rec.x & kKindNodes)) {
+          // a lane copies a row's scales of every 32: 16 (D = 128) or 8 bytes, and
+          // a head's first one aligned to no more than that
+          const int cnt = rec.x >> 8 & 255, c1 = rec.x >> 16 & 255;
+          const uint32_t dst = sS(kv, sc_in.i) + lane * (NG * 4);
+          const float *src = scales + (rec.z * nslot + rec.w + lane) * NG;
 #pragma unroll
-            for (int i = 0; i < kU; ++i) {
-              w[i][0] = lds64(raw_at + (i0 + i) * kRowsIt * D);
-              w[i][1] = lds64((raw_at ^ 8u) + (i0 + i) * kRowsIt * D);
-              s2[i] = lds32(sc_at + (i0 + i) * kRowsIt * NG * 4);
-            }
-#pragma unroll
-            for (int i = 0; i < kU; ++i) {
-              // a lane's rows are kRowsIt (4 or 8) apart: the swizzle of the
-              // second of a pair differs from the first's in one bit at most
-              const uint32_t at = dst + (i0 + i) * kRowsIt * 128 + (first_c ^ ((i * kRowsIt & 4) << 4));
-#pragma unroll
-              for (int q = 0; q < 2; ++q) {
-                const uint32_t wa = w[i][q].x ^ 0x80808080u, wb = w[i][q].y ^ 0x80808080u;
-                st_shared_v4(q ? at ^ 16u : at, hmul2(codes_to_half2(wa, kSelBytes01), s2[i]),
-                             hmul2(codes_to_half2(wa, kSelBytes23), s2[i]), hmul2(codes_to_half2(wb, kSelBytes01), s2[i]),
-                             hmul2(codes_to_half2(wb, kSelBytes23), s2[i]));
-              }
+          for (int k = 0; k < BN / 32; ++k) {
+            const int r = lane + 32 * k;
+            if (r < cnt) {
+              const float *from = r < c1 ? src + 32 * k * NG : scales + (rec.z * nslot + p.c.sink_cap + (r - c1)) * NG;
+              if constexpr (NG == 4) cp_async16(dst + 32 * k * (NG * 4), from);
+              else cp_async8(dst + 32 * k * (NG * 4), from);
             }
           }
-        } else {
-          // nodes: D/8 lanes to a row, a sixteenth of the tile's rows per warp
-          // and iteration
-          constexpr int kL = D / 8, kR = 32 / kL;
-          const int sub = lane / kL, ch = lane % kL;
-          const int cnt = min(kNodes, p.n - (t - pl.ts - pl.tr) * kNodes);
-          const uint2 alive = s_live[g % kInfo];
-          const uint32_t src = sR(raw.i) + (is_v ? Y::kCodes : 0), dst = operand + op.i * Y::kKV;
-#pragma unroll 1
-          for (int r0 = (turn >> 1) * (kNodes / 4); r0 < (turn >> 1) * (kNodes / 4) + kNodes / 4; r0 += kR) {
-            const int r = r0 + sub;
-            const bool use = r < cnt && ((r < 32 ? alive.x : alive.y) >> (r & 31) & 1u);
-            uint32_t w[4] = {0u, 0u, 0u, 0u};
-            if (use) ld_shared_v4(src + r * (2 * D) + ch * 16, w[0], w[1], w[2], w[3]);
-            float mx = 0.f;
-            bool bad = false;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float a = fabsf(bf16_lo(w[e])), b = fabsf(bf16_hi(w[e]));
-              bad = bad || !(a < INFINITY) || !(b < INFINITY);
-              mx = fmaxf(mx, fmaxf(a, b));
-            }
-            const uint32_t row_lanes = (kL == 32 ? 0xffffffffu : ((1u << kL) - 1u)) << (sub * kL);
-            bad = (__ballot_sync(0xffffffffu, bad) & row_lanes) != 0;
-#pragma unroll
-            for (int off = kL / 2; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-            if (!is_v) {
-              const int e = clamp_exp(14 - ilog2(mx));
-              const float up = pow2i(e);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) w[i] = pack_half2(bf16_lo(w[i]) * up, bf16_hi(w[i]) * up);
-              if (ch == 0) s_kf[g % kInfo][r] = pow2i(-e);
-            }
-            if (bad) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) w[i] = 0u;
-              if (ch == 0) atomicOr(&s_bad[g % kInfo][r / 32], 1u << (r & 31));
-            }
-            st_shared_v4(dst + (ch / 8) * (BN * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4), w[0], w[1], w[2], w[3]);
-          }
         }
-        // the MMA reads the tile through the async proxy
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&full[op.i]);
-          mbar_arrive(&raw_empty[raw.i]);
-        }
+        sc_in.next();
       }
-    }
-  } else if (warp == kWarpScan) {
-    // -------------------------------------------------- scales' exponents
-    // ahead of the conversion: a tile's largest scales fix the powers of two
-    // that its keys and values are taken with, and the scales become the fp16
-    // pairs that multiply the codes, in place
-    Ring<NR> raw;
-    int g = 0;
-    for (int x = x0; x < x1 && !fail;) {
-      const Seg s = seg_at(p, x, x1);
-      x += s.t1 - s.t0;
-      int e_v = INT_MAX;  // the exponent that V's operands have in O (unset)
-#pragma unroll 1
-      for (int t = live_tile(pl, s, s.t0); t < s.t1; t = live_tile(pl, s, t + 1), ++g, raw.next()) {
-        const int st = raw.i;
-        float4 info = make_float4(1.f, 1.f, 1.f, 0.f);
-        if (t < pl.ts + pl.tr) {
-          if (!ring_wait(&raw_full[st], raw.phase, p.err, abort_flag)) {
-            fail = true;
-            break;
-          }
-          const int left = (t >= pl.ts ? s.nv - (t - pl.ts) * BN : s.sl - t * BN);
-          const uint32_t rks = sR(st) + 2 * Y::kCodes, rvs = rks + Y::kScales;
-          constexpr int kPer = BN * NG / 32;
-          float ksc[kPer], vsc[kPer], km = 0.f, vm = 0.f;
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      if (i < 0) continue;
+      if (i >= noted) break;
+      const int4 rec = sm.rec[kv][i % kInfo];
+      const int cnt = rec.x >> 8 & 255;
+      if (rec.x & kFresh) e_v = INT_MAX;
+      float4 info = make_float4(1.f, 1.f, 0.f, 0.f);
+      int e;
+      if (!(rec.x & kKindNodes)) {
+        asm volatile("cp.async.wait_group 1;" ::: "memory");  // (a lane reads what it copied itself)
+        const uint32_t at = sS(kv, sc.i) + lane * (NG * 4);
+        constexpr int kPer = BN / 32;
+        float y[kPer][NG], most = 0.f;
 #pragma unroll
-          for (int i = 0; i < kPer; ++i) {
-            const int idx = lane + 32 * i;
-            // a slot behind the last: whatever is staged counts 0
-            ksc[i] = idx / NG < left ? lds_f32(rks + 4 * idx) : 0.f;
-            vsc[i] = idx / NG < left ? lds_f32(rvs + 4 * idx) : 0.f;
-            km = fmaxf(km, fabsf(ksc[i]));
-            vm = fmaxf(vm, fabsf(vsc[i]));
+        for (int k = 0; k < kPer; ++k) {
+          lds_row<NG>(at + 32 * k * (NG * 4), y[k]);
+          if (lane + 32 * k >= cnt) {  // a slot behind the last: whatever is staged counts 0
+#pragma unroll
+            for (int j = 0; j < NG; ++j) y[k][j] = 0.f;
           }
-          // (of values >= 0 the bits order as the values do)
-          km = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(km)));
-          vm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vm)));
-          // |code * scale| < 2^(ilog2 + 8): K below 2^15, V first below 2^12
-          const int e_k = clamp_exp(7 - ilog2(km));
-          if (vm > 0.f) {
-            const int want = min(kMostUp, clamp_exp(4 - ilog2(vm)));
+#pragma unroll
+          for (int j = 0; j < NG; ++j) most = fmaxf(most, fabsf(y[k][j]));
+        }
+        // (of values >= 0 the bits order as the values do)
+        most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
+        // scales below 2^15; V's first at 2^13, so that O is rescaled only where
+        // they grow by more
+        e = clamp_exp(14 - ilog2(most));
+        if (kv) {
+          if (most > 0.f) {
+            const int want = min(kMostUp, e - 1);
             if (e_v == INT_MAX) {
               e_v = want;  // every value so far was 0, and so is O
-            } else if (want + 3 < e_v) {
-              info.y = pow2i(max(want - e_v, -126));
+            } else if (want + 1 < e_v) {
+              info.x = pow2i(max(want - e_v, -126));
               e_v = want;
             }
           }
-          const float up_k = pow2i(e_k), up_v = e_v == INT_MAX ? 1.f : pow2i(e_v);
-          info.x = pow2i(-e_k);
+          e = e_v == INT_MAX ? kCodeBits : e_v;
+        }
+        const float up = pow2i(e);
 #pragma unroll
-          for (int i = 0; i < kPer; ++i) {
-            const int idx = lane + 32 * i;
-            const float a = ksc[i] * up_k, b = vsc[i] * up_v;
-            sts32(rks + 4 * idx, pack_half2(a, a));
-            sts32(rvs + 4 * idx, pack_half2(b, b));
-          }
-        } else {
-          const int j0 = (t - pl.ts - pl.tr) * kNodes + lane;
-          const int32_t *depth = p.depth + int64_t(s.b) * p.n;
-          const uint32_t lo = __ballot_sync(0xffffffffu, j0 < p.n && depth[min(j0, p.n - 1)] >= 0);
-          const uint32_t hi = __ballot_sync(0xffffffffu, j0 + 32 < p.n && depth[min(j0 + 32, p.n - 1)] >= 0);
-          if (lane == 0) {
-            s_live[g % kInfo] = make_uint2(lo, hi);
-            s_bad[g % kInfo][0] = s_bad[g % kInfo][1] = 0u;
-          }
-          if (!ring_wait(&raw_full[st], raw.phase, p.err, abort_flag)) {
-            fail = true;
-            break;
-          }
-          // nodes follow the segment's cached tiles: from here on O stays in this scale
-          if (e_v == INT_MAX) e_v = 0;
-        }
-        __syncwarp();
+        for (int k = 0; k < kPer; ++k) sts_row<NG>(at + 32 * k * (NG * 4), y[k], up);
+      } else {
+        const int32_t *depth = p.depth + int64_t(rec.z / p.c.n_kv_heads) * p.n + rec.y;
+        const uint32_t lo = __ballot_sync(0xffffffffu, lane < cnt && depth[min(lane, cnt - 1)] >= 0);
+        const uint32_t hi = __ballot_sync(0xffffffffu, lane + 32 < cnt && depth[min(lane + 32, cnt - 1)] >= 0);
         if (lane == 0) {
-          // 2^-e of K; the factor that O needs before this tile's V; 2^-e of V; e of V
-          info.z = e_v == INT_MAX ? 1.f : pow2i(-e_v);
-          info.w = e_v == INT_MAX ? 0.f : float(e_v);
-          s_info[g % kInfo] = info;
-          mbar_arrive(&scan_full[st]);
-          mbar_arrive(&raw_empty[st]);
+          sm.live[kv][i % kInfo] = make_uint2(lo, hi);
+          sm.bad[kv][i % kInfo][0] = sm.bad[kv][i % kInfo][1] = 0u;
         }
+        // (nodes follow the segment's cached tiles: O stays in this scale)
+        if (e_v == INT_MAX) e_v = kCodeBits;
+        e = kv ? e_v : kCodeBits;
+      }
+      __syncwarp();
+      if (lane == 0) {
+        // operands of codes hold code * scale * 2^(e - 24), and so O
+        info.y = pow2i(-e);
+        info.z = float(e - kCodeBits);
+        if (kv) sm.info[i % kInfo] = info;
+        else sm.down_k[i % kInfo] = info.y;
+        mbar_arrive(&sm.sc_full[kv][sc.i]);
+      }
+      // ---- the codes, or the nodes' rows
+      if (!ring_wait(&sm.raw_empty[kv][raw.i], raw.phase, abort_flag)) {
+        fail = true;
+        break;
+      }
+      uint64_t *bar = &sm.raw_full[kv][raw.i];
+      const uint32_t dst = sR(kv, raw.i);
+      expect_tx(bar, rec.x & kKindNodes ? cnt * (2 * D) : cnt * D, leader);
+      __syncwarp();
+      if (!(rec.x & kKindNodes)) {
+        const int c1 = rec.x >> 16 & 255;
+        if (leader && c1 > 0) bulk_copy(dst, codes + (rec.z * nslot + rec.w) * D, c1 * D, bar);
+        if (leader && c1 < cnt) bulk_copy(dst + c1 * D, codes + (rec.z * nslot + p.c.sink_cap) * D, (cnt - c1) * D, bar);
+      } else {
+#pragma unroll 1
+        for (int r = lane; r < cnt; r += 32) bulk_copy(dst + r * (2 * D), node_row(rec.z, rec.y + r), 2 * D, bar);
+      }
+      __syncwarp();
+      raw.next(), sc.next();
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp < kWarpFeedK) {
+    // -------------------------------------------------- operands
+    const int turn = warp - kWarpTurn, kv = turn & 1;
+    constexpr int kTurnRows = BN / 4;
+    const int row_w = (turn >> 1) * kTurnRows;  // the warp's first row
+    constexpr int kPieces = D / 16, kRowsIt = 32 / kPieces, kIts = kTurnRows / kRowsIt, kU = 4;
+    static_assert(kIts % kU == 0, "rows of a warp");
+    // A lane takes 16 codes of a row, which become two 16-byte chunks.  K-major
+    // (and for V MN-major) 128-byte swizzle: row * 128 + chunk ^ (row & 7) inside
+    // a box of 64 channels.  Of eight neighbouring lanes the four in the upper
+    // box (D = 128) have the other row of a pair: its swizzle differs in the
+    // lowest bit, so the eight cover all chunk positions, that is all banks, at
+    // once, as their 16-byte loads do.
+    const int piece = lane % kPieces, box = piece / 4, c0 = (2 * piece) & 7;
+    const int row_l = D == 128 ? (lane / kPieces) ^ box : lane / kPieces;
+    const uint32_t codes_off = (row_w + row_l) * D + piece * 16, scale_off = 4 * ((row_w + row_l) * NG + piece / 2);
+    const uint32_t operand = kv ? sV : sK;
+    const uint32_t row_off = operand + (row_w + row_l) * 128 + box * (BN * 128);
+    const uint32_t first_c = (c0 ^ (row_l & 7)) << 4;  // and the other chunk: ^ 16
+    Ring<NR> raw;
+    Ring<NS> sc;
+    Ring<NK> op;
+    op.phase = 1;
+    int flags = 0;
+#pragma unroll 1
+    for (int g = 0; !(flags & kLast); ++g, raw.next(), sc.next(), op.next()) {
+      if (!ring_wait(&sm.sc_full[kv][sc.i], sc.phase, abort_flag) ||
+          !ring_wait(&sm.raw_full[kv][raw.i], raw.phase, abort_flag) ||
+          !ring_wait(&sm.op_empty[kv][op.i], op.phase, abort_flag)) {
+        fail = true;
+        break;
+      }
+      flags = sm.rec[kv][g % kInfo].x;
+      if (!(flags & kKindNodes)) {
+        const uint32_t raw_at = sR(kv, raw.i) + codes_off, sc_at = sS(kv, sc.i) + scale_off;
+        const uint32_t dst = row_off + op.i * Y::kKV;
+#pragma unroll 1
+        for (int i0 = 0; i0 < kIts; i0 += kU) {
+          uint32_t x[kU][4], s2[kU];
+#pragma unroll
+          for (int i = 0; i < kU; ++i) {
+            ld_shared_v4(raw_at + (i0 + i) * kRowsIt * D, x[i][0], x[i][1], x[i][2], x[i][3]);
+            s2[i] = lds32(sc_at + (i0 + i) * kRowsIt * NG * 4);
+          }
+#pragma unroll
+          for (int i = 0; i < kU; ++i) {
+            // a lane's rows are kRowsIt (4 or 8) apart: their swizzles differ in
+            // one bit at most
+            const uint32_t at = dst + (i0 + i) * kRowsIt * 128 + (first_c ^ ((i * kRowsIt & 4) << 4));
+            const uint32_t off = hmul2(s2[i], kMinus128);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const uint32_t wa = x[i][2 * q] ^ 0x80808080u, wb = x[i][2 * q + 1] ^ 0x80808080u;
+              st_shared_v4(q ? at ^ 16u : at, scaled_codes(wa, kBytes01, s2[i], off), scaled_codes(wa, kBytes23, s2[i], off),
+                           scaled_codes(wb, kBytes01, s2[i], off), scaled_codes(wb, kBytes23, s2[i], off));
+            }
+          }
+        }
+      } else {
+        // nodes: D/8 lanes to a row, a quarter of the tile's rows per warp
+        constexpr int kL = D / 8, kR = 32 / kL;
+        const int sub = lane / kL, ch = lane % kL, cnt = flags >> 8 & 255;
+        const uint2 alive = sm.live[kv][g % kInfo];
+        const uint32_t src = sR(kv, raw.i), dst = operand + op.i * Y::kKV;
+#pragma unroll 1
+        for (int r0 = (turn >> 1) * (kNodes / 4); r0 < (turn >> 1) * (kNodes / 4) + kNodes / 4; r0 += kR) {
+          const int r = r0 + sub;
+          const bool use = r < cnt && ((r < 32 ? alive.x : alive.y) >> (r & 31) & 1u);
+          uint32_t x[4] = {0u, 0u, 0u, 0u};
+          if (use) ld_shared_v4(src + r * (2 * D) + ch * 16, x[0], x[1], x[2], x[3]);
+          uint32_t m2 = 0u;  // of magnitudes the bits order as the values do, infinities and NaN above all
+#pragma unroll
+          for (int e = 0; e < 4; ++e) m2 = max_u16x2(m2, x[e] & 0x7fff7fffu);
+          uint32_t most = max(m2 << 16, m2 & 0xffff0000u);
+#pragma unroll
+          for (int off = kL / 2; off >= 1; off >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, off));
+          const bool bad = most >= 0x7f800000u;
+          if (!kv) {
+            const int e = clamp_exp(14 - ilog2(__uint_as_float(most)));
+            const float up = pow2i(e);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = pack_half2(bf16_lo(x[i]) * up, bf16_hi(x[i]) * up);
+            if (ch == 0) sm.kf[g % kKf][r] = pow2i(-e);
+          }
+          if (bad) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = 0u;
+            if (ch == 0) atomicOr(&sm.bad[kv][g % kInfo][r / 32], 1u << (r & 31));
+          }
+          st_shared_v4(dst + (ch / 8) * (BN * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4), x[0], x[1], x[2], x[3]);
+        }
+      }
+      // the MMA reads the tile through the async proxy
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&sm.op_full[kv][op.i]);
+        mbar_arrive(&sm.raw_empty[kv][raw.i]);
+        mbar_arrive(&sm.sc_empty[kv][sc.i]);
       }
     }
   } else if (warp == kWarpS) {
@@ -621,173 +692,303 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
     const uint32_t leader = elect_one();
     constexpr uint32_t kId = idesc_f16(BM, BN, 0), kIdNodes = idesc_f16(BM, kNodes, 0);
     Ring<NK> kr;
-    Ring<2> sr;  // a buffer is free once PV has read the P in it
+    Ring<2> sr;  // a buffer is free once the softmax has read it
     sr.phase = 1;
     uint32_t q_phase = 0;
     const uint64_t dk = sdesc_sw128(sK, 16, 1024);
-    for (int x = x0; x < x1 && !fail;) {
-      const Seg s = seg_at(p, x, x1);
-      x += s.t1 - s.t0;
-      fail = !ring_wait(&q_full, q_phase, p.err, abort_flag);
-      q_phase ^= 1u;
+    int flags = 0;
 #pragma unroll 1
-      for (int t = live_tile(pl, s, s.t0); t < s.t1 && !fail; t = live_tile(pl, s, t + 1), kr.next(), sr.next()) {
-        if (!ring_wait(&k_full[kr.i], kr.phase, p.err, abort_flag) ||
-            !ring_wait(&pv_done[sr.i], sr.phase, p.err, abort_flag)) {
-          fail = true;
-          break;
-        }
-        tc_fence_after();
-        const uint64_t kd = dk + uint64_t(kr.i * (Y::kKV >> 4));
-        const uint32_t id = t < pl.ts + pl.tr ? kId : kIdNodes;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)  // 16 channels = 8 TMEM columns of Q's fp16 pairs
-          mma_ts(tmem + sr.i * BN, tQ + kk * 8, kd + (kk >> 2) * (BN * 128 >> 4) + (kk & 3) * 2, id, kk > 0 ? 1u : 0u, leader);
-        mma_commit(&s_full[sr.i], leader);
-        mma_commit(&k_empty[kr.i], leader);
+    for (int g = 0; !(flags & kLast); ++g, kr.next(), sr.next()) {
+      bool ok = ring_wait(&sm.op_full[0][kr.i], kr.phase, abort_flag) &&
+                ring_wait(&sm.s_empty[sr.i], sr.phase, abort_flag);
+      flags = sm.rec[0][g % kInfo].x;
+      if (ok && (flags & kFresh)) {
+        ok = ring_wait(&sm.q_full, q_phase, abort_flag);
+        q_phase ^= 1u;
       }
+      if (!ok) {
+        fail = true;
+        break;
+      }
+      tc_fence_after();
+      const uint64_t kd = dk + uint64_t(kr.i * (Y::kKV >> 4));
+      const uint32_t id = flags & kKindNodes ? kIdNodes : kId;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)  // 16 channels = 8 TMEM columns of Q's fp16 pairs
+        mma_ts(tmem + sr.i * BN, tQ + kk * 8, kd + (kk >> 2) * (BN * 128 >> 4) + (kk & 3) * 2, id, kk > 0 ? 1u : 0u, leader);
+      mma_commit(&sm.s_full[sr.i], leader);
+      mma_commit(&sm.op_empty[0][kr.i], leader);
     }
-  } else if (warp == kWarpPV) {
+  } else {
     // -------------------------------------------------- O += P(g) V(g)
     // (a segment's first product overwrites O: its P exists only once the
     // softmax warps have read the segment before out of it)
     const uint32_t leader = elect_one();
     constexpr uint32_t kId = idesc_f16(BM, D, 1), kIdNodes = idesc_bf16(BM, D, 1);
-    Ring<NV> vr;
-    Ring<2> pr;
+    Ring<NK> vr;
+    uint32_t p_phase = 0;
     const uint64_t dv = sdesc_sw128(sV, BN * 128, 1024);
-    for (int x = x0; x < x1 && !fail;) {
-      const Seg s = seg_at(p, x, x1);
-      x += s.t1 - s.t0;
-      uint32_t more = 0;
+    int flags = 0;
 #pragma unroll 1
-      for (int t = live_tile(pl, s, s.t0); t < s.t1 && !fail; t = live_tile(pl, s, t + 1), vr.next(), pr.next(), more = 1) {
-        if (!ring_wait(&v_full[vr.i], vr.phase, p.err, abort_flag) ||
-            !ring_wait(&p_full[pr.i], pr.phase, p.err, abort_flag)) {
-          fail = true;
-          break;
-        }
-        tc_fence_after();
-        const uint64_t vd = dv + uint64_t(vr.i * (Y::kKV >> 4));
-        const uint32_t tP = tmem + pr.i * BN;
-        if (t < pl.ts + pl.tr) {
-#pragma unroll
-          for (int kk = 0; kk < BN / 16; ++kk)
-            mma_ts(tO, tP + kk * 8, vd + kk * (16 * 128 >> 4), kId, kk > 0 ? 1u : more, leader);
-        } else {
-#pragma unroll
-          for (int kk = 0; kk < kNodes / 16; ++kk)
-            mma_ts(tO, tP + kk * 8, vd + kk * (16 * 128 >> 4), kIdNodes, kk > 0 ? 1u : more, leader);
-        }
-        mma_commit(&pv_done[pr.i], leader);
-        mma_commit(&v_empty[vr.i], leader);
+    for (int g = 0; !(flags & kLast); ++g, vr.next(), p_phase ^= 1u) {
+      if (!ring_wait(&sm.op_full[1][vr.i], vr.phase, abort_flag) || !ring_wait(&sm.p_full, p_phase, abort_flag)) {
+        fail = true;
+        break;
       }
+      flags = sm.rec[1][g % kInfo].x;
+      tc_fence_after();
+      const uint64_t vd = dv + uint64_t(vr.i * (Y::kKV >> 4));
+      const uint32_t id = flags & kKindNodes ? kIdNodes : kId, more = flags & kFresh ? 0u : 1u;
+#pragma unroll
+      for (int kk = 0; kk < BN / 16; ++kk)  // (nodes: half as many keys)
+        mma_ts(tO, tP + kk * 8, vd + kk * (16 * 128 >> 4), id, kk > 0 ? 1u : more,
+               kk >= kNodes / 16 && (flags & kKindNodes) ? 0u : leader);
+      mma_commit(&sm.pv_done, leader);
+      mma_commit(&sm.op_empty[1][vr.i], leader);
     }
   }
   } else {
     // -------------------------------------------------- softmax warps
     regs_inc<kRegsSoftmax>();
-    const uint32_t lane_base = uint32_t(warp * 32) << 16;
-    const int r_blk = tid & (kLanes - 1), copy = tid / kLanes;  // row of the block; which copy of it
-    const int col0 = copy * kCols;
-    const int R = p.n * p.G, r = blk * pl.rb + r_blk;
+    // a lane has two threads, one in either warpgroup, for halves of its columns
+    // of a tile and of its channels
+    const int wg = warp >> 2, tl = tid & (BM - 1);
+    const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
+    const int r_blk = tl & (kLanes - 1), copy = tl / kLanes;  // row of the block; which copy of it
+    const int col0 = copy * (BN / REP) + wg * kCols;
+    const int R = p.n * p.G, r = blk * pl.rb + r_blk, words = (p.n + 31) / 32;
     const bool exists = r_blk < pl.rb && r < R;
     auto node_of = [&](int row) { return p.G == 1 ? row : int(__umulhi(unsigned(row), p.g_magic)); };
     const int node = exists ? node_of(r) : 0;
-    const uint32_t my_t = sT + warp * (32 * Y::kRow);
-    Ring<2> sr;
-    Ring<NV> vr;
-    int g = 0;
-    for (int x = x0; x < x1 && !fail;) {
-      const Seg s = seg_at(p, x, x1);
-      const bool first_seg = x == x0;
-      x += s.t1 - s.t0;
-      const int hk = s.pair - s.b * p.c.n_kv_heads;
-      const int depth = exists ? p.depth[int64_t(s.b) * p.n + node] : -1;
-      // ---- Q: the warp's 32 rows, D / 8 lanes to a row, turned over to a row
-      // per lane in shared memory, as fp16 times 2^eq of the row
-      float c_row;
-      bool dead = !s.sane || depth < 0;
-      {
-        constexpr int kL = D / 8, kRows = 32 / kL, kIt = 32 / kRows;
-        const int sub = lane / kL, ch = lane % kL;
-        uint4 w[kIt];
+    const uint32_t my_t = sT + warp * Y::kT1;
+    int turns = 0;
+    // what the lane's other thread says
+    auto other = [&](float x) {
+      sm.mx[turns & 1][wg][tl] = x;
+      asm volatile("bar.sync %0, 64;" ::"r"(2 + (warp & 3)) : "memory");
+      return sm.mx[turns++ & 1][wg ^ 1][tl];
+    };
+    {
+      // P's columns of other copies stay 0
+      uint32_t zero[32];
 #pragma unroll
-        for (int i = 0; i < kIt; ++i) {
-          const int rb_ = (warp * 32 + i * kRows + sub) & (kLanes - 1), rw = blk * pl.rb + rb_;
-          const bool ok = rb_ < pl.rb && rw < R;
-          const int nd = ok ? node_of(rw) : 0;
-          const uint16_t *src = p.q + ((int64_t(s.b) * p.n + nd) * p.Hq + hk * p.G + (ok ? rw - nd * p.G : 0)) * D + 8 * ch;
-          w[i] = ok ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0u, 0u, 0u, 0u);
+      for (int i = 0; i < 32; ++i) zero[i] = 0u;
+      tmem_st32(tP + lane_base + 32 * wg, zero);
+      tmem_st_wait();
+    }
+    // ---- Q: half the channels of the warp's 32 rows, D / 16 lanes to a row,
+    // turned over to a row per lane in shared memory, as fp16 times 2^eq of the
+    // row
+    struct Row {
+      float c;    // 2^-eq log2(e) / sqrt(D)
+      int depth;
+      bool dead;  // padding, or not finite
+    };
+    constexpr int kL = D / 16, kRows = 32 / kL, kIt = 32 / kRows;
+    auto load_q = [&](const Seg &s, uint4 (&w)[kIt], Row &me) {
+      const int hk = s.pair - s.b * p.c.n_kv_heads, sub = lane / kL, ch = lane % kL;
+      me.depth = exists ? p.depth[int64_t(s.b) * p.n + node] : -1;
+#pragma unroll
+      for (int i = 0; i < kIt; ++i) {
+        const int rb_ = ((warp & 3) * 32 + i * kRows + sub) & (kLanes - 1), rw = blk * pl.rb + rb_;
+        const bool ok = rb_ < pl.rb && rw < R;
+        const int nd = ok ? node_of(rw) : 0;
+        const uint16_t *src =
+            p.q + ((int64_t(s.b) * p.n + nd) * p.Hq + hk * p.G + (ok ? rw - nd * p.G : 0)) * D + wg * (D / 2) + 8 * ch;
+        w[i] = ok ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0u, 0u, 0u, 0u);
+      }
+    };
+    auto turn_at = [](int row, int chunk) { return uint32_t(row * 128 + ((chunk ^ (row & 7)) << 4)); };
+    // (the products that read the Q before are done: the warp waited for its last S)
+    auto stage_q = [&](const Seg &s, const uint4 (&w)[kIt], Row &me) {
+      const int sub = lane / kL, ch = lane % kL;
+      uint32_t row[D / 4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {  // 16 rows at a time
+        __syncwarp();
+#pragma unroll
+        for (int i = h * kIt / 2; i < (h + 1) * kIt / 2; ++i)
+          st_shared_v4(my_t + turn_at((i * kRows + sub) & 15, ch), w[i].x, w[i].y, w[i].z, w[i].w);
+        __syncwarp();
+        if (lane / 16 == h) {
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i)
+            ld_shared_v4(my_t + turn_at(lane & 15, i), row[4 * i], row[4 * i + 1], row[4 * i + 2], row[4 * i + 3]);
         }
-        uint32_t row[D / 2];
-#pragma unroll
-        for (int h = 0; h < D / 64; ++h) {
-          __syncwarp();
-          if (D == 64 || ch / 8 == h) {
-#pragma unroll
-            for (int i = 0; i < kIt; ++i)
-              st_shared_v4(my_t + (i * kRows + sub) * Y::kRow + (ch & 7) * 16, w[i].x, w[i].y, w[i].z, w[i].w);
-          }
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            ld_shared_v4(my_t + lane * Y::kRow + i * 16, row[h * 32 + 4 * i], row[h * 32 + 4 * i + 1], row[h * 32 + 4 * i + 2],
-                         row[h * 32 + 4 * i + 3]);
-        }
-        float qm = 0.f;
-        bool finite = true;
-#pragma unroll
-        for (int i = 0; i < D / 2; ++i) {
-          const float a = fabsf(bf16_lo(row[i])), b = fabsf(bf16_hi(row[i]));
-          finite = finite && a < INFINITY && b < INFINITY;
-          qm = fmaxf(qm, fmaxf(a, b));
-        }
-        dead = dead || !finite;
-        const int eq = clamp_exp(14 - ilog2(qm));
-        const float up = pow2i(eq);
-#pragma unroll
-        for (int i = 0; i < D / 2; ++i) row[i] = dead ? 0u : pack_half2(bf16_lo(row[i]) * up, bf16_hi(row[i]) * up);
-        c_row = pow2i(-eq) * (1.4426950408889634f * rsqrtf(float(D)));
-        // (the products that read the Q before are done: the warp waited for its last S)
-#pragma unroll
-        for (int h = 0; h < D / 64; ++h) tmem_st32(tQ + lane_base + 32 * h, row + 32 * h);
-        tmem_st_wait();
-        tc_fence_before();
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&q_full);
-
+      uint32_t most = 0u;  // of magnitudes the bits order as the values do, infinities and NaN above all
+#pragma unroll
+      for (int i = 0; i < D / 4; ++i) most = max_u16x2(most, row[i] & 0x7fff7fffu);
+      const float qm = __uint_as_float(max(most << 16, most & 0xffff0000u));
+      const float both = other(qm < INFINITY ? qm : INFINITY), qa = fmaxf(qm < INFINITY ? qm : INFINITY, both);
+      me.dead = !s.sane || me.depth < 0 || !(qa < INFINITY);
+      const int eq = clamp_exp(14 - ilog2(qa));
+      const float up = pow2i(eq);
+#pragma unroll
+      for (int i = 0; i < D / 4; ++i) row[i] = me.dead ? 0u : pack_half2(bf16_lo(row[i]) * up, bf16_hi(row[i]) * up);
+      me.c = pow2i(-eq) * (1.4426950408889634f * rsqrtf(float(D)));
+      if constexpr (D == 128) tmem_st32(tQ + lane_base + 32 * wg, row);
+      else tmem_st16(tQ + lane_base + 16 * wg, row);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.q_full);
+    };
+    Ring<2> sr;
+    Ring<NK> vr;
+    uint32_t pv_phase = 0;  // of the tile before
+    int g = 0, x = x0;
+    bool first_seg = true;
+    Seg s = {}, next = {};
+    Row me = {}, next_row = {};
+    float m_used = -INFINITY, l = 0.f, down = 1.f;
+    // Rounds of: the next segment's queries, so that its products start while
+    // the one's before are written; the output of the one before; its tiles.
+    for (int round = 0;; ++round) {
+      const bool more = x < x1;
+      uint4 w[kIt];
+      if (more) {
+        next = seg_at(p, x, x1);
+        x += next.t1 - next.t0;
+        load_q(next, w, next_row);
+      }
+      if (round > 0) {
+        l += other(l);
+        if (me.dead) m_used = -INFINITY, l = 0.f;
+      }
+      if (more) stage_q(next, w, next_row);
+      if (round > 0) {
+        if (!fail) fail = !ring_wait(&sm.pv_done, pv_phase, abort_flag);
+        pv_phase ^= 1u;
+        tc_fence_after();
+        fail = softmax_any(fail);  // (the barriers below want all their warps)
+        const int hk = s.pair - s.b * p.c.n_kv_heads;
+        if (s.all) {
+          // copies merge: the row's weight of each, then the sum through shared memory
+          float m_all = m_used, l_all = l, scale;
+          if constexpr (REP > 1) {
+            if (wg == 0) sm.ml[tl] = make_float2(m_used, l);
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            m_all = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < REP; ++c) m_all = fmaxf(m_all, sm.ml[c * kLanes + r_blk].x);
+            l_all = 0.f;
+#pragma unroll
+            for (int c = 0; c < REP; ++c) {
+              const float2 o = sm.ml[c * kLanes + r_blk];
+              l_all += o.x == -INFINITY && o.y == 0.f ? 0.f : o.y * ex2(o.x - m_all);
+            }
+            scale = m_used == -INFINITY && l == 0.f ? 0.f : (l_all != 0.f ? ex2(m_used - m_all) * kUnits * down / l_all : 0.f);
+          } else {
+            scale = l != 0.f ? kUnits * down / l : 0.f;
+          }
+          const int h = hk * p.G + (r - node * p.G);
+          uint16_t *dst = p.out + ((int64_t(s.b) * p.n + node) * p.Hq + h) * D + wg * (D / 2);
+          // every copy finishes its part of the half row's channels, kC at a time,
+          // with what the others send it
+          constexpr int kPart = D / 2 / REP, kC = kPart < 16 ? kPart : 16;
+          auto send_at = [&](int chunk) { return uint32_t(lane * 64 + ((chunk ^ (lane >> 1 & 3)) << 4)); };
+          const uint32_t tO_half = tO + lane_base + wg * (D / 2);
+#pragma unroll 1
+          for (int ch = 0; ch < kPart; ch += kC) {
+            float o[kC];
+#pragma unroll
+            for (int k = 0; k < REP; ++k) {
+              // send copy + k's channels of this round, take the own ones from copy - k
+              uint32_t ov[kC];
+              const int to = (copy + k) % REP * kPart + ch;
+              if constexpr (kC == 16) tmem_ld16(tO_half + to, ov);
+                else tmem_ld8(tO_half + to, ov);
+                tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < kC; ++i) ov[i] = scale != 0.f ? __float_as_uint(__uint_as_float(ov[i]) * scale) : 0u;
+              if (k == 0) {
+#pragma unroll
+                for (int i = 0; i < kC; ++i) o[i] = __uint_as_float(ov[i]);
+              } else {
+#pragma unroll
+                for (int i = 0; i < kC; i += 4)
+                  st_shared_v4(my_t + send_at(i / 4), ov[i], ov[i + 1], ov[i + 2], ov[i + 3]);
+                asm volatile("bar.sync %0, 128;" ::"r"(6 + wg) : "memory");
+                const int from = (copy + REP - k) % REP;
+                const uint32_t src = sT + (wg * 4 + (from * kLanes + r_blk) / 32) * Y::kT1;
+#pragma unroll
+                for (int i = 0; i < kC; i += 4) {
+                  uint32_t a0, a1, a2, a3;
+                  ld_shared_v4(src + send_at(i / 4), a0, a1, a2, a3);
+                  o[i] += __uint_as_float(a0), o[i + 1] += __uint_as_float(a1);
+                  o[i + 2] += __uint_as_float(a2), o[i + 3] += __uint_as_float(a3);
+                }
+                asm volatile("bar.sync %0, 128;" ::"r"(6 + wg) : "memory");
+              }
+            }
+            if (exists && !fail) {
+#pragma unroll
+              for (int i = 0; i < kC; i += 8)
+                st_global_v4(dst + copy * kPart + ch + i, pack_bf16x2(o[i], o[i + 1]), pack_bf16x2(o[i + 2], o[i + 3]),
+                             pack_bf16x2(o[i + 4], o[i + 5]), pack_bf16x2(o[i + 6], o[i + 7]));
+            }
+          }
+          if (wg == 0 && copy == 0 && exists && p.lse && !fail)
+            p.lse[(int64_t(s.b) * p.Hq + h) * p.n + node] =
+                l_all != 0.f ? 0.6931471805599453f * (m_all - kPBias + log2f(l_all)) : -INFINITY;
+        } else if (!fail) {
+          float *part = p.parts + (size_t(blockIdx.x) * 2 + (first_seg ? 0 : 1)) * part_floats<D>();
+#pragma unroll 1
+            for (int ch = wg * (D / 2); ch < (wg + 1) * (D / 2); ch += 32) {
+              uint32_t ov[32];
+              tmem_ld32(tO + lane_base + ch, ov);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; i += 4)
+                *reinterpret_cast<float4 *>(part + ((ch + i) / 4 * BM + tl) * 4) =
+                    make_float4(__uint_as_float(ov[i]) * kUnits * down, __uint_as_float(ov[i + 1]) * kUnits * down,
+                                __uint_as_float(ov[i + 2]) * kUnits * down, __uint_as_float(ov[i + 3]) * kUnits * down);
+            }
+          if (wg == 0) *reinterpret_cast<float2 *>(part + BM * D + 2 * tl) = make_float2(m_used, l);
+        }
+        tc_fence_before();
+        first_seg = false;
+      }
+      if (!more || fail) break;
+      s = next;
+      me = next_row;
+      const bool dead = me.dead;
+      // a node tile's mask words of this thread's columns
+      const uint32_t *mask_row = p.mask + (int64_t(s.b) * p.n + node) * words;
+      uint32_t mk[2] = {0u, 0u};
+      auto load_mask = [&](int t_n) {
+        const int w_ = 2 * t_n + col0 / 32;
+        mk[0] = col0 < kNodes && w_ < words ? mask_row[w_] : 0u;
+        if constexpr (kCols == 64) mk[1] = col0 < kNodes && w_ + 1 < words ? mask_row[w_ + 1] : 0u;
+      };
+      load_mask(max(0, s.t0 - pl.ts - pl.tr));
       // ring entries below `low` are outside the row's window
       // (a dead row takes what comes and is put to 0 at the end)
-      const int low = dead ? 0 : int(min((long long)INT_MAX, max(0ll, (long long)depth + s.nv - p.window + 1)));
-      float m_used = -INFINITY, l = 0.f, down = 1.f;
-      bool any = false;
-      uint64_t *pv_last = nullptr;  // PV of the tile before: its barrier and parity
-      uint32_t pv_phase = 0;
-#pragma unroll 1
-      for (int t = live_tile(pl, s, s.t0); t < s.t1; t = live_tile(pl, s, t + 1), ++g, sr.next(), vr.next()) {
+      const int low = dead ? 0 : int(min((long long)INT_MAX, max(0ll, (long long)me.depth + s.nv - p.window + 1)));
+      m_used = -INFINITY, l = 0.f;
+      // a tile of cached keys or (kN) of nodes
+      const int first_t = min(live_tile(pl, s, s.t0), s.t1 - 1);
+      auto tile = [&](auto kind, int t) {
+        constexpr bool kN = decltype(kind)::value;
         const int u = sr.i;
-        const bool nodes = t >= pl.ts + pl.tr;
-        if (!fail) fail = !ring_wait(&s_full[u], sr.phase, p.err, abort_flag);
-        // what the warps that turn a node tile say of it: K's were done before S
-        if (nodes && !fail) fail = !ring_wait(&v_full[vr.i], vr.phase, p.err, abort_flag);
+        // what V's warps say of the tile (K's were done before S)
+        if (kN && !fail) fail = !ring_wait(&sm.op_full[1][vr.i], vr.phase, abort_flag);
         tc_fence_after();
-        uint64_t *const pv_prev = pv_last;
-        const uint32_t pv_prev_phase = pv_phase;
-        pv_last = &pv_done[u];
-        pv_phase = sr.phase;
-        const float4 info = s_info[g % kInfo];
-        down = info.z;
+        const uint32_t tS = tmem + u * BN + lane_base + col0;
         uint32_t v[kCols];
-        // never 0, which would make NaN of a masked column's -inf: |S| < 2^37, so at
-        // 2^-126 and below a score is 2^-89 at most and its weight 1 to every bit
-        float ct = fmaxf(c_row * info.x, 1.1754943508222875e-38f);
-        const uint32_t tS = tmem + u * BN + lane_base;
-        if (!nodes) {
+        if constexpr (kCols == 16) {
+          tmem_ld16(tS, v);
+        } else {
 #pragma unroll
-          for (int i = 0; i < kCols; i += 32) tmem_ld32(tS + col0 + i, v + i);
-          tmem_ld_wait();
+          for (int i = 0; i < kCols; i += 32) tmem_ld32(tS + i, v + i);
+        }
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.s_empty[u]);
+        if constexpr (!kN) {
           // columns [lo, hi) are seen
           const bool ring = t >= pl.ts;
           const int first = (ring ? t - pl.ts : t) * BN + col0;
@@ -797,33 +998,25 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
 #pragma unroll
             for (int i = 0; i < kCols; ++i) v[i] = i >= lo && i < hi ? v[i] : 0xff800000u;
           }
-        } else if (col0 < kNodes) {
-          // 64 columns: the copies behind them see nothing of a node tile
-          const int t_n = t - pl.ts - pl.tr, words = (p.n + 31) / 32;
-          constexpr int kC = kCols < kNodes ? kCols : kNodes;
+        } else {
+          // (columns from 64 on are not of this tile: their words are 0)
+          const uint2 alive = sm.live[0][g % kInfo];
 #pragma unroll
-          for (int i = 0; i < kC; i += 32) tmem_ld32(tS + col0 + i, v + i);
-          tmem_ld_wait();
-          const uint32_t *mk = p.mask + (int64_t(s.b) * p.n + node) * words;
-          const uint2 alive = s_live[g % kInfo];
+          for (int i = 0; i < kCols; i += 32) {
+            const int wd = (col0 / 32 + i / 32) & 1, sh = col0 & 31;
+            const uint32_t bad = (sm.bad[0][g % kInfo][wd] | sm.bad[1][g % kInfo][wd]) >> sh;
+            const uint32_t see = dead ? 0u : (mk[i / 32] & (wd ? alive.y : alive.x)) >> sh;
 #pragma unroll
-          for (int i = 0; i < kC; i += 32) {
-            const int wd = (col0 + i) / 32;
-            const uint32_t bad = s_bad[g % kInfo][wd];
-            uint32_t see = 0u;
-            if (!dead && 2 * t_n + wd < words) see = mk[2 * t_n + wd] & (wd ? alive.y : alive.x);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float sc = __uint_as_float(v[i + e]) * s_kf[g % kInfo][col0 + i + e];
+            for (int e = 0; e < 32 && i + e < kCols; ++e) {
+              const float sc = __uint_as_float(v[i + e]) * sm.kf[g % kKf][(col0 & (kNodes - 1)) + i + e];
               v[i + e] = see >> e & 1u ? (bad >> e & 1u ? 0x7fffffffu : __float_as_uint(sc)) : 0xff800000u;
             }
           }
-#pragma unroll
-          for (int i = kC; i < kCols; ++i) v[i] = 0xff800000u;
-        } else {
-#pragma unroll
-          for (int i = 0; i < kCols; ++i) v[i] = 0xff800000u;
+          load_mask(t - pl.ts - pl.tr + 1);
         }
+        // never 0, which would make NaN of a masked column's -inf: |S| < 2^37, so at
+        // 2^-126 and below a score is 2^-89 at most and its weight 1 to every bit
+        const float ct = fmaxf(me.c * sm.down_k[g % kInfo] * kUnits, 1.1754943508222875e-38f);
         float mxp[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) mxp[i] = __uint_as_float(v[i]);
@@ -833,17 +1026,17 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
           for (int i = 0; i < 8; ++i) mxp[i] = max3(mxp[i], __uint_as_float(v[j + i]), __uint_as_float(v[j + 8 + i]));
 #pragma unroll
         for (int i = 0; i < 8; ++i) mxp[i] = fmaxf(mxp[i], __uint_as_float(v[kCols - 8 + i]));
-        const float mx = ct * max3(max3(mxp[0], mxp[1], mxp[2]), max3(mxp[3], mxp[4], mxp[5]), fmaxf(mxp[6], mxp[7]));
+        const float mine = max3(max3(mxp[0], mxp[1], mxp[2]), max3(mxp[3], mxp[4], mxp[5]), fmaxf(mxp[6], mxp[7]));
+        const float mx = ct * fmaxf(mine, other(mine));
         const bool need = mx > m_used + kLazyLog2;  // the first tile with a key included
-        float alpha = info.y;  // what V's new exponent asks of O
+        float alpha = 1.f;
         if (need) {
-          const float a = ex2(m_used - mx);  // 0 at the first
-          alpha *= a;
-          l *= a;
+          alpha = ex2(m_used - mx);  // 0 at the first
+          l *= alpha;
           m_used = mx;
         }
         // nodes' weights carry V's exponent
-        const float shift = kPBias - (m_used == -INFINITY ? 0.f : m_used) + (nodes ? info.w : 0.f);
+        const float shift = kPBias - (m_used == -INFINITY ? 0.f : m_used) + (kN ? sm.info[g % kInfo].z : 0.f);
         const uint64_t c2 = pack_f32x2(ct, ct), nmc2 = pack_f32x2(shift, shift);
         float rsp[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -853,141 +1046,59 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
           a = ex2(a);
           b = ex2(b);
           add_f32x2(rsp[(i >> 1) & 1 ? 2 : 0], rsp[(i >> 1) & 1 ? 3 : 1], a, b);
-          v[i / 2] = nodes ? pack_bf16x2(a, b) : pack_half2(a, b);
+          v[i / 2] = kN ? pack_bf16x2(a, b) : pack_half2(a, b);
         }
         const float sum = (rsp[0] + rsp[1]) + (rsp[2] + rsp[3]);
-        l += nodes ? sum * info.z : sum;
-        if (any && __any_sync(0xffffffffu, alpha != 1.f)) {
-          // O once the PV before has landed
-          if (!fail) fail = !ring_wait(pv_prev, pv_prev_phase, p.err, abort_flag);
+        if (!kN && !fail) fail = !ring_wait(&sm.op_full[1][vr.i], vr.phase, abort_flag);
+        const float4 info = sm.info[g % kInfo];
+        down = info.y;
+        alpha *= info.x;  // what V's new exponent asks of O
+        l += kN ? sum * info.y * kUnits : sum;
+        if (t != first_t) {
+          // P and O once the PV before has landed
+          if (!fail) fail = !ring_wait(&sm.pv_done, pv_phase, abort_flag);
+          pv_phase ^= 1u;
           tc_fence_after();
+          if (__any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
-          for (int ch = 0; ch < D; ch += 32) {
-            uint32_t ov[32];
-            tmem_ld32(tO + lane_base + ch, ov);
-            tmem_ld_wait();
+            for (int ch = wg * (D / 2); ch < (wg + 1) * (D / 2); ch += 16) {
+              uint32_t ov[16];
+              tmem_ld16(tO + lane_base + ch, ov);
+              tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
-            tmem_st32(tO + lane_base + ch, ov);
+              for (int i = 0; i < 16; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+              tmem_st16(tO + lane_base + ch, ov);
+            }
           }
         }
-        any = true;
-        // P over S: this copy's columns, zeros in the others'
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t out[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            if constexpr (REP == 1) out[i] = v[h * 32 + i];
-            else if constexpr (REP == 2) out[i] = copy == h ? v[i] : 0u;
-            else out[i] = copy == 2 * h + i / 16 ? v[i % 16] : 0u;
-          }
-          tmem_st32(tS + 32 * h, out);
-        }
+        if constexpr (kCols == 64) tmem_st32(tP + lane_base + col0 / 2, v);
+        else if constexpr (kCols == 32) tmem_st16(tP + lane_base + col0 / 2, v);
+        else tmem_st8(tP + lane_base + col0 / 2, v);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[u]);
-      }
-      // ---- the segment's end
-      if (any && !fail) fail = !ring_wait(pv_last, pv_phase, p.err, abort_flag);
-      tc_fence_after();
-      if constexpr (REP > 1) fail = softmax_any(fail);  // (the barriers below want all four warps)
-      if (dead) m_used = -INFINITY, l = 0.f;
-      if (s.all) {
-        // copies merge: the row's weight of each, then the sum through shared memory
-        float scale = l > 0.f || !(l <= 0.f) ? down / l : 0.f;
-        float m_all = m_used, l_all = l;
-        if constexpr (REP > 1) {
-          s_ml[tid] = make_float2(m_used, l);
-          asm volatile("bar.sync 1, 128;" ::: "memory");
-          float mm = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < REP; ++c) mm = fmaxf(mm, s_ml[c * kLanes + r_blk].x);
-          l_all = 0.f;
-#pragma unroll
-          for (int c = 0; c < REP; ++c) {
-            const float2 o = s_ml[c * kLanes + r_blk];
-            l_all += o.x == -INFINITY && o.y == 0.f ? 0.f : o.y * ex2(o.x - mm);
-          }
-          m_all = mm;
-          scale = m_used == -INFINITY && l == 0.f ? 0.f : (l_all != 0.f ? ex2(m_used - mm) * down / l_all : 0.f);
-        }
-        const int64_t row = ((int64_t(s.b) * p.n + node) * p.Hq + hk * p.G + (r - node * p.G));
-        uint16_t *dst = p.out + row * D;
-        // 32 channels at a time; of several copies the first adds the others'
+        if (lane == 0) mbar_arrive(&sm.p_full);
+        ++g, sr.next(), vr.next();
+      };
+      // (which tiles, the warps know by themselves: after a wait that gave up they
+      // still meet at the same barriers)
 #pragma unroll 1
-        for (int ch = 0; ch < D; ch += 32) {
-          uint32_t ov[32];
-          if (any) {
-            tmem_ld32(tO + lane_base + ch, ov);
-            tmem_ld_wait();
-          }
-#pragma unroll
-          for (int i = 0; i < 32; ++i) ov[i] = any && scale != 0.f ? __float_as_uint(__uint_as_float(ov[i]) * scale) : 0u;
-          if constexpr (REP > 1) {
-            // a lane's 32 floats in its warp's buffer: 132 bytes would not keep 16-byte stores aligned, 144 does
-            if (copy > 0) {
-#pragma unroll
-              for (int i = 0; i < 32; i += 4)
-                st_shared_v4(my_t + lane * Y::kRow + 4 * i, ov[i], ov[i + 1], ov[i + 2], ov[i + 3]);
-            }
-            asm volatile("bar.sync 1, 128;" ::: "memory");
-            if (copy == 0) {
-#pragma unroll
-              for (int c = 1; c < REP; ++c) {
-                const uint32_t src = sT + (c * kLanes / 32 + warp) * (32 * Y::kRow) + lane * Y::kRow;
-#pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                  uint32_t a0, a1, a2, a3;
-                  ld_shared_v4(src + 4 * i, a0, a1, a2, a3);
-                  ov[i] = __float_as_uint(__uint_as_float(ov[i]) + __uint_as_float(a0));
-                  ov[i + 1] = __float_as_uint(__uint_as_float(ov[i + 1]) + __uint_as_float(a1));
-                  ov[i + 2] = __float_as_uint(__uint_as_float(ov[i + 2]) + __uint_as_float(a2));
-                  ov[i + 3] = __float_as_uint(__uint_as_float(ov[i + 3]) + __uint_as_float(a3));
-                }
-              }
-            }
-          }
-          if (copy == 0 && exists && !fail) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 8)
-              st_global_v4(dst + ch + i, pack_bf16x2(__uint_as_float(ov[i]), __uint_as_float(ov[i + 1])),
-                           pack_bf16x2(__uint_as_float(ov[i + 2]), __uint_as_float(ov[i + 3])),
-                           pack_bf16x2(__uint_as_float(ov[i + 4]), __uint_as_float(ov[i + 5])),
-                           pack_bf16x2(__uint_as_float(ov[i + 6]), __uint_as_float(ov[i + 7])));
-          }
-          if constexpr (REP > 1) asm volatile("bar.sync 1, 128;" ::: "memory");
-        }
-        if (copy == 0 && exists && p.lse && !fail)
-          p.lse[(int64_t(s.b) * p.Hq + hk * p.G + (r - node * p.G)) * p.n + node] =
-              l_all != 0.f ? 0.6931471805599453f * (m_all - kPBias + log2f(l_all)) : -INFINITY;
-      } else if (!fail) {
-        float *part = p.parts + (size_t(blockIdx.x) * 2 + (first_seg ? 0 : 1)) * part_floats<D>();
-        if (any) {
-#pragma unroll 1
-          for (int ch = 0; ch < D; ch += 32) {
-            uint32_t ov[32];
-            tmem_ld32(tO + lane_base + ch, ov);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<float4 *>(part + ((ch + i) / 4 * BM + tid) * 4) =
-                  make_float4(__uint_as_float(ov[i]) * down, __uint_as_float(ov[i + 1]) * down,
-                              __uint_as_float(ov[i + 2]) * down, __uint_as_float(ov[i + 3]) * down);
-          }
-        }
-        *reinterpret_cast<float2 *>(part + BM * D + 2 * tid) = make_float2(m_used, l);
+      for (int t = first_t; t < s.t1; t = live_tile(pl, s, t + 1)) {
+        if (!fail) fail = !ring_wait(&sm.s_full[sr.i], sr.phase, abort_flag);
+        if (t < pl.ts + pl.tr) tile(std::false_type{}, t);
+        else tile(std::true_type{}, t);
       }
-      tc_fence_before();
     }
   }
 
   // ---- common exit: on the error path give copies and MMAs still in flight a
   //      bounded time (about 2 ms) to land before shared memory and TMEM go
   tc_fence_before();
-  if (__syncthreads_or(fail || *abort_flag))
+  if (__syncthreads_or(fail || *abort_flag)) {
+    if (tid == 0) raise_device_error(p.err, ND_DEVERR_TIMEOUT);
+#pragma unroll 1
     for (int i = 0; i < 2000; ++i) __nanosleep(1000);
+  }
   __syncthreads();
   if (warp == kWarpS) {
     tc_fence_after();
