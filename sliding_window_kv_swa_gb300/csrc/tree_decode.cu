@@ -73,7 +73,7 @@ constexpr int kWarpTurn = 8, kWarpFeedK = 16, kWarpFeedV = 17, kWarpS = 18;
 // softmax thread holds up to 64 scores.
 constexpr int kRegsLaunch = 96, kRegsSoftmax = 144, kRegsOther = 64;
 static_assert(2 * 128 * kRegsSoftmax + 3 * 128 * kRegsOther <= kThreads * kRegsLaunch, "register split");
-constexpr int kAhead = 4;         // tiles that are asked into L2 ahead of their copies
+constexpr int kBatch = 8;         // tiles that are noted, and asked into L2, at once
 constexpr int kKf = 8;            // node tiles' key factors in flight: more than the tiles between operand and softmax
 constexpr float kLazyLog2 = 8.f;  // the maximum used may lag the true one by 2^8
 constexpr float kPBias = 7.f;     // P is scaled by 2^7
@@ -143,25 +143,25 @@ struct Lay {
   static constexpr int kKV = kBoxes * BN * 128;          // one K or V operand tile
   static constexpr int kCodes = BN * D, kScales = BN * NG * 4;
   static_assert(kNodes * D * 2 == kCodes, "a node tile's rows take the codes' place");
-  // stages: operands of K and of V, staged codes (or nodes' rows) of either, staged scales of either
-  static constexpr int NK = D == 128 ? 2 : 3, NR = D == 128 ? 2 : 5, NS = NR + 1;
-  static constexpr int kInfo = 16;                       // tile records in flight
-  static_assert(kInfo > NS + NK + 2 + kAhead, "tile records");
+  // stages: operands of K and of V; staged codes and scales (or nodes' rows) of either
+  static constexpr int NK = D == 128 ? 2 : 3, NR = D == 128 ? 2 : 5;
+  static constexpr int kRaw = kCodes + kScales;
+  static constexpr int kRec = 32, kInfo = 16;            // tiles noted; tiles between operand and softmax
+  static_assert(kRec >= 2 * kBatch + NR + NK + 2 && kInfo > NK + 3, "tile records");
   static constexpr int kT1 = 2048, kT = 8 * kT1;         // a softmax warp's turning buffer
-  static constexpr int oK = 0, oV = oK + NK * kKV, oR = oV + NK * kKV, oS = oR + 2 * NR * kCodes, oT = oS + 2 * NS * kScales,
-                       oSmall = oT + kT;
+  static constexpr int oK = 0, oV = oK + NK * kKV, oR = oV + NK * kKV, oT = oR + 2 * NR * kRaw, oSmall = oT + kT;
   // barriers; [2]: K, V
   struct Small {
-    uint64_t raw_full[2][NR], raw_empty[2][NR], sc_full[2][NS], sc_empty[2][NS], op_full[2][NK], op_empty[2][NK];
-    uint64_t s_full[2], s_empty[2], p_full, pv_done, q_full;  // s_: score buffers
-    int4 rec[2][kInfo];       // tiles, as the feeders see them ahead: flags (kFresh ...), first key, pair, slot
-    float4 info[kInfo];       // for the softmax: the factor that O needs before the tile's V; 2^-e of V; e - 24
-    float down_k[kInfo];      // 2^-e of K
-    uint2 live[2][kInfo];     // node tiles: nodes that are not padding
-    uint32_t bad[2][kInfo][2];  // and those whose key, value is not finite
-    float kf[kKf][kNodes];    // and 2^-e of their keys
-    float mx[2][2][BM];       // what the two halves of a row's columns tell each other, in turns
-    float2 ml[BM];            // and its copies
+    uint64_t raw_full[2][NR], raw_empty[2][NR], op_full[2][NK], op_empty[2][NK];
+    uint64_t s_full[2], s_empty[2], p_full[2], pv_done[2], q_full, v_known[4];  // s_: score buffers
+    int4 rec[2][kRec];           // tiles, as the feeders note them: flags (kFresh ...), first key, pair, slot
+    // for the softmax
+    int e[2][kInfo][4];          // exponents of each 32 keys
+    uint16_t live[kInfo][4];     // node tiles: nodes that are not padding, 16 to a word
+    uint16_t bad[2][kInfo][4];   // and those whose key, value is not finite
+    float kf[kKf][kNodes];       // and 2^-e of their keys
+    float m[2][BM];              // the rows' maxima, from a tile's softmax threads to the next one's
+    float2 ml[BM];               // and what their copies have
     uint32_t tmem;
     int abort;
   };
@@ -341,9 +341,9 @@ __device__ __forceinline__ int live_tile(const TreePlan &pl, const Seg &s, int t
 template <int D, int REP>
 __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_constant__ TreeParams p) {
   using Y = Lay<D>;
-  constexpr int NK = Y::NK, NR = Y::NR, NS = Y::NS, NG = Y::NG, kInfo = Y::kInfo;
+  constexpr int NK = Y::NK, NR = Y::NR, NG = Y::NG, kInfo = Y::kInfo, kRec = Y::kRec;
   constexpr int kLanes = BM / REP;     // rows, and lanes of a copy of them
-  constexpr int kCols = BN / REP / 2;  // a thread's columns of a tile
+  constexpr int kCols = BN / REP;      // a thread's columns of a tile
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   typename Y::Small &sm = *reinterpret_cast<typename Y::Small *>(smem_raw + Y::oSmall);
 
@@ -352,29 +352,25 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
   volatile int *abort_flag = &sm.abort;
   const uint32_t base = smem_u32(smem_raw);
   const uint32_t sK = base + Y::oK, sV = base + Y::oV, sT = base + Y::oT;
-  auto sR = [&](int kv, int st) { return base + Y::oR + (kv * NR + st) * Y::kCodes; };
-  auto sS = [&](int kv, int st) { return base + Y::oS + (kv * NS + st) * Y::kScales; };
+  auto sR = [&](int kv, int st) { return base + Y::oR + (kv * NR + st) * Y::kRaw; };
 
   if (tid == 0) {
     for (int kv = 0; kv < 2; ++kv) {
       for (int s = 0; s < NR; ++s) {
-        mbar_init(&sm.raw_full[kv][s], 1);   // the copies' transaction
-        mbar_init(&sm.raw_empty[kv][s], 4);  // the warps that turn it
-      }
-      for (int s = 0; s < NS; ++s) {
-        mbar_init(&sm.sc_full[kv][s], 1);
-        mbar_init(&sm.sc_empty[kv][s], 4);
+        mbar_init(&sm.raw_full[kv][s], NG == 4 ? 1 : 33);  // the bulk copies' transaction (D = 64: and the lanes' copies)
+        mbar_init(&sm.raw_empty[kv][s], 4);                // the warps that turn it
       }
       for (int s = 0; s < NK; ++s) {
         mbar_init(&sm.op_full[kv][s], 4);
         mbar_init(&sm.op_empty[kv][s], 1);
       }
       mbar_init(&sm.s_full[kv], 1);
-      mbar_init(&sm.s_empty[kv], 8);
+      mbar_init(&sm.s_empty[kv], 4);
+      mbar_init(&sm.p_full[kv], 4);
+      mbar_init(&sm.pv_done[kv], 1);
     }
-    mbar_init(&sm.p_full, 8);
-    mbar_init(&sm.pv_done, 1);
     mbar_init(&sm.q_full, 8);
+    for (int s = 0; s < 4; ++s) mbar_init(&sm.v_known[s], 4);
     sm.abort = 0;
     fence_barrier_init();
   }
@@ -403,10 +399,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
   regs_dec<kRegsOther>();
   if (warp == kWarpFeedK || warp == kWarpFeedV) {
     // -------------------------------------------------- feeders, one for K and one for V
-    // Per round i: note tile i + kAhead and ask its codes into L2 (two staged
-    // tiles are too few bytes in flight for memory's latency), copy tile i + 1's
-    // scales, turn tile i's scales into fp16 pairs and its exponent, copy its
-    // codes.
+    // Ahead of the copies tiles are noted and asked into L2, kBatch at a time, a
+    // lane to a tile (two staged tiles are too few bytes in flight for memory's
+    // latency).
     const int kv = warp == kWarpFeedV;
     const uint32_t leader = elect_one();
     const int8_t *const codes = kv ? p.c.v_codes : p.c.k_codes;
@@ -417,14 +412,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
       return (kv ? p.v : p.k) + (int64_t(b) * p.n + j) * (kv ? p.v_stride : p.k_stride) + (pair - b * p.c.n_kv_heads) * D;
     };
     Ring<NR> raw;
-    Ring<NS> sc, sc_in;
-    raw.phase = sc_in.phase = 1;  // the first round of an empty ring does not wait
-    int noted = 0, x = x0, t = 0, e_v = INT_MAX;  // e_v: the exponent that V's operands have in O (unset)
+    raw.phase = 1;  // the first round of an empty ring does not wait
+    int noted = 0, x = x0, t = 0;
     bool fresh = true;
     Seg s = {};
 #pragma unroll 1
-    for (int i = -kAhead;; ++i) {
-      if (!fresh || x < x1) {
+    for (int i = 0;; ++i, raw.next()) {
+      if (noted - i < kBatch && (!fresh || x < x1)) {
         if (fresh) {
           s = seg_at(p, x, x1);
           x += s.t1 - s.t0;
@@ -441,151 +435,92 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
             }
           }
         }
-        int4 rec = make_int4(fresh ? kFresh : 0, 0, s.pair, 0);
-        if (t < pl.ts + pl.tr) {
-          const bool ring = t >= pl.ts;
-          rec.y = (ring ? t - pl.ts : t) * BN;
-          const int cnt = max(0, min(BN, (ring ? s.nv : s.sl) - rec.y));
-          int c1 = cnt;
-          rec.w = rec.y;
-          if (ring) {
-            // two pieces where it wraps
-            unsigned w = unsigned(s.ring0) + unsigned(rec.y);
-            if (w >= unsigned(p.c.ring_cap)) w -= unsigned(p.c.ring_cap);
-            c1 = min(cnt, p.c.ring_cap - int(w));
-            rec.w = p.c.sink_cap + int(w);
-            rec.x |= kKindRing;
-          }
-          rec.x |= cnt << 8 | c1 << 16;
-          if (leader && c1 > 0) bulk_l2(codes + (s.pair * nslot + rec.w) * D, c1 * D);
-        } else {
-          rec.y = (t - pl.ts - pl.tr) * kNodes;
-          const int cnt = min(kNodes, p.n - rec.y);
-          rec.x |= kKindNodes | cnt << 8;
+        // lane j: the j-th live tile from t on
+        auto nth = [&](int j) {
+          int u = t + j;
+          if (t < pl.ts && u >= s.ts && j > 0) u += pl.ts - max(s.ts, t + 1) ;
+          if (t < pl.ts + pl.tr && u >= pl.ts + s.tr && j > 0) u += pl.tr - max(s.tr, t < pl.ts ? 0 : t + 1 - pl.ts);
+          return u;
+        };
+        const int u = nth(lane);
+        const bool mine = lane < kBatch && u < s.t1;
+        const int count = __popc(__ballot_sync(0xffffffffu, mine));
+        const bool end = nth(lane + 1) >= s.t1;
+        if (mine) {
+          int4 rec = make_int4((fresh && lane == 0 ? kFresh : 0) | (end ? kEnd : 0) | (end && x >= x1 ? kLast : 0), 0, s.pair, 0);
+          if (u < pl.ts + pl.tr) {
+            const bool ring = u >= pl.ts;
+            rec.y = (ring ? u - pl.ts : u) * BN;
+            const int cnt = max(0, min(BN, (ring ? s.nv : s.sl) - rec.y));
+            int c1 = cnt;
+            rec.w = rec.y;
+            if (ring) {
+              // two pieces where it wraps
+              unsigned w = unsigned(s.ring0) + unsigned(rec.y);
+              if (w >= unsigned(p.c.ring_cap)) w -= unsigned(p.c.ring_cap);
+              c1 = min(cnt, p.c.ring_cap - int(w));
+              rec.w = p.c.sink_cap + int(w);
+              rec.x |= kKindRing;
+            }
+            rec.x |= cnt << 8 | c1 << 16;
+            if (c1 > 0) {
+              const size_t at = s.pair * nslot + rec.w;
+              bulk_l2(codes + at * D, c1 * D);
+              // (in whole 16 bytes: at D = 64 a slot's scales are 8)
+              const size_t lo = (at * (NG * 4) + 15) & ~size_t(15), hi = ((at + c1) * (NG * 4)) & ~size_t(15);
+              if (hi > lo) bulk_l2(reinterpret_cast<const char *>(scales) + lo, uint32_t(hi - lo));
+            }
+          } else {
+            rec.y = (u - pl.ts - pl.tr) * kNodes;
+            const int cnt = min(kNodes, p.n - rec.y);
+            rec.x |= kKindNodes | cnt << 8;
 #pragma unroll 1
-          for (int r = lane; r < cnt; r += 32) {
-            const uint16_t *row = node_row(s.pair, rec.y + r);
-            prefetch_l2(row);
-            if (D == 128) prefetch_l2(row + 64);
+            for (int r = 0; r < cnt; ++r) prefetch_l2(node_row(s.pair, rec.y + r));
           }
+          sm.rec[kv][(noted + lane) % kRec] = rec;
         }
-        t = live_tile(pl, s, t + 1);
+        noted += count;
+        t = nth(count);
         fresh = t >= s.t1;
-        if (fresh) rec.x |= kEnd;
-        if (fresh && x >= x1) rec.x |= kLast;
-        if (lane == 0) sm.rec[kv][noted % kInfo] = rec;
-        ++noted;
         __syncwarp();
       }
-      if (i + 1 >= 0 && i + 1 < noted) {
-        const int4 rec = sm.rec[kv][(i + 1) % kInfo];
-        if (!ring_wait(&sm.sc_empty[kv][sc_in.i], sc_in.phase, abort_flag)) {
-          fail = true;
-          break;
-        }
-        if (!(rec.x & kKindNodes)) {
-          // a lane copies a row's scales of every 32: 16 (D = 128) or 8 bytes, and
-          // a head's first one aligned to no more than that
-          const int cnt = rec.x >> 8 & 255, c1 = rec.x >> 16 & 255;
-          const uint32_t dst = sS(kv, sc_in.i) + lane * (NG * 4);
-          const float *src = scales + (rec.z * nslot + rec.w + lane) * NG;
-#pragma unroll
-          for (int k = 0; k < BN / 32; ++k) {
-            const int r = lane + 32 * k;
-            if (r < cnt) {
-              const float *from = r < c1 ? src + 32 * k * NG : scales + (rec.z * nslot + p.c.sink_cap + (r - c1)) * NG;
-              if constexpr (NG == 4) cp_async16(dst + 32 * k * (NG * 4), from);
-              else cp_async8(dst + 32 * k * (NG * 4), from);
-            }
-          }
-        }
-        sc_in.next();
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-      if (i < 0) continue;
       if (i >= noted) break;
-      const int4 rec = sm.rec[kv][i % kInfo];
+      const int4 rec = sm.rec[kv][i % kRec];
       const int cnt = rec.x >> 8 & 255;
-      if (rec.x & kFresh) e_v = INT_MAX;
-      float4 info = make_float4(1.f, 1.f, 0.f, 0.f);
-      int e;
-      if (!(rec.x & kKindNodes)) {
-        asm volatile("cp.async.wait_group 1;" ::: "memory");  // (a lane reads what it copied itself)
-        const uint32_t at = sS(kv, sc.i) + lane * (NG * 4);
-        constexpr int kPer = BN / 32;
-        float y[kPer][NG], most = 0.f;
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-          lds_row<NG>(at + 32 * k * (NG * 4), y[k]);
-          if (lane + 32 * k >= cnt) {  // a slot behind the last: whatever is staged counts 0
-#pragma unroll
-            for (int j = 0; j < NG; ++j) y[k][j] = 0.f;
-          }
-#pragma unroll
-          for (int j = 0; j < NG; ++j) most = fmaxf(most, fabsf(y[k][j]));
-        }
-        // (of values >= 0 the bits order as the values do)
-        most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
-        // scales below 2^15; V's first at 2^13, so that O is rescaled only where
-        // they grow by more
-        e = clamp_exp(14 - ilog2(most));
-        if (kv) {
-          if (most > 0.f) {
-            const int want = min(kMostUp, e - 1);
-            if (e_v == INT_MAX) {
-              e_v = want;  // every value so far was 0, and so is O
-            } else if (want + 1 < e_v) {
-              info.x = pow2i(max(want - e_v, -126));
-              e_v = want;
-            }
-          }
-          e = e_v == INT_MAX ? kCodeBits : e_v;
-        }
-        const float up = pow2i(e);
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) sts_row<NG>(at + 32 * k * (NG * 4), y[k], up);
-      } else {
-        const int32_t *depth = p.depth + int64_t(rec.z / p.c.n_kv_heads) * p.n + rec.y;
-        const uint32_t lo = __ballot_sync(0xffffffffu, lane < cnt && depth[min(lane, cnt - 1)] >= 0);
-        const uint32_t hi = __ballot_sync(0xffffffffu, lane + 32 < cnt && depth[min(lane + 32, cnt - 1)] >= 0);
-        if (lane == 0) {
-          sm.live[kv][i % kInfo] = make_uint2(lo, hi);
-          sm.bad[kv][i % kInfo][0] = sm.bad[kv][i % kInfo][1] = 0u;
-        }
-        // (nodes follow the segment's cached tiles: O stays in this scale)
-        if (e_v == INT_MAX) e_v = kCodeBits;
-        e = kv ? e_v : kCodeBits;
-      }
-      __syncwarp();
-      if (lane == 0) {
-        // operands of codes hold code * scale * 2^(e - 24), and so O
-        info.y = pow2i(-e);
-        info.z = float(e - kCodeBits);
-        if (kv) sm.info[i % kInfo] = info;
-        else sm.down_k[i % kInfo] = info.y;
-        mbar_arrive(&sm.sc_full[kv][sc.i]);
-      }
-      // ---- the codes, or the nodes' rows
       if (!ring_wait(&sm.raw_empty[kv][raw.i], raw.phase, abort_flag)) {
         fail = true;
         break;
       }
       uint64_t *bar = &sm.raw_full[kv][raw.i];
       const uint32_t dst = sR(kv, raw.i);
-      expect_tx(bar, rec.x & kKindNodes ? cnt * (2 * D) : cnt * D, leader);
+      expect_tx(bar, rec.x & kKindNodes ? cnt * (2 * D) : cnt * (NG == 4 ? D + NG * 4 : D), leader);
       __syncwarp();
       if (!(rec.x & kKindNodes)) {
         const int c1 = rec.x >> 16 & 255;
-        if (leader && c1 > 0) bulk_copy(dst, codes + (rec.z * nslot + rec.w) * D, c1 * D, bar);
-        if (leader && c1 < cnt) bulk_copy(dst + c1 * D, codes + (rec.z * nslot + p.c.sink_cap) * D, (cnt - c1) * D, bar);
+        const size_t at = rec.z * nslot + rec.w, wrap = rec.z * nslot + p.c.sink_cap;
+        if (leader && c1 > 0) {
+          bulk_copy(dst, codes + at * D, c1 * D, bar);
+          if (NG == 4) bulk_copy(dst + Y::kCodes, scales + at * NG, c1 * (NG * 4), bar);
+          if (c1 < cnt) {
+            bulk_copy(dst + c1 * D, codes + wrap * D, (cnt - c1) * D, bar);
+            if (NG == 4) bulk_copy(dst + Y::kCodes + c1 * (NG * 4), scales + wrap * NG, (cnt - c1) * (NG * 4), bar);
+          }
+        }
+        if constexpr (NG != 4) {
+          // 8 bytes a slot: a head's first ones aligned to no more than that
+#pragma unroll
+          for (int k = 0; k < BN / 32; ++k) {
+            const int r = lane + 32 * k;
+            if (r < cnt) cp_async8(dst + Y::kCodes + r * (NG * 4), scales + (r < c1 ? at + r : wrap + (r - c1)) * NG);
+          }
+        }
       } else {
 #pragma unroll 1
         for (int r = lane; r < cnt; r += 32) bulk_copy(dst + r * (2 * D), node_row(rec.z, rec.y + r), 2 * D, bar);
       }
+      if constexpr (NG != 4) cp_async_arrive(bar);
       __syncwarp();
-      raw.next(), sc.next();
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp < kWarpFeedK) {
     // -------------------------------------------------- operands
     const int turn = warp - kWarpTurn, kv = turn & 1;
@@ -601,26 +536,49 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
     // once, as their 16-byte loads do.
     const int piece = lane % kPieces, box = piece / 4, c0 = (2 * piece) & 7;
     const int row_l = D == 128 ? (lane / kPieces) ^ box : lane / kPieces;
-    const uint32_t codes_off = (row_w + row_l) * D + piece * 16, scale_off = 4 * ((row_w + row_l) * NG + piece / 2);
+    const uint32_t codes_off = (row_w + row_l) * D + piece * 16, scale_off = Y::kCodes + 4 * ((row_w + row_l) * NG + piece / 2);
     const uint32_t operand = kv ? sV : sK;
     const uint32_t row_off = operand + (row_w + row_l) * 128 + box * (BN * 128);
     const uint32_t first_c = (c0 ^ (row_l & 7)) << 4;  // and the other chunk: ^ 16
     Ring<NR> raw;
-    Ring<NS> sc;
     Ring<NK> op;
     op.phase = 1;
     int flags = 0;
 #pragma unroll 1
-    for (int g = 0; !(flags & kLast); ++g, raw.next(), sc.next(), op.next()) {
-      if (!ring_wait(&sm.sc_full[kv][sc.i], sc.phase, abort_flag) ||
-          !ring_wait(&sm.raw_full[kv][raw.i], raw.phase, abort_flag) ||
-          !ring_wait(&sm.op_empty[kv][op.i], op.phase, abort_flag)) {
+    for (int g = 0; !(flags & kLast); ++g, raw.next(), op.next()) {
+      if (!ring_wait(&sm.raw_full[kv][raw.i], raw.phase, abort_flag)) {
         fail = true;
         break;
       }
-      flags = sm.rec[kv][g % kInfo].x;
+      const int4 rec = sm.rec[kv][g % kRec];
+      flags = rec.x;
+      const int cnt = flags >> 8 & 255;
+      const uint32_t stage = sR(kv, raw.i);
       if (!(flags & kKindNodes)) {
-        const uint32_t raw_at = sR(kv, raw.i) + codes_off, sc_at = sS(kv, sc.i) + scale_off;
+        // the exponent of the warp's 32 keys, a lane to a key, and their scales as
+        // pairs of fp16, in place: the largest scale goes to 2^14 .. 2^15
+        const uint32_t at = stage + Y::kCodes + (row_w + lane) * (NG * 4);
+        float y[NG], most = 0.f;
+        lds_row<NG>(at, y);
+#pragma unroll
+        for (int j = 0; j < NG; ++j) {
+          if (row_w + lane >= cnt) y[j] = 0.f;  // a slot behind the last: whatever is staged counts 0
+          most = fmaxf(most, fabsf(y[j]));
+        }
+        // (of values >= 0 the bits order as the values do)
+        most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
+        const int e = min(kMostUp, clamp_exp(14 - ilog2(most)));
+        sts_row<NG>(at, y, pow2i(e));
+        if (lane == 0) sm.e[kv][g % kInfo][turn >> 1] = e;
+      }
+      __syncwarp();
+      if (kv && lane == 0) mbar_arrive(&sm.v_known[g & 3]);
+      if (!ring_wait(&sm.op_empty[kv][op.i], op.phase, abort_flag)) {
+        fail = true;
+        break;
+      }
+      if (!(flags & kKindNodes)) {
+        const uint32_t raw_at = stage + codes_off, sc_at = stage + scale_off;
         const uint32_t dst = row_off + op.i * Y::kKV;
 #pragma unroll 1
         for (int i0 = 0; i0 < kIts; i0 += kU) {
@@ -645,17 +603,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
           }
         }
       } else {
-        // nodes: D/8 lanes to a row, a quarter of the tile's rows per warp
+        // nodes: D/8 lanes to a row, 16 of the tile's rows per warp
         constexpr int kL = D / 8, kR = 32 / kL;
-        const int sub = lane / kL, ch = lane % kL, cnt = flags >> 8 & 255;
-        const uint2 alive = sm.live[kv][g % kInfo];
-        const uint32_t src = sR(kv, raw.i), dst = operand + op.i * Y::kKV;
+        const int sub = lane / kL, ch = lane % kL, first = (turn >> 1) * 16;
+        const int32_t *depth = p.depth + int64_t(rec.z / p.c.n_kv_heads) * p.n + rec.y;
+        const uint32_t alive = __ballot_sync(0xffffffffu, lane < 16 && first + lane < cnt && depth[min(first + lane, cnt - 1)] >= 0);
+        uint32_t bads = 0u;
+        const uint32_t dst = operand + op.i * Y::kKV;
 #pragma unroll 1
-        for (int r0 = (turn >> 1) * (kNodes / 4); r0 < (turn >> 1) * (kNodes / 4) + kNodes / 4; r0 += kR) {
-          const int r = r0 + sub;
-          const bool use = r < cnt && ((r < 32 ? alive.x : alive.y) >> (r & 31) & 1u);
+        for (int r0 = 0; r0 < 16; r0 += kR) {
+          const int r = first + r0 + sub;
           uint32_t x[4] = {0u, 0u, 0u, 0u};
-          if (use) ld_shared_v4(src + r * (2 * D) + ch * 16, x[0], x[1], x[2], x[3]);
+          if (alive >> (r0 + sub) & 1u) ld_shared_v4(stage + r * (2 * D) + ch * 16, x[0], x[1], x[2], x[3]);
           uint32_t m2 = 0u;  // of magnitudes the bits order as the values do, infinities and NaN above all
 #pragma unroll
           for (int e = 0; e < 4; ++e) m2 = max_u16x2(m2, x[e] & 0x7fff7fffu);
@@ -673,9 +632,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
           if (bad) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[i] = 0u;
-            if (ch == 0) atomicOr(&sm.bad[kv][g % kInfo][r / 32], 1u << (r & 31));
           }
+          const uint32_t who = __ballot_sync(0xffffffffu, bad);
+#pragma unroll
+          for (int k = 0; k < kR; ++k) bads |= (who >> (k * kL) & 1u) << (r0 + k);
           st_shared_v4(dst + (ch / 8) * (BN * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4), x[0], x[1], x[2], x[3]);
+        }
+        if (lane == 0) {
+          sm.bad[kv][g % kInfo][turn >> 1] = uint16_t(bads);
+          if (!kv) sm.live[g % kInfo][turn >> 1] = uint16_t(alive);
         }
       }
       // the MMA reads the tile through the async proxy
@@ -684,7 +649,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
       if (lane == 0) {
         mbar_arrive(&sm.op_full[kv][op.i]);
         mbar_arrive(&sm.raw_empty[kv][raw.i]);
-        mbar_arrive(&sm.sc_empty[kv][sc.i]);
       }
     }
   } else if (warp == kWarpS) {
@@ -692,7 +656,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
     const uint32_t leader = elect_one();
     constexpr uint32_t kId = idesc_f16(BM, BN, 0), kIdNodes = idesc_f16(BM, kNodes, 0);
     Ring<NK> kr;
-    Ring<2> sr;  // a buffer is free once the softmax has read it
+    // a buffer is free once the softmax has read it, or with P over it PV
+    Ring<2> sr;
     sr.phase = 1;
     uint32_t q_phase = 0;
     const uint64_t dk = sdesc_sw128(sK, 16, 1024);
@@ -700,8 +665,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
 #pragma unroll 1
     for (int g = 0; !(flags & kLast); ++g, kr.next(), sr.next()) {
       bool ok = ring_wait(&sm.op_full[0][kr.i], kr.phase, abort_flag) &&
-                ring_wait(&sm.s_empty[sr.i], sr.phase, abort_flag);
-      flags = sm.rec[0][g % kInfo].x;
+                ring_wait(REP == 1 ? &sm.pv_done[sr.i] : &sm.s_empty[sr.i], sr.phase, abort_flag);
+      flags = sm.rec[0][g % kRec].x;
       if (ok && (flags & kFresh)) {
         ok = ring_wait(&sm.q_full, q_phase, abort_flag);
         q_phase ^= 1u;
@@ -726,49 +691,52 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
     const uint32_t leader = elect_one();
     constexpr uint32_t kId = idesc_f16(BM, D, 1), kIdNodes = idesc_bf16(BM, D, 1);
     Ring<NK> vr;
-    uint32_t p_phase = 0;
+    Ring<2> pr;
     const uint64_t dv = sdesc_sw128(sV, BN * 128, 1024);
     int flags = 0;
 #pragma unroll 1
-    for (int g = 0; !(flags & kLast); ++g, vr.next(), p_phase ^= 1u) {
-      if (!ring_wait(&sm.op_full[1][vr.i], vr.phase, abort_flag) || !ring_wait(&sm.p_full, p_phase, abort_flag)) {
+    for (int g = 0; !(flags & kLast); ++g, vr.next(), pr.next()) {
+      if (!ring_wait(&sm.op_full[1][vr.i], vr.phase, abort_flag) || !ring_wait(&sm.p_full[pr.i], pr.phase, abort_flag)) {
         fail = true;
         break;
       }
-      flags = sm.rec[1][g % kInfo].x;
+      flags = sm.rec[1][g % kRec].x;
       tc_fence_after();
       const uint64_t vd = dv + uint64_t(vr.i * (Y::kKV >> 4));
       const uint32_t id = flags & kKindNodes ? kIdNodes : kId, more = flags & kFresh ? 0u : 1u;
 #pragma unroll
       for (int kk = 0; kk < BN / 16; ++kk)  // (nodes: half as many keys)
-        mma_ts(tO, tP + kk * 8, vd + kk * (16 * 128 >> 4), id, kk > 0 ? 1u : more,
+        mma_ts(tO, (REP == 1 ? tmem + pr.i * BN : tP) + kk * 8, vd + kk * (16 * 128 >> 4), id, kk > 0 ? 1u : more,
                kk >= kNodes / 16 && (flags & kKindNodes) ? 0u : leader);
-      mma_commit(&sm.pv_done, leader);
+      mma_commit(&sm.pv_done[pr.i], leader);
       mma_commit(&sm.op_empty[1][vr.i], leader);
     }
   }
   } else {
     // -------------------------------------------------- softmax warps
     regs_inc<kRegsSoftmax>();
-    // a lane has two threads, one in either warpgroup, for halves of its columns
-    // of a tile and of its channels
-    const int wg = warp >> 2, tl = tid & (BM - 1);
-    const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
+    // A lane has two threads, one in either warpgroup: for every other tile, and
+    // for half of its channels of Q and of the output.  A tile's thread gets the
+    // row's maximum from the one of the tile before as soon as that has it, so
+    // the two warpgroups work on neighbouring tiles side by side.
+    const int wg = warp >> 2, quad = warp & 3, tl = tid & (BM - 1);
+    const uint32_t lane_base = uint32_t(quad * 32) << 16;
     const int r_blk = tl & (kLanes - 1), copy = tl / kLanes;  // row of the block; which copy of it
-    const int col0 = copy * (BN / REP) + wg * kCols;
+    const int col0 = copy * kCols;
     const int R = p.n * p.G, r = blk * pl.rb + r_blk, words = (p.n + 31) / 32;
     const bool exists = r_blk < pl.rb && r < R;
-    auto node_of = [&](int row) { return p.G == 1 ? row : int(__umulhi(unsigned(row), p.g_magic)); };
-    const int node = exists ? node_of(r) : 0;
+    const int node = exists ? (p.G == 1 ? r : int(__umulhi(unsigned(r), p.g_magic))) : 0, head = exists ? r - node * p.G : 0;
     const uint32_t my_t = sT + warp * Y::kT1;
-    int turns = 0;
     // what the lane's other thread says
-    auto other = [&](float x) {
-      sm.mx[turns & 1][wg][tl] = x;
-      asm volatile("bar.sync %0, 64;" ::"r"(2 + (warp & 3)) : "memory");
-      return sm.mx[turns++ & 1][wg ^ 1][tl];
+    auto other = [&](float x, float y) {
+      float2 *half = reinterpret_cast<float2 *>(smem_raw + Y::oT);  // (what the copies send comes later)
+      half[wg * BM + tl] = make_float2(x, y);
+      asm volatile("bar.sync %0, 64;" ::"r"(2 + quad) : "memory");
+      const float2 o = half[(wg ^ 1) * BM + tl];
+      asm volatile("bar.sync %0, 64;" ::"r"(2 + quad) : "memory");
+      return o;
     };
-    {
+    if constexpr (REP > 1) {
       // P's columns of other copies stay 0
       uint32_t zero[32];
 #pragma unroll
@@ -776,94 +744,75 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
       tmem_st32(tP + lane_base + 32 * wg, zero);
       tmem_st_wait();
     }
-    // ---- Q: half the channels of the warp's 32 rows, D / 16 lanes to a row,
-    // turned over to a row per lane in shared memory, as fp16 times 2^eq of the
-    // row
     struct Row {
       float c;    // 2^-eq log2(e) / sqrt(D)
       int depth;
       bool dead;  // padding, or not finite
     };
-    constexpr int kL = D / 16, kRows = 32 / kL, kIt = 32 / kRows;
-    auto load_q = [&](const Seg &s, uint4 (&w)[kIt], Row &me) {
-      const int hk = s.pair - s.b * p.c.n_kv_heads, sub = lane / kL, ch = lane % kL;
-      me.depth = exists ? p.depth[int64_t(s.b) * p.n + node] : -1;
-#pragma unroll
-      for (int i = 0; i < kIt; ++i) {
-        const int rb_ = ((warp & 3) * 32 + i * kRows + sub) & (kLanes - 1), rw = blk * pl.rb + rb_;
-        const bool ok = rb_ < pl.rb && rw < R;
-        const int nd = ok ? node_of(rw) : 0;
-        const uint16_t *src =
-            p.q + ((int64_t(s.b) * p.n + nd) * p.Hq + hk * p.G + (ok ? rw - nd * p.G : 0)) * D + wg * (D / 2) + 8 * ch;
-        w[i] = ok ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0u, 0u, 0u, 0u);
-      }
-    };
-    auto turn_at = [](int row, int chunk) { return uint32_t(row * 128 + ((chunk ^ (row & 7)) << 4)); };
-    // (the products that read the Q before are done: the warp waited for its last S)
-    auto stage_q = [&](const Seg &s, const uint4 (&w)[kIt], Row &me) {
-      const int sub = lane / kL, ch = lane % kL;
-      uint32_t row[D / 4];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {  // 16 rows at a time
-        __syncwarp();
-#pragma unroll
-        for (int i = h * kIt / 2; i < (h + 1) * kIt / 2; ++i)
-          st_shared_v4(my_t + turn_at((i * kRows + sub) & 15, ch), w[i].x, w[i].y, w[i].z, w[i].w);
-        __syncwarp();
-        if (lane / 16 == h) {
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i)
-            ld_shared_v4(my_t + turn_at(lane & 15, i), row[4 * i], row[4 * i + 1], row[4 * i + 2], row[4 * i + 3]);
-        }
-      }
-      __syncwarp();
-      uint32_t most = 0u;  // of magnitudes the bits order as the values do, infinities and NaN above all
-#pragma unroll
-      for (int i = 0; i < D / 4; ++i) most = max_u16x2(most, row[i] & 0x7fff7fffu);
-      const float qm = __uint_as_float(max(most << 16, most & 0xffff0000u));
-      const float both = other(qm < INFINITY ? qm : INFINITY), qa = fmaxf(qm < INFINITY ? qm : INFINITY, both);
-      me.dead = !s.sane || me.depth < 0 || !(qa < INFINITY);
-      const int eq = clamp_exp(14 - ilog2(qa));
-      const float up = pow2i(eq);
-#pragma unroll
-      for (int i = 0; i < D / 4; ++i) row[i] = me.dead ? 0u : pack_half2(bf16_lo(row[i]) * up, bf16_hi(row[i]) * up);
-      me.c = pow2i(-eq) * (1.4426950408889634f * rsqrtf(float(D)));
-      if constexpr (D == 128) tmem_st32(tQ + lane_base + 32 * wg, row);
-      else tmem_st16(tQ + lane_base + 16 * wg, row);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.q_full);
-    };
-    Ring<2> sr;
     Ring<NK> vr;
-    uint32_t pv_phase = 0;  // of the tile before
     int g = 0, x = x0;
     bool first_seg = true;
     Seg s = {}, next = {};
     Row me = {}, next_row = {};
-    float m_used = -INFINITY, l = 0.f, down = 1.f;
+    float m_own = -INFINITY, l = 0.f;
+    int e_o = INT_MAX;  // O holds 2^(e_o - 24) V (unset: every V so far was 0); as of this thread's last tile
     // Rounds of: the next segment's queries, so that its products start while
     // the one's before are written; the output of the one before; its tiles.
     for (int round = 0;; ++round) {
       const bool more = x < x1;
-      uint4 w[kIt];
+      // the products that read the Q before are done once the last S is; the other
+      // warpgroup may have been the one to see it
+      if (round > 0 && !fail) fail = !ring_wait(&sm.s_full[(g - 1) & 1], ((g - 1) >> 1) & 1, abort_flag);
       if (more) {
+        // ---- Q: half a row, as fp16 times 2^eq of the row (its lines were asked
+        // into L2; a row per lane reads each of them eight times, from L1 but once)
         next = seg_at(p, x, x1);
         x += next.t1 - next.t0;
-        load_q(next, w, next_row);
+        const int64_t at = int64_t(next.b) * p.n + node;
+        const uint4 *src = reinterpret_cast<const uint4 *>(
+            p.q + (at * p.Hq + (next.pair - next.b * p.c.n_kv_heads) * p.G + head) * D + wg * (D / 2));
+        uint32_t row[D / 4];
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const uint4 w = exists ? src[i] : make_uint4(0u, 0u, 0u, 0u);
+          row[4 * i] = w.x, row[4 * i + 1] = w.y, row[4 * i + 2] = w.z, row[4 * i + 3] = w.w;
+        }
+        next_row.depth = exists ? p.depth[at] : -1;
+        uint32_t most = 0u;  // of magnitudes the bits order as the values do, infinities and NaN above all
+#pragma unroll
+        for (int i = 0; i < D / 4; ++i) most = max_u16x2(most, row[i] & 0x7fff7fffu);
+        most = max(most << 16, most & 0xffff0000u);
+        const float2 o = other(__uint_as_float(min(most, 0x7f800000u)), 0.f);
+        const float qa = fmaxf(__uint_as_float(min(most, 0x7f800000u)), o.x);
+        next_row.dead = !next.sane || next_row.depth < 0 || !(qa < INFINITY);
+        const int eq = clamp_exp(14 - ilog2(qa));
+        const float up = next_row.dead ? 0.f : pow2i(eq);
+#pragma unroll
+        for (int i = 0; i < D / 4; ++i) row[i] = next_row.dead ? 0u : pack_half2(bf16_lo(row[i]) * up, bf16_hi(row[i]) * up);
+        next_row.c = pow2i(-eq) * (1.4426950408889634f * rsqrtf(float(D)));
+        if constexpr (D == 128) tmem_st32(tQ + lane_base + 32 * wg, row);
+        else tmem_st16(tQ + lane_base + 16 * wg, row);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.q_full);
       }
       if (round > 0) {
-        l += other(l);
-        if (me.dead) m_used = -INFINITY, l = 0.f;
-      }
-      if (more) stage_q(next, w, next_row);
-      if (round > 0) {
-        if (!fail) fail = !ring_wait(&sm.pv_done, pv_phase, abort_flag);
-        pv_phase ^= 1u;
+        // ---- the output of the segment before
+        const int last = g - 1;
+        if (!fail) fail = !ring_wait(&sm.pv_done[last & 1], (last >> 1) & 1, abort_flag);
         tc_fence_after();
+        const float2 o = other(m_own, l);
+        const float m_used = me.dead ? -INFINITY : fmaxf(m_own, o.x);
+        // (a half that saw nothing has l = 0)
+        l = (l == 0.f ? 0.f : l * ex2(m_own - m_used)) + (o.y == 0.f ? 0.f : o.y * ex2(o.x - m_used));
+        if (me.dead) l = 0.f;
         fail = softmax_any(fail);  // (the barriers below want all their warps)
-        const int hk = s.pair - s.b * p.c.n_kv_heads;
+        const int h = (s.pair - s.b * p.c.n_kv_heads) * p.G + head;
+        // (e_o only falls)
+        const float2 o_e = other(e_o == INT_MAX ? 0.f : 1.f, float(e_o == INT_MAX ? kCodeBits : e_o));
+        if (o_e.x != 0.f) e_o = e_o == INT_MAX ? int(o_e.y) : min(e_o, int(o_e.y));
+        const float down = e_o == INT_MAX ? pow2i(-kCodeBits) : pow2i(-e_o);
         if (s.all) {
           // copies merge: the row's weight of each, then the sum through shared memory
           float m_all = m_used, l_all = l, scale;
@@ -876,14 +825,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
             l_all = 0.f;
 #pragma unroll
             for (int c = 0; c < REP; ++c) {
-              const float2 o = sm.ml[c * kLanes + r_blk];
-              l_all += o.x == -INFINITY && o.y == 0.f ? 0.f : o.y * ex2(o.x - m_all);
+              const float2 part = sm.ml[c * kLanes + r_blk];
+              l_all += part.x == -INFINITY && part.y == 0.f ? 0.f : part.y * ex2(part.x - m_all);
             }
             scale = m_used == -INFINITY && l == 0.f ? 0.f : (l_all != 0.f ? ex2(m_used - m_all) * kUnits * down / l_all : 0.f);
           } else {
             scale = l != 0.f ? kUnits * down / l : 0.f;
           }
-          const int h = hk * p.G + (r - node * p.G);
           uint16_t *dst = p.out + ((int64_t(s.b) * p.n + node) * p.Hq + h) * D + wg * (D / 2);
           // every copy finishes its part of the half row's channels, kC at a time,
           // with what the others send it
@@ -892,42 +840,37 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
           const uint32_t tO_half = tO + lane_base + wg * (D / 2);
 #pragma unroll 1
           for (int ch = 0; ch < kPart; ch += kC) {
-            float o[kC];
+            float sum[kC];
 #pragma unroll
+            for (int i = 0; i < kC; ++i) sum[i] = 0.f;
+#pragma unroll 1
             for (int k = 0; k < REP; ++k) {
               // send copy + k's channels of this round, take the own ones from copy - k
               uint32_t ov[kC];
-              const int to = (copy + k) % REP * kPart + ch;
+              const int to = ((copy + k) & (REP - 1)) * kPart + ch;
               if constexpr (kC == 16) tmem_ld16(tO_half + to, ov);
-                else tmem_ld8(tO_half + to, ov);
-                tmem_ld_wait();
+              else tmem_ld8(tO_half + to, ov);
+              tmem_ld_wait();
 #pragma unroll
               for (int i = 0; i < kC; ++i) ov[i] = scale != 0.f ? __float_as_uint(__uint_as_float(ov[i]) * scale) : 0u;
-              if (k == 0) {
+              if (REP > 1 && k > 0) {
 #pragma unroll
-                for (int i = 0; i < kC; ++i) o[i] = __uint_as_float(ov[i]);
-              } else {
-#pragma unroll
-                for (int i = 0; i < kC; i += 4)
-                  st_shared_v4(my_t + send_at(i / 4), ov[i], ov[i + 1], ov[i + 2], ov[i + 3]);
+                for (int i = 0; i < kC; i += 4) st_shared_v4(my_t + send_at(i / 4), ov[i], ov[i + 1], ov[i + 2], ov[i + 3]);
                 asm volatile("bar.sync %0, 128;" ::"r"(6 + wg) : "memory");
-                const int from = (copy + REP - k) % REP;
-                const uint32_t src = sT + (wg * 4 + (from * kLanes + r_blk) / 32) * Y::kT1;
+                const int from = (copy - k) & (REP - 1);
+                const uint32_t at = sT + (wg * 4 + (from * kLanes + r_blk) / 32) * Y::kT1;
 #pragma unroll
-                for (int i = 0; i < kC; i += 4) {
-                  uint32_t a0, a1, a2, a3;
-                  ld_shared_v4(src + send_at(i / 4), a0, a1, a2, a3);
-                  o[i] += __uint_as_float(a0), o[i + 1] += __uint_as_float(a1);
-                  o[i + 2] += __uint_as_float(a2), o[i + 3] += __uint_as_float(a3);
-                }
+                for (int i = 0; i < kC; i += 4) ld_shared_v4(at + send_at(i / 4), ov[i], ov[i + 1], ov[i + 2], ov[i + 3]);
                 asm volatile("bar.sync %0, 128;" ::"r"(6 + wg) : "memory");
               }
+#pragma unroll
+              for (int i = 0; i < kC; ++i) sum[i] += __uint_as_float(ov[i]);
             }
             if (exists && !fail) {
 #pragma unroll
               for (int i = 0; i < kC; i += 8)
-                st_global_v4(dst + copy * kPart + ch + i, pack_bf16x2(o[i], o[i + 1]), pack_bf16x2(o[i + 2], o[i + 3]),
-                             pack_bf16x2(o[i + 4], o[i + 5]), pack_bf16x2(o[i + 6], o[i + 7]));
+                st_global_v4(dst + copy * kPart + ch + i, pack_bf16x2(sum[i], sum[i + 1]), pack_bf16x2(sum[i + 2], sum[i + 3]),
+                             pack_bf16x2(sum[i + 4], sum[i + 5]), pack_bf16x2(sum[i + 6], sum[i + 7]));
             }
           }
           if (wg == 0 && copy == 0 && exists && p.lse && !fail)
@@ -936,157 +879,203 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
         } else if (!fail) {
           float *part = p.parts + (size_t(blockIdx.x) * 2 + (first_seg ? 0 : 1)) * part_floats<D>();
 #pragma unroll 1
-            for (int ch = wg * (D / 2); ch < (wg + 1) * (D / 2); ch += 32) {
-              uint32_t ov[32];
-              tmem_ld32(tO + lane_base + ch, ov);
-              tmem_ld_wait();
+          for (int ch = wg * (D / 2); ch < (wg + 1) * (D / 2); ch += 16) {
+            uint32_t ov[16];
+            tmem_ld16(tO + lane_base + ch, ov);
+            tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 32; i += 4)
-                *reinterpret_cast<float4 *>(part + ((ch + i) / 4 * BM + tl) * 4) =
-                    make_float4(__uint_as_float(ov[i]) * kUnits * down, __uint_as_float(ov[i + 1]) * kUnits * down,
-                                __uint_as_float(ov[i + 2]) * kUnits * down, __uint_as_float(ov[i + 3]) * kUnits * down);
-            }
+            for (int i = 0; i < 16; i += 4)
+              *reinterpret_cast<float4 *>(part + ((ch + i) / 4 * BM + tl) * 4) =
+                  make_float4(__uint_as_float(ov[i]) * kUnits * down, __uint_as_float(ov[i + 1]) * kUnits * down,
+                              __uint_as_float(ov[i + 2]) * kUnits * down, __uint_as_float(ov[i + 3]) * kUnits * down);
+          }
           if (wg == 0) *reinterpret_cast<float2 *>(part + BM * D + 2 * tl) = make_float2(m_used, l);
         }
         tc_fence_before();
+        // (no P of the next segment before all of this one's O has been read)
+        asm volatile("bar.sync 1, 256;" ::: "memory");
         first_seg = false;
       }
       if (!more || fail) break;
       s = next;
       me = next_row;
       const bool dead = me.dead;
-      // a node tile's mask words of this thread's columns
       const uint32_t *mask_row = p.mask + (int64_t(s.b) * p.n + node) * words;
-      uint32_t mk[2] = {0u, 0u};
-      auto load_mask = [&](int t_n) {
-        const int w_ = 2 * t_n + col0 / 32;
-        mk[0] = col0 < kNodes && w_ < words ? mask_row[w_] : 0u;
-        if constexpr (kCols == 64) mk[1] = col0 < kNodes && w_ + 1 < words ? mask_row[w_ + 1] : 0u;
-      };
-      load_mask(max(0, s.t0 - pl.ts - pl.tr));
       // ring entries below `low` are outside the row's window
       // (a dead row takes what comes and is put to 0 at the end)
       const int low = dead ? 0 : int(min((long long)INT_MAX, max(0ll, (long long)me.depth + s.nv - p.window + 1)));
-      m_used = -INFINITY, l = 0.f;
-      // a tile of cached keys or (kN) of nodes
+      m_own = -INFINITY, l = 0.f, e_o = INT_MAX;
       const int first_t = min(live_tile(pl, s, s.t0), s.t1 - 1);
-      auto tile = [&](auto kind, int t) {
+      // a tile of cached keys or (kN) of nodes
+      auto tile = [&](auto kind, int t, bool last) {
         constexpr bool kN = decltype(kind)::value;
-        const int u = sr.i;
-        // what V's warps say of the tile (K's were done before S)
+        constexpr int kC = kCols < 64 ? kCols : 64;  // columns at a time
+        const int u = g & 1;
+        // what V's warps say of a node tile (K's were done before S)
         if (kN && !fail) fail = !ring_wait(&sm.op_full[1][vr.i], vr.phase, abort_flag);
         tc_fence_after();
-        const uint32_t tS = tmem + u * BN + lane_base + col0;
-        uint32_t v[kCols];
-        if constexpr (kCols == 16) {
-          tmem_ld16(tS, v);
-        } else {
+        const uint32_t tS = tmem + u * BN + lane_base;
+        uint32_t v[kC];
+        // scores of columns col .. col + kC, -inf where the row does not see
+        auto load = [&](int col) {
 #pragma unroll
-          for (int i = 0; i < kCols; i += 32) tmem_ld32(tS + i, v + i);
-        }
-        tmem_ld_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.s_empty[u]);
-        if constexpr (!kN) {
-          // columns [lo, hi) are seen
-          const bool ring = t >= pl.ts;
-          const int first = (ring ? t - pl.ts : t) * BN + col0;
-          const int hi = (ring ? s.nv : s.sl) - first;
-          const int lo = ring ? max(low, first) - first : 0;
-          if (__any_sync(0xffffffffu, lo > 0 || hi < kCols)) {
+          for (int i = 0; i < kC; i += 32) tmem_ld32(tS + col + i, v + i);
+          tmem_ld_wait();
+          if constexpr (!kN) {
+            const bool ring = t >= pl.ts;
+            const int first = (ring ? t - pl.ts : t) * BN + col;
+            const int hi = (ring ? s.nv : s.sl) - first;
+            const int lo = ring ? max(low, first) - first : 0;
+            if (__any_sync(0xffffffffu, lo > 0 || hi < kC)) {
 #pragma unroll
-            for (int i = 0; i < kCols; ++i) v[i] = i >= lo && i < hi ? v[i] : 0xff800000u;
-          }
-        } else {
-          // (columns from 64 on are not of this tile: their words are 0)
-          const uint2 alive = sm.live[0][g % kInfo];
+              for (int i = 0; i < kC; ++i) v[i] = i >= lo && i < hi ? v[i] : 0xff800000u;
+            }
+          } else {
+            // (64 columns: those behind them are not of this tile)
 #pragma unroll
-          for (int i = 0; i < kCols; i += 32) {
-            const int wd = (col0 / 32 + i / 32) & 1, sh = col0 & 31;
-            const uint32_t bad = (sm.bad[0][g % kInfo][wd] | sm.bad[1][g % kInfo][wd]) >> sh;
-            const uint32_t see = dead ? 0u : (mk[i / 32] & (wd ? alive.y : alive.x)) >> sh;
+            for (int i = 0; i < kC; i += 32) {
+              const int wd = (t - pl.ts - pl.tr) * 2 + (col + i) / 32, at = (col + i) & (kNodes - 1);
+              uint32_t see = 0u, bad = 0u;
+              if (!dead && col < kNodes && wd < words) {
+                auto word = [&](const uint16_t *h) { return uint32_t(h[at / 16]) | uint32_t(h[at / 16 + 1]) << 16; };
+                see = mask_row[wd] & word(sm.live[g % kInfo]);
+                bad = word(sm.bad[0][g % kInfo]) | word(sm.bad[1][g % kInfo]);
+              }
 #pragma unroll
-            for (int e = 0; e < 32 && i + e < kCols; ++e) {
-              const float sc = __uint_as_float(v[i + e]) * sm.kf[g % kKf][(col0 & (kNodes - 1)) + i + e];
-              v[i + e] = see >> e & 1u ? (bad >> e & 1u ? 0x7fffffffu : __float_as_uint(sc)) : 0xff800000u;
+              for (int e = 0; e < 32; ++e) {
+                const float sc = __uint_as_float(v[i + e]) * sm.kf[g % kKf][at + e];
+                v[i + e] = see >> e & 1u ? (bad >> e & 1u ? 0x7fffffffu : __float_as_uint(sc)) : 0xff800000u;
+              }
             }
           }
-          load_mask(t - pl.ts - pl.tr + 1);
+        };
+        // a score's factor, by 32 keys (nodes: all the same, and with 2^-e in the
+        // scores); never 0, which would make NaN of a masked column's -inf: |S| <
+        // 2^37, so at 2^-126 and below a score is 2^-89 at most and its weight 1 to
+        // every bit
+        auto factor = [&](int col) {
+          return kN ? fmaxf(me.c, 1.1754943508222875e-38f)
+                    : fmaxf(me.c * pow2i(-sm.e[0][g % kInfo][col / 32]) * kUnits, 1.1754943508222875e-38f);
+        };
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int col = col0; col < col0 + kCols; col += kC) {
+          load(col);
+#pragma unroll
+          for (int h = 0; h < kC; h += 32) {
+            float mxp[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              mxp[i] = max3(__uint_as_float(v[h + i]), __uint_as_float(v[h + 4 + i]), __uint_as_float(v[h + 8 + i]));
+#pragma unroll
+            for (int j = 12; j < 28; j += 8)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) mxp[i] = max3(mxp[i], __uint_as_float(v[h + j + i]), __uint_as_float(v[h + j + 4 + i]));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mxp[i] = fmaxf(mxp[i], __uint_as_float(v[h + 28 + i]));
+            mx = fmaxf(mx, factor(col + h) * max3(mxp[0], mxp[1], fmaxf(mxp[2], mxp[3])));
+          }
         }
-        // never 0, which would make NaN of a masked column's -inf: |S| < 2^37, so at
-        // 2^-126 and below a score is 2^-89 at most and its weight 1 to every bit
-        const float ct = fmaxf(me.c * sm.down_k[g % kInfo] * kUnits, 1.1754943508222875e-38f);
-        float mxp[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) mxp[i] = __uint_as_float(v[i]);
-#pragma unroll
-        for (int j = 8; j + 16 <= kCols; j += 16)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) mxp[i] = max3(mxp[i], __uint_as_float(v[j + i]), __uint_as_float(v[j + 8 + i]));
-#pragma unroll
-        for (int i = 0; i < 8; ++i) mxp[i] = fmaxf(mxp[i], __uint_as_float(v[kCols - 8 + i]));
-        const float mine = max3(max3(mxp[0], mxp[1], mxp[2]), max3(mxp[3], mxp[4], mxp[5]), fmaxf(mxp[6], mxp[7]));
-        const float mx = ct * fmaxf(mine, other(mine));
-        const bool need = mx > m_used + kLazyLog2;  // the first tile with a key included
-        float alpha = 1.f;
-        if (need) {
-          alpha = ex2(m_used - mx);  // 0 at the first
-          l *= alpha;
+        float m_used = -INFINITY, alpha = 1.f;
+        if (t != first_t) {
+          asm volatile("bar.sync %0, 64;" ::"r"(8 + 4 * wg + quad) : "memory");
+          m_used = sm.m[u ^ 1][tl];
+        }
+        if (mx > m_used + kLazyLog2) {  // the first tile with a key included
+          alpha = ex2(m_used - mx);     // 0 at the first
           m_used = mx;
         }
-        // nodes' weights carry V's exponent
-        const float shift = kPBias - (m_used == -INFINITY ? 0.f : m_used) + (kN ? sm.info[g % kInfo].z : 0.f);
-        const uint64_t c2 = pack_f32x2(ct, ct), nmc2 = pack_f32x2(shift, shift);
-        float rsp[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < kCols; i += 2) {
-          float a, b;
-          fma_f32x2(a, b, __uint_as_float(v[i]), __uint_as_float(v[i + 1]), c2, nmc2);
-          a = ex2(a);
-          b = ex2(b);
-          add_f32x2(rsp[(i >> 1) & 1 ? 2 : 0], rsp[(i >> 1) & 1 ? 3 : 1], a, b);
-          v[i / 2] = kN ? pack_bf16x2(a, b) : pack_half2(a, b);
+        if (!last) {
+          sm.m[u][tl] = m_used;
+          asm volatile("bar.arrive %0, 64;" ::"r"(8 + 4 * (wg ^ 1) + quad) : "memory");
         }
-        const float sum = (rsp[0] + rsp[1]) + (rsp[2] + rsp[3]);
-        if (!kN && !fail) fail = !ring_wait(&sm.op_full[1][vr.i], vr.phase, abort_flag);
-        const float4 info = sm.info[g % kInfo];
-        down = info.y;
-        alpha *= info.x;  // what V's new exponent asks of O
-        l += kN ? sum * info.y * kUnits : sum;
+        if (m_own != m_used) {
+          l *= ex2(m_own - m_used);  // (0 * 0 at the first)
+          m_own = m_used;
+        }
+        // the power of two that O holds V in: it falls where a tile's values are
+        // larger than those before, and with it O.  (V's warps know tiles in order,
+        // so the tile before, the other warpgroup's, is known too.)
+        if (!fail) fail = !ring_wait(&sm.v_known[g & 3], (g >> 2) & 1, abort_flag);
+        auto e_of = [&](int tile) {
+          const int4 e = *reinterpret_cast<const int4 *>(sm.e[1][tile % kInfo]);
+          return min(min(e.x, e.y), min(e.z, e.w));
+        };
         if (t != first_t) {
-          // P and O once the PV before has landed
-          if (!fail) fail = !ring_wait(&sm.pv_done, pv_phase, abort_flag);
-          pv_phase ^= 1u;
+          if (!kN || t == pl.ts + pl.tr) e_o = min(e_o, e_of(g - 1));
+          else if (e_o == INT_MAX) e_o = kCodeBits;  // (nodes alone so far)
+        }
+        const int e_now = kN ? (e_o == INT_MAX ? kCodeBits : e_o) : min(e_o, e_of(g));
+        if (e_now < e_o && e_o != INT_MAX) alpha *= pow2i(max(e_now - e_o, -126));
+        e_o = e_now;
+        const float base_shift = kPBias - (m_used == -INFINITY ? 0.f : m_used);
+        // P and O may change once the PV before has landed (P over S: only O)
+        auto pv_before = [&]() {
+          if (!fail) fail = !ring_wait(&sm.pv_done[u ^ 1], ((g - 1) >> 1) & 1, abort_flag);
           tc_fence_after();
-          if (__any_sync(0xffffffffu, alpha != 1.f)) {
+        };
 #pragma unroll 1
-            for (int ch = wg * (D / 2); ch < (wg + 1) * (D / 2); ch += 16) {
-              uint32_t ov[16];
-              tmem_ld16(tO + lane_base + ch, ov);
-              tmem_ld_wait();
+        for (int col = col0; col < col0 + kCols; col += kC) {
+          if (REP == 1) load(col);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
-              tmem_st16(tO + lane_base + ch, ov);
+          for (int h = 0; h < kC; h += 32) {
+            // weights carry what V's operand lacks of O's scale: never more than 1
+            // for codes, and where that is below 2^-60, V does not matter
+            const int up = kN ? e_now - kCodeBits : max(e_now - sm.e[1][g % kInfo][(col + h) / 32], -60);
+            const float ct = factor(col + h), shift = base_shift + float(up);
+            const uint64_t c2 = pack_f32x2(ct, ct), nmc2 = pack_f32x2(shift, shift);
+            float rsp[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = h; i < h + 32; i += 2) {
+              float a, b;
+              fma_f32x2(a, b, __uint_as_float(v[i]), __uint_as_float(v[i + 1]), c2, nmc2);
+              a = ex2(a);
+              b = ex2(b);
+              add_f32x2(rsp[(i >> 1) & 1 ? 2 : 0], rsp[(i >> 1) & 1 ? 3 : 1], a, b);
+              v[i / 2] = kN ? pack_bf16x2(a, b) : pack_half2(a, b);
             }
+            const float sum = (rsp[0] + rsp[1]) + (rsp[2] + rsp[3]);
+            l += kN ? sum * pow2i(-e_now) * kUnits : sum * pow2i(-up);
+          }
+          if constexpr (REP == 1) {
+            tmem_st32(tS + col / 2, v);
+          } else {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.s_empty[u]);
+            if (t != first_t) pv_before();
+            if constexpr (kC == 64) tmem_st32(tP + lane_base + col / 2, v);
+            else tmem_st16(tP + lane_base + col / 2, v);
           }
         }
-        if constexpr (kCols == 64) tmem_st32(tP + lane_base + col0 / 2, v);
-        else if constexpr (kCols == 32) tmem_st16(tP + lane_base + col0 / 2, v);
-        else tmem_st8(tP + lane_base + col0 / 2, v);
+        if (t != first_t && __any_sync(0xffffffffu, alpha != 1.f)) {
+          if (REP == 1) pv_before();
+#pragma unroll 1
+          for (int ch = 0; ch < D; ch += 16) {
+            uint32_t ov[16];
+            tmem_ld16(tO + lane_base + ch, ov);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+            tmem_st16(tO + lane_base + ch, ov);
+          }
+        }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.p_full);
-        ++g, sr.next(), vr.next();
+        if (lane == 0) mbar_arrive(&sm.p_full[u]);
       };
       // (which tiles, the warps know by themselves: after a wait that gave up they
       // still meet at the same barriers)
 #pragma unroll 1
-      for (int t = first_t; t < s.t1; t = live_tile(pl, s, t + 1)) {
-        if (!fail) fail = !ring_wait(&sm.s_full[sr.i], sr.phase, abort_flag);
-        if (t < pl.ts + pl.tr) tile(std::false_type{}, t);
-        else tile(std::true_type{}, t);
+      for (int t = first_t; t < s.t1; ++g, vr.next()) {
+        const int t_next = live_tile(pl, s, t + 1);
+        if ((g & 1) == wg) {
+          if (!fail) fail = !ring_wait(&sm.s_full[g & 1], (g >> 1) & 1, abort_flag);
+          if (t < pl.ts + pl.tr) tile(std::false_type{}, t, t_next >= s.t1);
+          else tile(std::true_type{}, t, t_next >= s.t1);
+        }
+        t = t_next;
       }
     }
   }
