@@ -73,7 +73,7 @@ constexpr int kWarpTurn = 8, kWarpFeedK = 16, kWarpFeedV = 17, kWarpS = 18;
 // softmax thread holds up to 64 scores.
 constexpr int kRegsLaunch = 96, kRegsSoftmax = 144, kRegsOther = 64;
 static_assert(2 * 128 * kRegsSoftmax + 3 * 128 * kRegsOther <= kThreads * kRegsLaunch, "register split");
-constexpr int kBatch = 8;         // tiles that are noted, and asked into L2, at once
+constexpr int kBatch = 4;         // tiles that are noted, and asked into L2, at once
 constexpr int kKf = 8;            // node tiles' key factors in flight: more than the tiles between operand and softmax
 constexpr float kLazyLog2 = 8.f;  // the maximum used may lag the true one by 2^8
 constexpr float kPBias = 7.f;     // P is scaled by 2^7
@@ -580,14 +580,25 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
       if (!(flags & kKindNodes)) {
         const uint32_t raw_at = stage + codes_off, sc_at = stage + scale_off;
         const uint32_t dst = row_off + op.i * Y::kKV;
+        uint32_t ahead[kU][4], ahead_s[kU];  // the next group's loads run ahead of this one's stores
+        auto load = [&](int i0) {
+#pragma unroll
+          for (int i = 0; i < kU; ++i) {
+            ld_shared_v4(raw_at + (i0 + i) * kRowsIt * D, ahead[i][0], ahead[i][1], ahead[i][2], ahead[i][3]);
+            ahead_s[i] = lds32(sc_at + (i0 + i) * kRowsIt * NG * 4);
+          }
+        };
+        load(0);
 #pragma unroll 1
         for (int i0 = 0; i0 < kIts; i0 += kU) {
           uint32_t x[kU][4], s2[kU];
 #pragma unroll
           for (int i = 0; i < kU; ++i) {
-            ld_shared_v4(raw_at + (i0 + i) * kRowsIt * D, x[i][0], x[i][1], x[i][2], x[i][3]);
-            s2[i] = lds32(sc_at + (i0 + i) * kRowsIt * NG * 4);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[i][j] = ahead[i][j] ^ 0x80808080u;
+            s2[i] = ahead_s[i];
           }
+          if (i0 + kU < kIts) load(i0 + kU);
 #pragma unroll
           for (int i = 0; i < kU; ++i) {
             // a lane's rows are kRowsIt (4 or 8) apart: their swizzles differ in
@@ -596,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
             const uint32_t off = hmul2(s2[i], kMinus128);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-              const uint32_t wa = x[i][2 * q] ^ 0x80808080u, wb = x[i][2 * q + 1] ^ 0x80808080u;
+              const uint32_t wa = x[i][2 * q], wb = x[i][2 * q + 1];
               st_shared_v4(q ? at ^ 16u : at, scaled_codes(wa, kBytes01, s2[i], off), scaled_codes(wa, kBytes23, s2[i], off),
                            scaled_codes(wb, kBytes01, s2[i], off), scaled_codes(wb, kBytes23, s2[i], off));
             }
@@ -656,8 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
     const uint32_t leader = elect_one();
     constexpr uint32_t kId = idesc_f16(BM, BN, 0), kIdNodes = idesc_f16(BM, kNodes, 0);
     Ring<NK> kr;
-    // a buffer is free once the softmax has read it, or with P over it PV
-    Ring<2> sr;
+    Ring<2> sr;  // a buffer is free once the softmax has read it
     sr.phase = 1;
     uint32_t q_phase = 0;
     const uint64_t dk = sdesc_sw128(sK, 16, 1024);
@@ -665,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
 #pragma unroll 1
     for (int g = 0; !(flags & kLast); ++g, kr.next(), sr.next()) {
       bool ok = ring_wait(&sm.op_full[0][kr.i], kr.phase, abort_flag) &&
-                ring_wait(REP == 1 ? &sm.pv_done[sr.i] : &sm.s_empty[sr.i], sr.phase, abort_flag);
+                ring_wait(&sm.s_empty[sr.i], sr.phase, abort_flag);
       flags = sm.rec[0][g % kRec].x;
       if (ok && (flags & kFresh)) {
         ok = ring_wait(&sm.q_full, q_phase, abort_flag);
@@ -706,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
       const uint32_t id = flags & kKindNodes ? kIdNodes : kId, more = flags & kFresh ? 0u : 1u;
 #pragma unroll
       for (int kk = 0; kk < BN / 16; ++kk)  // (nodes: half as many keys)
-        mma_ts(tO, (REP == 1 ? tmem + pr.i * BN : tP) + kk * 8, vd + kk * (16 * 128 >> 4), id, kk > 0 ? 1u : more,
+        mma_ts(tO, tP + kk * 8, vd + kk * (16 * 128 >> 4), id, kk > 0 ? 1u : more,
                kk >= kNodes / 16 && (flags & kKindNodes) ? 0u : leader);
       mma_commit(&sm.pv_done[pr.i], leader);
       mma_commit(&sm.op_empty[1][vr.i], leader);
@@ -1009,7 +1019,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
         if (e_now < e_o && e_o != INT_MAX) alpha *= pow2i(max(e_now - e_o, -126));
         e_o = e_now;
         const float base_shift = kPBias - (m_used == -INFINITY ? 0.f : m_used);
-        // P and O may change once the PV before has landed (P over S: only O)
+        // P and O may change once the PV before has landed
         auto pv_before = [&]() {
           if (!fail) fail = !ring_wait(&sm.pv_done[u ^ 1], ((g - 1) >> 1) & 1, abort_flag);
           tc_fence_after();
@@ -1037,19 +1047,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
             const float sum = (rsp[0] + rsp[1]) + (rsp[2] + rsp[3]);
             l += kN ? sum * pow2i(-e_now) * kUnits : sum * pow2i(-up);
           }
-          if constexpr (REP == 1) {
-            tmem_st32(tS + col / 2, v);
-          } else {
+          if (col + kC == col0 + kCols) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.s_empty[u]);
-            if (t != first_t) pv_before();
-            if constexpr (kC == 64) tmem_st32(tP + lane_base + col / 2, v);
-            else tmem_st16(tP + lane_base + col / 2, v);
           }
+          if (col == col0 && t != first_t) pv_before();
+          if constexpr (kC == 64) tmem_st32(tP + lane_base + col / 2, v);
+          else tmem_st16(tP + lane_base + col / 2, v);
         }
         if (t != first_t && __any_sync(0xffffffffu, alpha != 1.f)) {
-          if (REP == 1) pv_before();
 #pragma unroll 1
           for (int ch = 0; ch < D; ch += 16) {
             uint32_t ov[16];
