@@ -443,7 +443,17 @@ ND_API int nd_tree_layout(const int32_t *parents, const int32_t *n_nodes, const 
  *   window >= 1; n_q_heads / n_kv_heads 1..8; head_dim 64 or 128; n 1..256;
  *   batch * n_kv_heads at most 2^20; 1 <= sink_cap + ring_cap <= 2^31 - 4097
  * A row that sees no key, and padding, get out = 0, lse = -inf, and so does a
- * query head with a NaN or an infinity, as in nd_swa_sink_decode.
+ * query head with a NaN or an infinity, as in nd_swa_sink_decode.  A row that
+ * sees a node whose key or value (of its KV head) holds one is NaN in all
+ * channels and lse; rows that do not see it are not touched by it.
+ * Precision: cached keys and values become fp16 after a power-of-two scaling per
+ * 32 slots (and for values one that follows the largest so far): a key is within
+ * 2^-10 of code * scale or 2^-21 of the largest among its 32, whichever is more,
+ * a value within 2^-10 of itself or 2^-21 of the largest among its 32; scales
+ * below 2^-74 count as less.  Nodes' keys are exact down to 2^-28 of the largest
+ * of their row, their values exact and their weights within 2^-9 of themselves;
+ * a cached slot's weight is within 2^-11 of itself or 2^-32 of the largest.
+ * Products and sums are fp32.
  * Partial results go to the workspace (device, 16-byte aligned) of
  * nd_tree_decode_workspace_size(batch, n, n_q_heads, n_kv_heads, head_dim,
  * sink_cap + ring_cap) bytes (0: none is needed, NULL allowed).

@@ -110,48 +110,131 @@ struct CommitParams {
   int n, max_path;
   const int32_t *path, *path_len;
   int *err;
+  int parts;  // CTAs of a sequence
 };
 
-// One warp to a (token, head, K or V) row; lane l holds channels l * CPL ...
+// The path's rows (token, head, K or V), D / 8 lanes to a row, kU rows of a lane's
+// loads in flight: a chain of three latencies (metadata and path, rows, stores)
+// with as many bytes behind each as there are.  A sequence with many rows and
+// few neighbours is a cluster of CTAs; its metadata advance once all of them have
+// read them.
+// 512 sequences of up to 16 tokens of 8 heads of 128 (26 MB on average): 21 us,
+// 64 of up to 6 of 2 heads of 64: 3.6.  The codec costs more instructions than the
+// rows' latency hides: with its exact division tried per value instead of once
+// for a lane's eight, 26 and 5.5 us; a row to a warp, 55 and 4.2.
 template <int D>
 __global__ void __launch_bounds__(256) tree_commit_kernel(const __grid_constant__ CommitParams p) {
-  constexpr int CPL = D / 32;
+  constexpr int kL = D / 8, kU = 4;
   const nd_kv_cache &c = p.c;
-  const int b = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cap = c.ring_cap;
+  const int parts = p.parts, b = blockIdx.x / parts, part = blockIdx.x % parts, cap = c.ring_cap;
+  const int sub = threadIdx.x / kL, ch = threadIdx.x % kL, per = blockDim.x / kL;
   pdl_wait();
-  const int rs = c.ring_start[b], rl = c.ring_len[b], sl = c.sink_len[b], len = p.path_len[b];
-  const int32_t *path = p.path + size_t(b) * p.max_path;
+  const int rs = c.ring_start[b], rl = c.ring_len[b], sl = c.sink_len[b], sq = c.seq_len[b], len = p.path_len[b];
+  const int32_t *path = p.path + int64_t(b) * p.max_path;
   bool ok = sl >= 0 && sl <= c.sink_cap && rl >= 0 && rl <= cap && rs >= 0 && rs < cap && len >= 0 && len <= p.max_path;
   if (ok)
     for (int t = threadIdx.x; t < len; t += blockDim.x) ok = ok && path[t] >= 0 && path[t] < p.n;
-  if (!__syncthreads_and(ok)) {  // (every thread has read the metadata)
-    if (threadIdx.x == 0) raise_device_error(p.err, ND_DEVERR_METADATA);
+  ok = __syncthreads_and(ok);  // the same in all CTAs of the sequence
+  if (parts > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  if (ok) {
+    const int first = max(0, len - cap);  // tokens before it are overwritten within the path
+    const int Hkv = c.n_kv_heads, per_token = 2 * Hkv, rows = (len - first) * per_token, step = per * parts;
+    const unsigned slot0 = unsigned((int64_t(rs) + rl + first) % cap);
+#pragma unroll 1
+    for (int r0 = part * per; r0 < rows; r0 += kU * step) {
+      uint4 w[kU];
+      size_t at[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        // (K's rows of a token, then V's; past the end: the last row, not stored)
+        const int r = min(r0 + u * step + sub, rows - 1), t = r / per_token, k = r - t * per_token, is_v = k >= Hkv, h = is_v ? k - Hkv : k;
+        const int64_t node = int64_t(b) * p.n + path[first + t];
+        const uint16_t *src = (is_v ? p.v + node * p.v_stride : p.k + node * p.k_stride) + h * D + ch * 8;
+        w[u] = *reinterpret_cast<const uint4 *>(src);
+        const unsigned ring = slot0 + t;  // t < cap
+        const int slot = c.sink_cap + int(ring >= unsigned(cap) ? ring - cap : ring);
+        at[u] = ((size_t(b) * Hkv + h) * (size_t(c.sink_cap) + cap) + slot) * 2 + is_v;
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        if (r0 + u * step >= rows) break;  // (the same for the CTA)
+        const uint32_t x[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+        float y[8], amax = 0.f;
+        bool finite = true;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          finite = finite && (x[i] & 0x7f80u) != 0x7f80u && (x[i] & 0x7f800000u) != 0x7f800000u;
+          y[2 * i] = bf16_lo(x[i]), y[2 * i + 1] = bf16_hi(x[i]);
+          amax = fmaxf(amax, fmaxf(fabsf(y[2 * i]), fabsf(y[2 * i + 1])));
+        }
+        // a group of 32 channels is four neighbouring lanes'
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        const float scale = __fdiv_rn(amax, 127.0f), inv = __frcp_rn(scale);
+        // the codec (nd_common.cuh): the nearest integer to x * inv is the code
+        // unless one of the lane's eight lies near a half, the scale is tiny or a value
+        // not finite.  1.5 * 2^23 added leaves the integer in the low bits.
+        uint32_t m[8];
+        float near = 1.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float q = y[i] * inv, big = q + 12582912.f;
+          near = fminf(near, fabsf(fabsf(q - (big - 12582912.f)) - 0.5f));
+          m[i] = __float_as_uint(big);
+        }
+        if (!(near > 1e-4f && scale >= 1e-30f && scale < INFINITY && finite)) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float q = 0.f;
+            if (amax != 0.f) q = fminf(fmaxf(codec_rint(y[i], scale, inv), -127.f), 127.f);
+            m[i] = uint32_t(int(q));
+          }
+        }
+        uint32_t o[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          o[i] = prmt(prmt(m[4 * i], m[4 * i + 1], 0x0040u), prmt(m[4 * i + 2], m[4 * i + 3], 0x0040u), 0x5410u);
+        if (r0 + u * step + sub < rows) {
+          const size_t row = at[u] >> 1;
+          const bool is_v = at[u] & 1;
+          *reinterpret_cast<uint2 *>((is_v ? c.v_codes : c.k_codes) + row * D + ch * 8) = make_uint2(o[0], o[1]);
+          if (ch % 4 == 0) ((is_v ? c.v_scale : c.k_scale) + row * (D / 32))[ch / 4] = scale;
+        }
+      }
+    }
+  }
+  if (parts > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+  if (part != 0 || threadIdx.x != 0) return;
+  if (!ok) {
+    raise_device_error(p.err, ND_DEVERR_METADATA);
     return;
   }
-  const int first = max(0, len - cap);  // tokens before it are overwritten within the path
-  const int rows = (len - first) * c.n_kv_heads * 2;
-  for (int r = warp; r < rows; r += blockDim.x >> 5) {
-    const int t = first + r / (2 * c.n_kv_heads), h = (r >> 1) % c.n_kv_heads, is_v = r & 1;
-    const int slot = c.sink_cap + int((int64_t(rs) + rl + t) % cap);
-    const int64_t node = int64_t(b) * p.n + path[t];
-    const uint16_t *src = (is_v ? p.v + node * p.v_stride : p.k + node * p.k_stride) + h * D + lane * CPL;
-    float x[CPL];
-    int code[CPL];
-#pragma unroll
-    for (int i = 0; i < CPL; ++i) x[i] = __uint_as_float(uint32_t(src[i]) << 16);
-    const float scale = quant_lanes<CPL>(x, code);
-    const size_t at = (size_t(b) * c.n_kv_heads + h) * (c.sink_cap + cap) + slot;
-    int8_t *dst = (is_v ? c.v_codes : c.k_codes) + at * D + lane * CPL;
-#pragma unroll
-    for (int i = 0; i < CPL; ++i) dst[i] = int8_t(code[i]);
-    if (lane % (32 / CPL) == 0) ((is_v ? c.v_scale : c.k_scale) + at * (D / 32))[lane / (32 / CPL)] = scale;
-  }
-  if (threadIdx.x == 0) {
-    const int64_t over = int64_t(rl) + len - cap;
-    c.ring_len[b] = over > 0 ? cap : rl + len;
-    if (over > 0) c.ring_start[b] = int((rs + over) % cap);
-    c.seq_len[b] += len;
-  }
+  const int64_t over = int64_t(rl) + len - cap;
+  c.ring_len[b] = over > 0 ? cap : rl + len;
+  if (over > 0) c.ring_start[b] = int((rs + over) % cap);
+  c.seq_len[b] = sq + len;
+}
+
+template <int D>
+cudaError_t launch_commit(CommitParams p, cudaStream_t stream) {
+  // 16 rows (D = 128) to a CTA and pass, four passes in flight: more CTAs where a
+  // path has more rows than that and the sequences leave room
+  const int64_t rows = int64_t(p.max_path) * p.c.n_kv_heads * 2, at_once = 4 * (256 / (D / 8));
+  p.parts = 1;
+  while (p.parts < 8 && rows > at_once * p.parts && int64_t(p.c.batch) * p.parts < 304) p.parts *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.c.batch * p.parts);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.parts;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.parts > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, tree_commit_kernel<D>, p);
 }
 
 int threads_for(int n) { return n > 0 ? (n + 31) / 32 * 32 : 32; }
@@ -176,13 +259,12 @@ cudaError_t launch_tree_commit(const nd_kv_cache &c, const void *k, const void *
                                int n, const int32_t *path, const int32_t *path_len, int max_path, int *err,
                                cudaStream_t stream) {
   const CommitParams p = {c, static_cast<const uint16_t *>(k), static_cast<const uint16_t *>(v), k_stride, v_stride, n,
-                          max_path, path, path_len, err};
-  const dim3 grid(c.batch), block(256);
+                          max_path, path, path_len, err, 1};
   switch (c.head_dim) {
-    case 32: return launch_pdl(tree_commit_kernel<32>, grid, block, 0, stream, p);
-    case 64: return launch_pdl(tree_commit_kernel<64>, grid, block, 0, stream, p);
-    case 128: return launch_pdl(tree_commit_kernel<128>, grid, block, 0, stream, p);
-    case 256: return launch_pdl(tree_commit_kernel<256>, grid, block, 0, stream, p);
+    case 32: return launch_commit<32>(p, stream);
+    case 64: return launch_commit<64>(p, stream);
+    case 128: return launch_commit<128>(p, stream);
+    case 256: return launch_commit<256>(p, stream);
   }
   return cudaErrorInvalidValue;
 }

@@ -166,6 +166,30 @@ def test_commit_refuses_bad_paths_and_leaves_the_sequence():
         np.testing.assert_array_equal(host(getattr(cache, f)), getattr(ref, f), err_msg=f)
 
 
+def test_commit_equals_appends_for_any_value():
+    """Values beside half-integers, subnormal scales, zeros, infinities and NaN: the codes of nd_kv_append_quant, bit for bit."""
+    rng = philox(20450)
+    B, n, Hkv, d, W = 2, 12, 3, 128, 16
+    bits = rng.integers(0, 1 << 16, (B, n, 2 * Hkv, d)).astype(np.uint16)      # any bf16 at all, one in 256 not finite
+    bits[0, 0] = 0
+    bits[0, 1] &= 0x803F                                                       # subnormal
+    whole = (rng.integers(-127, 128, (n, 2 * Hkv, d)) + 0.5).astype(np.float32)  # quotients on the halves of a scale of 1
+    whole[..., ::32] = 127.0
+    bits[1] = (whole.view(np.uint32) >> 16).astype(np.uint16)
+    x = dev_bf16(bits)
+    k, v = x[:, :, :Hkv], x[:, :, Hkv:]
+    a, b = (nd().KVCache.empty(B, Hkv, d, 0, W) for _ in range(2))
+    path = np.tile(np.arange(n, dtype=np.int32), (B, 1))
+    nd().nd_tree_commit(a, k, v, i32(path), i32(np.full(B, n, np.int32)))
+    for t in range(n):
+        nd().nd_kv_append_quant(b, k[:, t].contiguous(), v[:, t].contiguous())
+    for f in CODES:
+        x, y = getattr(a, f), getattr(b, f)
+        if x.dtype == torch.float32:
+            x, y = x.view(torch.int32), y.view(torch.int32)
+        assert torch.equal(x, y), f
+
+
 def test_calls_in_a_graph_and_on_another_stream():
     rng = philox(20600)
     B, n, m, Hkv, d, S, W = 3, 20, 6, 2, 64, 2, 9

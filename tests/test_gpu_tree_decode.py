@@ -171,6 +171,48 @@ def test_a_row_with_a_nan_or_an_infinity_leaves_the_others():
     assert torch.equal(got[0][same], want[0][same])
 
 
+def test_a_node_that_is_not_finite_reaches_the_rows_that_see_it_alone():
+    """Rows that see such a node are NaN (all channels, and lse); the others' outputs are those without it."""
+    rng = philox(22470)
+    B, n, Hq, Hkv, d, S, W = 2, 70, 8, 2, 64, 40, 50
+    ref = tu.random_cache(rng, B, Hkv, d, S, W)
+    depth, _, mask, see = tu.layout(tu.random_parents(rng, B, n, reach=3), None, ref.seq_len, 0, 9)
+    (q, k, v), x = nodes(rng, B, n, Hq, Hkv, d)
+    k2, v2 = k.clone(), v.clone()
+    k2[0, 5, 0, 7], k2[0, 66, 1, 0], v2[1, 9, 1, 63], v2[1, 65, 0, 1] = float("nan"), float("inf"), float("-inf"), float("nan")
+    lse = torch.empty((B, Hq, n), dtype=torch.float32, device="cuda")
+    out = nd().nd_tree_decode(q, tu.device_cache(ref), k2, v2, i32(depth), i32(mask), 60, lse=lse)
+    want, wlse = tu.decode_rows(x[0], ref, x[1], x[2], depth, see, 60)
+    got, glse = host(out), host(lse)
+    hit = np.zeros((B, n, Hq), bool)
+    for b, node, head in ((0, 5, 0), (0, 66, 1), (1, 9, 1), (1, 65, 0)):
+        hit[b, :, head * 4:head * 4 + 4] |= see[b, :, node][:, None]
+    assert np.isnan(got[hit]).all() and np.isnan(glse.transpose(0, 2, 1)[hit]).all() and hit.any()
+    assert_close_bf16(got[~hit], want[~hit])
+    np.testing.assert_allclose(glse.transpose(0, 2, 1)[~hit], wlse.transpose(0, 2, 1)[~hit], atol=LSE_TOL, rtol=0)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_values_that_grow_along_the_cache(d):
+    """Keys and values whose scales grow (and fall) by tiles: O is rescaled on the way.  A score is off by 2^-10 sum |q k| /
+    sqrt(d), so a weight by that of itself and an output by twice that of sum p |v|, plus its rounding."""
+    rng = philox(22550 + d)
+    B, n, Hq, Hkv, S, W = 1, 40, 4, 2, 900, 300
+    for grow in (1.0, -1.0):
+        ref = tu.random_cache(rng, B, Hkv, d, S, W)
+        steps = np.floor(grow * np.arange(S + W) / 60).astype(np.float32)
+        ref.v_scale *= np.exp2(steps)[None, None, :, None]
+        ref.k_scale *= np.float32(0.5)
+        ref.v_scale[:, :, 128:256] = 0.0
+        depth, _, mask, see = tu.layout(tu.random_parents(rng, B, n), None, ref.seq_len, 0, 400)
+        (q, k, v), x = nodes(rng, B, n, Hq, Hkv, d)
+        out = host(nd().nd_tree_decode(q, tu.device_cache(ref), k, v, i32(depth), i32(mask), 400))
+        want, _ = tu.decode_rows(x[0], ref, x[1], x[2], depth, see, 400)
+        reach = 2.0 ** -10 * 5.0 * np.abs(x[0]).sum(-1).max() / np.sqrt(d)
+        top = np.abs(want).max()
+        assert np.abs(out - want).max() <= 2 * reach * max(top, 1.0) * 4 + 2.0 ** -8 * top
+
+
 def test_large_and_small_values():
     """Keys and values of very different sizes: scores up to a few hundred, values down to 2^-20 of the largest."""
     rng = philox(22500)
