@@ -73,7 +73,7 @@ constexpr int kWarpTurn = 8, kWarpFeedK = 16, kWarpFeedV = 17, kWarpS = 18;
 // softmax thread holds up to 64 scores.
 constexpr int kRegsLaunch = 96, kRegsSoftmax = 144, kRegsOther = 64;
 static_assert(2 * 128 * kRegsSoftmax + 3 * 128 * kRegsOther <= kThreads * kRegsLaunch, "register split");
-constexpr int kBatch = 4;         // tiles that are noted, and asked into L2, at once
+constexpr int kBatch = 4;         // tiles that are noted at once
 constexpr int kKf = 8;            // node tiles' key factors in flight: more than the tiles between operand and softmax
 constexpr float kLazyLog2 = 8.f;  // the maximum used may lag the true one by 2^8
 constexpr float kPBias = 7.f;     // P is scaled by 2^7
@@ -81,6 +81,7 @@ constexpr int kCodeBits = 24;     // operands made of codes hold 2^-24 of code *
 constexpr int kMostUp = 88;       // V's largest e: a node's value times 2^(88 - 24 + 15) stays finite up to 2^48
 constexpr float kUnits = 16777216.f;  // 2^24
 constexpr int kCtas = 152;        // one per SM
+constexpr int kFewTiles = 4;      // of a pair
 
 // ------------------------------------------------------------ the split
 struct TreePlan {
@@ -116,10 +117,12 @@ TreePlan tree_plan(int batch, int n, int n_q_heads, int n_kv_heads, int sink_cap
   p.pairs = batch * n_kv_heads;
   const long long tiles = (long long)p.pairs * p.t;
   const int most = kCtas / p.nb;
-  // whole pairs where that leaves at most a sixteenth of the CTAs' time idle
-  p.whole = (long long)((p.pairs + most - 1) / most) * most * 16 <= (long long)p.pairs * 17;
-  const long long units = p.whole ? p.pairs : tiles;
-  p.ctas = int(units < most ? units : most);
+  // whole pairs where that leaves at most a sixteenth of the CTAs' time idle, or
+  // the parts would be shorter than their merge; else two tiles a stretch at least
+  p.whole = (long long)((p.pairs + most - 1) / most) * most * 16 <= (long long)p.pairs * 17 ||
+            (p.t <= kFewTiles && p.pairs <= most);
+  const long long units = p.whole ? p.pairs : tiles, ctas = p.whole ? units : (units + 1) / 2;
+  p.ctas = int(ctas < most ? ctas : most);
   p.even = int(units / p.ctas);
   p.odd = int(units - (long long)p.even * p.ctas);
   return p;
@@ -198,10 +201,7 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_
                "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
                : "memory");
 }
-// Asks memory into L2.
-__device__ __forceinline__ void bulk_l2(const void *src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(reinterpret_cast<uint64_t>(src)), "r"(bytes) : "memory");
-}
+// Asks a line into L2.
 __device__ __forceinline__ void prefetch_l2(const void *src) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<uint64_t>(src)) : "memory");
 }
@@ -399,9 +399,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
   regs_dec<kRegsOther>();
   if (warp == kWarpFeedK || warp == kWarpFeedV) {
     // -------------------------------------------------- feeders, one for K and one for V
-    // Ahead of the copies tiles are noted and asked into L2, kBatch at a time, a
-    // lane to a tile (two staged tiles are too few bytes in flight for memory's
-    // latency).
+    // Ahead of the copies tiles are noted, kBatch at a time, a lane to a tile, and
+    // queries and nodes asked into L2.  (Asking the codes too costs more than it
+    // gives: 140 against 133 us at 128 sessions of 16 nodes.)
     const int kv = warp == kWarpFeedV;
     const uint32_t leader = elect_one();
     const int8_t *const codes = kv ? p.c.v_codes : p.c.k_codes;
@@ -463,13 +463,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
               rec.x |= kKindRing;
             }
             rec.x |= cnt << 8 | c1 << 16;
-            if (c1 > 0) {
-              const size_t at = s.pair * nslot + rec.w;
-              bulk_l2(codes + at * D, c1 * D);
-              // (in whole 16 bytes: at D = 64 a slot's scales are 8)
-              const size_t lo = (at * (NG * 4) + 15) & ~size_t(15), hi = ((at + c1) * (NG * 4)) & ~size_t(15);
-              if (hi > lo) bulk_l2(reinterpret_cast<const char *>(scales) + lo, uint32_t(hi - lo));
-            }
           } else {
             rec.y = (u - pl.ts - pl.tr) * kNodes;
             const int cnt = min(kNodes, p.n - rec.y);
@@ -1132,23 +1125,29 @@ __global__ void __launch_bounds__(512) tree_merge_kernel(const __grid_constant__
   const int blk = blockIdx.y, r_blk = warp * 8 + lane / 4, r = blk * pl.rb + r_blk, R = p.n * p.G;
   const int quad = blockIdx.z * 4 + lane % 4, copies = BM / p.lanes;
   if (r_blk >= pl.rb || r >= R) return;
-  auto part = [&](int c) {
-    const int which = c == c0 && pl.start(c) < pair * pl.t ? 1 : 0;
-    return p.parts + ((size_t(c) * pl.nb + blk) * 2 + which) * part_floats<D>();
-  };
+  // the i-th triple: stretch by stretch, copy by copy; four loads in flight
+  const int total = (c1 - c0 + 1) * copies, low = p.lanes == 32 ? 2 : p.lanes == 64 ? 1 : 0;
+  const bool later = pl.start(c0) < pair * pl.t;  // the pair is not the first of its first stretch
   float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c = c0; c <= c1; ++c) {
-    const float *src = part(c);
-    for (int k = 0; k < copies; ++k) {
-      const int at = k * p.lanes + r_blk;
-      const float2 ml = *reinterpret_cast<const float2 *>(src + BM * D + 2 * at);
-      if (ml.x == -INFINITY && ml.y == 0.f) continue;  // saw nothing
-      const float4 v = *reinterpret_cast<const float4 *>(src + (quad * BM + at) * 4);
-      const float mn = fmaxf(m, ml.x), a = mn == -INFINITY ? 0.f : ex2(m - mn), b = mn == -INFINITY ? 1.f : ex2(ml.x - mn);
+#pragma unroll 1
+  for (int i0 = 0; i0 < total; i0 += 4) {
+    float2 ml[4];
+    float4 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = min(i0 + j, total - 1), c = c0 + (i >> low), at = (i & (copies - 1)) * p.lanes + r_blk;
+      const float *src = p.parts + ((size_t(c) * pl.nb + blk) * 2 + (c == c0 && later ? 1 : 0)) * part_floats<D>();
+      ml[j] = *reinterpret_cast<const float2 *>(src + BM * D + 2 * at);
+      v[j] = *reinterpret_cast<const float4 *>(src + (quad * BM + at) * 4);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (i0 + j >= total || (ml[j].x == -INFINITY && ml[j].y == 0.f)) continue;  // (saw nothing)
+      const float mn = fmaxf(m, ml[j].x), a = mn == -INFINITY ? 0.f : ex2(m - mn), b = mn == -INFINITY ? 1.f : ex2(ml[j].x - mn);
       m = mn;
-      l = l * a + ml.y * b;
-      o = make_float4(o.x * a + v.x * b, o.y * a + v.y * b, o.z * a + v.z * b, o.w * a + v.w * b);
+      l = l * a + ml[j].y * b;
+      o = make_float4(o.x * a + v[j].x * b, o.y * a + v[j].y * b, o.z * a + v[j].z * b, o.w * a + v[j].w * b);
     }
   }
   const float inv = l != 0.f ? 1.f / l : 0.f;
