@@ -273,8 +273,9 @@ def test_offsets_that_pass_32_bits_in_a_region_mostly_empty():
         t = torch.empty((B, Hkv, cap + W, src.shape[3]), dtype=src.dtype, device="cuda")
         t[:, :, :S], t[:, :, cap:] = src[:, :, :S], src[:, :, S:]
         big[f] = t
-    cache = nd().KVCache(**big, sink_len=small.sink_len, ring_start=small.ring_start, ring_len=small.ring_len, seq_len=small.seq_len,
-                         sink_cap=cap, ring_cap=W)
+    # (metadata of its own: each cache is appended to below)
+    meta = {f: getattr(small, f).clone() for f in ("sink_len", "ring_start", "ring_len", "seq_len")}
+    cache = nd().KVCache(**big, **meta, sink_cap=cap, ring_cap=W)
     out = nd().nd_tree_decode(q, cache, k, v, i32(depth), i32(mask), 99)
     want, _ = tu.decode_rows(x[0], ref, x[1], x[2], depth, see, 99)
     assert_close_bf16(host(out), want)
