@@ -85,7 +85,7 @@ constexpr int kWarpTurn = 8, kWarpFeedK = 16, kWarpFeedV = 17, kWarpS = 18;
 // softmax thread holds up to 64 scores.
 constexpr int kRegsLaunch = 96, kRegsSoftmax = 144, kRegsOther = 64;
 static_assert(2 * 128 * kRegsSoftmax + 3 * 128 * kRegsOther <= kThreads * kRegsLaunch, "register split");
-constexpr int kBatch = 4;         // tiles that are noted at once
+constexpr int kBatch = 8;         // tiles that are noted at once
 constexpr int kKf = 8;            // node tiles' key factors in flight: more than the tiles between operand and softmax
 constexpr float kLazyLog2 = 8.f;  // the maximum used may lag the true one by 2^8
 constexpr float kPBias = 7.f;     // P is scaled by 2^7
@@ -429,8 +429,47 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
     bool fresh = true;
     Seg s = {};
 #pragma unroll 1
-    for (int i = 0;; ++i, raw.next()) {
-      if (noted - i < kBatch && (!fresh || x < x1)) {
+    for (int i = -1;; ++i) {
+      if (i >= 0) {
+        if (i >= noted) break;
+        const int4 rec = sm.rec[kv][i % kRec];
+        const int cnt = rec.x >> 8 & 255;
+        if (!ring_wait(&sm.raw_empty[kv][raw.i], raw.phase, abort_flag)) {
+          fail = true;
+          break;
+        }
+        uint64_t *bar = &sm.raw_full[kv][raw.i];
+        const uint32_t dst = sR(kv, raw.i);
+        expect_tx(bar, rec.x & kKindNodes ? cnt * (2 * D) : cnt * (NG == 4 ? D + NG * 4 : D), leader);
+        __syncwarp();
+        if (!(rec.x & kKindNodes)) {
+          const int c1 = rec.x >> 16 & 255;
+          const size_t at = rec.z * nslot + rec.w, wrap = rec.z * nslot + p.c.sink_cap;
+          if (leader && c1 > 0) {
+            bulk_copy(dst, codes + at * D, c1 * D, bar);
+            if (NG == 4) bulk_copy(dst + Y::kCodes, scales + at * NG, c1 * (NG * 4), bar);
+            if (c1 < cnt) {
+              bulk_copy(dst + c1 * D, codes + wrap * D, (cnt - c1) * D, bar);
+              if (NG == 4) bulk_copy(dst + Y::kCodes + c1 * (NG * 4), scales + wrap * NG, (cnt - c1) * (NG * 4), bar);
+            }
+          }
+          if constexpr (NG != 4) {
+            // 8 bytes a slot: a head's first ones aligned to no more than that
+#pragma unroll
+            for (int k = 0; k < BN / 32; ++k) {
+              const int r = lane + 32 * k;
+              if (r < cnt) cp_async8(dst + Y::kCodes + r * (NG * 4), scales + (r < c1 ? at + r : wrap + (r - c1)) * NG);
+            }
+          }
+        } else {
+#pragma unroll 1
+          for (int r = lane; r < cnt; r += 32) bulk_copy(dst + r * (2 * D), node_row(rec.z, rec.y + r), 2 * D, bar);
+        }
+        if constexpr (NG != 4) cp_async_arrive(bar);
+        __syncwarp();
+        raw.next();
+      }
+      if (noted - i <= kBatch && (!fresh || x < x1)) {
         if (fresh) {
           s = seg_at(p, x, x1);
           x += s.t1 - s.t0;
@@ -489,42 +528,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
         fresh = t >= s.t1;
         __syncwarp();
       }
-      if (i >= noted) break;
-      const int4 rec = sm.rec[kv][i % kRec];
-      const int cnt = rec.x >> 8 & 255;
-      if (!ring_wait(&sm.raw_empty[kv][raw.i], raw.phase, abort_flag)) {
-        fail = true;
-        break;
-      }
-      uint64_t *bar = &sm.raw_full[kv][raw.i];
-      const uint32_t dst = sR(kv, raw.i);
-      expect_tx(bar, rec.x & kKindNodes ? cnt * (2 * D) : cnt * (NG == 4 ? D + NG * 4 : D), leader);
-      __syncwarp();
-      if (!(rec.x & kKindNodes)) {
-        const int c1 = rec.x >> 16 & 255;
-        const size_t at = rec.z * nslot + rec.w, wrap = rec.z * nslot + p.c.sink_cap;
-        if (leader && c1 > 0) {
-          bulk_copy(dst, codes + at * D, c1 * D, bar);
-          if (NG == 4) bulk_copy(dst + Y::kCodes, scales + at * NG, c1 * (NG * 4), bar);
-          if (c1 < cnt) {
-            bulk_copy(dst + c1 * D, codes + wrap * D, (cnt - c1) * D, bar);
-            if (NG == 4) bulk_copy(dst + Y::kCodes + c1 * (NG * 4), scales + wrap * NG, (cnt - c1) * (NG * 4), bar);
-          }
-        }
-        if constexpr (NG != 4) {
-          // 8 bytes a slot: a head's first ones aligned to no more than that
-#pragma unroll
-          for (int k = 0; k < BN / 32; ++k) {
-            const int r = lane + 32 * k;
-            if (r < cnt) cp_async8(dst + Y::kCodes + r * (NG * 4), scales + (r < c1 ? at + r : wrap + (r - c1)) * NG);
-          }
-        }
-      } else {
-#pragma unroll 1
-        for (int r = lane; r < cnt; r += 32) bulk_copy(dst + r * (2 * D), node_row(rec.z, rec.y + r), 2 * D, bar);
-      }
-      if constexpr (NG != 4) cp_async_arrive(bar);
-      __syncwarp();
     }
   } else if (warp < kWarpFeedK) {
     // -------------------------------------------------- operands
@@ -1029,7 +1032,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
           if (!fail) fail = !ring_wait(&sm.pv_done[u ^ 1], ((g - 1) >> 1) & 1, abort_flag);
           tc_fence_after();
         };
-#pragma unroll 1
+#pragma unroll
         for (int col = col0; col < col0 + kCols; col += kC) {
           if (REP == 1) load(col);
 #pragma unroll
