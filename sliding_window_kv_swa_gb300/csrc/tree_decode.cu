@@ -56,14 +56,15 @@
 //
 // What bounds it.  Below about 150 rows the read of the codes, above the
 // products.  Measured (D = 128): 128 sessions of 16 nodes (64 rows) over 1280
-// slots of 8 heads 132 us, the bytes 62 (47 % of the copy rate); 8 sessions of 64
-// nodes (256 rows) over 33024 slots 337 us, the products 142 (42 %).  A tile takes
-// 3300 cycles in either, of which no unit is busy for half (issue slots 45 %,
-// tensor pipe 27 %, shared memory about 50 %): with conversion, exponentials and
-// products all left out the roles' waits and bookkeeping alone take 107 and 208
-// us.  Tried on the way and without effect on these two: 16 warps that convert,
-// four that stage Q beside the softmax, three staged tiles and one operand, the
-// conversion's scales found by a warp of their own; asking codes into L2 cost 5 %.
+// slots of 8 heads 129 us, the bytes 62 (48 % of the copy rate); 8 sessions of 64
+// nodes (256 rows) over 33024 slots 273 us, the products 142 (52 %).  No unit is
+// busy for much more than half of that: with conversion, exponentials and
+// products all left out, the roles' waits and bookkeeping alone took 107 (of 132)
+// and 208 (of 337) us.  A warp issues an instruction every five cycles, held up by
+// latencies, by the others and by instruction fetches: code that is not needed for
+// most tiles costs all of them (see tile() and ring_wait()).  Without effect on
+// these two: 16 warps that convert, four that stage Q beside the softmax, three
+// staged tiles and one operand; asking codes into L2 cost 5 %.
 #include <atomic>
 #include <climits>
 #include <type_traits>
@@ -924,9 +925,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
       const int low = dead ? 0 : int(min((long long)INT_MAX, max(0ll, (long long)me.depth + s.nv - p.window + 1)));
       m_own = -INFINITY, l = 0.f, e_o = INT_MAX;
       const int first_t = min(live_tile(pl, s, s.t0), s.t1 - 1);
-      // a tile of cached keys or (kN) of nodes
+      // a tile of cached keys, all of them seen by the warp's rows (0) or not (1), or of
+      // nodes (2).  With 128 columns to a thread most tiles are of kind 0, which has
+      // code of its own, the shortest (303 to 275 us at 8 sessions of 64 nodes); with
+      // fewer, of short caches, one code for both is better (129 against 137 at 128 of
+      // 16).
       auto tile = [&](auto kind, int t, bool last) {
-        constexpr bool kN = decltype(kind)::value;
+        constexpr bool kN = decltype(kind)::value == 2, kMasked = decltype(kind)::value == 1;
         constexpr int kC = kCols < 64 ? kCols : 64;  // columns at a time
         const int u = g & 1;
         // what V's warps say of a node tile (K's were done before S)
@@ -939,7 +944,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
 #pragma unroll
           for (int i = 0; i < kC; i += 32) tmem_ld32(tS + col + i, v + i);
           tmem_ld_wait();
-          if constexpr (!kN) {
+          if constexpr (kMasked) {
             const bool ring = t >= pl.ts;
             const int first = (ring ? t - pl.ts : t) * BN + col;
             const int hi = (ring ? s.nv : s.sl) - first;
@@ -948,7 +953,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
 #pragma unroll
               for (int i = 0; i < kC; ++i) v[i] = i >= lo && i < hi ? v[i] : 0xff800000u;
             }
-          } else {
+          } else if constexpr (kN) {
             // (64 columns: those behind them are not of this tile)
 #pragma unroll
             for (int i = 0; i < kC; i += 32) {
@@ -1087,8 +1092,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
         const int t_next = live_tile(pl, s, t + 1);
         if ((g & 1) == wg) {
           if (!fail) fail = !ring_wait(&sm.s_full[g & 1], (g >> 1) & 1, abort_flag);
-          if (t < pl.ts + pl.tr) tile(std::false_type{}, t, t_next >= s.t1);
-          else tile(std::true_type{}, t, t_next >= s.t1);
+          const bool ring = t >= pl.ts;
+          const int first = (ring ? t - pl.ts : t) * BN + col0;
+          if (t >= pl.ts + pl.tr) {
+            tile(std::integral_constant<int, 2>{}, t, t_next >= s.t1);
+          } else if (REP > 1 || __any_sync(0xffffffffu, (ring ? s.nv : s.sl) - first < kCols || (ring && low > first))) {
+            tile(std::integral_constant<int, 1>{}, t, t_next >= s.t1);
+          } else {
+            if constexpr (REP == 1) tile(std::integral_constant<int, 0>{}, t, t_next >= s.t1);
+          }
         }
         t = t_next;
       }
