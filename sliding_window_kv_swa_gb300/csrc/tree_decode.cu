@@ -59,8 +59,8 @@
 // slots of 8 heads 129 us, the bytes 62 (48 % of the copy rate); 8 sessions of 64
 // nodes (256 rows) over 33024 slots 273 us, the products 142 (52 %).  No unit is
 // busy for much more than half of that: with conversion, exponentials and
-// products all left out, the roles' waits and bookkeeping alone took 107 (of 132)
-// and 208 (of 337) us.  A warp issues an instruction every five cycles, held up by
+// products all left out, the roles' waits and bookkeeping alone took 111 (of 139)
+// and 208 (of 366) us.  A warp issues an instruction every five cycles, held up by
 // latencies, by the others and by instruction fetches: code that is not needed for
 // most tiles costs all of them (see tile() and ring_wait()).  Without effect on
 // these two: 16 warps that convert, four that stage Q beside the softmax, three
@@ -409,328 +409,328 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
   // (each side of the split has its setmaxnreg to itself: behind a common one the
   // compiler takes the smaller bound for all roles)
   if (warp >= kWarpTurn) {
-  regs_dec<kRegsOther>();
-  if (warp == kWarpFeedK || warp == kWarpFeedV) {
-    // -------------------------------------------------- feeders, one for K and one for V
-    // Ahead of the copies tiles are noted, kBatch at a time, a lane to a tile, and
-    // queries and nodes asked into L2.  (Asking the codes too costs more than it
-    // gives: 140 against 133 us at 128 sessions of 16 nodes.)
-    const int kv = warp == kWarpFeedV;
-    const uint32_t leader = elect_one();
-    const int8_t *const codes = kv ? p.c.v_codes : p.c.k_codes;
-    const float *const scales = kv ? p.c.v_scale : p.c.k_scale;
-    const size_t nslot = size_t(p.c.sink_cap) + p.c.ring_cap;
-    auto node_row = [&](int pair, int j) {
-      const int b = pair / p.c.n_kv_heads;
-      return (kv ? p.v : p.k) + (int64_t(b) * p.n + j) * (kv ? p.v_stride : p.k_stride) + (pair - b * p.c.n_kv_heads) * D;
-    };
-    Ring<NR> raw;
-    raw.phase = 1;  // the first round of an empty ring does not wait
-    int noted = 0, x = x0, t = 0;
-    bool fresh = true;
-    Seg s = {};
+    regs_dec<kRegsOther>();
+    if (warp == kWarpFeedK || warp == kWarpFeedV) {
+      // -------------------------------------------------- feeders, one for K and one for V
+      // Ahead of the copies tiles are noted, kBatch at a time, a lane to a tile, and
+      // queries and nodes asked into L2.  (Asking the codes too costs more than it
+      // gives: 140 against 133 us at 128 sessions of 16 nodes.)
+      const int kv = warp == kWarpFeedV;
+      const uint32_t leader = elect_one();
+      const int8_t *const codes = kv ? p.c.v_codes : p.c.k_codes;
+      const float *const scales = kv ? p.c.v_scale : p.c.k_scale;
+      const size_t nslot = size_t(p.c.sink_cap) + p.c.ring_cap;
+      auto node_row = [&](int pair, int j) {
+        const int b = pair / p.c.n_kv_heads;
+        return (kv ? p.v : p.k) + (int64_t(b) * p.n + j) * (kv ? p.v_stride : p.k_stride) + (pair - b * p.c.n_kv_heads) * D;
+      };
+      Ring<NR> raw;
+      raw.phase = 1;  // the first round of an empty ring does not wait
+      int noted = 0, x = x0, t = 0;
+      bool fresh = true;
+      Seg s = {};
 #pragma unroll 1
-    for (int i = -1;; ++i) {
-      if (i >= 0) {
-        if (i >= noted) break;
-        const int4 rec = sm.rec[kv][i % kRec];
-        const int cnt = rec.x >> 8 & 255;
-        if (!ring_wait(&sm.raw_empty[kv][raw.i], raw.phase, abort_flag)) {
+      for (int i = -1;; ++i) {
+        if (i >= 0) {
+          if (i >= noted) break;
+          const int4 rec = sm.rec[kv][i % kRec];
+          const int cnt = rec.x >> 8 & 255;
+          if (!ring_wait(&sm.raw_empty[kv][raw.i], raw.phase, abort_flag)) {
+            fail = true;
+            break;
+          }
+          uint64_t *bar = &sm.raw_full[kv][raw.i];
+          const uint32_t dst = sR(kv, raw.i);
+          expect_tx(bar, rec.x & kKindNodes ? cnt * (2 * D) : cnt * (NG == 4 ? D + NG * 4 : D), leader);
+          __syncwarp();
+          if (!(rec.x & kKindNodes)) {
+            const int c1 = rec.x >> 16 & 255;
+            const size_t at = rec.z * nslot + rec.w, wrap = rec.z * nslot + p.c.sink_cap;
+            if (leader && c1 > 0) {
+              bulk_copy(dst, codes + at * D, c1 * D, bar);
+              if (NG == 4) bulk_copy(dst + Y::kCodes, scales + at * NG, c1 * (NG * 4), bar);
+              if (c1 < cnt) {
+                bulk_copy(dst + c1 * D, codes + wrap * D, (cnt - c1) * D, bar);
+                if (NG == 4) bulk_copy(dst + Y::kCodes + c1 * (NG * 4), scales + wrap * NG, (cnt - c1) * (NG * 4), bar);
+              }
+            }
+            if constexpr (NG != 4) {
+              // 8 bytes a slot: a head's first ones aligned to no more than that
+#pragma unroll
+              for (int k = 0; k < BN / 32; ++k) {
+                const int r = lane + 32 * k;
+                if (r < cnt) cp_async8(dst + Y::kCodes + r * (NG * 4), scales + (r < c1 ? at + r : wrap + (r - c1)) * NG);
+              }
+            }
+          } else {
+#pragma unroll 1
+            for (int r = lane; r < cnt; r += 32) bulk_copy(dst + r * (2 * D), node_row(rec.z, rec.y + r), 2 * D, bar);
+          }
+          if constexpr (NG != 4) cp_async_arrive(bar);
+          __syncwarp();
+          raw.next();
+        }
+        if (noted - i <= kBatch && (!fresh || x < x1)) {
+          if (fresh) {
+            s = seg_at(p, x, x1);
+            x += s.t1 - s.t0;
+            // at least one tile, though it may hold nothing
+            t = min(live_tile(pl, s, s.t0), s.t1 - 1);
+            if (!kv && !s.sane && lane == 0) raise_device_error(p.err, ND_DEVERR_METADATA);
+            if (kv) {  // ask for its queries
+              const int hk = s.pair - s.b * p.c.n_kv_heads, r1 = min(p.n * p.G, (blk + 1) * pl.rb);
+              constexpr int kLines = D * 2 / 128;
+#pragma unroll 1
+              for (int k = lane; k < (r1 - blk * pl.rb) * kLines; k += 32) {
+                const int r = blk * pl.rb + k / kLines, nd = p.G == 1 ? r : int(__umulhi(unsigned(r), p.g_magic));
+                prefetch_l2(p.q + ((int64_t(s.b) * p.n + nd) * p.Hq + hk * p.G + (r - nd * p.G)) * D + k % kLines * 64);
+              }
+            }
+          }
+          // lane j: the j-th live tile from t on
+          auto nth = [&](int j) {
+            int u = t + j;
+            if (t < pl.ts && u >= s.ts && j > 0) u += pl.ts - max(s.ts, t + 1) ;
+            if (t < pl.ts + pl.tr && u >= pl.ts + s.tr && j > 0) u += pl.tr - max(s.tr, t < pl.ts ? 0 : t + 1 - pl.ts);
+            return u;
+          };
+          const int u = nth(lane);
+          const bool mine = lane < kBatch && u < s.t1;
+          const int count = __popc(__ballot_sync(0xffffffffu, mine));
+          const bool end = nth(lane + 1) >= s.t1;
+          if (mine) {
+            int4 rec = make_int4((fresh && lane == 0 ? kFresh : 0) | (end ? kEnd : 0) | (end && x >= x1 ? kLast : 0), 0, s.pair, 0);
+            if (u < pl.ts + pl.tr) {
+              const bool ring = u >= pl.ts;
+              rec.y = (ring ? u - pl.ts : u) * BN;
+              const int cnt = max(0, min(BN, (ring ? s.nv : s.sl) - rec.y));
+              int c1 = cnt;
+              rec.w = rec.y;
+              if (ring) {
+                // two pieces where it wraps
+                unsigned w = unsigned(s.ring0) + unsigned(rec.y);
+                if (w >= unsigned(p.c.ring_cap)) w -= unsigned(p.c.ring_cap);
+                c1 = min(cnt, p.c.ring_cap - int(w));
+                rec.w = p.c.sink_cap + int(w);
+                rec.x |= kKindRing;
+              }
+              rec.x |= cnt << 8 | c1 << 16;
+            } else {
+              rec.y = (u - pl.ts - pl.tr) * kNodes;
+              const int cnt = min(kNodes, p.n - rec.y);
+              rec.x |= kKindNodes | cnt << 8;
+#pragma unroll 1
+              for (int r = 0; r < cnt; ++r) prefetch_l2(node_row(s.pair, rec.y + r));
+            }
+            sm.rec[kv][(noted + lane) % kRec] = rec;
+          }
+          noted += count;
+          t = nth(count);
+          fresh = t >= s.t1;
+          __syncwarp();
+        }
+      }
+    } else if (warp < kWarpFeedK) {
+      // -------------------------------------------------- operands
+      const int turn = warp - kWarpTurn, kv = turn & 1;
+      constexpr int kTurnRows = BN / 4;
+      const int row_w = (turn >> 1) * kTurnRows;  // the warp's first row
+      constexpr int kPieces = D / 16, kRowsIt = 32 / kPieces, kIts = kTurnRows / kRowsIt, kU = 4;
+      static_assert(kIts % kU == 0, "rows of a warp");
+      // A lane takes 16 codes of a row, which become two 16-byte chunks.  K-major
+      // (and for V MN-major) 128-byte swizzle: row * 128 + chunk ^ (row & 7) inside
+      // a box of 64 channels.  Of eight neighbouring lanes the four in the upper
+      // box (D = 128) have the other row of a pair: its swizzle differs in the
+      // lowest bit, so the eight cover all chunk positions, that is all banks, at
+      // once, as their 16-byte loads do.
+      const int piece = lane % kPieces, box = piece / 4, c0 = (2 * piece) & 7;
+      const int row_l = D == 128 ? (lane / kPieces) ^ box : lane / kPieces;
+      const uint32_t codes_off = (row_w + row_l) * D + piece * 16, scale_off = Y::kCodes + 4 * ((row_w + row_l) * NG + piece / 2);
+      const uint32_t operand = kv ? sV : sK;
+      const uint32_t row_off = operand + (row_w + row_l) * 128 + box * (BN * 128);
+      const uint32_t first_c = (c0 ^ (row_l & 7)) << 4;  // and the other chunk: ^ 16
+      Ring<NR> raw;
+      Ring<NK> op;
+      op.phase = 1;
+      int flags = 0;
+#pragma unroll 1
+      for (int g = 0; !(flags & kLast); ++g, raw.next(), op.next()) {
+        if (!ring_wait(&sm.raw_full[kv][raw.i], raw.phase, abort_flag)) {
           fail = true;
           break;
         }
-        uint64_t *bar = &sm.raw_full[kv][raw.i];
-        const uint32_t dst = sR(kv, raw.i);
-        expect_tx(bar, rec.x & kKindNodes ? cnt * (2 * D) : cnt * (NG == 4 ? D + NG * 4 : D), leader);
-        __syncwarp();
-        if (!(rec.x & kKindNodes)) {
-          const int c1 = rec.x >> 16 & 255;
-          const size_t at = rec.z * nslot + rec.w, wrap = rec.z * nslot + p.c.sink_cap;
-          if (leader && c1 > 0) {
-            bulk_copy(dst, codes + at * D, c1 * D, bar);
-            if (NG == 4) bulk_copy(dst + Y::kCodes, scales + at * NG, c1 * (NG * 4), bar);
-            if (c1 < cnt) {
-              bulk_copy(dst + c1 * D, codes + wrap * D, (cnt - c1) * D, bar);
-              if (NG == 4) bulk_copy(dst + Y::kCodes + c1 * (NG * 4), scales + wrap * NG, (cnt - c1) * (NG * 4), bar);
-            }
-          }
-          if constexpr (NG != 4) {
-            // 8 bytes a slot: a head's first ones aligned to no more than that
+        const int4 rec = sm.rec[kv][g % kRec];
+        flags = rec.x;
+        const int cnt = flags >> 8 & 255;
+        const uint32_t stage = sR(kv, raw.i);
+        if (!(flags & kKindNodes)) {
+          // the exponent of the warp's 32 keys, a lane to a key, and their scales as
+          // pairs of fp16, in place: the largest scale goes to 2^14 .. 2^15
+          const uint32_t at = stage + Y::kCodes + (row_w + lane) * (NG * 4);
+          float y[NG], most = 0.f;
+          lds_row<NG>(at, y);
 #pragma unroll
-            for (int k = 0; k < BN / 32; ++k) {
-              const int r = lane + 32 * k;
-              if (r < cnt) cp_async8(dst + Y::kCodes + r * (NG * 4), scales + (r < c1 ? at + r : wrap + (r - c1)) * NG);
+          for (int j = 0; j < NG; ++j) {
+            if (row_w + lane >= cnt) y[j] = 0.f;  // a slot behind the last: whatever is staged counts 0
+            most = fmaxf(most, fabsf(y[j]));
+          }
+          // (of values >= 0 the bits order as the values do)
+          most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
+          const int e = min(kMostUp, clamp_exp(14 - ilog2(most)));
+          sts_row<NG>(at, y, pow2i(e));
+          if (lane == 0) sm.e[kv][g % kInfo][turn >> 1] = e;
+        }
+        __syncwarp();
+        if (kv && lane == 0) mbar_arrive(&sm.v_known[g & 3]);
+        if (!ring_wait(&sm.op_empty[kv][op.i], op.phase, abort_flag)) {
+          fail = true;
+          break;
+        }
+        if (!(flags & kKindNodes)) {
+          const uint32_t raw_at = stage + codes_off, sc_at = stage + scale_off;
+          const uint32_t dst = row_off + op.i * Y::kKV;
+          uint32_t ahead[kU][4], ahead_s[kU];  // the next group's loads run ahead of this one's stores
+          auto load = [&](int i0) {
+#pragma unroll
+            for (int i = 0; i < kU; ++i) {
+              ld_shared_v4(raw_at + (i0 + i) * kRowsIt * D, ahead[i][0], ahead[i][1], ahead[i][2], ahead[i][3]);
+              ahead_s[i] = lds32(sc_at + (i0 + i) * kRowsIt * NG * 4);
+            }
+          };
+          load(0);
+#pragma unroll 1
+          for (int i0 = 0; i0 < kIts; i0 += kU) {
+            uint32_t x[kU][4], s2[kU];
+#pragma unroll
+            for (int i = 0; i < kU; ++i) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) x[i][j] = ahead[i][j] ^ 0x80808080u;
+              s2[i] = ahead_s[i];
+            }
+            if (i0 + kU < kIts) load(i0 + kU);
+#pragma unroll
+            for (int i = 0; i < kU; ++i) {
+              // a lane's rows are kRowsIt (4 or 8) apart: their swizzles differ in
+              // one bit at most
+              const uint32_t at = dst + (i0 + i) * kRowsIt * 128 + (first_c ^ ((i * kRowsIt & 4) << 4));
+              const uint32_t off = hmul2(s2[i], kMinus128);
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                const uint32_t wa = x[i][2 * q], wb = x[i][2 * q + 1];
+                st_shared_v4(q ? at ^ 16u : at, scaled_codes(wa, kBytes01, s2[i], off), scaled_codes(wa, kBytes23, s2[i], off),
+                             scaled_codes(wb, kBytes01, s2[i], off), scaled_codes(wb, kBytes23, s2[i], off));
+              }
             }
           }
         } else {
+          // nodes: D/8 lanes to a row, 16 of the tile's rows per warp
+          constexpr int kL = D / 8, kR = 32 / kL;
+          const int sub = lane / kL, ch = lane % kL, first = (turn >> 1) * 16;
+          const int32_t *depth = p.depth + int64_t(rec.z / p.c.n_kv_heads) * p.n + rec.y;
+          const uint32_t alive = __ballot_sync(0xffffffffu, lane < 16 && first + lane < cnt && depth[min(first + lane, cnt - 1)] >= 0);
+          uint32_t bads = 0u;
+          const uint32_t dst = operand + op.i * Y::kKV;
 #pragma unroll 1
-          for (int r = lane; r < cnt; r += 32) bulk_copy(dst + r * (2 * D), node_row(rec.z, rec.y + r), 2 * D, bar);
+          for (int r0 = 0; r0 < 16; r0 += kR) {
+            const int r = first + r0 + sub;
+            uint32_t x[4] = {0u, 0u, 0u, 0u};
+            if (alive >> (r0 + sub) & 1u) ld_shared_v4(stage + r * (2 * D) + ch * 16, x[0], x[1], x[2], x[3]);
+            uint32_t m2 = 0u;  // of magnitudes the bits order as the values do, infinities and NaN above all
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m2 = max_u16x2(m2, x[e] & 0x7fff7fffu);
+            uint32_t most = max(m2 << 16, m2 & 0xffff0000u);
+#pragma unroll
+            for (int off = kL / 2; off >= 1; off >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, off));
+            const bool bad = most >= 0x7f800000u;
+            if (!kv) {
+              const int e = clamp_exp(14 - ilog2(__uint_as_float(most)));
+              const float up = pow2i(e);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) x[i] = pack_half2(bf16_lo(x[i]) * up, bf16_hi(x[i]) * up);
+              if (ch == 0) sm.kf[g % kKf][r] = pow2i(-e);
+            }
+            if (bad) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) x[i] = 0u;
+            }
+            const uint32_t who = __ballot_sync(0xffffffffu, bad);
+#pragma unroll
+            for (int k = 0; k < kR; ++k) bads |= (who >> (k * kL) & 1u) << (r0 + k);
+            st_shared_v4(dst + (ch / 8) * (BN * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4), x[0], x[1], x[2], x[3]);
+          }
+          if (lane == 0) {
+            sm.bad[kv][g % kInfo][turn >> 1] = uint16_t(bads);
+            if (!kv) sm.live[g % kInfo][turn >> 1] = uint16_t(alive);
+          }
         }
-        if constexpr (NG != 4) cp_async_arrive(bar);
+        // the MMA reads the tile through the async proxy
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        raw.next();
-      }
-      if (noted - i <= kBatch && (!fresh || x < x1)) {
-        if (fresh) {
-          s = seg_at(p, x, x1);
-          x += s.t1 - s.t0;
-          // at least one tile, though it may hold nothing
-          t = min(live_tile(pl, s, s.t0), s.t1 - 1);
-          if (!kv && !s.sane && lane == 0) raise_device_error(p.err, ND_DEVERR_METADATA);
-          if (kv) {  // ask for its queries
-            const int hk = s.pair - s.b * p.c.n_kv_heads, r1 = min(p.n * p.G, (blk + 1) * pl.rb);
-            constexpr int kLines = D * 2 / 128;
-#pragma unroll 1
-            for (int k = lane; k < (r1 - blk * pl.rb) * kLines; k += 32) {
-              const int r = blk * pl.rb + k / kLines, nd = p.G == 1 ? r : int(__umulhi(unsigned(r), p.g_magic));
-              prefetch_l2(p.q + ((int64_t(s.b) * p.n + nd) * p.Hq + hk * p.G + (r - nd * p.G)) * D + k % kLines * 64);
-            }
-          }
-        }
-        // lane j: the j-th live tile from t on
-        auto nth = [&](int j) {
-          int u = t + j;
-          if (t < pl.ts && u >= s.ts && j > 0) u += pl.ts - max(s.ts, t + 1) ;
-          if (t < pl.ts + pl.tr && u >= pl.ts + s.tr && j > 0) u += pl.tr - max(s.tr, t < pl.ts ? 0 : t + 1 - pl.ts);
-          return u;
-        };
-        const int u = nth(lane);
-        const bool mine = lane < kBatch && u < s.t1;
-        const int count = __popc(__ballot_sync(0xffffffffu, mine));
-        const bool end = nth(lane + 1) >= s.t1;
-        if (mine) {
-          int4 rec = make_int4((fresh && lane == 0 ? kFresh : 0) | (end ? kEnd : 0) | (end && x >= x1 ? kLast : 0), 0, s.pair, 0);
-          if (u < pl.ts + pl.tr) {
-            const bool ring = u >= pl.ts;
-            rec.y = (ring ? u - pl.ts : u) * BN;
-            const int cnt = max(0, min(BN, (ring ? s.nv : s.sl) - rec.y));
-            int c1 = cnt;
-            rec.w = rec.y;
-            if (ring) {
-              // two pieces where it wraps
-              unsigned w = unsigned(s.ring0) + unsigned(rec.y);
-              if (w >= unsigned(p.c.ring_cap)) w -= unsigned(p.c.ring_cap);
-              c1 = min(cnt, p.c.ring_cap - int(w));
-              rec.w = p.c.sink_cap + int(w);
-              rec.x |= kKindRing;
-            }
-            rec.x |= cnt << 8 | c1 << 16;
-          } else {
-            rec.y = (u - pl.ts - pl.tr) * kNodes;
-            const int cnt = min(kNodes, p.n - rec.y);
-            rec.x |= kKindNodes | cnt << 8;
-#pragma unroll 1
-            for (int r = 0; r < cnt; ++r) prefetch_l2(node_row(s.pair, rec.y + r));
-          }
-          sm.rec[kv][(noted + lane) % kRec] = rec;
-        }
-        noted += count;
-        t = nth(count);
-        fresh = t >= s.t1;
-        __syncwarp();
-      }
-    }
-  } else if (warp < kWarpFeedK) {
-    // -------------------------------------------------- operands
-    const int turn = warp - kWarpTurn, kv = turn & 1;
-    constexpr int kTurnRows = BN / 4;
-    const int row_w = (turn >> 1) * kTurnRows;  // the warp's first row
-    constexpr int kPieces = D / 16, kRowsIt = 32 / kPieces, kIts = kTurnRows / kRowsIt, kU = 4;
-    static_assert(kIts % kU == 0, "rows of a warp");
-    // A lane takes 16 codes of a row, which become two 16-byte chunks.  K-major
-    // (and for V MN-major) 128-byte swizzle: row * 128 + chunk ^ (row & 7) inside
-    // a box of 64 channels.  Of eight neighbouring lanes the four in the upper
-    // box (D = 128) have the other row of a pair: its swizzle differs in the
-    // lowest bit, so the eight cover all chunk positions, that is all banks, at
-    // once, as their 16-byte loads do.
-    const int piece = lane % kPieces, box = piece / 4, c0 = (2 * piece) & 7;
-    const int row_l = D == 128 ? (lane / kPieces) ^ box : lane / kPieces;
-    const uint32_t codes_off = (row_w + row_l) * D + piece * 16, scale_off = Y::kCodes + 4 * ((row_w + row_l) * NG + piece / 2);
-    const uint32_t operand = kv ? sV : sK;
-    const uint32_t row_off = operand + (row_w + row_l) * 128 + box * (BN * 128);
-    const uint32_t first_c = (c0 ^ (row_l & 7)) << 4;  // and the other chunk: ^ 16
-    Ring<NR> raw;
-    Ring<NK> op;
-    op.phase = 1;
-    int flags = 0;
-#pragma unroll 1
-    for (int g = 0; !(flags & kLast); ++g, raw.next(), op.next()) {
-      if (!ring_wait(&sm.raw_full[kv][raw.i], raw.phase, abort_flag)) {
-        fail = true;
-        break;
-      }
-      const int4 rec = sm.rec[kv][g % kRec];
-      flags = rec.x;
-      const int cnt = flags >> 8 & 255;
-      const uint32_t stage = sR(kv, raw.i);
-      if (!(flags & kKindNodes)) {
-        // the exponent of the warp's 32 keys, a lane to a key, and their scales as
-        // pairs of fp16, in place: the largest scale goes to 2^14 .. 2^15
-        const uint32_t at = stage + Y::kCodes + (row_w + lane) * (NG * 4);
-        float y[NG], most = 0.f;
-        lds_row<NG>(at, y);
-#pragma unroll
-        for (int j = 0; j < NG; ++j) {
-          if (row_w + lane >= cnt) y[j] = 0.f;  // a slot behind the last: whatever is staged counts 0
-          most = fmaxf(most, fabsf(y[j]));
-        }
-        // (of values >= 0 the bits order as the values do)
-        most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
-        const int e = min(kMostUp, clamp_exp(14 - ilog2(most)));
-        sts_row<NG>(at, y, pow2i(e));
-        if (lane == 0) sm.e[kv][g % kInfo][turn >> 1] = e;
-      }
-      __syncwarp();
-      if (kv && lane == 0) mbar_arrive(&sm.v_known[g & 3]);
-      if (!ring_wait(&sm.op_empty[kv][op.i], op.phase, abort_flag)) {
-        fail = true;
-        break;
-      }
-      if (!(flags & kKindNodes)) {
-        const uint32_t raw_at = stage + codes_off, sc_at = stage + scale_off;
-        const uint32_t dst = row_off + op.i * Y::kKV;
-        uint32_t ahead[kU][4], ahead_s[kU];  // the next group's loads run ahead of this one's stores
-        auto load = [&](int i0) {
-#pragma unroll
-          for (int i = 0; i < kU; ++i) {
-            ld_shared_v4(raw_at + (i0 + i) * kRowsIt * D, ahead[i][0], ahead[i][1], ahead[i][2], ahead[i][3]);
-            ahead_s[i] = lds32(sc_at + (i0 + i) * kRowsIt * NG * 4);
-          }
-        };
-        load(0);
-#pragma unroll 1
-        for (int i0 = 0; i0 < kIts; i0 += kU) {
-          uint32_t x[kU][4], s2[kU];
-#pragma unroll
-          for (int i = 0; i < kU; ++i) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x[i][j] = ahead[i][j] ^ 0x80808080u;
-            s2[i] = ahead_s[i];
-          }
-          if (i0 + kU < kIts) load(i0 + kU);
-#pragma unroll
-          for (int i = 0; i < kU; ++i) {
-            // a lane's rows are kRowsIt (4 or 8) apart: their swizzles differ in
-            // one bit at most
-            const uint32_t at = dst + (i0 + i) * kRowsIt * 128 + (first_c ^ ((i * kRowsIt & 4) << 4));
-            const uint32_t off = hmul2(s2[i], kMinus128);
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const uint32_t wa = x[i][2 * q], wb = x[i][2 * q + 1];
-              st_shared_v4(q ? at ^ 16u : at, scaled_codes(wa, kBytes01, s2[i], off), scaled_codes(wa, kBytes23, s2[i], off),
-                           scaled_codes(wb, kBytes01, s2[i], off), scaled_codes(wb, kBytes23, s2[i], off));
-            }
-          }
-        }
-      } else {
-        // nodes: D/8 lanes to a row, 16 of the tile's rows per warp
-        constexpr int kL = D / 8, kR = 32 / kL;
-        const int sub = lane / kL, ch = lane % kL, first = (turn >> 1) * 16;
-        const int32_t *depth = p.depth + int64_t(rec.z / p.c.n_kv_heads) * p.n + rec.y;
-        const uint32_t alive = __ballot_sync(0xffffffffu, lane < 16 && first + lane < cnt && depth[min(first + lane, cnt - 1)] >= 0);
-        uint32_t bads = 0u;
-        const uint32_t dst = operand + op.i * Y::kKV;
-#pragma unroll 1
-        for (int r0 = 0; r0 < 16; r0 += kR) {
-          const int r = first + r0 + sub;
-          uint32_t x[4] = {0u, 0u, 0u, 0u};
-          if (alive >> (r0 + sub) & 1u) ld_shared_v4(stage + r * (2 * D) + ch * 16, x[0], x[1], x[2], x[3]);
-          uint32_t m2 = 0u;  // of magnitudes the bits order as the values do, infinities and NaN above all
-#pragma unroll
-          for (int e = 0; e < 4; ++e) m2 = max_u16x2(m2, x[e] & 0x7fff7fffu);
-          uint32_t most = max(m2 << 16, m2 & 0xffff0000u);
-#pragma unroll
-          for (int off = kL / 2; off >= 1; off >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, off));
-          const bool bad = most >= 0x7f800000u;
-          if (!kv) {
-            const int e = clamp_exp(14 - ilog2(__uint_as_float(most)));
-            const float up = pow2i(e);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = pack_half2(bf16_lo(x[i]) * up, bf16_hi(x[i]) * up);
-            if (ch == 0) sm.kf[g % kKf][r] = pow2i(-e);
-          }
-          if (bad) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = 0u;
-          }
-          const uint32_t who = __ballot_sync(0xffffffffu, bad);
-#pragma unroll
-          for (int k = 0; k < kR; ++k) bads |= (who >> (k * kL) & 1u) << (r0 + k);
-          st_shared_v4(dst + (ch / 8) * (BN * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4), x[0], x[1], x[2], x[3]);
-        }
         if (lane == 0) {
-          sm.bad[kv][g % kInfo][turn >> 1] = uint16_t(bads);
-          if (!kv) sm.live[g % kInfo][turn >> 1] = uint16_t(alive);
+          mbar_arrive(&sm.op_full[kv][op.i]);
+          mbar_arrive(&sm.raw_empty[kv][raw.i]);
         }
       }
-      // the MMA reads the tile through the async proxy
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&sm.op_full[kv][op.i]);
-        mbar_arrive(&sm.raw_empty[kv][raw.i]);
-      }
-    }
-  } else if (warp == kWarpS) {
-    // -------------------------------------------------- S(g) = Q K(g)^T
-    const uint32_t leader = elect_one();
-    constexpr uint32_t kId = idesc_f16(BM, BN, 0), kIdNodes = idesc_f16(BM, kNodes, 0);
-    Ring<NK> kr;
-    Ring<2> sr;  // a buffer is free once the softmax has read it
-    sr.phase = 1;
-    uint32_t q_phase = 0;
-    const uint64_t dk = sdesc_sw128(sK, 16, 1024);
-    int flags = 0;
+    } else if (warp == kWarpS) {
+      // -------------------------------------------------- S(g) = Q K(g)^T
+      const uint32_t leader = elect_one();
+      constexpr uint32_t kId = idesc_f16(BM, BN, 0), kIdNodes = idesc_f16(BM, kNodes, 0);
+      Ring<NK> kr;
+      Ring<2> sr;  // a buffer is free once the softmax has read it
+      sr.phase = 1;
+      uint32_t q_phase = 0;
+      const uint64_t dk = sdesc_sw128(sK, 16, 1024);
+      int flags = 0;
 #pragma unroll 1
-    for (int g = 0; !(flags & kLast); ++g, kr.next(), sr.next()) {
-      bool ok = ring_wait(&sm.op_full[0][kr.i], kr.phase, abort_flag) &&
-                ring_wait(&sm.s_empty[sr.i], sr.phase, abort_flag);
-      flags = sm.rec[0][g % kRec].x;
-      if (ok && (flags & kFresh)) {
-        ok = ring_wait(&sm.q_full, q_phase, abort_flag);
-        q_phase ^= 1u;
-      }
-      if (!ok) {
-        fail = true;
-        break;
-      }
-      tc_fence_after();
-      const uint64_t kd = dk + uint64_t(kr.i * (Y::kKV >> 4));
-      const uint32_t id = flags & kKindNodes ? kIdNodes : kId;
+      for (int g = 0; !(flags & kLast); ++g, kr.next(), sr.next()) {
+        bool ok = ring_wait(&sm.op_full[0][kr.i], kr.phase, abort_flag) &&
+                  ring_wait(&sm.s_empty[sr.i], sr.phase, abort_flag);
+        flags = sm.rec[0][g % kRec].x;
+        if (ok && (flags & kFresh)) {
+          ok = ring_wait(&sm.q_full, q_phase, abort_flag);
+          q_phase ^= 1u;
+        }
+        if (!ok) {
+          fail = true;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t kd = dk + uint64_t(kr.i * (Y::kKV >> 4));
+        const uint32_t id = flags & kKindNodes ? kIdNodes : kId;
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)  // 16 channels = 8 TMEM columns of Q's fp16 pairs
-        mma_ts(tmem + sr.i * BN, tQ + kk * 8, kd + (kk >> 2) * (BN * 128 >> 4) + (kk & 3) * 2, id, kk > 0 ? 1u : 0u, leader);
-      mma_commit(&sm.s_full[sr.i], leader);
-      mma_commit(&sm.op_empty[0][kr.i], leader);
-    }
-  } else {
-    // -------------------------------------------------- O += P(g) V(g)
-    // (a segment's first product overwrites O: its P exists only once the
-    // softmax warps have read the segment before out of it)
-    const uint32_t leader = elect_one();
-    constexpr uint32_t kId = idesc_f16(BM, D, 1), kIdNodes = idesc_bf16(BM, D, 1);
-    Ring<NK> vr;
-    Ring<2> pr;
-    const uint64_t dv = sdesc_sw128(sV, BN * 128, 1024);
-    int flags = 0;
+        for (int kk = 0; kk < D / 16; ++kk)  // 16 channels = 8 TMEM columns of Q's fp16 pairs
+          mma_ts(tmem + sr.i * BN, tQ + kk * 8, kd + (kk >> 2) * (BN * 128 >> 4) + (kk & 3) * 2, id, kk > 0 ? 1u : 0u, leader);
+        mma_commit(&sm.s_full[sr.i], leader);
+        mma_commit(&sm.op_empty[0][kr.i], leader);
+      }
+    } else {
+      // -------------------------------------------------- O += P(g) V(g)
+      // (a segment's first product overwrites O: its P exists only once the
+      // softmax warps have read the segment before out of it)
+      const uint32_t leader = elect_one();
+      constexpr uint32_t kId = idesc_f16(BM, D, 1), kIdNodes = idesc_bf16(BM, D, 1);
+      Ring<NK> vr;
+      Ring<2> pr;
+      const uint64_t dv = sdesc_sw128(sV, BN * 128, 1024);
+      int flags = 0;
 #pragma unroll 1
-    for (int g = 0; !(flags & kLast); ++g, vr.next(), pr.next()) {
-      if (!ring_wait(&sm.op_full[1][vr.i], vr.phase, abort_flag) || !ring_wait(&sm.p_full[pr.i], pr.phase, abort_flag)) {
-        fail = true;
-        break;
-      }
-      flags = sm.rec[1][g % kRec].x;
-      tc_fence_after();
-      const uint64_t vd = dv + uint64_t(vr.i * (Y::kKV >> 4));
-      const uint32_t id = flags & kKindNodes ? kIdNodes : kId, more = flags & kFresh ? 0u : 1u;
+      for (int g = 0; !(flags & kLast); ++g, vr.next(), pr.next()) {
+        if (!ring_wait(&sm.op_full[1][vr.i], vr.phase, abort_flag) || !ring_wait(&sm.p_full[pr.i], pr.phase, abort_flag)) {
+          fail = true;
+          break;
+        }
+        flags = sm.rec[1][g % kRec].x;
+        tc_fence_after();
+        const uint64_t vd = dv + uint64_t(vr.i * (Y::kKV >> 4));
+        const uint32_t id = flags & kKindNodes ? kIdNodes : kId, more = flags & kFresh ? 0u : 1u;
 #pragma unroll
-      for (int kk = 0; kk < BN / 16; ++kk)  // (nodes: half as many keys)
-        mma_ts(tO, tP + kk * 8, vd + kk * (16 * 128 >> 4), id, kk > 0 ? 1u : more,
-               kk >= kNodes / 16 && (flags & kKindNodes) ? 0u : leader);
-      mma_commit(&sm.pv_done[pr.i], leader);
-      mma_commit(&sm.op_empty[1][vr.i], leader);
+        for (int kk = 0; kk < BN / 16; ++kk)  // (nodes: half as many keys)
+          mma_ts(tO, tP + kk * 8, vd + kk * (16 * 128 >> 4), id, kk > 0 ? 1u : more,
+                 kk >= kNodes / 16 && (flags & kKindNodes) ? 0u : leader);
+        mma_commit(&sm.pv_done[pr.i], leader);
+        mma_commit(&sm.op_empty[1][vr.i], leader);
+      }
     }
-  }
   } else {
     // -------------------------------------------------- softmax warps
     regs_inc<kRegsSoftmax>();

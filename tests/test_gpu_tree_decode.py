@@ -106,6 +106,24 @@ def test_without_a_cache_and_with_arbitrary_masks(Hq, Hkv, d):
         check(ref, a, b, depth, see, mask, 6)
 
 
+def test_metadata_out_of_range_are_flagged_and_give_nothing():
+    rng = philox(22240)
+    B, n, Hq, Hkv, d, S, W = 4, 10, 8, 2, 64, 300, 40
+    ref = tu.random_cache(rng, B, Hkv, d, S, W)
+    depth, _, mask, see = tu.layout(tu.random_parents(rng, B, n), None, ref.seq_len, 0, 30)
+    (q, k, v), x = nodes(rng, B, n, Hq, Hkv, d)
+    want, _ = tu.decode_rows(x[0], ref, x[1], x[2], depth, see, 30)
+    cache = tu.device_cache(ref)
+    cache.sink_len[0], cache.ring_len[1], cache.ring_start[3] = S + 1, -1, W
+    lse = torch.empty((B, Hq, n), dtype=torch.float32, device="cuda")
+    out = nd().nd_tree_decode(q, cache, k, v, i32(depth), i32(mask), 30, lse=lse)
+    torch.cuda.synchronize()
+    assert nd().nd_device_errors(clear=True) == 2
+    for b in (0, 1, 3):
+        assert (out[b] == 0).all() and (lse[b] == -float("inf")).all()
+    assert_close_bf16(host(out)[2], want[2])
+
+
 def test_depths_far_beyond_the_window():
     rng = philox(22250)
     B, n, Hq, Hkv, d = 1, 6, 8, 2, 64
