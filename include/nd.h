@@ -441,7 +441,8 @@ ND_API int nd_tree_layout(const int32_t *parents, const int32_t *n_nodes, const 
  *   out    bf16 [batch][n][n_q_heads][head_dim]
  *   lse    fp32 [batch][n_q_heads][n] natural-log softmax denominator, or NULL
  *   window >= 1; n_q_heads / n_kv_heads 1..8; head_dim 64 or 128; n 1..256;
- *   batch * n_kv_heads at most 2^20; 1 <= sink_cap + ring_cap <= 2^31 - 4097
+ *   batch * n_kv_heads at most 2^20; 1 <= slots = sink_cap + ring_cap <= 2^31 -
+ *   4097; batch * n_kv_heads * (ceil(slots/128) + 1 + ceil(n/64)) below 2^30
  * A row that sees no key, and padding, get out = 0, lse = -inf, and so does a
  * query head with a NaN or an infinity, as in nd_swa_sink_decode.  A row that
  * sees a node whose key or value (of its KV head) holds one is NaN in all
@@ -483,7 +484,7 @@ ND_API int nd_tree_decode(const void *q, const nd_kv_cache *cache, const void *k
  *   path_len   int32 [batch]: how many (0: none holds)
  *   next       int32 [batch], or NULL: the target of the path's last node, of an
  *              empty path root_target (-1 if that is NULL)
- * max_path >= 1.  Bad parents and n_nodes are handled as by nd_tree_layout.
+ * max_path 1..65536.  Bad parents and n_nodes are handled as by nd_tree_layout.
  */
 ND_API int nd_tree_accept(const int32_t *parents, const int32_t *n_nodes, const int32_t *tokens,
                           const int32_t *target, const int32_t *root_target, int batch, int n,
@@ -496,7 +497,8 @@ ND_API int nd_tree_accept(const int32_t *parents, const int32_t *n_nodes, const 
  * path[b][0], path[b][1], ...  Afterwards seq_len has advanced by path_len[b].
  *   k_new, v_new, k_stride, v_stride, n  as nd_tree_decode
  *   path      int32 [batch][max_path]; path_len int32 [batch], 0..max_path
- * Requires ring_cap > 0, max_path >= 1, head_dim 32, 64, 128 or 256.  A
+ * Requires ring_cap > 0, max_path 1..65536 with max_path * n_kv_heads at most
+ * 2^29, head_dim 32, 64, 128 or 256.  A
  * path_len outside its range, or a node outside 0..n-1 among the first
  * path_len, sets device error flag 2 and leaves the sequence untouched.
  */

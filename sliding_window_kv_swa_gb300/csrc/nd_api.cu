@@ -905,6 +905,8 @@ int nd_rope_positions(const void *q, const void *k, nd_dtype dtype, int batch, i
 // offsets of their nodes in 64 bits).
 static constexpr int kMostTrees = 1 << 24;
 
+static constexpr int kMostPath = 1 << 16;
+
 static int validate_tree(int batch, int n) {
   if (batch < 0 || n < 0) return ND_ERR_INVALID_ARG;
   return n > ND_TREE_MAX_NODES || batch > kMostTrees ? ND_ERR_UNSUPPORTED : ND_OK;
@@ -929,6 +931,7 @@ int nd_tree_accept(const int32_t *parents, const int32_t *n_nodes, const int32_t
   int st = validate_tree(batch, n);
   if (st != ND_OK) return st;
   if (max_path < 1) return ND_ERR_INVALID_ARG;
+  if (max_path > kMostPath) return ND_ERR_UNSUPPORTED;
   if (batch == 0) return ND_OK;
   if ((n > 0 && (!parents || !tokens || !target)) || !path || !path_len) return ND_ERR_INVALID_ARG;
   if ((st = check_device(nullptr)) != ND_OK) return st;
@@ -943,6 +946,7 @@ int nd_tree_commit(const nd_kv_cache *cache, const void *k_new, const void *v_ne
   if ((st = validate_tree(cache->batch, n)) != ND_OK) return st;
   const int d = cache->head_dim, Hkv = cache->n_kv_heads;
   if (max_path < 1 || cache->ring_cap <= 0 || Hkv > 65536) return ND_ERR_INVALID_ARG;
+  if (max_path > kMostPath || int64_t(max_path) * Hkv > (1 << 29)) return ND_ERR_UNSUPPORTED;
   if (d != 32 && d != 64 && d != 128 && d != 256) return ND_ERR_UNSUPPORTED;
   if (cache->batch == 0) return ND_OK;
   if (!path || !path_len) return ND_ERR_INVALID_ARG;
@@ -980,7 +984,8 @@ int nd_tree_decode(const void *q, const nd_kv_cache *cache, const void *k_new, c
   if (!stride_ok(k_stride, Hkv, d, 2) || !stride_ok(v_stride, Hkv, d, 2)) return ND_ERR_INVALID_ARG;
   const int64_t slots = int64_t(cache->sink_cap) + cache->ring_cap;
   if (slots < 1) return ND_ERR_INVALID_ARG;
-  if (!tree_sizes_ok(cache->batch, Hkv, slots) || !tree_decode_fits(cache->batch, n, Hkv, cache->sink_cap, cache->ring_cap))
+  // (as the workspace query has it: a size of 0 never stands for a refused one)
+  if (!tree_sizes_ok(cache->batch, Hkv, slots) || !tree_decode_fits(cache->batch, n, Hkv, int(slots), 1))
     return ND_ERR_UNSUPPORTED;
   const size_t need = nd_tree_decode_workspace_size(cache->batch, n, n_q_heads, Hkv, d, int(slots));
   if (need && (!workspace || workspace_bytes < need || !aligned16(workspace))) return ND_ERR_WORKSPACE;

@@ -40,6 +40,7 @@ def test_tree_accept():
 
     assert call(B=-1) == INVALID and call(n=-1) == INVALID and call(m=0) == INVALID
     assert call(n=257) == UNSUPPORTED and call(B=(1 << 24) + 1) == UNSUPPORTED
+    assert call(m=65537) == UNSUPPORTED
     for name in ("parents", "tokens", "target", "path", "length"):
         assert call(**{name: None}) == INVALID
     assert call(B=0) == OK
@@ -51,6 +52,7 @@ def test_tree_commit():
 
     assert call(c=None) == INVALID and call(c=cache(ptr=4104)) == INVALID and call(c=cache(d=48)) == INVALID
     assert call(c=cache(W=0)) == INVALID and call(c=cache(d=96)) == UNSUPPORTED
+    assert call(m=65537) == UNSUPPORTED and call(c=cache(Hkv=16384), m=65536, ks=1 << 20, vs=1 << 20) == UNSUPPORTED
     assert call(n=-1) == INVALID and call(n=257) == UNSUPPORTED and call(m=0) == INVALID
     for name in ("k", "v"):
         assert call(**{name: BAD}) == INVALID and call(**{name: None}) == INVALID
@@ -87,6 +89,18 @@ def test_tree_decode_workspace_size_of_bad_arguments_is_zero():
     assert size(0, 4, 8, 2, 64, 100) == 0 and size(1, 0, 8, 2, 64, 100) == 0 and size(1, 4, 8, 3, 64, 100) == 0
     assert size(1, 257, 8, 2, 64, 100) == 0 and size(1, 4, 0, 2, 64, 100) == 0 and size(1, 4, 8, 0, 64, 100) == 0
     assert size(1, 4, 8, 2, 0, 100) == 0 and size(1, 4, 8, 2, 64, 0) == 0
+
+
+def test_tree_decode_refuses_what_the_workspace_size_is_no_answer_for():
+    # 153 pairs of as many slots as leave 2^30 tiles: one region takes a tile less than the query allows for
+    pairs, per = 153, (1 << 30) // 153
+    W = (per - 1) * 128                     # and a tile of nodes: 153 * per < 2^30 <= 153 * (per + 1)
+    assert pairs * per < 1 << 30 <= pairs * (per + 1) and W < 2 ** 31 - 4096
+    assert nd.nd_tree_decode_workspace_size(pairs, 1, 1, 1, 64, W) == 0
+    c = cache(B=pairs, Hkv=1, S=0, W=W)
+    st = lib().nd_tree_decode(A, ctypes.byref(c), A, A, L(64), L(64), A, A, 1, 1, 8, A, None, None, Z(0), None)
+    assert st == UNSUPPORTED
+    assert nd.nd_tree_decode_workspace_size(pairs, 1, 1, 1, 64, W - 128) > 0
 
 
 def rope_cfg(r=64, inter=0, inv=0, scaling=0, theta=1e4, factor=4.0, low=1.0, high=32.0, orig=4096.0, mag=1.0):
