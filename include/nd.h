@@ -459,7 +459,8 @@ ND_API int nd_tree_layout(const int32_t *parents, const int32_t *n_nodes, const 
  * region not much longer than its contents is the faster one.
  * Partial results go to the workspace (device, 16-byte aligned) of
  * nd_tree_decode_workspace_size(batch, n, n_q_heads, n_kv_heads, head_dim,
- * sink_cap + ring_cap) bytes (0: none is needed, NULL allowed).
+ * sink_cap + ring_cap) bytes (0: none is needed, NULL allowed; also the size of
+ * what nd_tree_decode refuses).
  */
 ND_API size_t nd_tree_decode_workspace_size(int batch, int n, int n_q_heads, int n_kv_heads,
                                             int head_dim, int max_slots);

@@ -962,9 +962,15 @@ static bool tree_sizes_ok(int64_t batch, int n_kv_heads, int64_t slots) {
   return batch * n_kv_heads <= (1 << 20) && slots <= kMostSlots;
 }
 
+// The shapes that tree_decode.cu's plan is made for: a node's group of heads is
+// at most 8 of the 128 rows of a product.
+static bool tree_shape_ok(int n, int n_q_heads, int n_kv_heads, int head_dim) {
+  return n <= ND_TREE_MAX_NODES && n_q_heads / n_kv_heads <= 8 && (head_dim == 64 || head_dim == 128);
+}
+
 size_t nd_tree_decode_workspace_size(int batch, int n, int n_q_heads, int n_kv_heads, int head_dim, int max_slots) {
-  if (batch <= 0 || n <= 0 || n > ND_TREE_MAX_NODES || n_q_heads <= 0 || n_kv_heads <= 0 || n_q_heads % n_kv_heads ||
-      head_dim <= 0 || max_slots <= 0 || !tree_sizes_ok(batch, n_kv_heads, max_slots) ||
+  if (batch <= 0 || n <= 0 || n_q_heads <= 0 || n_kv_heads <= 0 || n_q_heads % n_kv_heads || max_slots <= 0 ||
+      !tree_shape_ok(n, n_q_heads, n_kv_heads, head_dim) || !tree_sizes_ok(batch, n_kv_heads, max_slots) ||
       !tree_decode_fits(batch, n, n_kv_heads, max_slots, 1))
     return 0;
   return round_up(tree_decode_workspace_bytes(batch, n, n_q_heads, n_kv_heads, head_dim, max_slots), 256);
@@ -977,7 +983,7 @@ int nd_tree_decode(const void *q, const nd_kv_cache *cache, const void *k_new, c
   if (st != ND_OK) return st;
   const int d = cache->head_dim, Hkv = cache->n_kv_heads;
   if (n < 0 || window < 1 || n_q_heads <= 0 || n_q_heads % Hkv) return ND_ERR_INVALID_ARG;
-  if (n > ND_TREE_MAX_NODES || n_q_heads / Hkv > 8 || (d != 64 && d != 128)) return ND_ERR_UNSUPPORTED;
+  if (!tree_shape_ok(n, n_q_heads, Hkv, d)) return ND_ERR_UNSUPPORTED;
   if (cache->batch == 0 || n == 0) return ND_OK;
   if (!q || !k_new || !v_new || !out || !depth || !mask) return ND_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(out)) return ND_ERR_INVALID_ARG;

@@ -4,13 +4,17 @@ anything is enqueued (no GPU is needed); and what the binding makes."""
 import contextlib
 import copy
 import ctypes
+import os
 import pickle
+import subprocess
+import sys
 
 import pytest
 import torch
 
 import sliding_window_kv_swa_gb300 as nd
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 OK, INVALID, UNSUPPORTED, CUDA, WORKSPACE = range(5)
 P, Z, F, L = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_float, ctypes.c_int64
 A, BAD = P(4096), P(4104)   # aligned and misaligned addresses; nothing is read
@@ -101,6 +105,21 @@ def test_tree_decode_refuses_what_the_workspace_size_is_no_answer_for():
     st = lib().nd_tree_decode(A, ctypes.byref(c), A, A, L(64), L(64), A, A, 1, 1, 8, A, None, None, Z(0), None)
     assert st == UNSUPPORTED
     assert nd.nd_tree_decode_workspace_size(pairs, 1, 1, 1, 64, W - 128) > 0
+
+
+REFUSED_SHAPES = [(256, 80, 1, 64), (256, 128, 1, 128), (1, 9, 1, 64), (64, 18, 2, 128), (2, 2 ** 30, 1, 64), (5, 8, 2, 32),
+                  (5, 8, 2, 96), (5, 8, 2, 256), (5, 8, 2, 2 ** 31 - 1)]    # n, Hq, Hkv, d
+
+
+def test_tree_decode_workspace_size_of_refused_shapes_is_zero():
+    # in a process of its own: a division by the CTAs that such groups leave (none) ends it
+    code = f"import sliding_window_kv_swa_gb300 as nd; print([nd.nd_tree_decode_workspace_size(1, *s, 20000) for s in {REFUSED_SHAPES}])"
+    done = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT)
+    assert done.returncode == 0 and done.stdout.strip() == str([0] * len(REFUSED_SHAPES)), (done.returncode, done.stdout, done.stderr)
+    for n, Hq, Hkv, d in REFUSED_SHAPES[:-1]:
+        c = cache(Hkv=Hkv, d=d, S=20000, W=0)
+        st = lib().nd_tree_decode(A, ctypes.byref(c), A, A, L(Hkv * d), L(Hkv * d), A, A, n, Hq, 8, A, None, None, Z(0), None)
+        assert st == UNSUPPORTED, (n, Hq, Hkv, d)
 
 
 def rope_cfg(r=64, inter=0, inv=0, scaling=0, theta=1e4, factor=4.0, low=1.0, high=32.0, orig=4096.0, mag=1.0):
