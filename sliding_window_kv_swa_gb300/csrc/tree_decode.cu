@@ -781,7 +781,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
       const bool more = x < x1;
       // the products that read the Q before are done once the last S is; the other
       // warpgroup may have been the one to see it
-      if (round > 0 && !fail) fail = !ring_wait(&sm.s_full[(g - 1) & 1], ((g - 1) >> 1) & 1, abort_flag);
+      if (round > 0) {
+        if (!fail) fail = !ring_wait(&sm.s_full[(g - 1) & 1], ((g - 1) >> 1) & 1, abort_flag);
+        tc_fence_after();  // Q is overwritten behind those products' reads
+      }
       if (more) {
         // ---- Q: half a row, as fp16 times 2^eq of the row (its lines were asked
         // into L2; a row per lane reads each of them eight times, from L1 but once)

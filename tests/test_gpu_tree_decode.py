@@ -353,3 +353,25 @@ def test_the_whole_step():
         tu.commit(ref, host(kr).astype(np.float32), x[2], wp, wl)
         for f in tu.FIELDS:
             np.testing.assert_array_equal(host(getattr(cache, f)), getattr(ref, f), err_msg=f)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,n", [(16, 16, 64, 13), (32, 8, 128, 16), (8, 2, 128, 40)])
+def test_a_ctas_many_pairs_are_those_of_calls_of_their_own(Hq, Hkv, d, n):
+    """A CTA walks several short (sequence, KV head) pairs, whose queries replace one another while the products before still end;
+    a call of few sequences gives each pair a CTA.  Neither splits a pair, so the outputs are equal bit for bit, every time."""
+    rng = philox(22800 + d + n)
+    ctas = 152 // -(-n * (Hq // Hkv) // 128)      # per block of 128 rows
+    B, S, W, window = 4 * ctas // Hkv, 40, 100, 60
+    ref = tu.random_cache(rng, B, Hkv, d, S, W)
+    depth, _, mask, _ = tu.layout(tu.random_parents(rng, B, n), None, ref.seq_len, 0, window)
+    (q, k, v), _ = nodes(rng, B, n, Hq, Hkv, d)
+    q[1::2] = -q[::2][:len(q[1::2])]
+    cache, dd, dm = tu.device_cache(ref), i32(depth), i32(mask)
+    want = torch.empty_like(q)
+    few = ctas // Hkv
+    for b in range(0, B, few):
+        part = slice(b, min(b + few, B))
+        one = nd().KVCache(*(getattr(cache, f)[part].contiguous() for f in tu.FIELDS), S, W)
+        nd().nd_tree_decode(q[part], one, k[part], v[part], dd[part], dm[part], window, out=want[part])
+    for _ in range(20):
+        assert torch.equal(nd().nd_tree_decode(q, cache, k, v, dd, dm, window), want)
