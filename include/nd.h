@@ -445,8 +445,9 @@ ND_API int nd_tree_layout(const int32_t *parents, const int32_t *n_nodes, const 
  *   4097; batch * n_kv_heads * (ceil(slots/128) + 1 + ceil(n/64)) below 2^30
  * A row that sees no key, and padding, get out = 0, lse = -inf, and so does a
  * query head with a NaN or an infinity, as in nd_swa_sink_decode.  A row that
- * sees a node whose key or value (of its KV head) holds one is NaN in all
- * channels and lse; rows that do not see it are not touched by it.
+ * sees a node whose key or value (of its KV head) holds one, or a cached slot
+ * with a NaN or an infinity among its scales, is NaN in all channels and lse;
+ * rows that do not see it are not touched by it.
  * Precision: cached keys and values become fp16 after a power-of-two scaling per
  * 32 slots (and for values one that follows the largest so far): a key is within
  * 2^-10 of code * scale or 2^-21 of the largest among its 32, whichever is more,

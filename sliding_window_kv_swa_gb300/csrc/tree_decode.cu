@@ -26,9 +26,11 @@
 // behind and all of it scaled by 2^7.  Sums, maxima and partials are fp32.
 //
 // Masked places.  A weight of 0 times a NaN or an infinity would be NaN, so
-// slots and nodes that nothing may see are 0 in the operands; a node whose key
+// slots and nodes that nothing may see are 0 in the operands.  A node whose key
 // or value is not finite is 0 too and makes NaN of the scores of the rows that
-// see it.  A row that sees nothing (or whose query is not finite) ends with m =
+// see it; so is a cached slot with a scale that is not finite, which counts nothing
+// for its keys' exponent and makes NaN of the sums of the rows that see it (the
+// window may hide it from deeper ones).  A row that sees nothing (or whose query is not finite) ends with m =
 // -inf and l = 0 and comes out 0.
 //
 // Lanes.  The products have 128 rows whatever R is.  With R <= 64 (32) the rows
@@ -180,6 +182,7 @@ struct Lay {
     float2 ml[BM];               // and what their copies have
     uint32_t tmem;
     int abort;
+    int any_bad;                 // a slot so far has a scale that is not finite
   };
   static constexpr int kBytes = oSmall + int(sizeof(Small));
   static_assert(kBytes <= 227 * 1024, "shared memory");
@@ -220,6 +223,14 @@ __device__ __forceinline__ void prefetch_l2(const void *src) {
 }
 __device__ __forceinline__ void cp_async8(uint32_t dst, const void *src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+// A predicated store, not a branch: with one among the codes' warps the compiler
+// spills in every role (128 sessions of 16 nodes 136 us against 129, 8 of 64 over
+// 33024 slots 309 against 272).
+__device__ __forceinline__ void set_if(int *flag, bool x) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %0, 0;\n @p st.shared.u32 [%1], 1;\n}\n" ::"r"(uint32_t(x)),
+               "r"(smem_u32(flag))
+               : "memory");
 }
 // A row's NG scales; and put back as pairs of fp16, times a power of two.
 template <int NG>
@@ -351,6 +362,27 @@ __device__ __forceinline__ int live_tile(const TreePlan &pl, const Seg &s, int t
   return t;
 }
 
+// The newest of a segment's ring entries with a scale that is not finite, INT_MAX
+// where a sink has one, -1 where none has; a walk over the segment's scales by each
+// warp, taken only by CTAs that have met such a slot.
+template <int NG>
+__device__ __noinline__ int bad_slots(const nd_kv_cache &c, int pair, int sink0, int sink1, int e0, int e1, int ring0) {
+  const size_t base = pair * (size_t(c.sink_cap) + c.ring_cap);
+  int newest = -1;
+#pragma unroll 1
+  for (int i = e0 - (sink1 - sink0) + int(threadIdx.x & 31); i < e1; i += 32) {  // sinks, as it were, before the entries
+    const bool sink = i < e0;
+    unsigned w = unsigned(ring0) + unsigned(max(i, 0));
+    if (w >= unsigned(c.ring_cap)) w -= unsigned(c.ring_cap);
+    const size_t at = (base + (sink ? size_t(sink1 - (e0 - i)) : size_t(c.sink_cap) + w)) * NG;
+    bool bad = false;
+#pragma unroll
+    for (int j = 0; j < NG; ++j) bad = bad || !(fabsf(c.k_scale[at + j]) < INFINITY) || !(fabsf(c.v_scale[at + j]) < INFINITY);
+    if (bad) newest = sink ? INT_MAX : max(newest, i);
+  }
+  return __reduce_max_sync(0xffffffffu, newest);
+}
+
 template <int D, int REP>
 __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_constant__ TreeParams p) {
   using Y = Lay<D>;
@@ -385,6 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
     mbar_init(&sm.q_full, 8);
     for (int s = 0; s < 4; ++s) mbar_init(&sm.v_known[s], 4);
     sm.abort = 0;
+    sm.any_bad = 0;
     fence_barrier_init();
   }
   if (warp == kWarpS) {
@@ -569,11 +602,17 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
           const uint32_t at = stage + Y::kCodes + (row_w + lane) * (NG * 4);
           float y[NG], most = 0.f;
           lds_row<NG>(at, y);
+          // a slot behind the last, whatever is staged, and one that is not finite count 0
+          const bool held = row_w + lane < cnt;
+          bool ok = held;
+#pragma unroll
+          for (int j = 0; j < NG; ++j) ok = ok & (fabsf(y[j]) < INFINITY);
 #pragma unroll
           for (int j = 0; j < NG; ++j) {
-            if (row_w + lane >= cnt) y[j] = 0.f;  // a slot behind the last: whatever is staged counts 0
+            if (!ok) y[j] = 0.f;
             most = fmaxf(most, fabsf(y[j]));
           }
+          set_if(&sm.any_bad, held & !ok);
           // (of values >= 0 the bits order as the values do)
           most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
           const int e = min(kMostUp, clamp_exp(14 - ilog2(most)));
@@ -768,6 +807,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
       int depth;
       bool dead;  // padding, or not finite
     };
+    // ring entries below it are outside the row's window
+    // (a dead row takes what comes and is put to 0 at the end)
+    auto first_seen = [&](const Row &row, const Seg &seg) {
+      return row.dead ? 0 : int(min((long long)INT_MAX, max(0ll, (long long)row.depth + seg.nv - p.window + 1)));
+    };
     Ring<NK> vr;
     int g = 0, x = x0;
     bool first_seg = true;
@@ -824,6 +868,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
         const int last = g - 1;
         if (!fail) fail = !ring_wait(&sm.pv_done[last & 1], (last >> 1) & 1, abort_flag);
         tc_fence_after();
+        if (__any_sync(0xffffffffu, *(volatile int *)&sm.any_bad)) {
+          // the rows that see a slot that is not finite
+          const int newest = bad_slots<NG>(p.c, s.pair, min(s.sl, s.t0 * BN), min(s.sl, min(s.t1, pl.ts) * BN),
+                                           min(s.nv, max(0, s.t0 - pl.ts) * BN), min(s.nv, max(0, s.t1 - pl.ts) * BN), s.ring0);
+          if (newest >= first_seen(me, s)) l = __uint_as_float(0x7fffffffu);
+        }
         const float2 o = other(m_own, l);
         const float m_used = me.dead ? -INFINITY : fmaxf(m_own, o.x);
         // (a half that saw nothing has l = 0)
@@ -923,9 +973,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
       me = next_row;
       const bool dead = me.dead;
       const uint32_t *mask_row = p.mask + (int64_t(s.b) * p.n + node) * words;
-      // ring entries below `low` are outside the row's window
-      // (a dead row takes what comes and is put to 0 at the end)
-      const int low = dead ? 0 : int(min((long long)INT_MAX, max(0ll, (long long)me.depth + s.nv - p.window + 1)));
+      const int low = first_seen(me, s);
       m_own = -INFINITY, l = 0.f, e_o = INT_MAX;
       const int first_t = min(live_tile(pl, s, s.t0), s.t1 - 1);
       // a tile of cached keys, all of them seen by the warp's rows (0) or not (1), or of

@@ -375,3 +375,57 @@ def test_a_ctas_many_pairs_are_those_of_calls_of_their_own(Hq, Hkv, d, n):
         nd().nd_tree_decode(q[part], one, k[part], v[part], dd[part], dm[part], window, out=want[part])
     for _ in range(20):
         assert torch.equal(nd().nd_tree_decode(q, cache, k, v, dd, dm, window), want)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(8, 2, 64), (8, 2, 128)])
+@pytest.mark.parametrize("n,S,W,window", [(5, 40, 50, 6), (12, 5, 200, 150), (70, 60, 300, 290), (40, 200, 9000, 8990)])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_a_slot_that_is_not_finite_reaches_the_rows_that_see_it_alone(Hq, Hkv, d, n, S, W, window, bad):
+    """A ring entry that the window leaves behind a few nodes down, and a sink: rows that see one are NaN, channels and lse; the
+    others are, bit for bit, what they are where the slots' scales are 0, and within the tolerance of the cache without them."""
+    rng = philox(22900 + n + d)
+    B, G = 3, Hq // Hkv
+    ref = tu.random_cache(rng, B, Hkv, d, S, W, [(S, 2 * W + 7), (S, W), (S, W // 2)])
+    parents = tu.random_parents(rng, B, n, reach=2, roots=0)
+    parents[:, 0] = -1
+    depth, _, mask, see = tu.layout(parents, None, ref.seq_len, 0, window)
+    (q, k, v), x = nodes(rng, B, n, Hq, Hkv, d)
+    hit, clean, spoilt = np.zeros((B, n, Hq), bool), tu.device_cache(ref), tu.device_cache(ref)
+    for b, h, which, group in ((0, 0, "k_scale", 0), (0, 1, "v_scale", 1), (1, 1, "k_scale", 1), (1, 1, "v_scale", 0)):
+        rl, rs = int(ref.ring_len[b]), int(ref.ring_start[b])
+        e = max(rl - window, 0) + 2                          # at depth 0 among the oldest that the window reaches
+        slot = S + (rs + e) % W
+        getattr(clean, which)[b, h, slot], getattr(spoilt, which)[b, h, slot] = 0.0, 0.0
+        getattr(spoilt, which)[b, h, slot, group] = bad
+        hit[b, :, h * G:(h + 1) * G] |= ((depth[b] >= 0) & (depth[b] + rl - e < window))[:, None]
+    assert hit[0].any() and (n < 12 or not hit[0].all())
+    clean.v_scale[2, 0, S - 1], spoilt.v_scale[2, 0, S - 1] = 0.0, bad    # a sink: all rows of its head
+    hit[2, :, :G] = True
+    lse, lse0 = (torch.empty((B, Hq, n), dtype=torch.float32, device="cuda") for _ in range(2))
+    out = nd().nd_tree_decode(q, spoilt, k, v, i32(depth), i32(mask), window, lse=lse)
+    other = nd().nd_tree_decode(q, clean, k, v, i32(depth), i32(mask), window, lse=lse0)
+    t = torch.from_numpy(hit).cuda()
+    assert torch.isnan(out[t]).all() and torch.isnan(lse.transpose(1, 2)[t]).all()
+    assert torch.equal(out[~t], other[~t]) and torch.equal(lse.transpose(1, 2)[~t], lse0.transpose(1, 2)[~t])
+    want, _ = tu.decode_rows(x[0], ref, x[1], x[2], depth, see, window)
+    assert_close_bf16(host(out)[~hit], want[~hit])
+
+
+def test_an_appended_infinity_is_left_behind_by_deep_nodes():
+    """A token with an infinity goes into the cache as its codec has it; nodes deeper than the window do not see it."""
+    rng = philox(22950)
+    B, n, Hq, Hkv, d, S, W, window = 1, 12, 8, 2, 64, 20, 40, 6
+    ref = tu.random_cache(rng, B, Hkv, d, S, W)
+    cache = tu.device_cache(ref)
+    bits, x = normal_bf16(rng, (B, 2 * Hkv, d))
+    kv = dev_bf16(bits)
+    kv[0, 0, 9], kv[0, 3, 40] = float("inf"), float("-inf")              # the key of head 0, the value of head 1
+    nd().nd_kv_append_quant(cache, kv[:, :Hkv].contiguous(), kv[:, Hkv:].contiguous())
+    oracle.kv_append(ref, x[:, :Hkv], x[:, Hkv:])                        # (finite ones in its place)
+    parents = np.arange(n, dtype=np.int32)[None] - 1
+    depth, _, mask, see = tu.layout(parents, None, ref.seq_len, 0, window)
+    (q, k, v), y = nodes(rng, B, n, Hq, Hkv, d)
+    out = host(nd().nd_tree_decode(q, cache, k, v, i32(depth), i32(mask), window))
+    want, _ = tu.decode_rows(y[0], ref, y[1], y[2], depth, see, window)
+    assert np.isnan(out[0, :window - 1]).all()
+    assert_close_bf16(out[0, window - 1:], want[0, window - 1:])
