@@ -453,9 +453,12 @@ ND_API int nd_tree_layout(const int32_t *parents, const int32_t *n_nodes, const 
  * 2^-10 of code * scale or 2^-21 of the largest among its 32, whichever is more,
  * a value within 2^-10 of itself or 2^-21 of the largest among its 32; scales
  * below 2^-74 count as less.  Nodes' keys are exact down to 2^-28 of the largest
- * of their row, their values exact and their weights within 2^-9 of themselves;
- * a cached slot's weight is within 2^-11 of itself or 2^-32 of the largest.
- * Products and sums are fp32.
+ * of their row, their values exact and their weights within 2^-8 of themselves;
+ * a cached slot's weight is within 2^-11 of itself or 2^(k-32) of the row's
+ * largest, whichever is more, 2^k being the power of two by which the largest
+ * value scale among the slots up to its tile of 128, whether the row sees them or
+ * not, exceeds the largest among its 32 (weights beside values 2^33 larger may
+ * come out as 0).  Products and sums are fp32.
  * How the work is split goes by the cache's capacities, not by what it holds: a
  * region not much longer than its contents is the faster one.
  * Partial results go to the workspace (device, 16-byte aligned) of

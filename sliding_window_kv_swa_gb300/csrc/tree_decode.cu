@@ -21,7 +21,7 @@
 // lowers it.  q (bf16) becomes fp16 exactly after a power of two per row (channels
 // 2^-28 below the row's largest lose bits).  A node's key gets a power of two of
 // its own and is then exact in the same way; its values stay bf16, and their
-// weights are bf16 (2^-9 of themselves) with O's power of two, which bf16's range
+// weights are bf16 (2^-8 of themselves) with O's power of two, which bf16's range
 // has room for.  Cached keys' weights are fp16 with the running maximum up to 2^8
 // behind and all of it scaled by 2^7.  Sums, maxima and partials are fp32.
 //
@@ -30,8 +30,8 @@
 // or value is not finite is 0 too and makes NaN of the scores of the rows that
 // see it; so is a cached slot with a scale that is not finite, which counts nothing
 // for its keys' exponent and makes NaN of the sums of the rows that see it (the
-// window may hide it from deeper ones).  A row that sees nothing (or whose query is not finite) ends with m =
-// -inf and l = 0 and comes out 0.
+// window may hide it from deeper ones).  A row that sees nothing (or whose query
+// is not finite) ends with m = -inf and l = 0 and comes out 0.
 //
 // Lanes.  The products have 128 rows whatever R is.  With R <= 64 (32) the rows
 // stand two (four) times in Q, and each copy takes its own half (quarter) of a
@@ -1093,8 +1093,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
           if (REP == 1) load(col);
 #pragma unroll
           for (int h = 0; h < kC; h += 32) {
-            // weights carry what V's operand lacks of O's scale: never more than 1
-            // for codes, and where that is below 2^-60, V does not matter
+            // weights carry what V's operand lacks of O's scale, never more than 1 for
+            // codes: fp16 keeps them to 2^(-32-up) of the row's largest.  Below 2^-60
+            // none is left of them (fp16 ends at 2^-25 of what is at most 2^15)
             const int up = kN ? e_now - kCodeBits : max(e_now - sm.e[1][g % kInfo][(col + h) / 32], -60);
             const float ct = factor(col + h), shift = base_shift + float(up);
             const uint64_t c2 = pack_f32x2(ct, ct), nmc2 = pack_f32x2(shift, shift);

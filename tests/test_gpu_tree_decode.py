@@ -429,3 +429,55 @@ def test_an_appended_infinity_is_left_behind_by_deep_nodes():
     want, _ = tu.decode_rows(y[0], ref, y[1], y[2], depth, see, window)
     assert np.isnan(out[0, :window - 1]).all()
     assert_close_bf16(out[0, window - 1:], want[0, window - 1:])
+
+
+def check_bounds(ref, q, k, v, depth, see, window, zero_seen=0.9):
+    """Every channel within its own bound (tree_util.decode_bounds), which a zero output would not be."""
+    mask = tu.mask_words(see)
+    to = lambda a: torch.from_numpy(np.ascontiguousarray(a, np.float32)).cuda().to(torch.bfloat16)
+    lse = torch.empty((q.shape[0], q.shape[2], q.shape[1]), dtype=torch.float32, device="cuda")
+    got = host(nd().nd_tree_decode(to(q), tu.device_cache(ref), to(k), to(v), i32(depth), i32(mask), window, lse=lse))
+    want, bound, wlse, lse_bound = tu.decode_bounds(q, ref, k, v, depth, see, window)
+    assert (np.abs(want) > bound).mean() >= zero_seen
+    worst = (np.abs(got - want) / np.maximum(bound, 1e-300)).max()
+    assert worst <= 1, worst
+    seen = np.isfinite(wlse)
+    assert (np.abs(host(lse)[seen] - wlse[seen]) <= lse_bound[seen]).all()
+    return got, want, bound
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [8, 24, 80])                       # 4, 2 and 1 copies of the rows
+@pytest.mark.parametrize("S,W,grow", [(900, 300, 1 / 300), (900, 300, -1 / 300), (0, 700, 1 / 40), (0, 700, -1 / 40), (0, 700, -1 / 26)])
+def test_values_that_grow_or_fall_hold_to_each_channels_bound(d, n, S, W, grow):
+    """Value scales by powers of two along the cache, up to 2^26: with S = 0 the nodes' depths reach over the whole ring, so deep
+    ones see small values beside large ones that they do not.  Scores are small (keys 2^-6), so that a bound is mostly the
+    values': leaving out the first tile's, or a zero output, is far outside it."""
+    rng = philox(23000 + d + n)
+    B, Hq, Hkv = 1, 4, 2
+    ref = tu.random_cache(rng, B, Hkv, d, S, W, [(S, 2 * W + 7)])
+    place = np.concatenate([np.arange(S), S + (np.arange(W) - ref.ring_start[0]) % W])   # of a slot, sinks before the ring
+    ref.v_scale *= np.exp2(np.floor(grow * place)).astype(np.float32)[None, None, :, None]
+    ref.k_scale *= np.float32(2.0 ** -6)
+    step, window = (1, 400) if S else (W // n, W)
+    depth = step * np.arange(n, dtype=np.int32)[None]
+    see = np.eye(n, dtype=bool)[None]
+    _, (q, k, v) = nodes(rng, B, n, Hq, Hkv, d)
+    v = v if S else v * 2.0 ** np.floor(grow * W)
+    got, want, bound = check_bounds(ref, q, k * 2.0 ** -6, v, depth, see, window)
+    lost, _, _, _ = tu.decode_bounds(q, ref, k * 2.0 ** -6, v, depth, see, window, drop=range(128))
+    if S or grow < 0:
+        assert (np.abs(lost - want) > bound)[0, 0].mean() > 0.25
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_scores_of_many_sizes_hold_to_each_channels_bound(d):
+    """Scales of keys and values that differ from slot to slot; a short cache with as many nodes, whose weights are bf16."""
+    rng = philox(23100 + d)
+    for S, W, n, spread in ((150, 60, 18, 8), (0, 16, 60, 0), (700, 500, 5, 5)):
+        ref = tu.random_cache(rng, 1, 2, d, S, W)
+        ref.k_scale *= np.exp2(rng.integers(-6 - spread, -3, ref.k_scale.shape)).astype(np.float32)
+        ref.v_scale *= np.exp2(rng.integers(-spread, 3, ref.v_scale.shape)).astype(np.float32)
+        depth, _, _, see = tu.layout(tu.random_parents(rng, 1, n), None, ref.seq_len, 0, 99)
+        _, (q, k, v) = nodes(rng, 1, n, 8, 2, d)
+        check_bounds(ref, q, k * 2.0 ** -3, v, depth, see, 99)
