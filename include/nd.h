@@ -458,7 +458,9 @@ ND_API int nd_tree_layout(const int32_t *parents, const int32_t *n_nodes, const 
  * largest, whichever is more, 2^k being the power of two by which the largest
  * value scale among the slots up to its tile of 128, whether the row sees them or
  * not, exceeds the largest among its 32 (weights beside values 2^33 larger may
- * come out as 0).  Products and sums are fp32.
+ * come out as 0).  Products and sums are fp32.  Queries, keys and values are to
+ * stay below 2^40 and scores (q . k / sqrt(head_dim)) below 2^20 in magnitude:
+ * larger ones may overflow on the way.
  * How the work is split goes by the cache's capacities, not by what it holds: a
  * region not much longer than its contents is the faster one.
  * Partial results go to the workspace (device, 16-byte aligned) of

@@ -950,6 +950,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
                 l_all != 0.f ? 0.6931471805599453f * (m_all - kPBias + log2f(l_all)) : -INFINITY;
         } else if (!fail) {
           float *part = p.parts + (size_t(blockIdx.x) * 2 + (first_seg ? 0 : 1)) * part_floats<D>();
+          const float by = kUnits * down;  // (first: O times 2^24 may be too large)
 #pragma unroll 1
           for (int ch = wg * (D / 2); ch < (wg + 1) * (D / 2); ch += 16) {
             uint32_t ov[16];
@@ -958,8 +959,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
 #pragma unroll
             for (int i = 0; i < 16; i += 4)
               *reinterpret_cast<float4 *>(part + ((ch + i) / 4 * BM + tl) * 4) =
-                  make_float4(__uint_as_float(ov[i]) * kUnits * down, __uint_as_float(ov[i + 1]) * kUnits * down,
-                              __uint_as_float(ov[i + 2]) * kUnits * down, __uint_as_float(ov[i + 3]) * kUnits * down);
+                  make_float4(__uint_as_float(ov[i]) * by, __uint_as_float(ov[i + 1]) * by,
+                              __uint_as_float(ov[i + 2]) * by, __uint_as_float(ov[i + 3]) * by);
           }
           if (wg == 0) *reinterpret_cast<float2 *>(part + BM * D + 2 * tl) = make_float2(m_used, l);
         }

@@ -481,3 +481,25 @@ def test_scores_of_many_sizes_hold_to_each_channels_bound(d):
         depth, _, _, see = tu.layout(tu.random_parents(rng, 1, n), None, ref.seq_len, 0, 99)
         _, (q, k, v) = nodes(rng, 1, n, 8, 2, d)
         check_bounds(ref, q, k * 2.0 ** -3, v, depth, see, 99)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("S,W", [(40, 30), (5000, 64)])          # whole, split and merged
+def test_magnitudes_up_to_2_40(d, S, W):
+    """Values up to 2^39.9, alone or behind cached ones that are all 0; queries as large with keys as small."""
+    rng = philox(23200 + d)
+    n = 7
+    for cached, new in ((2.0 ** 37, 2.0 ** 37), (0.0, 2.0 ** 37), (2.0 ** 37, 2.0 ** -60), (2.0 ** -60, 2.0 ** -60)):
+        ref = tu.random_cache(rng, 1, 2, d, S, W)
+        ref.v_scale *= np.float32(cached)
+        ref.k_scale *= np.float32(2.0 ** -43)
+        depth, _, _, see = tu.layout(tu.random_parents(rng, 1, n), None, ref.seq_len, 0, 99)
+        _, (q, k, v) = nodes(rng, 1, n, 8, 2, d)
+        check_bounds(ref, q * 2.0 ** 37, k * 2.0 ** -43, v * new, depth, see, 99, 0.8)
+    # scores up to 2^19: a key or two take all the weight
+    ref.k_scale *= np.float32(2.0 ** 22)
+    ref.v_scale *= np.float32(2.0 ** 60)
+    to = lambda a: torch.from_numpy(np.ascontiguousarray(a, np.float32)).cuda().to(torch.bfloat16)
+    got = host(nd().nd_tree_decode(to(q * 2.0 ** 37), tu.device_cache(ref), to(k * 2.0 ** -21), to(v), i32(depth), i32(tu.mask_words(see)), 99))
+    top = max(np.abs(oracle.dequant_g32(ref.v_codes, ref.v_scale)).max(), np.abs(v).max())
+    assert np.isfinite(got).all() and np.abs(got).max() <= top * (1 + 2.0 ** -7) and (got != 0).mean() > 0.99
