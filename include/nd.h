@@ -793,12 +793,12 @@ ND_API int nd_qk_norm_rope_append(const void *q, const nd_kv_cache *cache, const
  *   inverse = 1: turned by -p * f_i instead (times magnitude): the gradient
  *     with respect to the unrotated heads, given the one of the rotated
  * r is a multiple of 16, at most head_dim; theta, factor, orig_len and
- * magnitude are finite and > 0 and 0 <= low < high (the fields that a scaling does not use
- * are not checked).
+ * magnitude are finite and > 0 and 0 <= low < high < infinity (the fields that a
+ * scaling does not use are not checked).
  * q, k, strides, positions, q_out, k_out, dtype, head_dim and the sizes as
  * nd_qk_norm_rope (either side may have 0 heads).  The angle is reduced to a
- * fraction of a turn in 64-bit integers, within 2^-53 |p| turns and an fp32
- * rounding; sine, cosine and the rotation are fp32, rounded once to dtype.
+ * fraction of a turn in 64-bit integers, within 2^-53 |p| max(1, f_i) turns and an
+ * fp32 rounding; sine, cosine and the rotation are fp32, rounded once to dtype.
  */
 typedef enum { ND_ROPE_PLAIN = 0, ND_ROPE_LINEAR = 1, ND_ROPE_BY_PARTS = 2 } nd_rope_scaling;
 typedef struct {

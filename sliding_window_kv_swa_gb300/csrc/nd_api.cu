@@ -3,6 +3,7 @@
 // Nothing here allocates memory; nothing here synchronises except
 // nd_device_errors().
 #include <cuda_runtime.h>
+#include <float.h>
 #include <limits.h>
 #include <stdint.h>
 
@@ -866,7 +867,7 @@ int nd_shared_prefix_decode(const void *q, const nd_kv_cache *prefix, const nd_k
 }
 
 // finite and > 0 (NaN fails every comparison)
-static bool positive(float x) { return x > 0.f && x < 1e30f; }
+static bool positive(float x) { return x > 0.f && x <= FLT_MAX; }
 
 static int validate_rope(const nd_rope_cfg *c, int head_dim) {
   if (!c || c->rotary_dim <= 0 || c->rotary_dim > head_dim) return ND_ERR_INVALID_ARG;
@@ -874,7 +875,7 @@ static int validate_rope(const nd_rope_cfg *c, int head_dim) {
   if (!positive(c->theta) || !positive(c->magnitude)) return ND_ERR_INVALID_ARG;
   if (c->scaling != ND_ROPE_PLAIN && c->scaling != ND_ROPE_LINEAR && c->scaling != ND_ROPE_BY_PARTS) return ND_ERR_INVALID_ARG;
   if (c->scaling != ND_ROPE_PLAIN && !positive(c->factor)) return ND_ERR_INVALID_ARG;
-  if (c->scaling == ND_ROPE_BY_PARTS && !(positive(c->orig_len) && c->low >= 0.f && c->low < c->high && c->high < 1e30f))
+  if (c->scaling == ND_ROPE_BY_PARTS && !(positive(c->orig_len) && c->low >= 0.f && c->low < c->high && c->high <= FLT_MAX))
     return ND_ERR_INVALID_ARG;
   return c->rotary_dim % 16 ? ND_ERR_UNSUPPORTED : ND_OK;
 }

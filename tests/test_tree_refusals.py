@@ -151,6 +151,17 @@ def test_rope_positions():
     assert call(B=1 << 16, T=1 << 15) == UNSUPPORTED
 
 
+def test_rope_positions_takes_every_finite_value():
+    def call(**kw):
+        return lib().nd_rope_positions(A, A, 1, 0, 3, 4, 2, 64, L(256), L(128), ctypes.byref(rope_cfg(**kw)), None, A, A, None)
+
+    for x in (1e-45, 1e30, 3.4e38):
+        for kw in (dict(theta=x), dict(mag=x), dict(scaling=1, factor=x), dict(scaling=2, factor=x), dict(scaling=2, orig=x)):
+            assert call(**kw) == OK, kw
+    assert call(scaling=2, high=1e30) == OK and call(scaling=2, low=1e30, high=3.4e38) == OK
+    assert call(scaling=2, high=float("inf")) == INVALID and call(theta=float("inf")) == INVALID and call(mag=float("nan")) == INVALID
+
+
 def test_the_binding_refuses_host_tensors_and_wrong_shapes():
     i = torch.zeros(1, 3, dtype=torch.int32)
     x = torch.zeros(1, 3, 2, 64, dtype=torch.bfloat16)
