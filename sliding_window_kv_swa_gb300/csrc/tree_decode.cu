@@ -151,9 +151,9 @@ __host__ __device__ constexpr size_t part_floats() {
 }
 
 // ------------------------------------------------------------ the kernel
-// A tile's record: what it is made of, whether its segment begins or ends with
-// it and the stretch ends, keys (bits 8-15) and those in the first piece (16-23).
-constexpr int kKindRing = 1, kKindNodes = 2, kFresh = 4, kEnd = 8, kLast = 16;
+// A tile's record: whether it is nodes, whether its segment begins and the stretch
+// ends with it, keys (bits 8-15) and those in the first piece (16-23).
+constexpr int kKindNodes = 1, kFresh = 2, kLast = 4;
 
 template <int D>
 struct Lay {
@@ -532,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
           const int count = __popc(__ballot_sync(0xffffffffu, mine));
           const bool end = nth(lane + 1) >= s.t1;
           if (mine) {
-            int4 rec = make_int4((fresh && lane == 0 ? kFresh : 0) | (end ? kEnd : 0) | (end && x >= x1 ? kLast : 0), 0, s.pair, 0);
+            int4 rec = make_int4((fresh && lane == 0 ? kFresh : 0) | (end && x >= x1 ? kLast : 0), 0, s.pair, 0);
             if (u < pl.ts + pl.tr) {
               const bool ring = u >= pl.ts;
               rec.y = (ring ? u - pl.ts : u) * BN;
@@ -545,7 +545,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_kernel(const __grid_c
                 if (w >= unsigned(p.c.ring_cap)) w -= unsigned(p.c.ring_cap);
                 c1 = min(cnt, p.c.ring_cap - int(w));
                 rec.w = p.c.sink_cap + int(w);
-                rec.x |= kKindRing;
               }
               rec.x |= cnt << 8 | c1 << 16;
             } else {
