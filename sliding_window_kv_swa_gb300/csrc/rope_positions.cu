@@ -254,8 +254,13 @@ const Turns &rope_turns(const nd_rope_cfg &c) {
   return t;
 }
 
-// As for the norm with rotation (qk_norm.cu): a warp to a token where its heads
-// fill two row sets and the rows are many.
+// A warp to a token where its heads fill two row sets (a warp's rows: 4 of bf16 at
+// D = 128) and the rows are many.  By token against by row, us: bf16, 40 heads of
+// 128, 1280 sets 3.2 and 2.7, 2560 3.4 and 3.4, 5120 3.3 and 4.5, 40960 15.3 and 24.3
+// (neighbours and a quarter of each head turned alike); 72 heads of 32 cross there
+// too, 20 heads of 256 at 1900.  fp32 crosses later: 40 heads of 128, 2560 sets 4.2
+// and 2.7, 5120 4.2 and 3.6, 10240 4.2 and 5.3.  5 heads of 64, less than a set, by
+// token lose at every length: 2560 sets 5.2 and 3.2.
 constexpr int kMinSets = 2, kFewSets = 2600;
 
 template <typename E, int D, bool kNeighbours>

@@ -22,9 +22,10 @@ __device__ __forceinline__ int node_count(const int32_t *n_nodes, int b, int n, 
 }
 
 // A thread per node walks up to its root: the steps are the depth, the first
-// `window` nodes on the way the mask.  One sequence of 8 nodes 1.9 us, 512 of 256
-// nodes (depths to 80; 23 MB written) 8.5: the longest walk, about 30 cycles a
-// step, and the mask's words behind it.
+// `window` nodes on the way the mask.  One sequence of 8 nodes 1.8 us, 512 of 256
+// nodes (depths to 80; 5.2 MB written) 8.7 to 9.4: 5.2 without the mask's words,
+// 5.8 without the walk.  The words are indexed by node, so they lie in local memory,
+// and every step within the window loads and stores one there.
 struct LayoutParams {
   const int32_t *parents, *n_nodes, *seq_len, *pos_base;
   int n, window;
@@ -126,9 +127,10 @@ struct CommitParams {
 // few neighbours is a cluster of CTAs; its metadata advance once all of them have
 // read them.
 // 512 sequences of up to 16 tokens of 8 heads of 128 (26 MB on average): 21 us,
-// 64 of up to 6 of 2 heads of 64: 3.6.  The codec costs more instructions than the
-// rows' latency hides: with its exact division tried per value instead of once
-// for a lane's eight, 26 and 5.5 us; a row to a warp, 55 and 4.2.
+// 64 of up to 6 of 2 heads of 64: 3.6.  80 registers a thread are three CTAs an SM,
+// so 512 sequences are a second round for 56 of them, and the codec costs more
+// instructions than so few warps' latencies hide: with its exact division tried per
+// value instead of once for a lane's eight, 26 and 5.5 us; a row to a warp, 55 and 4.2.
 template <int D>
 __global__ void __launch_bounds__(256) tree_commit_kernel(const __grid_constant__ CommitParams p) {
   constexpr int kL = D / 8, kU = 4;

@@ -59,10 +59,10 @@
 // What bounds it.  Below about 150 rows the read of the codes, above the
 // products.  Measured (D = 128): 128 sessions of 16 nodes (64 rows) over 1280
 // slots of 8 heads 129 us, the bytes 62 (48 % of the copy rate); 8 sessions of 64
-// nodes (256 rows) over 33024 slots 273 us, the products 142 (52 %).  No unit is
-// busy for much more than half of that: with conversion, exponentials and
-// products all left out, the roles' waits and bookkeeping alone took 111 (of 139)
-// and 208 (of 366) us.  A warp issues an instruction every five cycles, held up by
+// nodes (256 rows) over 33024 slots 270 to 275 us in a graph, 283 to 287 call by
+// call, the products 142 (50 to 53 %).  No unit is busy for much more than half of
+// that: with conversion, exponentials and products all left out, the roles' waits
+// and bookkeeping alone took 111 (of 139) and 208 (of 366) us.  A warp issues an instruction every five cycles, held up by
 // latencies, by the others and by instruction fetches: code that is not needed for
 // most tiles costs all of them (see tile() and ring_wait()).  Without effect on
 // these two: 16 warps that convert, four that stage Q beside the softmax, three
@@ -96,7 +96,13 @@ constexpr int kCodeBits = 24;     // operands made of codes hold 2^-24 of code *
 constexpr int kMostUp = 88;       // V's largest e: a node's value times 2^(88 - 24 + 15) stays finite up to 2^48
 constexpr float kUnits = 16777216.f;  // 2^24
 constexpr int kCtas = 152;        // one per SM
-constexpr int kFewTiles = 4;      // of a pair (4 pairs of 4 tiles: 9.3 us whole, 16.7 a tile to a CTA and merged)
+// A pair of so few tiles is not split while every pair has a CTA: whole against
+// split, 3 and 4 tiles (cached ones and nodes) of 2 to 128 pairs took 8.6 to 10 us
+// against 11 to 19 with heads of 64 (8 nodes, 4 query heads per KV head), 11.3 to
+// 13.3 against 13.2 to 24.7 with heads of 128 (16 nodes).  At 8 tiles 20 pairs are as
+// fast either way (11.8 against 13.3, 16.7 against 15.4), 64 and more faster whole
+// (12.0 against 20.5, 17.1 against 24.4).
+constexpr int kFewTiles = 4;
 
 // ------------------------------------------------------------ the split
 struct TreePlan {
