@@ -503,3 +503,26 @@ def test_magnitudes_up_to_2_40(d, S, W):
     got = host(nd().nd_tree_decode(to(q * 2.0 ** 37), tu.device_cache(ref), to(k * 2.0 ** -21), to(v), i32(depth), i32(tu.mask_words(see)), 99))
     top = max(np.abs(oracle.dequant_g32(ref.v_codes, ref.v_scale)).max(), np.abs(v).max())
     assert np.isfinite(got).all() and np.abs(got).max() <= top * (1 + 2.0 ** -7) and (got != 0).mean() > 0.99
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,n", [(16, 16, 64, 5), (32, 8, 128, 16), (8, 2, 128, 40)])
+def test_slots_that_are_not_finite_in_some_of_a_ctas_pairs(Hq, Hkv, d, n):
+    """Among many short pairs to a CTA every seventh sequence has such a slot: its head's rows are NaN, all others' outputs are,
+    bit for bit, those where the slots' scales are 0."""
+    rng = philox(23300 + d + n)
+    ctas = 152 // -(-n * (Hq // Hkv) // 128)
+    B, S, W, window = 4 * ctas // Hkv, 40, 100, 60
+    ref = tu.random_cache(rng, B, Hkv, d, S, W)
+    depth, _, mask, _ = tu.layout(tu.random_parents(rng, B, n), None, ref.seq_len, 0, window)
+    (q, k, v), _ = nodes(rng, B, n, Hq, Hkv, d)
+    clean, spoilt = tu.device_cache(ref), tu.device_cache(ref)
+    hit = torch.zeros((B, n, Hq), dtype=torch.bool, device="cuda")
+    for b in range(3, B, 7):
+        h, slot, which = b % Hkv, (b * 11) % S, ("k_scale", "v_scale")[b % 2]
+        getattr(clean, which)[b, h, slot], getattr(spoilt, which)[b, h, slot] = 0.0, float("inf") if b % 3 else float("nan")
+        hit[b, :, h * (Hq // Hkv):(h + 1) * (Hq // Hkv)] = True
+    dd, dm = i32(depth), i32(mask)
+    want = nd().nd_tree_decode(q, clean, k, v, dd, dm, window)
+    for _ in range(5):
+        got = nd().nd_tree_decode(q, spoilt, k, v, dd, dm, window)
+        assert torch.isnan(got[hit]).all() and torch.equal(got[~hit], want[~hit])
